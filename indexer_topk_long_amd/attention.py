@@ -9,7 +9,7 @@ cu[b] .. cu[b+1]-1 of the call, at the last positions of its kv_len[b] tokens.
 from __future__ import annotations
 
 import ctypes
-import math
+import functools
 
 from ._binding import _c_i32, _c_i64, _c_p, _c_sz, LtkError, _expect, library
 
@@ -50,8 +50,8 @@ def _fn(name: str):
     return _FN[name]
 
 
-def _check(t, name, dtype, shape, device):
-    """A contiguous tensor of this dtype, shape (None: any size) and device."""
+def _refuse(t, name, dtype, shape, device):
+    """Raises the first thing wrong with a tensor: type, shape (None: any size), layout, device."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if len(t.shape) != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
@@ -59,29 +59,39 @@ def _check(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be [{want}], got {tuple(t.shape)}")
     if not (t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous device tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}: all tensors must share one device")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device}: all tensors must share one device")
+
+
+def _check(t, name, dtype, shape, device):
+    """The address of a contiguous tensor of exactly this dtype, shape and device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, device)
 
 
 def _cache(cache):
+    """(ltk_kv_cache, device index) of a (k, v, k_scale, v_scale)."""
     import torch
     _expect(isinstance(cache, (tuple, list)) and len(cache) == 4, "cache must be (k, v, k_scale, v_scale)")
     k, v, ks, vs = cache
-    dev, shape = k.device, tuple(k.shape)
-    pk = _check(k, "cache k", torch.float8_e4m3fn, (None,) * 4, None)
+    f8, f32, shape, dev = torch.float8_e4m3fn, torch.float32, k.shape, k.get_device()
+    if k.dtype is not f8 or len(shape) != 4 or dev < 0 or not k.is_contiguous():
+        _refuse(k, "cache k", f8, (None,) * 4, dev)
     n, hkv, page, d = shape
-    return _CCache(pk, _check(v, "cache v", torch.float8_e4m3fn, shape, dev),
-                   _check(ks, "k_scale", torch.float32, (n, hkv), dev),
-                   _check(vs, "v_scale", torch.float32, (n, hkv), dev), n, hkv, page, d), dev
+    per = (n, hkv)
+    return _CCache(k.data_ptr(), _check(v, "cache v", f8, shape, dev), _check(ks, "k_scale", f32, per, dev),
+                   _check(vs, "v_scale", f32, per, dev), n, hkv, page, d), dev
 
 
 def _batch(page_table, cu, kv_len, dev):
     import torch
-    pt = _check(page_table, "page_table", torch.int32, (None, None), dev)
-    B = page_table.shape[0]
-    pc = None if cu is None else _check(cu, "cu", torch.int32, (B + 1,), dev)
-    return _CBatch(pt, pc, _check(kv_len, "kv_len", torch.int32, (B,), dev), B, page_table.shape[1])
+    i32 = torch.int32
+    if len(page_table.shape) != 2:
+        _refuse(page_table, "page_table", i32, (None, None), dev)
+    B, mp = page_table.shape
+    pt = _check(page_table, "page_table", i32, (B, mp), dev)
+    pc = None if cu is None else _check(cu, "cu", i32, (B + 1,), dev)
+    return _CBatch(pt, pc, _check(kv_len, "kv_len", i32, (B,), dev), B, mp)
 
 
 class _On:
@@ -90,17 +100,16 @@ class _On:
 
     def __init__(self, device):
         import torch
-        self.cuda, self.index = torch.cuda, device.index
-        self.was = torch.cuda.current_device()
+        self.torch, self.index, self.was = torch, device, torch.cuda.current_device()
 
     def __enter__(self):
         if self.was != self.index:
-            self.cuda.set_device(self.index)
-        return self.cuda.current_stream(self.index).cuda_stream
+            self.torch.cuda.set_device(self.index)
+        return self.torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.was != self.index:
-            self.cuda.set_device(self.was)
+            self.torch.cuda.set_device(self.was)
 
 
 def _raise(rc, where):
@@ -120,20 +129,21 @@ def kv_append(k, v, cache, page_table, cu, kv_len, inv_freq=None, q=None, interl
     import torch
     c, dev = _cache(cache)
     b = _batch(page_table, cu, kv_len, dev)
-    T = k.shape[0]
-    pk = _check(k, "k", torch.bfloat16, (T, c.n_kv_heads, c.head_dim), dev)
-    pv = _check(v, "v", torch.bfloat16, (T, c.n_kv_heads, c.head_dim), dev)
+    T, bf16 = k.shape[0], torch.bfloat16
+    rows = (T, c.n_kv_heads, c.head_dim)
+    pk, pv = _check(k, "k", bf16, rows, dev), _check(v, "v", bf16, rows, dev)
     pf, rot = None, 0
     if inv_freq is not None:
-        pf, rot = _check(inv_freq, "inv_freq", torch.float64, (None,), dev), 2 * inv_freq.shape[0]
+        half = inv_freq.numel()
+        pf, rot = _check(inv_freq, "inv_freq", torch.float64, (half,), dev), 2 * half
     pq = po = None
     Hq = 0
     if q is not None:
-        pq = _check(q, "q", torch.bfloat16, (T, None, c.head_dim), dev)
-        Hq = q.shape[1]
+        Hq = q.shape[1] if len(q.shape) == 3 else None
+        pq = _check(q, "q", bf16, (T, Hq, c.head_dim), dev)
         if q_out is None:
             q_out = torch.empty_like(q)
-        po = _check(q_out, "q_out", torch.bfloat16, tuple(q.shape), dev)
+        po = _check(q_out, "q_out", bf16, q.shape, dev)
     else:
         _expect(q_out is None, "q_out without q")
     with _On(dev) as stream:
@@ -142,6 +152,7 @@ def kv_append(k, v, cache, page_table, cu, kv_len, inv_freq=None, q=None, interl
     return q_out
 
 
+@functools.lru_cache(maxsize=1024)   # sizes only
 def attend_workspace_bytes(kind: int, T: int, Hq: int, n_kv_heads: int, head_dim: int, n_seq: int,
                            entries: int) -> int:
     """Workspace bytes of an attend call (litetopk_attend_workspace_bytes)."""
@@ -153,24 +164,28 @@ def attend_workspace_bytes(kind: int, T: int, Hq: int, n_kv_heads: int, head_dim
 
 def _queries(q, c, scale, out, dev):
     import torch
-    pq = _check(q, "q", torch.bfloat16, (None, None, c.head_dim), dev)
-    T, Hq = q.shape[0], q.shape[1]
+    T, Hq = q.shape[:2] if len(q.shape) == 3 else (None, 0)
+    pq = _check(q, "q", torch.bfloat16, (T, Hq, c.head_dim), dev)
     _expect(Hq >= 1 and Hq % max(c.n_kv_heads, 1) == 0, f"q has {Hq} heads, the cache {c.n_kv_heads}: not a multiple")
     if out is None:
         out = torch.empty_like(q)
-    po = _check(out, "out", torch.bfloat16, tuple(q.shape), dev)
-    return pq, T, Hq, po, out, (1.0 / math.sqrt(c.head_dim) if scale is None else float(scale))
+        po = out.data_ptr()
+    else:
+        po = _check(out, "out", torch.bfloat16, q.shape, dev)
+    return pq, T, Hq, po, out, (c.head_dim ** -0.5 if scale is None else float(scale))
 
 
-def _space(kind, T, Hq, c, n_seq, entries, dev, workspace):
-    import torch
+def _space(kind, T, Hq, c, n_seq, entries, workspace, dev):
+    """(address, bytes, tensor) of the call's workspace."""
     need = attend_workspace_bytes(kind, T, Hq, c.n_kv_heads, c.head_dim, n_seq, entries)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        import torch
+        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+        return workspace.data_ptr(), need, workspace
     size = workspace.numel() * workspace.element_size()
     if size < need:
         raise ValueError(f"workspace too small: {size} bytes, {need} needed")
-    return _check(workspace, "workspace", workspace.dtype, (None,) * workspace.dim(), dev), size, workspace
+    return _check(workspace, "workspace", workspace.dtype, workspace.shape, dev), size, workspace
 
 
 def attend(q, cache, page_table, cu, kv_len, scale=None, window: int = 0, n_sink: int = 0, out=None, workspace=None):
@@ -181,7 +196,7 @@ def attend(q, cache, page_table, cu, kv_len, scale=None, window: int = 0, n_sink
     c, dev = _cache(cache)
     b = _batch(page_table, cu, kv_len, dev)
     pq, T, Hq, po, out, scale = _queries(q, c, scale, out, dev)
-    pw, nw, workspace = _space(ATTEND, T, Hq, c, b.n_seq, max(b.max_pages * c.page_size, 1), dev, workspace)
+    pw, nw, workspace = _space(ATTEND, T, Hq, c, b.n_seq, max(b.max_pages * c.page_size, 1), workspace, dev)
     with _On(dev) as stream:
         _raise(_fn("litetopk_attend")(ctypes.byref(c), ctypes.byref(b), pq, T, Hq, scale, window, n_sink, po, pw, nw,
                                       stream), "litetopk_attend")
@@ -196,10 +211,10 @@ def attend_selected(q, cache, page_table, cu, kv_len, idx, scale=None, out=None,
     c, dev = _cache(cache)
     b = _batch(page_table, cu, kv_len, dev)
     pq, T, Hq, po, out, scale = _queries(q, c, scale, out, dev)
-    pi = _check(idx, "idx", torch.int32, (T, None), dev)
-    topk = idx.shape[1]
+    topk = idx.shape[1] if len(idx.shape) == 2 else None
+    pi = _check(idx, "idx", torch.int32, (T, topk), dev)
     _expect(1 <= topk <= 65536, f"idx must hold 1 to 65536 keys a row, got {topk}")
-    pw, nw, workspace = _space(ATTEND_SELECTED, T, Hq, c, b.n_seq, topk, dev, workspace)
+    pw, nw, workspace = _space(ATTEND_SELECTED, T, Hq, c, b.n_seq, topk, workspace, dev)
     with _On(dev) as stream:
         _raise(_fn("litetopk_attend_selected")(ctypes.byref(c), ctypes.byref(b), pq, T, Hq, pi, topk, scale, po, pw,
                                                nw, stream), "litetopk_attend_selected")
@@ -218,12 +233,12 @@ def attend_packed(q, cache, page_table, kv_len, shared, masks, lens, group: int,
     _expect(1 <= group <= 32, f"group must lie in 1 .. 32, got {group}")
     pq, T, Hq, po, out, scale = _queries(q, c, scale, out, dev)
     ng = (T + group - 1) // group
-    ps = _check(shared, "shared", torch.int32, (ng, None), dev)
-    cap = shared.shape[1]
+    cap = shared.shape[1] if len(shared.shape) == 2 else None
+    ps = _check(shared, "shared", torch.int32, (ng, cap), dev)
     _expect(1 <= cap <= 1 << 26, f"shared must hold 1 to 2^26 entries a group, got {cap}")
     pm = _check(masks, "masks", torch.uint32, (ng, cap), dev)
     pl = _check(lens, "lens", torch.int32, (ng,), dev)
-    pw, nw, workspace = _space(ATTEND_PACKED, T, Hq, c, 1, cap, dev, workspace)
+    pw, nw, workspace = _space(ATTEND_PACKED, T, Hq, c, 1, cap, workspace, dev)
     with _On(dev) as stream:
         _raise(_fn("litetopk_attend_packed")(ctypes.byref(c), ctypes.byref(b), pq, T, Hq, ps, pm, pl, group, cap, scale,
                                              po, pw, nw, stream), "litetopk_attend_packed")

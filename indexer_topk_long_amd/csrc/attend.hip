@@ -36,6 +36,7 @@ constexpr int kWaves = 4;
 constexpr int kTile = 32;            // keys per wave step
 constexpr float kNoRef = -1e30f;     // reference before the first visible key
 constexpr float kSlack = 8.0f;       // scores may pass the reference by 2^8: weights up to 256 in fp16
+constexpr int kMinPer = 2 * kWaves;  // least key tiles of a workgroup's range: two per wave
 constexpr int kListChunk = 2048;     // list entries staged in LDS at a time
 
 __device__ __forceinline__ float max_groups(float x) {   // over the four 16-lane groups
@@ -67,10 +68,26 @@ struct KvTile {
     uint32_t v[8][D / 64];          // the lane's 8 keys, bytes c D/16 ..
 };
 
-// Per-key constants of one half, for the lane's keys 4 g + i.
-struct HalfScale {
-    float c[4], lv[4], iv[4];   // scale log2(e) ks, log2(vs), 1 / vs
+// Constants of a key: scale log2(e) ks, log2(vs), 1 / vs.  Dense tiles have
+// one set per half (a page holds at least 16 keys), listed keys one each.
+struct PageScale {
+    float c_, lv_, iv_;
+    __device__ __forceinline__ float c(int) const { return c_; }
+    __device__ __forceinline__ float lv(int) const { return lv_; }
+    __device__ __forceinline__ float iv(int) const { return iv_; }
 };
+struct KeyScale {
+    at_f32x4 c_, lv_, iv_;   // the lane's keys 4 g + i
+    __device__ __forceinline__ float c(int i) const { return c_[i]; }
+    __device__ __forceinline__ float lv(int i) const { return lv_[i]; }
+    __device__ __forceinline__ float iv(int i) const { return iv_[i]; }
+};
+
+// v_log_f32 is base 2; both it and v_rcp_f32 are exact on powers of two and
+// within 1 ulp elsewhere.
+__device__ __forceinline__ PageScale page_scale(float c2, float ks, float vs) {
+    return PageScale{c2 * ks, __builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs)};
+}
 
 // Running state of 16 query rows: reference, weight sum (of the lane's keys)
 // and the D / 16 x 4 accumulators of row c, dimensions (4 g + r) D/16 + e.
@@ -89,88 +106,97 @@ __device__ __forceinline__ void rescale(RowState<D>& st, float m_new) {
     st.m = m_new;
 }
 
-// Values as matrix operands: operand e holds byte e of the lane's 8 keys.
+// Word w of the lane's value bytes as matrix operands: operand e holds byte
+// 4 w + e of its 8 keys.
 template <int D>
-__device__ __forceinline__ void value_operands(const KvTile<D>& t, at_f16x8 (&a)[D / 16]) {
+__device__ __forceinline__ void value_operands(const KvTile<D>& t, int w, at_f16x8 (&a)[4]) {
 #pragma unroll
-    for (int w = 0; w < D / 64; ++w)
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {   // key pair (2p, 2p + 1)
-            const uint32_t lo = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x05010400u);
-            const uint32_t hi = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x07030602u);
-            const at_f16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
-            const at_f16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
-            const at_f16x2 x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
-            const at_f16x2 x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
-            a[4 * w + 0][2 * p] = x0[0], a[4 * w + 0][2 * p + 1] = x0[1];
-            a[4 * w + 1][2 * p] = x1[0], a[4 * w + 1][2 * p + 1] = x1[1];
-            a[4 * w + 2][2 * p] = x2[0], a[4 * w + 2][2 * p + 1] = x2[1];
-            a[4 * w + 3][2 * p] = x3[0], a[4 * w + 3][2 * p + 1] = x3[1];
-        }
+    for (int p = 0; p < 4; ++p) {   // key pair (2p, 2p + 1)
+        const uint32_t lo = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x05010400u);
+        const uint32_t hi = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x07030602u);
+        const at_f16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+        const at_f16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+        const at_f16x2 x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+        const at_f16x2 x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+        a[0][2 * p] = x0[0], a[0][2 * p + 1] = x0[1];
+        a[1][2 * p] = x1[0], a[1][2 * p + 1] = x1[1];
+        a[2][2 * p] = x2[0], a[2][2 * p + 1] = x2[1];
+        a[3][2 * p] = x3[0], a[3][2 * p + 1] = x3[1];
+    }
 }
 
-// One 32-key tile against MT x 16 query rows.  mask(mt, key) says whether the
-// lane's query row of tile mt sees key (0..31) of the tile; called only where
-// MASK.
-template <int D, int MT, bool MASK, class Mask>
-__device__ __forceinline__ void tile_step(const KvTile<D>& t, const at_bf16x8 (&q)[MT][D / 32], const HalfScale (&hs)[2],
-                                          RowState<D> (&st)[MT], int g, Mask mask) {
-    at_bf16x8 kf[2][D / 32];
+// One 32-key tile against MT x 16 query rows.  query(mt, j) is operand j of
+// row tile mt; mask(mt, key) says whether the lane's row of tile mt sees key
+// (0..31) of the tile, asked only where `masked` (the same in all lanes).
+//
+// The scheduling barriers keep the parts apart: left alone, the compiler
+// converts all of a tile's bytes first and holds 64 registers of operands.
+template <int D, int MT, class Query, class Scale, class Mask>
+__device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const Scale (&hs)[2], RowState<D> (&st)[MT],
+                                          bool masked, int g, Mask mask) {
+    at_f32x4 s[MT][2];
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+    for (int a = 0; a < 2; ++a) {
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-            kf[a][2 * h] = bf16_of(t.k[a][h][0], t.k[a][h][1]);
-            kf[a][2 * h + 1] = bf16_of(t.k[a][h][2], t.k[a][h][3]);
+        for (int mt = 0; mt < MT; ++mt) s[mt][a] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            const at_bf16x8 kf = bf16_of(t.k[a][j / 2][2 * (j % 2)], t.k[a][j / 2][2 * (j % 2) + 1]);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                s[mt][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, query(mt, j), s[mt][a], 0, 0, 0);
         }
-    at_f16x8 vf[D / 16];
-    value_operands<D>(t, vf);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    at_f16x8 p[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        at_f32x4 s[2];
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            s[a] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c)
-                s[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[a][c], q[mt][c], s[a], 0, 0, 0);
-        }
         float y[8], top = kNoRef;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float x = __builtin_fmaf(s[a][i], hs[a].c[i], hs[a].lv[i]);
-                if constexpr (MASK) x = mask(mt, 16 * a + 4 * g + i) ? x : -INFINITY;
-                y[4 * a + i] = x;
-                top = fmaxf(top, x);
-            }
+            for (int i = 0; i < 4; ++i) y[4 * a + i] = __builtin_fmaf(s[mt][a][i], hs[a].c(i), hs[a].lv(i));
+        if (masked) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[4 * a + i] = mask(mt, 16 * a + 4 * g + i) ? y[4 * a + i] : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
         if (__any(top > st[mt].m + kSlack)) rescale<D>(st[mt], fmaxf(st[mt].m, max_groups(top)));
-        at_f16x8 p;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
                 const float p0 = __builtin_amdgcn_exp2f(y[4 * a + i] - st[mt].m);
                 const float p1 = __builtin_amdgcn_exp2f(y[4 * a + i + 1] - st[mt].m);
-                st[mt].l = __builtin_fmaf(p0, hs[a].iv[i], st[mt].l);
-                st[mt].l = __builtin_fmaf(p1, hs[a].iv[i + 1], st[mt].l);
+                st[mt].l = __builtin_fmaf(p0, hs[a].iv(i), st[mt].l);
+                st[mt].l = __builtin_fmaf(p1, hs[a].iv(i + 1), st[mt].l);
                 const at_f32x2 pp{p0, p1};
                 const at_f16x2 ph = __builtin_convertvector(pp, at_f16x2);
-                p[4 * a + i] = ph[0], p[4 * a + i + 1] = ph[1];
+                p[mt][4 * a + i] = ph[0], p[mt][4 * a + i + 1] = ph[1];
             }
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e)
-            st[mt].o[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[e], p, st[mt].o[e], 0, 0, 0);
+    for (int w = 0; w < D / 64; ++w) {
+        at_f16x8 vf[4];
+        value_operands<D>(t, w, vf);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                st[mt].o[4 * w + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[e], p[mt], st[mt].o[4 * w + e], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
 // The waves' states joined through LDS, then the unit's rows written: bf16
-// rows when the unit has one split, else fp32 partial rows and (m, l).
-//   part layout per (unit, split): [16 MT] rows of D floats, then [16 MT] (m, l)
+// rows where this workgroup saw all of the unit's keys (part == NULL), else
+// fp32 partial rows: [16 MT] rows of D floats, then [16 MT] (m, l).
 template <int D, int MT, class Row>
-__device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT], float* sh, int64_t slot, int splits,
-                                       Row row_of) {
+__device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT], float* sh, float* part, Row row_of) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
     constexpr int kStride = D + 4;   // floats per row in LDS: rows start 4 banks apart
     float* so = sh;                          // [kWaves][16][kStride]
@@ -208,7 +234,7 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
         }
         const int64_t row = row_of(mt * 16 + r);   // row * Hq + head, -1 past the unit
         if (row < 0) continue;
-        if (splits == 1) {
+        if (!part) {
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
             uint32_t w[D / 32];
 #pragma unroll
@@ -219,12 +245,11 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
             else
                 *reinterpret_cast<at_u32x2*>(dst) = at_u32x2{w[0], w[1]};
         } else {
-            float* dst = a.part + slot * (16 * MT) * (D + 2);
 #pragma unroll
             for (int e = 0; e < D / 16; e += 4)
-                *reinterpret_cast<at_f32x4*>(dst + (size_t)(mt * 16 + r) * D + d0 + e) = at_f32x4{o[e], o[e + 1], o[e + 2], o[e + 3]};
+                *reinterpret_cast<at_f32x4*>(part + (size_t)(mt * 16 + r) * D + d0 + e) = at_f32x4{o[e], o[e + 1], o[e + 2], o[e + 3]};
             if ((threadIdx.x & 15) == 0) {
-                float* ml = dst + (size_t)16 * MT * D + (mt * 16 + r) * 2;
+                float* ml = part + (size_t)16 * MT * D + (mt * 16 + r) * 2;
                 ml[0] = m;
                 ml[1] = sum;
             }
@@ -233,52 +258,103 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
 }
 
 template <int D, int MT>
+constexpr int waves_per_simd() {
+    return MT == 4 ? (D == 64 ? 2 : 1) : MT == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);
+}
+
+template <int D, int MT>
+constexpr int part_floats() {
+    return 16 * MT * (D + 2);
+}
+
+template <int D, int MT>
 constexpr size_t finish_lds() {
     return (size_t)(kWaves * 16 * (D + 4) + kWaves * 16 * 2) * 4;
 }
 
-// Rows of a dense unit: sequence b's rows times the G query heads of one
-// key/value head, flattened as (row, head), 16 MT of them from r0 on.
-struct DenseUnit {
+// Dense work is cut evenly over the workgroups whatever the sequences'
+// lengths are.  Sequence b has units (key/value head, row tile): its rows
+// times the G heads of a key/value head, flattened as (row, head), 16 MT a
+// tile; each unit counts tiles_of(b) key tiles, those its last row sees.  The
+// tiles of all units of all sequences lie on one line, and workgroup w takes
+// [w per, (w + 1) per) of it, across unit borders.  A unit that lies in one
+// workgroup's range is written at once; the parts of the others are joined by
+// attend_join_kernel.  A workgroup leaves at most two such parts: of the unit
+// its range begins in, and of the one that goes on past its end.
+struct SeqWork {
     SeqRows sr;
-    int b, f0, f1;              // flattened range [f0, f1); empty when f0 >= f1
-    int pos_lo, pos_hi;         // positions of its first and last row
-    int sink_tiles, win_tile0;  // key tiles: [0, sink_tiles) and from win_tile0 on
-    int lo, hi;                 // visible keys: < n_sink (sinks) or in [lo, hi)
-    int tiles, per;             // key tiles in all, and per split
+    int tiles;       // key tiles per unit, at least 1 (a unit that sees nothing is one empty tile)
+    int row_tiles;
 };
 
+// Key tiles of the rows at positions pos_lo .. pos_hi: [0, sink_tiles) and
+// from win_tile0 on, tiles in all; keys below n_sink or in [lo, hi) are seen.
+struct KeyRange32 {
+    int lo, hi, sink_tiles, win_tile0, tiles;
+};
+__device__ __forceinline__ KeyRange32 key_range(const AttendArgs& a, int pos_lo, int pos_hi) {
+    KeyRange32 k;
+    k.hi = min(max(pos_hi + 1, 0), a.bt.max_pages << a.c.page_shift);
+    k.lo = a.window > 0 ? min(max(pos_lo - a.window + 1, 0), k.hi) : 0;
+    k.sink_tiles = a.window > 0 ? (min(a.n_sink, k.lo) + kTile - 1) / kTile : 0;
+    k.win_tile0 = max(k.lo / kTile, k.sink_tiles);
+    k.tiles = k.sink_tiles + max((k.hi + kTile - 1) / kTile - k.win_tile0, 0);
+    return k;
+}
+
 template <int MT>
-__device__ __forceinline__ DenseUnit dense_unit(const AttendArgs& a, int u) {
-    constexpr int RT = 16 * MT;
-    DenseUnit d;
-    d.b = unit_seq(a.bt, u, a.T, a.G, RT, 1);
-    d.sr = seq_rows(a.bt, d.b, a.T);
-    const int nth = u - unit_first(a.bt, d.b, a.T, a.G, RT, 1);
-    const int n = (d.sr.r1 - d.sr.r0) * a.G;
-    d.f0 = nth * RT;
-    d.f1 = min(d.f0 + RT, n);
-    if (nth < 0 || d.f0 >= n) {
-        d.f0 = d.f1 = 0;
-        return d;
+__device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int b) {
+    SeqWork w;
+    w.sr = seq_rows(a.bt, b, a.T);
+    const int n = w.sr.r1 - w.sr.r0, end = w.sr.pos0 + n;
+    w.row_tiles = (int)(((int64_t)n * a.G + 16 * MT - 1) / (16 * MT));
+    // no row tile sees more: all tiles up to the last row's, or with a window
+    // the sinks' and those that the window of its rows' positions can touch
+    const int64_t all = (min(max(end, 0), a.bt.max_pages << a.c.page_shift) + kTile - 1) / kTile;
+    int64_t most = all;
+    if (a.window > 0) {
+        const int span = min(n, (16 * MT + a.G - 1) / a.G + 1);
+        most = min(all, ((int64_t)a.n_sink + kTile - 1) / kTile + ((int64_t)a.window + span + kTile - 2) / kTile + 1);
     }
-    d.pos_lo = d.sr.pos0 + d.f0 / a.G;
-    d.pos_hi = d.sr.pos0 + (d.f1 - 1) / a.G;
-    const int cap = a.bt.max_pages << a.c.page_shift;
-    d.hi = min(max(d.pos_hi + 1, 0), cap);
-    d.lo = a.window > 0 ? min(max(d.pos_lo - a.window + 1, 0), d.hi) : 0;
-    const int sinks = a.window > 0 ? min(a.n_sink, d.lo) : 0;
-    d.sink_tiles = (sinks + kTile - 1) / kTile;
-    d.win_tile0 = max(d.lo / kTile, d.sink_tiles);
-    d.tiles = d.sink_tiles + max((d.hi + kTile - 1) / kTile - d.win_tile0, 0);
-    // whole rounds of the waves
-    d.per = ((d.tiles + a.splits - 1) / a.splits + kWaves - 1) / kWaves * kWaves;
-    return d;
+    w.tiles = max((int)most, 1);
+    return w;
+}
+
+constexpr int kPlanSeqs = 64 * kWaves;   // sequences looked at together
+struct PlanLds {
+    int64_t wave[kWaves];
+};
+
+// Work of sequence b (0 past the batch).
+template <int MT>
+__device__ __forceinline__ int64_t work_of(const AttendArgs& a, int b) {
+    if (b >= a.bt.n_seq) return 0;
+    const SeqWork w = seq_work<MT>(a, b);
+    return (int64_t)w.tiles * w.row_tiles * a.c.Hkv;
+}
+
+// Inclusive scan over the workgroup's threads; total of all in `sum`.
+__device__ __forceinline__ int64_t block_scan(int64_t x, PlanLds& ls, int64_t& sum) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) ls.wave[wave] = x;
+    __syncthreads();
+    sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) x += ls.wave[w];
+        sum += ls.wave[w];
+    }
+    return x;
 }
 
 template <int D, int MT>
-__device__ __forceinline__ void load_queries(const AttendArgs& a, at_bf16x8 (&q)[MT][D / 32], int64_t (&row)[MT], int c,
-                                             int g) {
+__device__ __forceinline__ void load_queries(const AttendArgs& a, at_bf16x8 (&q)[MT][D / 32], int64_t (&row)[MT], int g) {
     // row[mt]: row * Hq + head of the lane's query row, or -1
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -290,29 +366,22 @@ __device__ __forceinline__ void load_queries(const AttendArgs& a, at_bf16x8 (&q)
                 w = *reinterpret_cast<const at_u32x4*>(a.q + row[mt] * D + 64 * (j / 2) + 16 * g + 8 * (j % 2));
             q[mt][j] = __builtin_bit_cast(at_bf16x8, w);
         }
-    (void)c;
 }
 
 // ------------------------------------------------------------ dense keys
 
+// One unit's key tiles [t0, t1) against its rows [f0, f1) (flattened).
 template <int D, int MT>
-__global__ __launch_bounds__(64 * kWaves) void attend_kernel(AttendArgs a) {
-    extern __shared__ float sh[];
-    const int h = blockIdx.x % a.c.Hkv, rest = blockIdx.x / a.c.Hkv;
-    const int split = rest % a.splits, u = rest / a.splits;
-    const DenseUnit d = dense_unit<MT>(a, u);
-    if (d.f0 >= d.f1) return;
-    const int t0 = split * d.per, t1 = min(t0 + d.per, d.tiles);
-    if (split > 0 && t0 >= t1) return;   // split 0 of a unit that sees nothing writes its zeros
-    const int used = max((d.tiles + d.per - 1) / max(d.per, 1), 1);
+__device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& sr, int b, int h, int f0, int f1,
+                                           const KeyRange32& kr, int t0, int t1, float* sh, float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-
+    const int pos_lo = sr.pos0 + f0 / a.G, pos_hi = sr.pos0 + (f1 - 1) / a.G;
     auto row_of = [&](int r) -> int64_t {
-        const int f = d.f0 + r;
-        if (f >= d.f1) return -1;
+        const int f = f0 + r;
+        if (f >= f1) return -1;
         const int i = f / a.G;
-        return (int64_t)(d.sr.r0 + i) * a.Hq + h * a.G + (f - i * a.G);
+        return (int64_t)(sr.r0 + i) * a.Hq + h * a.G + (f - i * a.G);
     };
     at_bf16x8 q[MT][D / 32];
     int64_t row[MT];
@@ -321,45 +390,47 @@ __global__ __launch_bounds__(64 * kWaves) void attend_kernel(AttendArgs a) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         row[mt] = row_of(mt * 16 + c);
-        pos[mt] = row[mt] < 0 ? -1 : d.sr.pos0 + (d.f0 + mt * 16 + c) / a.G;
+        pos[mt] = row[mt] < 0 ? -1 : sr.pos0 + (f0 + mt * 16 + c) / a.G;
         st[mt].m = kNoRef;
         st[mt].l = 0.0f;
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) st[mt].o[e] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    load_queries<D, MT>(a, q, row, c, g);
+    load_queries<D, MT>(a, q, row, g);
+    auto query = [&](int mt, int j) { return q[mt][j]; };
 
-    const int32_t* table = a.bt.table + (size_t)d.b * a.bt.max_pages;
+    const int32_t* table = a.bt.table + (size_t)b * a.bt.max_pages;
     const int page = 1 << a.c.page_shift;
     struct Where {
         int key0, pid[2];   // page of each half, -1 when it has none
+        float ks[2], vs[2];
     };
-    auto where = [&](int t) {
-        Where w;
-        w.key0 = (t < d.sink_tiles ? t : d.win_tile0 + t - d.sink_tiles) * kTile;
+    auto ids = [&](int t, Where& w) {
+        w.key0 = (t < kr.sink_tiles ? t : kr.win_tile0 + t - kr.sink_tiles) * kTile;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            w.pid[x] = table[min((w.key0 + 16 * x) >> a.c.page_shift, a.bt.max_pages - 1)];
+    };
+    auto load = [&](KvTile<D>& t, Where& w) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int key = w.key0 + 16 * x, pg = key >> a.c.page_shift;
-            const int id = table[min(pg, a.bt.max_pages - 1)];
+            const int key = w.key0 + 16 * x;
             // (a page with no visible key is not looked at: its scale and bytes may be anything)
-            const bool seen = key < d.hi && (key + 15 >= d.lo || key < a.n_sink);
-            w.pid[x] = (seen && id >= 0 && id < a.c.n_pages) ? id : -1;
-        }
-        return w;
-    };
-    auto load = [&](KvTile<D>& t, const Where& w) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const size_t base = ((((size_t)max(w.pid[x], 0) * a.c.Hkv + h) << a.c.page_shift) +
-                                 ((w.key0 + 16 * x) & (page - 1))) * D;
+            const bool seen = key < kr.hi && (key + 15 >= kr.lo || key < a.n_sink);
+            const bool ok = seen && w.pid[x] >= 0 && w.pid[x] < a.c.n_pages;
+            const size_t tile = (size_t)(ok ? w.pid[x] : 0) * a.c.Hkv + h;
+            w.pid[x] = ok ? w.pid[x] : -1;
+            w.ks[x] = ok ? a.c.ks[tile] : 1.0f;
+            w.vs[x] = ok ? a.c.vs[tile] : 1.0f;
+            const size_t base = ((tile << a.c.page_shift) + (key & (page - 1))) * D;
             const uint8_t* kp = a.c.k + base;
             const uint8_t* vp = a.c.v + base;
 #pragma unroll
             for (int j = 0; j < D / 64; ++j)
-                t.k[x][j] = *reinterpret_cast<const at_u32x4*>(kp + c * D + 64 * j + 16 * g);
+                t.k[x][j] = *reinterpret_cast<const at_u32x4*>(kp + (c * D + 64 * j + 16 * g));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint8_t* p = vp + (4 * g + i) * D + c * (D / 16);
+                const uint8_t* p = vp + ((4 * g + i) * D + c * (D / 16));
                 if constexpr (D == 128) {
                     const at_u32x2 z = *reinterpret_cast<const at_u32x2*>(p);
                     t.v[4 * x + i][0] = z[0];
@@ -371,58 +442,114 @@ __global__ __launch_bounds__(64 * kWaves) void attend_kernel(AttendArgs a) {
         }
     };
     auto step = [&](KvTile<D>& t, const Where& w) {
-        HalfScale hs[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const size_t at = (size_t)max(w.pid[x], 0) * a.c.Hkv + h;
-            const float ks = w.pid[x] >= 0 ? a.c.ks[at] : 1.0f, vs = w.pid[x] >= 0 ? a.c.vs[at] : 1.0f;
-            const float cc = a.c2 * ks, lv = __builtin_amdgcn_logf(vs), iv = 1.0f / vs;   // v_log_f32: base 2
-#pragma unroll
-            for (int i = 0; i < 4; ++i) hs[x].c[i] = cc, hs[x].lv[i] = lv, hs[x].iv[i] = iv;
-        }
+        const PageScale hs[2] = {page_scale(a.c2, w.ks[0], w.vs[0]), page_scale(a.c2, w.ks[1], w.vs[1])};
         const int last = w.key0 + kTile - 1;
-        const bool whole = w.pid[0] >= 0 && w.pid[1] >= 0 && last <= d.pos_lo && last < d.hi &&
-                           (a.window <= 0 || w.key0 > d.pos_hi - a.window || last < a.n_sink) && d.f1 - d.f0 == 16 * MT;
-        if (whole) {
-            tile_step<D, MT, false>(t, q, hs, st, g, [](int, int) { return true; });
-            return;
+        const bool whole = w.pid[0] >= 0 && w.pid[1] >= 0 && last <= pos_lo && last < kr.hi &&
+                           (a.window <= 0 || w.key0 > pos_hi - a.window || last < a.n_sink);
+        if (!whole) {
+            // bytes of keys that no row sees may be NaN: their weights are 0, so the values must be finite
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = w.key0 + 16 * x + 4 * g + i;
+                    const bool ok = w.pid[x] >= 0 && key < kr.hi && (key >= kr.lo || key < a.n_sink);
+#pragma unroll
+                    for (int j = 0; j < D / 64; ++j) t.v[4 * x + i][j] = ok ? t.v[4 * x + i][j] : 0u;
+                }
         }
-        // bytes of keys that no row sees may be NaN: their weights are 0, so the values must be finite
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = w.key0 + 16 * x + 4 * g + i;
-                const bool ok = w.pid[x] >= 0 && key < d.hi && (key >= d.lo || key < a.n_sink);
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j) t.v[4 * x + i][j] = ok ? t.v[4 * x + i][j] : 0u;
-            }
-        tile_step<D, MT, true>(t, q, hs, st, g, [&](int mt, int k) {
+        tile_step<D, MT>(t, query, hs, st, !whole, g, [&](int mt, int k) {
             const int key = w.key0 + k;
-            return (k < 16 ? w.pid[0] : w.pid[1]) >= 0 && key <= pos[mt] && key < d.hi &&
+            return (k < 16 ? w.pid[0] : w.pid[1]) >= 0 && key <= pos[mt] && key < kr.hi &&
                    (a.window <= 0 || key > pos[mt] - a.window || key < a.n_sink);
         });
     };
 
+    // page ids two rounds ahead, keys and values one
     KvTile<D> ta, tb;
+    Where wa, wb;
     int t = t0 + wave;
     if (t < t1) {
-        Where wa = where(t), wb = wa;
+        ids(t, wa);
+        if (t + kWaves < t1) ids(t + kWaves, wb);
         load(ta, wa);
         while (true) {
-            const bool more = t + kWaves < t1;
-            if (more) wb = where(t + kWaves), load(tb, wb);
+            Where wn;
+            if (t + kWaves < t1) load(tb, wb);
+            if (t + 2 * kWaves < t1) ids(t + 2 * kWaves, wn);
             step(ta, wa);
-            if (!more) break;
+            if (t + kWaves >= t1) break;
             t += kWaves;
-            const bool more2 = t + kWaves < t1;
-            if (more2) wa = where(t + kWaves), load(ta, wa);
+            wa = wn;
+            if (t + kWaves < t1) load(ta, wa);
+            if (t + 2 * kWaves < t1) ids(t + 2 * kWaves, wn);
             step(tb, wb);
-            if (!more2) break;
+            if (t + kWaves >= t1) break;
             t += kWaves;
+            wb = wn;
         }
     }
-    finish<D, MT>(a, st, sh, ((int64_t)u * a.c.Hkv + h) * a.splits + split, used, row_of);
+    finish<D, MT>(a, st, sh, part, row_of);
+}
+
+// Header of the workspace of a dense call, written by workgroup 0 for the
+// join: the line's total and share, then each sequence's place on it.
+struct DenseHead {
+    int64_t total, per;
+    int64_t first[];   // [n_seq]
+};
+
+template <int D, int MT>
+__global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend_kernel(AttendArgs a) {
+    extern __shared__ float sh[];
+    __shared__ PlanLds ls;
+    __shared__ int64_t s_at;   // place of sequence s_b on the line
+    __shared__ int s_b;
+    DenseHead* head = reinterpret_cast<DenseHead*>(a.head);
+    // the total, then the sequence that this workgroup's range begins in
+    int64_t total = 0, sum;
+    for (int b0 = 0; b0 < a.bt.n_seq; b0 += kPlanSeqs) {
+        const int64_t w = work_of<MT>(a, b0 + threadIdx.x), x = block_scan(w, ls, sum);
+        if (blockIdx.x == 0 && b0 + (int)threadIdx.x < a.bt.n_seq) head->first[b0 + threadIdx.x] = total + x - w;
+        total += sum;
+    }
+    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)a.min_per);
+    if (blockIdx.x == 0 && threadIdx.x == 0) head->total = total, head->per = per;
+    int64_t at = (int64_t)blockIdx.x * per;
+    const int64_t end = min(at + per, total);
+    if (at >= end) return;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.bt.n_seq; b0 += kPlanSeqs) {
+        const int64_t w = work_of<MT>(a, b0 + threadIdx.x), x = before + block_scan(w, ls, sum);
+        if (x - w <= at && at < x) s_b = b0 + threadIdx.x, s_at = x - w;
+        before += sum;
+        if (at < before) break;
+    }
+    __syncthreads();
+    int b = __builtin_amdgcn_readfirstlane(s_b);
+    int64_t first = s_at;
+    SeqWork w = seq_work<MT>(a, b);
+    while (true) {
+        const int units = w.row_tiles * a.c.Hkv;
+        int u = (int)((at - first) / w.tiles);
+        for (; u < units && at < end; ++u) {
+            const int64_t us = first + (int64_t)u * w.tiles;   // the unit's place
+            const int h = u / w.row_tiles, f0 = (u - h * w.row_tiles) * 16 * MT;
+            const int f1 = min(f0 + 16 * MT, (w.sr.r1 - w.sr.r0) * a.G);
+            const KeyRange32 kr = key_range(a, w.sr.pos0 + f0 / a.G, w.sr.pos0 + (f1 - 1) / a.G);
+            const int t0 = (int)(at - us), t1 = (int)min(end - us, (int64_t)w.tiles);
+            const bool whole = t0 == 0 && t1 == w.tiles;
+            const bool begins = at == (int64_t)blockIdx.x * per;
+            float* part = whole ? nullptr : a.part + ((int64_t)blockIdx.x * 2 + (begins ? 0 : 1)) * part_floats<D, MT>();
+            dense_unit<D, MT>(a, w.sr, b, h, f0, f1, kr, t0, min(t1, kr.tiles), sh, part);
+            at = us + t1;
+            __syncthreads();   // finish() has read its LDS
+        }
+        if (at >= end) return;
+        first += (int64_t)units * w.tiles;
+        do w = seq_work<MT>(a, ++b);
+        while (w.row_tiles == 0);
+    }
 }
 
 // --------------------------------------------------- listed keys (one row)
@@ -438,7 +565,7 @@ struct ListLds {
 // 16 MT heads); its list is idx[row], or with PACKED the entries of the row's
 // group whose mask holds the row's bit.
 template <int D, int MT, bool PACKED>
-__global__ __launch_bounds__(64 * kWaves) void attend_list_kernel(AttendArgs a) {
+__global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend_list_kernel(AttendArgs a) {
     extern __shared__ float sh[];
     ListLds& ls = *reinterpret_cast<ListLds*>(sh);
     __shared__ int s_cnt[kWaves];
@@ -490,7 +617,8 @@ __global__ __launch_bounds__(64 * kWaves) void attend_list_kernel(AttendArgs a) 
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) st[mt].o[e] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    load_queries<D, MT>(a, q, row, c, g);
+    load_queries<D, MT>(a, q, row, g);
+    auto query = [&](int mt, int j) { return q[mt][j]; };
     const int32_t* table = a.bt.table + (size_t)b * a.bt.max_pages;
     const int page = 1 << a.c.page_shift;
     const int end = min(max(pos + 1, 0), a.bt.max_pages << a.c.page_shift);   // keys the row may see
@@ -515,18 +643,16 @@ __global__ __launch_bounds__(64 * kWaves) void attend_list_kernel(AttendArgs a) 
         }
     };
     auto step = [&](KvTile<D>& x, int at, int cnt) {
-        HalfScale hs[2];
+        KeyScale hs[2];
 #pragma unroll
-        for (int z = 0; z < 2; ++z)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = at + 16 * z + 4 * g + i;
-                hs[z].c[i] = ls.c[k], hs[z].lv[i] = ls.lv[k], hs[z].iv[i] = ls.iv[k];
-            }
-        if (at + kTile <= cnt)
-            tile_step<D, MT, false>(x, q, hs, st, g, [](int, int) { return true; });
-        else   // padded entries repeat the last key
-            tile_step<D, MT, true>(x, q, hs, st, g, [&](int, int k) { return at + k < cnt; });
+        for (int z = 0; z < 2; ++z) {
+            const int k = at + 16 * z + 4 * g;
+            hs[z].c_ = *reinterpret_cast<const at_f32x4*>(ls.c + k);
+            hs[z].lv_ = *reinterpret_cast<const at_f32x4*>(ls.lv + k);
+            hs[z].iv_ = *reinterpret_cast<const at_f32x4*>(ls.iv + k);
+        }
+        // (padded entries repeat the last key)
+        tile_step<D, MT>(x, query, hs, st, at + kTile > cnt, g, [&](int, int k) { return at + k < cnt; });
     };
 
     for (int c0 = e0; c0 < e1; c0 += kListChunk) {
@@ -558,11 +684,9 @@ __global__ __launch_bounds__(64 * kWaves) void attend_list_kernel(AttendArgs a) 
             if (pid >= 0) {
                 const int at = base + __popcll(have & ((1ull << lane) - 1ull));
                 const size_t pg = (size_t)pid * a.c.Hkv + h;
-                const float vs = a.c.vs[pg];
                 ls.row[at] = (int)((pg << a.c.page_shift) + (s & (page - 1)));
-                ls.c[at] = a.c2 * a.c.ks[pg];
-                ls.lv[at] = __builtin_amdgcn_logf(vs);
-                ls.iv[at] = 1.0f / vs;
+                const PageScale ps = page_scale(a.c2, a.c.ks[pg], a.c.vs[pg]);
+                ls.c[at] = ps.c_, ls.lv[at] = ps.lv_, ls.iv[at] = ps.iv_;
             }
             __syncthreads();
         }
@@ -595,8 +719,8 @@ __global__ __launch_bounds__(64 * kWaves) void attend_list_kernel(AttendArgs a) 
         }
     }
     __syncthreads();   // the list is done with: finish() reuses its LDS
-    const int64_t unit = ((int64_t)t * ht + tile) * a.c.Hkv + h;
-    finish<D, MT>(a, st, sh, unit * a.splits + split, used, row_of);
+    const int64_t slot = (((int64_t)t * ht + tile) * a.c.Hkv + h) * a.splits + split;
+    finish<D, MT>(a, st, sh, used > 1 ? a.part + slot * part_floats<D, MT>() : nullptr, row_of);
 }
 
 // ------------------------------------------------------- joining the splits
@@ -610,9 +734,11 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     __shared__ float s_ml[kGroups][2];
     const int64_t r = blockIdx.x;   // row * Hq + head
     const int t = (int)(r / a.Hq), head = (int)(r % a.Hq), h = head / a.G, g = head - h * a.G;
-    int64_t unit;
-    int used, at;
+    int used, at;                  // parts of the row's unit, and the row in it
+    int64_t slot0, slot1;          // the first part's slot, and the second's (the others follow it by slot_step)
+    int slot_step = 1;
     if constexpr (KIND == LTK_ATTEND) {
+        const DenseHead* hd = reinterpret_cast<const DenseHead*>(a.head);
         int b = 0, hi = a.bt.n_seq - 1;
         while (b < hi) {
             const int mid = (b + hi + 1) >> 1;
@@ -621,13 +747,18 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
             else
                 hi = mid - 1;
         }
-        const SeqRows sr = seq_rows(a.bt, b, a.T);
-        if (t < sr.r0 || t >= sr.r1) return;
-        const int f = (t - sr.r0) * a.G + g, u = unit_first(a.bt, b, a.T, a.G, RT, 1) + f / RT;
-        const DenseUnit d = dense_unit<MT>(a, u);
-        unit = (int64_t)u * a.c.Hkv + h;
-        used = (d.tiles + d.per - 1) / max(d.per, 1);
+        const SeqWork w = seq_work<MT>(a, b);
+        if (t < w.sr.r0 || t >= w.sr.r1) return;
+        const int64_t per = hd->per;
+        const int f = (t - w.sr.r0) * a.G + g;
+        const int64_t us = hd->first[b] + ((int64_t)h * w.row_tiles + f / RT) * w.tiles;
+        const int64_t w0 = us / per, w1 = (us + w.tiles - 1) / per;
+        used = (int)(w1 - w0) + 1;
         at = f % RT;
+        // every part but the first begins its workgroup's range
+        slot0 = 2 * w0 + (us == w0 * per ? 0 : 1);
+        slot1 = 2 * (w0 + 1);
+        slot_step = 2;
     } else {
         if constexpr (KIND == LTK_ATTEND_SELECTED) {
             if (t < cu_at(a.bt, 0, a.T) || t >= cu_at(a.bt, a.bt.n_seq, a.T)) return;
@@ -636,16 +767,16 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
         const int n = KIND == LTK_ATTEND_PACKED ? min(max(a.lens[t / a.group], 0), a.cap) : a.cap;
         const int per = (n + a.splits - 1) / a.splits;
         used = (n + per - 1) / max(per, 1);
-        unit = ((int64_t)t * ht + g / RT) * a.c.Hkv + h;
+        slot0 = (((int64_t)t * ht + g / RT) * a.c.Hkv + h) * a.splits;
+        slot1 = slot0 + 1;
         at = g % RT;
     }
-    if (used <= 1) return;   // written by its only split
+    if (used <= 1) return;   // written by its only workgroup
     const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-    const float* base = a.part + unit * a.splits * (int64_t)(RT * (D + 2));
     float m = kNoRef, l = 0.0f;
     at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = grp; s < used; s += kGroups) {
-        const float* p = base + (int64_t)s * (RT * (D + 2));
+        const float* p = a.part + (s == 0 ? slot0 : slot1 + (int64_t)(s - 1) * slot_step) * part_floats<D, MT>();
         const float ms = p[RT * D + at * 2], lsum = p[RT * D + at * 2 + 1];
         const at_f32x4 x = *reinterpret_cast<const at_f32x4*>(p + at * D + 4 * lane);
         const float mn = fmaxf(m, ms), f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(ms - mn);
@@ -676,24 +807,28 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 
 template <int KIND, int D, int MT>
 hipError_t launch(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
-    const int64_t blocks = p.units * p.splits;
     const int64_t rows = (int64_t)a.T * a.Hq;
-    if (blocks > 0x7fffffff || rows > 0x7fffffff) return hipErrorInvalidValue;
-    if (blocks == 0) return hipSuccess;
+    if (p.blocks > 0x7fffffff || rows > 0x7fffffff) return hipErrorInvalidValue;
     if constexpr (KIND == LTK_ATTEND) {
-        attend_kernel<D, MT><<<(unsigned)blocks, 64 * kWaves, finish_lds<D, MT>(), st>>>(a);
+        attend_kernel<D, MT><<<(unsigned)p.blocks, 64 * kWaves, finish_lds<D, MT>(), st>>>(a);
     } else {
         constexpr size_t lds = std::max(finish_lds<D, MT>(), sizeof(ListLds));
-        attend_list_kernel<D, MT, KIND == LTK_ATTEND_PACKED><<<(unsigned)blocks, 64 * kWaves, lds, st>>>(a);
+        attend_list_kernel<D, MT, KIND == LTK_ATTEND_PACKED><<<(unsigned)p.blocks, 64 * kWaves, lds, st>>>(a);
     }
-    if (p.splits > 1) attend_join_kernel<D, MT, KIND><<<(unsigned)rows, 256, 0, st>>>(a);
+    if (p.join) attend_join_kernel<D, MT, KIND><<<(unsigned)rows, 256, 0, st>>>(a);
     return hipGetLastError();
+}
+
+template <int KIND, int D>
+hipError_t launch_rows(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
+    if (p.mt == 1) return launch<KIND, D, 1>(p, a, st);
+    if (p.mt == 2) return launch<KIND, D, 2>(p, a, st);
+    return launch<KIND, D, 4>(p, a, st);
 }
 
 template <int KIND>
 hipError_t launch_kind(int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
-    if (D == 64) return p.mt == 1 ? launch<KIND, 64, 1>(p, a, st) : launch<KIND, 64, 2>(p, a, st);
-    return p.mt == 1 ? launch<KIND, 128, 1>(p, a, st) : launch<KIND, 128, 2>(p, a, st);
+    return D == 64 ? launch_rows<KIND, 64>(p, a, st) : launch_rows<KIND, 128>(p, a, st);
 }
 
 }  // namespace
@@ -701,23 +836,36 @@ hipError_t launch_kind(int D, const AttendPlan& p, const AttendArgs& a, hipStrea
 AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries) {
     AttendPlan p{};
     const int G = Hq / Hkv;
+    const size_t part = (size_t)(D + 2) * 16 * sizeof(float);   // of 16 rows
     if (kind == LTK_ATTEND) {
-        p.mt = (int64_t)T * G > 16 * (int64_t)std::max(n_seq, 1) ? 2 : 1;   // more than 16 (row, head) pairs a sequence
-        p.units = unit_bound(n_seq, T, G, 16 * p.mt, 1) * Hkv;
-    } else {
-        p.mt = G > 16 ? 2 : 1;
-        p.units = (int64_t)T * ((G + 16 * p.mt - 1) / (16 * p.mt)) * Hkv;
+        // rows that share keys: 16, 32 or 64 to a workgroup
+        const int64_t shared = (int64_t)T * G / std::max(n_seq, 1);
+        p.mt = shared > 32 ? 4 : shared > 16 ? 2 : 1;
+        // one range of key tiles a workgroup
+        const int64_t units = ((int64_t)T * G / (16 * p.mt) + n_seq) * Hkv, tiles = (entries + kTile - 1) / kTile;
+        const int64_t most = (units * tiles + kMinPer - 1) / kMinPer;
+        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, p.mt == 4 ? 512 : 1024));
+        p.join = p.blocks > 1;
+        p.head_bytes = (sizeof(DenseHead) + (size_t)n_seq * 8 + 255) / 256 * 256;
+        p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * p.mt * part : 0);
+        return p;
     }
+    p.mt = G > 32 ? 4 : G > 16 ? 2 : 1;
+    const int64_t units = (int64_t)T * ((G + 16 * p.mt - 1) / (16 * p.mt)) * Hkv;
     // about 1,024 workgroups (four per CU), each with at least one 32-key tile per wave
     const int64_t most = std::max<int64_t>(1, (entries + kTile * kWaves - 1) / (kTile * kWaves));
-    p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, 1024 / std::max<int64_t>(p.units, 1)));
-    p.ws_bytes = 256;
-    if (p.splits > 1)
-        p.ws_bytes = std::max<size_t>(256, (size_t)p.units * p.splits * (16 * p.mt) * (D + 2) * sizeof(float));
+    p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, 1024 / std::max<int64_t>(units, 1)));
+    p.blocks = units * p.splits;
+    p.join = p.splits > 1;
+    p.ws_bytes = std::max<size_t>(256, p.join ? (size_t)p.blocks * p.mt * part : 0);
     return p;
 }
 
-hipError_t launch_attend(int kind, int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
+hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, void* ws, hipStream_t st) {
+    a.splits = p.splits;
+    a.min_per = kMinPer;
+    a.head = ws;
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.head_bytes);
     if (kind == LTK_ATTEND) return launch_kind<LTK_ATTEND>(D, p, a, st);
     if (kind == LTK_ATTEND_SELECTED) return launch_kind<LTK_ATTEND_SELECTED>(D, p, a, st);
     return launch_kind<LTK_ATTEND_PACKED>(D, p, a, st);

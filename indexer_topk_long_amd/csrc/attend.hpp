@@ -99,20 +99,23 @@ struct AttendArgs {
     const uint32_t* masks;   // packed
     const int32_t* lens;     // packed
     int cap, group;
-    int splits;
-    float* part;             // [unit, split, rows] partial rows and their statistics
+    int splits;              // list kinds: key splits per unit
+    int min_per;             // attend: least key tiles of a workgroup's range
+    void* head;              // attend: the plan for the join
+    float* part;             // partial rows and their statistics
 };
 
-// Work split of an attend call, fixed by its sizes alone so that the
-// workspace size and the call agree.
+// Launch of an attend call, fixed by its sizes alone so that the workspace
+// size and the call agree.
 struct AttendPlan {
-    int mt;            // 16-row tiles per workgroup: rows per unit = 16 * mt
-    int64_t units;     // (row tile, key/value head) units, upper bound
-    int splits;        // key splits per unit
-    size_t ws_bytes;
+    int mt;            // 16-row tiles per unit
+    int64_t blocks;
+    int splits;
+    bool join;         // units may be cut: partial rows and a joining launch
+    size_t head_bytes, ws_bytes;
 };
 AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries);
 
-hipError_t launch_attend(int kind, int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st);
+hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, void* ws, hipStream_t st);
 
 }  // namespace ltk

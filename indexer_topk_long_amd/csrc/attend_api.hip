@@ -41,10 +41,8 @@ int run_attend(int kind, const ltk_kv_cache* cache, AttendArgs& a, int64_t entri
     if (a.T == 0 || a.bt.n_seq == 0) return LTK_OK;
     const int st = litetopk_device_check();
     if (st != LTK_OK) return st;
-    a.splits = p.splits;
-    a.part = static_cast<float*>(ws);
-    return launch_attend(kind, cache->head_dim, p, a, static_cast<hipStream_t>(stream)) == hipSuccess ? LTK_OK
-                                                                                                      : LTK_EHIP;
+    return launch_attend(kind, cache->head_dim, p, a, ws, static_cast<hipStream_t>(stream)) == hipSuccess ? LTK_OK
+                                                                                                          : LTK_EHIP;
 }
 
 // The arguments every attend call shares.
