@@ -26,7 +26,7 @@
  *  - rows outside every sequence (at or past cu[n_seq]) are not written;
  *  - a list entry outside [0, kv_len) or after the row's position is no key.
  * Bytes and scales that hold no key of the sequence may be anything (NaN
- * included); everything else must be finite, scales also > 0.
+ * included); everything else must be finite, scales also normal and > 0.
  */
 #ifndef LITETOPK_ATTEND_H
 #define LITETOPK_ATTEND_H
@@ -98,9 +98,10 @@ int litetopk_kv_append(const ltk_kv_cache* cache, const ltk_kv_batch* batch, con
 
 /* Bytes of workspace an attend call of `kind` needs (at least 256; 0 for
  * invalid sizes).  `entries` bounds the keys a row reads: max_pages *
- * page_size (attend), topk (selected) or cap (packed). */
+ * page_size (attend), topk (selected) or cap (packed); `group` is the packed
+ * call's (ignored otherwise). */
 size_t litetopk_attend_workspace_bytes(int32_t kind, int32_t T, int32_t Hq, int32_t n_kv_heads, int32_t head_dim,
-                                       int32_t n_seq, int64_t entries);
+                                       int32_t n_seq, int64_t entries, int32_t group);
 
 /* Causal attention: the row at position p sees the keys s <= p, and with
  * window > 0 only those with s > p - window or s < n_sink.

@@ -45,7 +45,7 @@ def _fn(name: str):
                                  _c_sz, _c_p]
         else:
             f.restype = _c_sz
-            f.argtypes = [_c_i32] * 6 + [_c_i64]
+            f.argtypes = [_c_i32] * 6 + [_c_i64, _c_i32]
         _FN[name] = f
     return _FN[name]
 
@@ -154,9 +154,9 @@ def kv_append(k, v, cache, page_table, cu, kv_len, inv_freq=None, q=None, interl
 
 @functools.lru_cache(maxsize=1024)   # sizes only
 def attend_workspace_bytes(kind: int, T: int, Hq: int, n_kv_heads: int, head_dim: int, n_seq: int,
-                           entries: int) -> int:
+                           entries: int, group: int = 0) -> int:
     """Workspace bytes of an attend call (litetopk_attend_workspace_bytes)."""
-    n = _fn("litetopk_attend_workspace_bytes")(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries)
+    n = _fn("litetopk_attend_workspace_bytes")(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries, group)
     if n == 0:
         raise LtkError(-1, "litetopk_attend_workspace_bytes")
     return int(n)
@@ -175,9 +175,9 @@ def _queries(q, c, scale, out, dev):
     return pq, T, Hq, po, out, (c.head_dim ** -0.5 if scale is None else float(scale))
 
 
-def _space(kind, T, Hq, c, n_seq, entries, workspace, dev):
+def _space(kind, T, Hq, c, n_seq, entries, workspace, dev, group=0):
     """(address, bytes, tensor) of the call's workspace."""
-    need = attend_workspace_bytes(kind, T, Hq, c.n_kv_heads, c.head_dim, n_seq, entries)
+    need = attend_workspace_bytes(kind, T, Hq, c.n_kv_heads, c.head_dim, n_seq, entries, group)
     if workspace is None:
         import torch
         workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
@@ -238,7 +238,7 @@ def attend_packed(q, cache, page_table, kv_len, shared, masks, lens, group: int,
     _expect(1 <= cap <= 1 << 26, f"shared must hold 1 to 2^26 entries a group, got {cap}")
     pm = _check(masks, "masks", torch.uint32, (ng, cap), dev)
     pl = _check(lens, "lens", torch.int32, (ng,), dev)
-    pw, nw, workspace = _space(ATTEND_PACKED, T, Hq, c, 1, cap, workspace, dev)
+    pw, nw, workspace = _space(ATTEND_PACKED, T, Hq, c, 1, cap, workspace, dev, group)
     with _On(dev) as stream:
         _raise(_fn("litetopk_attend_packed")(ctypes.byref(c), ctypes.byref(b), pq, T, Hq, ps, pm, pl, group, cap, scale,
                                              po, pw, nw, stream), "litetopk_attend_packed")

@@ -34,8 +34,6 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kTile = 32;            // keys per wave step
-constexpr float kNoRef = -1e30f;     // reference before the first visible key
-constexpr float kSlack = 8.0f;       // scores may pass the reference by 2^8: weights up to 256 in fp16
 constexpr int kMinPer = 2 * kWaves;  // least key tiles of a workgroup's range: two per wave
 constexpr int kListChunk = 2048;     // list entries staged in LDS at a time
 
@@ -52,15 +50,6 @@ __device__ __forceinline__ float sum_groups(float x) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// 8 e4m3 bytes as bf16, exact
-__device__ __forceinline__ at_bf16x8 bf16_of(uint32_t a, uint32_t b) {
-    const at_bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
-    const at_bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
-    const at_bf16x2 x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
-    const at_bf16x2 x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
-    return at_bf16x8{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
-}
-
 // The wave's share of 32 keys: halves A (keys 0..15) and B (16..31).
 template <int D>
 struct KvTile {
@@ -68,26 +57,12 @@ struct KvTile {
     uint32_t v[8][D / 64];          // the lane's 8 keys, bytes c D/16 ..
 };
 
-// Constants of a key: scale log2(e) ks, log2(vs), 1 / vs.  Dense tiles have
-// one set per half (a page holds at least 16 keys), listed keys one each.
-struct PageScale {
-    float c_, lv_, iv_;
-    __device__ __forceinline__ float c(int) const { return c_; }
-    __device__ __forceinline__ float lv(int) const { return lv_; }
-    __device__ __forceinline__ float iv(int) const { return iv_; }
-};
-struct KeyScale {
+struct KeyScale {   // listed keys: one set each
     at_f32x4 c_, lv_, iv_;   // the lane's keys 4 g + i
     __device__ __forceinline__ float c(int i) const { return c_[i]; }
     __device__ __forceinline__ float lv(int i) const { return lv_[i]; }
     __device__ __forceinline__ float iv(int i) const { return iv_[i]; }
 };
-
-// v_log_f32 is base 2; both it and v_rcp_f32 are exact on powers of two and
-// within 1 ulp elsewhere.
-__device__ __forceinline__ PageScale page_scale(float c2, float ks, float vs) {
-    return PageScale{c2 * ks, __builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs)};
-}
 
 // Running state of 16 query rows: reference, weight sum (of the lane's keys)
 // and the D / 16 x 4 accumulators of row c, dimensions (4 g + r) D/16 + e.
@@ -295,7 +270,7 @@ struct KeyRange32 {
 __device__ __forceinline__ KeyRange32 key_range(const AttendArgs& a, int pos_lo, int pos_hi) {
     KeyRange32 k;
     k.hi = min(max(pos_hi + 1, 0), a.bt.max_pages << a.c.page_shift);
-    k.lo = a.window > 0 ? min(max(pos_lo - a.window + 1, 0), k.hi) : 0;
+    k.lo = a.window > 0 ? min(max(max(pos_lo, 0) - a.window + 1, 0), k.hi) : 0;
     k.sink_tiles = a.window > 0 ? (min(a.n_sink, k.lo) + kTile - 1) / kTile : 0;
     k.win_tile0 = max(k.lo / kTile, k.sink_tiles);
     k.tiles = k.sink_tiles + max((k.hi + kTile - 1) / kTile - k.win_tile0, 0);
@@ -833,9 +808,11 @@ hipError_t launch_kind(int D, const AttendPlan& p, const AttendArgs& a, hipStrea
 
 }  // namespace
 
-AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries) {
+AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group) {
     AttendPlan p{};
     const int G = Hq / Hkv;
+    if (kind == LTK_ATTEND ? (int64_t)T * G > 64 * (int64_t)std::max(n_seq, 1) : kind == LTK_ATTEND_PACKED && group > 1)
+        return attend_tile_plan(kind, T, Hq, Hkv, D, n_seq, entries, group);
     const size_t part = (size_t)(D + 2) * 16 * sizeof(float);   // of 16 rows
     if (kind == LTK_ATTEND) {
         // rows that share keys: 16, 32 or 64 to a workgroup
@@ -866,6 +843,7 @@ hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, vo
     a.min_per = kMinPer;
     a.head = ws;
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.head_bytes);
+    if (p.tile) return launch_attend_tile(kind, D, p, a, st);
     if (kind == LTK_ATTEND) return launch_kind<LTK_ATTEND>(D, p, a, st);
     if (kind == LTK_ATTEND_SELECTED) return launch_kind<LTK_ATTEND_SELECTED>(D, p, a, st);
     return launch_kind<LTK_ATTEND_PACKED>(D, p, a, st);

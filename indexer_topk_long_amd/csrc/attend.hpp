@@ -83,6 +83,32 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, at_bf16x2));
 }
 
+constexpr float kNoRef = -1e30f;     // reference before the first visible key
+constexpr float kSlack = 8.0f;       // scores may pass the reference by 2^8: weights up to 256 in fp16
+
+// 8 e4m3 bytes as bf16, exact
+__device__ __forceinline__ at_bf16x8 bf16_of(uint32_t a, uint32_t b) {
+    const at_bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+    const at_bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+    const at_bf16x2 x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+    const at_bf16x2 x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+    return at_bf16x8{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
+}
+
+// Constants of a key: scale log2(e) ks, log2(vs), 1 / vs.  Dense tiles have
+// one set per half (a page holds at least 16 keys), listed keys one each.
+struct PageScale {
+    float c_, lv_, iv_;
+    __device__ __forceinline__ float c(int) const { return c_; }
+    __device__ __forceinline__ float lv(int) const { return lv_; }
+    __device__ __forceinline__ float iv(int) const { return iv_; }
+};
+// v_log_f32 is base 2; both it and v_rcp_f32 are exact on powers of two and
+// within 1 ulp elsewhere.
+__device__ __forceinline__ PageScale page_scale(float c2, float ks, float vs) {
+    return PageScale{c2 * ks, __builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs)};
+}
+
 hipError_t launch_kv_append(const KvCache& c, const KvBatch& bt, int D, const uint16_t* k, const uint16_t* v,
                             const uint16_t* q, int T, int Hq, const double* inv_freq, int rot, int interleaved,
                             uint16_t* q_out, hipStream_t st);
@@ -108,14 +134,18 @@ struct AttendArgs {
 // Launch of an attend call, fixed by its sizes alone so that the workspace
 // size and the call agree.
 struct AttendPlan {
-    int mt;            // 16-row tiles per unit
+    bool tile;         // the kernels of attend_tile.hip (128 rows a unit), else those of attend.hip
+    int mt;            // attend.hip: 16-row tiles per unit
     int64_t blocks;
     int splits;
     bool join;         // units may be cut: partial rows and a joining launch
     size_t head_bytes, ws_bytes;
 };
-AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries);
+// `group` is the packed kind's (else 0).
+AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group);
+AttendPlan attend_tile_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group);
 
 hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, void* ws, hipStream_t st);
+hipError_t launch_attend_tile(int kind, int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st);
 
 }  // namespace ltk

@@ -36,7 +36,7 @@ int check_heads(int32_t T, int32_t Hq, int32_t Hkv) {
 
 int run_attend(int kind, const ltk_kv_cache* cache, AttendArgs& a, int64_t entries, void* ws, size_t ws_bytes,
                void* stream) {
-    const AttendPlan p = attend_plan(kind, a.T, a.Hq, a.c.Hkv, cache->head_dim, a.bt.n_seq, entries);
+    const AttendPlan p = attend_plan(kind, a.T, a.Hq, a.c.Hkv, cache->head_dim, a.bt.n_seq, entries, a.group);
     if (ws_bytes < p.ws_bytes) return LTK_EWORKSPACE;
     if (a.T == 0 || a.bt.n_seq == 0) return LTK_OK;
     const int st = litetopk_device_check();
@@ -90,12 +90,12 @@ int litetopk_kv_append(const ltk_kv_cache* cache, const ltk_kv_batch* batch, con
 }
 
 size_t litetopk_attend_workspace_bytes(int32_t kind, int32_t T, int32_t Hq, int32_t n_kv_heads, int32_t head_dim,
-                                       int32_t n_seq, int64_t entries) {
+                                       int32_t n_seq, int64_t entries, int32_t group) {
     if (kind < LTK_ATTEND || kind > LTK_ATTEND_PACKED || T < 0 || n_kv_heads < 1 || Hq < 1 || Hq % n_kv_heads != 0 ||
         n_seq < 0 || entries < 1 || entries > 0x7fffffff || (int64_t)T * Hq > 0x7fffffff ||
-        (head_dim != 64 && head_dim != 128))
+        (head_dim != 64 && head_dim != 128) || (kind == LTK_ATTEND_PACKED && (group < 1 || group > 32)))
         return 0;
-    return attend_plan(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries).ws_bytes;
+    return attend_plan(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries, group).ws_bytes;
 }
 
 int litetopk_attend(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void* q, int32_t T, int32_t Hq,

@@ -138,7 +138,8 @@ def test_workspace_sizes():
     assert one >= 8 * 16 * 128 * 4           # partial rows of a split call
     assert ws(A.ATTEND, 8192, 64, 8, 128, 1, 1 << 17) >= 256
     for bad in [(3, 1, 8, 8, 128, 1, 10), (0, -1, 8, 8, 128, 1, 10), (0, 1, 8, 3, 128, 1, 10),
-                (0, 1, 8, 8, 96, 1, 10), (0, 1, 8, 8, 128, 1, 0), (0, 1, 8, 8, 128, -1, 10), (0, 1, 0, 8, 128, 1, 10)]:
+                (0, 1, 8, 8, 96, 1, 10), (0, 1, 8, 8, 128, 1, 0), (0, 1, 8, 8, 128, -1, 10), (0, 1, 0, 8, 128, 1, 10),
+                (2, 1, 8, 8, 128, 1, 10), (2, 1, 8, 8, 128, 1, 10, 33)]:
         with pytest.raises(ltk.LtkError):
             ws(*bad)
 
@@ -148,7 +149,7 @@ def test_a_short_workspace_is_refused():
     assert _attend("attend", wsb=need - 1) == EWS
     need = A.attend_workspace_bytes(A.ATTEND_SELECTED, 4, 8, 4, 128, 3, 4096)
     assert need > 256 and _attend("selected", topk=4096, wsb=need - 1) == EWS
-    need = A.attend_workspace_bytes(A.ATTEND_PACKED, 4, 8, 4, 128, 1, 4096)
+    need = A.attend_workspace_bytes(A.ATTEND_PACKED, 4, 8, 4, 128, 1, 4096, 8)
     assert _attend("packed", n_seq=1, cap=4096, wsb=need - 1) == EWS
 
 
