@@ -234,7 +234,7 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
 
 template <int D, int MT>
 constexpr int waves_per_simd() {
-    return MT == 4 ? (D == 64 ? 2 : 1) : MT == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);
+    return MT == 4 ? (D == 64 ? 2 : 1) : MT == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 3 : 2);
 }
 
 template <int D, int MT>
@@ -288,7 +288,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int b) {
     const int64_t all = (min(max(end, 0), a.bt.max_pages << a.c.page_shift) + kTile - 1) / kTile;
     int64_t most = all;
     if (a.window > 0) {
-        const int span = min(n, (16 * MT + a.G - 1) / a.G + 1);
+        const int span = min(n, uniform((16 * MT + a.G - 1) / a.G) + 1);
         most = min(all, ((int64_t)a.n_sink + kTile - 1) / kTile + ((int64_t)a.window + span + kTile - 2) / kTile + 1);
     }
     w.tiles = max((int)most, 1);
@@ -351,7 +351,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
                                            const KeyRange32& kr, int t0, int t1, float* sh, float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int pos_lo = sr.pos0 + f0 / a.G, pos_hi = sr.pos0 + (f1 - 1) / a.G;
+    const int pos_lo = sr.pos0 + uniform(f0 / a.G), pos_hi = sr.pos0 + uniform((f1 - 1) / a.G);
     auto row_of = [&](int r) -> int64_t {
         const int f = f0 + r;
         if (f >= f1) return -1;
@@ -376,28 +376,28 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 
     const int32_t* table = a.bt.table + (size_t)b * a.bt.max_pages;
     const int page = 1 << a.c.page_shift;
+    // the wave's steps are the tiles t0 + wave, t0 + wave + kWaves, ..; a lane
+    // holds the page of one half of one of the next 32
+    PageLanes pl;
+    auto key0_of = [&](int t) { return (t < kr.sink_tiles ? t : kr.win_tile0 + t - kr.sink_tiles) * kTile; };
+    auto tile_of = [&](int n) { return t0 + wave + n * kWaves; };
+    auto lane_key = [&](int block) {
+        const int t = tile_of(32 * block + (lane >> 1));
+        return t < t1 ? key0_of(t) + 16 * (lane & 1) : -1;
+    };
+    // (a page with no visible key is not looked at: its scale and bytes may be anything)
+    auto seen = [&](int key) { return (key < kr.hi) & ((key + 15 >= kr.lo) | (key < a.n_sink)); };
     struct Where {
         int key0, pid[2];   // page of each half, -1 when it has none
-        float ks[2], vs[2];
     };
-    auto ids = [&](int t, Where& w) {
-        w.key0 = (t < kr.sink_tiles ? t : kr.win_tile0 + t - kr.sink_tiles) * kTile;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            w.pid[x] = table[min((w.key0 + 16 * x) >> a.c.page_shift, a.bt.max_pages - 1)];
-    };
-    auto load = [&](KvTile<D>& t, Where& w) {
+    auto load = [&](KvTile<D>& t, Where& w, int n) {
+        if (n % 32 == 0) pl.turn(table, a, h, n / 32, lane_key, seen);
+        w.key0 = key0_of(tile_of(n));
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int key = w.key0 + 16 * x;
-            // (a page with no visible key is not looked at: its scale and bytes may be anything)
-            const bool seen = key < kr.hi && (key + 15 >= kr.lo || key < a.n_sink);
-            const bool ok = seen && w.pid[x] >= 0 && w.pid[x] < a.c.n_pages;
-            const size_t tile = (size_t)(ok ? w.pid[x] : 0) * a.c.Hkv + h;
-            w.pid[x] = ok ? w.pid[x] : -1;
-            w.ks[x] = ok ? a.c.ks[tile] : 1.0f;
-            w.vs[x] = ok ? a.c.vs[tile] : 1.0f;
-            const size_t base = ((tile << a.c.page_shift) + (key & (page - 1))) * D;
+            w.pid[x] = pl.page(2 * (n % 32) + x);
+            const size_t tile = (size_t)max(w.pid[x], 0) * a.c.Hkv + h;
+            const size_t base = ((tile << a.c.page_shift) + ((w.key0 + 16 * x) & (page - 1))) * D;
             const uint8_t* kp = a.c.k + base;
             const uint8_t* vp = a.c.v + base;
 #pragma unroll
@@ -416,8 +416,13 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
             }
         }
     };
-    auto step = [&](KvTile<D>& t, const Where& w) {
-        const PageScale hs[2] = {page_scale(a.c2, w.ks[0], w.vs[0]), page_scale(a.c2, w.ks[1], w.vs[1])};
+    auto scales = [&](PageScale (&hs)[2], int n) {   // before the loads of step n + 1, which may turn the lanes
+        if (n % 32 == 0) pl.scales(a.c2);
+        hs[0] = pl.scale(2 * (n % 32));
+        hs[1] = pl.scale(2 * (n % 32) + 1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto step = [&](KvTile<D>& t, const Where& w, const PageScale (&hs)[2]) {
         const int last = w.key0 + kTile - 1;
         const bool whole = w.pid[0] >= 0 && w.pid[1] >= 0 && last <= pos_lo && last < kr.hi &&
                            (a.window <= 0 || w.key0 > pos_hi - a.window || last < a.n_sink);
@@ -428,40 +433,35 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int key = w.key0 + 16 * x + 4 * g + i;
-                    const bool ok = w.pid[x] >= 0 && key < kr.hi && (key >= kr.lo || key < a.n_sink);
+                    const bool ok = (w.pid[x] >= 0) & (key < kr.hi) & ((key >= kr.lo) | (key < a.n_sink));
 #pragma unroll
                     for (int j = 0; j < D / 64; ++j) t.v[4 * x + i][j] = ok ? t.v[4 * x + i][j] : 0u;
                 }
         }
         tile_step<D, MT>(t, query, hs, st, !whole, g, [&](int mt, int k) {
             const int key = w.key0 + k;
-            return (k < 16 ? w.pid[0] : w.pid[1]) >= 0 && key <= pos[mt] && key < kr.hi &&
-                   (a.window <= 0 || key > pos[mt] - a.window || key < a.n_sink);
+            const int from = a.window > 0 ? max(pos[mt], 0) - a.window : -1;
+            return ((k < 16 ? w.pid[0] : w.pid[1]) >= 0) & (key <= pos[mt]) & (key < kr.hi) &
+                   ((key > from) | (key < a.n_sink));
         });
     };
 
-    // page ids two rounds ahead, keys and values one
-    KvTile<D> ta, tb;
-    Where wa, wb;
-    int t = t0 + wave;
-    if (t < t1) {
-        ids(t, wa);
-        if (t + kWaves < t1) ids(t + kWaves, wb);
-        load(ta, wa);
-        while (true) {
-            Where wn;
-            if (t + kWaves < t1) load(tb, wb);
-            if (t + 2 * kWaves < t1) ids(t + 2 * kWaves, wn);
-            step(ta, wa);
-            if (t + kWaves >= t1) break;
-            t += kWaves;
-            wa = wn;
-            if (t + kWaves < t1) load(ta, wa);
-            if (t + 2 * kWaves < t1) ids(t + 2 * kWaves, wn);
-            step(tb, wb);
-            if (t + kWaves >= t1) break;
-            t += kWaves;
-            wb = wn;
+    const int steps = (t1 - t0 - wave + kWaves - 1) / kWaves;
+    if (steps > 0) {
+        KvTile<D> ta, tb;
+        Where wa, wb;
+        PageScale hs[2];
+        pl.read(table, a, 0, lane_key);
+        load(ta, wa, 0);
+        for (int n = 0;; n += 2) {   // a step's keys and values are loaded during the step before
+            scales(hs, n);
+            if (n + 1 < steps) load(tb, wb, n + 1);
+            step(ta, wa, hs);
+            if (n + 1 >= steps) break;
+            scales(hs, n + 1);
+            if (n + 2 < steps) load(ta, wa, n + 2);
+            step(tb, wb, hs);
+            if (n + 2 >= steps) break;
         }
     }
     finish<D, MT>(a, st, sh, part, row_of);
@@ -486,7 +486,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += kPlanSeqs) {
         const int64_t w = work_of<MT>(a, b0 + threadIdx.x), x = block_scan(w, ls, sum);
         if (blockIdx.x == 0 && b0 + (int)threadIdx.x < a.bt.n_seq) head->first[b0 + threadIdx.x] = total + x - w;
-        total += sum;
+        total += uniform(sum);
     }
     const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)a.min_per);
     if (blockIdx.x == 0 && threadIdx.x == 0) head->total = total, head->per = per;
@@ -497,21 +497,21 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += kPlanSeqs) {
         const int64_t w = work_of<MT>(a, b0 + threadIdx.x), x = before + block_scan(w, ls, sum);
         if (x - w <= at && at < x) s_b = b0 + threadIdx.x, s_at = x - w;
-        before += sum;
+        before += uniform(sum);
         if (at < before) break;
     }
     __syncthreads();
-    int b = __builtin_amdgcn_readfirstlane(s_b);
-    int64_t first = s_at;
+    int b = uniform(s_b);
+    int64_t first = uniform(s_at);
     SeqWork w = seq_work<MT>(a, b);
     while (true) {
         const int units = w.row_tiles * a.c.Hkv;
-        int u = (int)((at - first) / w.tiles);
+        int u = uniform((int)((at - first) / w.tiles));
         for (; u < units && at < end; ++u) {
             const int64_t us = first + (int64_t)u * w.tiles;   // the unit's place
-            const int h = u / w.row_tiles, f0 = (u - h * w.row_tiles) * 16 * MT;
+            const int h = uniform(u / w.row_tiles), f0 = (u - h * w.row_tiles) * 16 * MT;
             const int f1 = min(f0 + 16 * MT, (w.sr.r1 - w.sr.r0) * a.G);
-            const KeyRange32 kr = key_range(a, w.sr.pos0 + f0 / a.G, w.sr.pos0 + (f1 - 1) / a.G);
+            const KeyRange32 kr = key_range(a, w.sr.pos0 + uniform(f0 / a.G), w.sr.pos0 + uniform((f1 - 1) / a.G));
             const int t0 = (int)(at - us), t1 = (int)min(end - us, (int64_t)w.tiles);
             const bool whole = t0 == 0 && t1 == w.tiles;
             const bool begins = at == (int64_t)blockIdx.x * per;
@@ -545,11 +545,11 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
     ListLds& ls = *reinterpret_cast<ListLds*>(sh);
     __shared__ int s_cnt[kWaves];
     constexpr int RT = 16 * MT;
-    const int h = blockIdx.x % a.c.Hkv;
-    int rest = blockIdx.x / a.c.Hkv;
-    const int split = rest % a.splits;
-    rest /= a.splits;
-    const int ht = (a.G + RT - 1) / RT, tile = rest % ht, t = rest / ht;
+    const int h = uniform((int)(blockIdx.x % a.c.Hkv));
+    int rest = uniform((int)(blockIdx.x / a.c.Hkv));
+    const int split = uniform(rest % a.splits);
+    rest = uniform(rest / a.splits);
+    const int ht = (a.G + RT - 1) / RT, tile = uniform(rest % ht), t = uniform(rest / ht);
     int b = 0, pos;
     if constexpr (PACKED) {
         pos = max(a.bt.len[0], 0) - a.T + t;
@@ -568,11 +568,11 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
     }
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int grp = PACKED ? t / a.group : 0, bit = PACKED ? t % a.group : 0;
+    const int grp = PACKED ? uniform(t / a.group) : 0, bit = PACKED ? t - grp * a.group : 0;
     const int32_t* list = a.list + (size_t)(PACKED ? grp : t) * a.cap;
     const uint32_t* masks = PACKED ? a.masks + (size_t)grp * a.cap : nullptr;
     const int n = PACKED ? min(max(a.lens[grp], 0), a.cap) : a.cap;
-    const int per = (n + a.splits - 1) / a.splits;
+    const int per = uniform((n + a.splits - 1) / a.splits);
     const int e0 = split * per, e1 = min(e0 + per, n);
     if (split > 0 && e0 >= e1) return;
     const int used = max((n + per - 1) / max(per, 1), 1);
@@ -821,7 +821,7 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
         // one range of key tiles a workgroup
         const int64_t units = ((int64_t)T * G / (16 * p.mt) + n_seq) * Hkv, tiles = (entries + kTile - 1) / kTile;
         const int64_t most = (units * tiles + kMinPer - 1) / kMinPer;
-        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, p.mt == 4 ? 512 : 1024));
+        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, p.mt == 4 ? 256 : 1024));
         p.join = p.blocks > 1;
         p.head_bytes = (sizeof(DenseHead) + (size_t)n_seq * 8 + 255) / 256 * 256;
         p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * p.mt * part : 0);

@@ -74,6 +74,14 @@ inline int64_t unit_bound(int64_t n_seq, int64_t T, int64_t mul, int64_t per, in
     return T * mul / per + extra * n_seq;
 }
 
+// A value that all lanes hold, in scalar registers: what is derived from it
+// (page ids above all) is then loaded through the scalar cache and does not
+// queue behind the tiles' loads.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x));
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -109,10 +117,6 @@ __device__ __forceinline__ PageScale page_scale(float c2, float ks, float vs) {
     return PageScale{c2 * ks, __builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs)};
 }
 
-hipError_t launch_kv_append(const KvCache& c, const KvBatch& bt, int D, const uint16_t* k, const uint16_t* v,
-                            const uint16_t* q, int T, int Hq, const double* inv_freq, int rot, int interleaved,
-                            uint16_t* q_out, hipStream_t st);
-
 struct AttendArgs {
     KvCache c;
     KvBatch bt;
@@ -130,6 +134,48 @@ struct AttendArgs {
     void* head;              // attend: the plan for the join
     float* part;             // partial rows and their statistics
 };
+
+// Page ids and scales of the next 64 groups of 16 keys, one a lane, so that a
+// loop over keys reads the page table and the scales once per 64 groups, a
+// block ahead, and takes each step's from a lane.  (Loaded through the scalar
+// cache step by step, every wait for LDS or for a scale would also wait for
+// the ids of the step after, since scalar loads return out of order.)
+struct PageLanes {
+    int id, ahead;      // checked ids of this block (-1: no page, or no key of it is seen); the next block's as read
+    float ks, vs;       // as read
+    PageScale s;
+
+    // key_of(block): first key of the lane's group, < 0 past the end.
+    template <class KeyOf>
+    __device__ __forceinline__ void read(const int32_t* table, const AttendArgs& a, int block, KeyOf key_of) {
+        const int key = key_of(block);
+        ahead = key >= 0 ? table[min(key >> a.c.page_shift, a.bt.max_pages - 1)] : -1;
+    }
+    // Makes `block` the current one; its scales are on their way afterwards.
+    template <class KeyOf, class Seen>
+    __device__ __forceinline__ void turn(const int32_t* table, const AttendArgs& a, int h, int block, KeyOf key_of,
+                                         Seen seen) {
+        const int key = key_of(block);
+        id = (key >= 0) & (ahead >= 0) & (ahead < a.c.n_pages) & seen(key) ? ahead : -1;
+        read(table, a, block + 1, key_of);
+        const size_t tile = (size_t)max(id, 0) * a.c.Hkv + h;
+        ks = 1.0f, vs = 1.0f;
+        if (id >= 0) ks = a.c.ks[tile], vs = a.c.vs[tile];
+    }
+    __device__ __forceinline__ void scales(float c2) { s = page_scale(c2, ks, vs); }
+    __device__ __forceinline__ int page(int lane) const { return __builtin_amdgcn_readlane(id, lane); }
+    __device__ __forceinline__ PageScale scale(int lane) const {
+        return PageScale{lane_of(s.c_, lane), lane_of(s.lv_, lane), lane_of(s.iv_, lane)};
+    }
+    static __device__ __forceinline__ float lane_of(float x, int lane) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), lane));
+    }
+};
+
+hipError_t launch_kv_append(const KvCache& c, const KvBatch& bt, int D, const uint16_t* k, const uint16_t* v,
+                            const uint16_t* q, int T, int Hq, const double* inv_freq, int rot, int interleaved,
+                            uint16_t* q_out, hipStream_t st);
+
 
 // Launch of an attend call, fixed by its sizes alone so that the workspace
 // size and the call agree.

@@ -127,6 +127,30 @@ __device__ __forceinline__ void store_stage(const Part<D>& p, const Raw& r, Stag
     }
 }
 
+// N matrix instructions whose LDS operands are read kAhead at a time, one
+// batch ahead of their use.  The scheduling barriers hold the order: left
+// alone, the compiler keeps one operand and waits for LDS before every
+// instruction.
+constexpr int kAhead = 2;
+template <int N, class V, class Read, class Use>
+__device__ __forceinline__ void pipelined(Read read, Use use) {
+    V f[2][kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) f[0][i] = read(i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < N / kAhead; ++n) {
+        if (n + 1 < N / kAhead) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) f[(n + 1) & 1][i] = read((n + 1) * kAhead + i);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) use(n * kAhead + i, f[n & 1][i]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 // Running state of a wave's 32 rows: lane (c, g) = (lane % 32, lane / 32)
 // holds row c, of its accumulators the dimensions 32 t + 8 (r / 4) + 4 g + r % 4.
 template <int D>
@@ -144,15 +168,12 @@ __device__ __forceinline__ void step_keys(const Stage<D>& s, const at_bf16x8 (&q
     const int lane = threadIdx.x & 63, c = lane & 31, g = lane >> 5;
     at_f32x16 x[2];
 #pragma unroll
-    for (int hb = 0; hb < 2; ++hb) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[hb][r] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            const at_bf16x8 kf = *reinterpret_cast<const at_bf16x8*>(s.k + k_at<D>(32 * hb + c, 2 * j + g));
-            x[hb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[j], x[hb], 0, 0, 0);
-        }
-    }
+    for (int r = 0; r < 16; ++r) x[0][r] = x[1][r] = 0.0f;
+    pipelined<D / 8, at_bf16x8>(   // n = 2 j + hb
+        [&](int n) { return *reinterpret_cast<const at_bf16x8*>(s.k + k_at<D>(32 * (n & 1) + c, (n & ~1) + g)); },
+        [&](int n, const at_bf16x8& kf) {
+            x[n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[n >> 1], x[n & 1], 0, 0, 0);
+        });
     // scores relative to the reference
     float top = kNoRef;
 #pragma unroll
@@ -194,13 +215,15 @@ __device__ __forceinline__ void step_keys(const Stage<D>& s, const at_bf16x8 (&q
                 p[2 * hb + (i >> 1)][4 * (i & 1) + r + 1] = ph[1];
             }
         }
-#pragma unroll
-    for (int t = 0; t < D / 32; ++t)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const at_f16x8 vf = *reinterpret_cast<const at_f16x8*>(s.v + v_at(32 * t + c, 2 * w + g));
+    pipelined<D / 8, at_f16x8>(    // n = (D / 32) w + t
+        [&](int n) {
+            const int w = n / (D / 32), t = n % (D / 32);
+            return *reinterpret_cast<const at_f16x8*>(s.v + v_at(32 * t + c, 2 * w + g));
+        },
+        [&](int n, const at_f16x8& vf) {
+            const int w = n / (D / 32), t = n % (D / 32);
             st.o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[w], st.o[t], 0, 0, 0);
-        }
+        });
 }
 
 // The unit's rows, flattened (row, head) from f0 to f1: row r0 + f / G, head
@@ -284,7 +307,7 @@ __device__ __forceinline__ SeqLine seq_line(const AttendArgs& a, int b) {
     s.sr = seq_rows(a.bt, b, a.T);
     const int n = s.sr.r1 - s.sr.r0;
     s.tiles = (int)(((int64_t)n * a.G + kRows - 1) / kRows);
-    s.Q = (kRows + a.G - 1) / a.G;
+    s.Q = uniform((kRows + a.G - 1) / a.G);
     const int64_t cap = (int64_t)a.bt.max_pages << a.c.page_shift;
     s.A = max(min((int64_t)s.sr.pos0 + 1 + s.Q, cap), (int64_t)1);
     // a window's rows see at most the sinks, the window and the tiles' borders
@@ -324,12 +347,13 @@ template <int D>
 __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& sr, int b, const UnitRows& u,
                                            const KeyTiles& kt, int t0, int t1, Lds<D, false>& ls, float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = lane & 31, g = lane >> 5, tid = threadIdx.x;
+    const int c = lane & 31, g = lane >> 5;
     const int fw = u.f0 + 32 * wave;                      // the wave's rows [fw, fw1)
     const int fw1 = min(fw + 32, u.f1);
-    const int pos_lo = sr.pos0 + fw / a.G, pos_hi = sr.pos0 + (max(fw1, 1) - 1) / a.G;
+    const int pos_lo = sr.pos0 + uniform(fw / a.G), pos_hi = sr.pos0 + uniform((max(fw1, 1) - 1) / a.G);
     const int64_t row = out_row(a, u, fw + c);
     const int pos = row < 0 ? -1 : sr.pos0 + (fw + c) / a.G;
+    const int from = a.window > 0 ? max(pos, 0) - a.window : -1;   // the lane's row sees keys behind it, and the sinks
     at_bf16x8 q[D / 16];
     WaveState<D> st;
     begin_rows<D>(a, row, q, st);
@@ -338,30 +362,30 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     const int page = 1 << a.c.page_shift;
     const Part<D> p;
     auto key0_of = [&](int t) { return (t < kt.sink_tiles ? t : kt.win_tile0 + t - kt.sink_tiles) * kKeys; };
-    // Pages of a step's four 16-key groups; -1: no page, or none of its keys is seen
+    // pages of a step's four 16-key groups; a lane holds one of the next 16 steps'
+    // (named, not an array: an array copied from step to step stays in scratch
+    // memory, and the wait for it is a wait for every load in flight)
     struct Ids {
-        int pid[4];
+        int p0, p1, p2, p3;
+        __device__ __forceinline__ int get(int i) const { return i == 0 ? p0 : i == 1 ? p1 : i == 2 ? p2 : p3; }
+        __device__ __forceinline__ bool all() const { return (p0 | p1 | p2 | p3) >= 0; }
     };
-    auto ids = [&](int t, Ids& x) {
-        const int key0 = key0_of(t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = key0 + 16 * i;
-            const int id = table[min(key >> a.c.page_shift, a.bt.max_pages - 1)];
-            const bool seen = key < kt.hi && (key + 15 >= kt.lo || key < a.n_sink);
-            x.pid[i] = seen && id >= 0 && id < a.c.n_pages ? id : -1;
-        }
+    PageLanes pl;
+    auto lane_key = [&](int block) {
+        const int t = t0 + 16 * block + (lane >> 2);
+        return t < t1 ? key0_of(t) + 16 * (lane & 3) : -1;
     };
+    // (a page with no visible key is not looked at: its scale and bytes may be anything)
+    auto seen = [&](int key) { return (key < kt.hi) & ((key + 15 >= kt.lo) | (key < a.n_sink)); };
     auto cache_row = [&](const Ids& x, int key0, int grp, int key) -> size_t {   // grp: key / 16 of the step
-        int id = x.pid[0];
-#pragma unroll
-        for (int i = 1; i < 4; ++i) id = grp == i ? x.pid[i] : id;
-        return (((size_t)max(id, 0) * a.c.Hkv + u.h) << a.c.page_shift) + ((key0 + key) & (page - 1));
+        return (((size_t)max(x.get(grp), 0) * a.c.Hkv + u.h) << a.c.page_shift) + ((key0 + key) & (page - 1));
     };
     Raw raw;
-    float ks = 1.0f, vs = 1.0f;
-    auto load = [&](int t, const Ids& x) {
-        const int key0 = key0_of(t);
+    auto load = [&](int t, Ids& x) {
+        const int n = t - t0, key0 = key0_of(t);
+        if (n % 16 == 0) pl.turn(table, a, u.h, n / 16, lane_key, seen);
+        const int at = 4 * (n % 16);
+        x = Ids{pl.page(at), pl.page(at + 1), pl.page(at + 2), pl.page(at + 3)};
         if (p.keys) {
 #pragma unroll
             for (int y = 0; y < 2; ++y)
@@ -373,35 +397,29 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 #pragma unroll
             for (int i = 0; i < 8; ++i) raw.v[i] = *reinterpret_cast<const uint32_t*>(v + (p.val_key(i) - p.val_key(0)) * D);
         }
-        if (tid < 4) {
-            const int id = tid == 0 ? x.pid[0] : tid == 1 ? x.pid[1] : tid == 2 ? x.pid[2] : x.pid[3];
-            const size_t tile = (size_t)max(id, 0) * a.c.Hkv + u.h;
-            ks = id >= 0 ? a.c.ks[tile] : 1.0f;
-            vs = id >= 0 ? a.c.vs[tile] : 1.0f;
-        }
     };
     auto seen_by_all = [&](int key0, const Ids& x, int lo, int hi) {   // every key of the step by rows at lo .. hi
-        return x.pid[0] >= 0 && x.pid[1] >= 0 && x.pid[2] >= 0 && x.pid[3] >= 0 && key0 + kKeys - 1 <= lo &&
+        return x.all() && key0 + kKeys - 1 <= lo &&
                key0 + kKeys <= kt.hi && (a.window <= 0 || key0 > hi - a.window || key0 + kKeys <= a.n_sink);
     };
     auto store = [&](int t, const Ids& x, Stage<D>& s) {
         const int key0 = key0_of(t);
-        const bool clean = x.pid[0] >= 0 && x.pid[1] >= 0 && x.pid[2] >= 0 && x.pid[3] >= 0 && key0 + kKeys <= kt.hi &&
+        const bool clean = x.all() && key0 + kKeys <= kt.hi &&
                            (key0 >= kt.lo || key0 + kKeys <= a.n_sink);
         if (!clean) {
             // bytes of keys that no row sees may be NaN: their weights are 0, so the values must be finite
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int key = key0 + p.val_key(i), grp = p.chunk >> 1;
-                const int id = grp == 0 ? x.pid[0] : grp == 1 ? x.pid[1] : grp == 2 ? x.pid[2] : x.pid[3];
-                const bool ok = id >= 0 && key < kt.hi && (key >= kt.lo || key < a.n_sink);
+                const int key = key0 + p.val_key(i);
+                const bool ok = (x.get(p.chunk >> 1) >= 0) & (key < kt.hi) & ((key >= kt.lo) | (key < a.n_sink));
                 raw.v[i] = ok ? raw.v[i] : 0u;
             }
         }
         store_stage<D>(p, raw, s);
-        if (tid < 4) {
-            const PageScale ps = page_scale(a.c2, ks, vs);
-            s.scale[tid] = at_f32x4{ps.c_, ps.lv_, ps.iv_, 0.0f};
+        const int n = t - t0;
+        if (wave == 0) {   // (before the loads of step t + 1, which may turn the lanes)
+            if (n % 16 == 0) pl.scales(a.c2);
+            if ((lane >> 2) == n % 16) s.scale[lane & 3] = at_f32x4{pl.s.c_, pl.s.lv_, pl.s.iv_, 0.0f};
         }
     };
     auto step = [&](int t, const Ids& x, const Stage<D>& s) {
@@ -414,24 +432,22 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int key = key0 + 32 * hb + 8 * (r >> 2) + 4 * g + (r & 3);
-                const bool ok = x.pid[2 * hb + (r >> 3)] >= 0 && key <= pos && key < kt.hi &&
-                                (a.window <= 0 || key > pos - a.window || key < a.n_sink);
+                const bool ok = (x.get(2 * hb + (r >> 3)) >= 0) & (key <= pos) & (key < kt.hi) &
+                                ((key > from) | (key < a.n_sink));
                 y[r] = ok ? y[r] : -INFINITY;
             }
         });
     };
 
     // step t computes from one stage while t + 1 is written to the other and
-    // t + 2 is on its way; page ids are read one step before that
+    // t + 2 is on its way
     if (t0 < t1) {
         Ids now, next, far;
-        ids(t0, now);
+        pl.read(table, a, 0, lane_key);
         load(t0, now);
-        next = far = now;
-        if (t0 + 1 < t1) ids(t0 + 1, next);
         store(t0, now, ls.st[0]);
+        next = far = now;
         if (t0 + 1 < t1) load(t0 + 1, next);
-        if (t0 + 2 < t1) ids(t0 + 2, far);
         __syncthreads();
         for (int t = t0; t < t1; ++t) {
             const int x = (t - t0) & 1;
@@ -440,7 +456,6 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
             step(t, now, ls.st[x]);
             now = next;
             next = far;
-            if (t + 3 < t1) ids(t + 3, far);
             __syncthreads();
         }
     }
@@ -491,7 +506,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_kernel(AttendArgs a) 
     int64_t total = 0, sum;
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += kThreads) {
         scan_256(line_of(a, b0 + threadIdx.x), sc, sum);
-        total += sum;
+        total += uniform(sum);
     }
     const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kMinKeys);
     // Workgroups go to the eight XCDs in turn: each XCD takes a stretch of the
@@ -507,16 +522,16 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_kernel(AttendArgs a) 
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += kThreads) {
         const int64_t w = line_of(a, b0 + threadIdx.x), x = before + scan_256(w, sc, sum);
         if (x - w <= at && at < x) sc.b = b0 + threadIdx.x, sc.at = x - w;
-        before += sum;
+        before += uniform(sum);
         if (at < before) break;
     }
     __syncthreads();
-    int b = __builtin_amdgcn_readfirstlane(sc.b);
-    int64_t first = sc.at;
+    int b = uniform(sc.b);
+    int64_t first = uniform(sc.at);
     SeqLine s = seq_line(a, b);
     while (true) {
         const int64_t per_head = s.before(s.tiles);
-        int h = (int)((at - first) / per_head);
+        int h = uniform((int)((at - first) / per_head));
         const int64_t off = at - first - h * per_head;
         int i = 0, hi = s.tiles - 1;   // the row tile that holds off
         while (i < hi) {
@@ -534,7 +549,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_kernel(AttendArgs a) 
                 u.h = h;
                 u.f0 = i * kRows;
                 u.f1 = min(u.f0 + kRows, (s.sr.r1 - s.sr.r0) * a.G);
-                const KeyTiles kt = key_tiles(a, s.sr.pos0 + u.f0 / a.G, s.sr.pos0 + (u.f1 - 1) / a.G);
+                const KeyTiles kt = key_tiles(a, s.sr.pos0 + uniform(u.f0 / a.G), s.sr.pos0 + uniform((u.f1 - 1) / a.G));
                 // a step belongs to the range that its first key lies in
                 const int64_t k0 = at - us, k1 = min(end - us, cost);
                 const int t0 = (int)((k0 + kKeys - 1) / kKeys), t1 = (int)((k1 + kKeys - 1) / kKeys);
@@ -574,19 +589,19 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArg
     extern __shared__ at_u32x4 sh[];
     Lds<D, true>& ls = *reinterpret_cast<Lds<D, true>*>(sh);
     Ring& ring = ls.ring[0];
-    const int ht = (a.group * a.G + kRows - 1) / kRows;
+    const int ht = (a.group * a.G + kRows - 1) / kRows;   // row tiles of a group
     UnitRows u;
-    u.h = blockIdx.x % a.c.Hkv;
-    int rest = blockIdx.x / a.c.Hkv;
-    const int tile = rest % ht;
-    rest /= ht;
-    const int split = rest % a.splits, grp = rest / a.splits;
+    u.h = uniform((int)(blockIdx.x % a.c.Hkv));
+    int rest = uniform((int)(blockIdx.x / a.c.Hkv));
+    const int tile = uniform(rest % ht);
+    rest = uniform(rest / ht);
+    const int split = uniform(rest % a.splits), grp = uniform(rest / a.splits);
     u.r0 = grp * a.group;
     u.f0 = tile * kRows;
     u.f1 = min(u.f0 + kRows, min(a.group, a.T - u.r0) * a.G);
     if (u.f0 >= u.f1) return;
     const int n = min(max(a.lens[grp], 0), a.cap);
-    const int per = ((n + kKeys - 1) / kKeys + a.splits - 1) / a.splits * kKeys;
+    const int per = uniform(((n + kKeys - 1) / kKeys + a.splits - 1) / a.splits * kKeys);
     const int e0 = split * per, e1 = min(e0 + per, n);
     if (split > 0 && e0 >= e1) return;
     const int used = per > 0 ? (n + per - 1) / per : 1;
