@@ -22,7 +22,7 @@
 //    to; pairing keys byte by byte gives, for each e < D / 16, the operand
 //    whose row c is dimension c D / 16 + e.
 // Softmax statistics stay in the lane: m moves only when a score passes it by
-// 2^8, so most tiles need no exchange between lanes; the weights' sums of the
+// 8, so most tiles need no exchange between lanes; the weights' sums of the
 // four lane groups are joined once at the end.
 #include <algorithm>
 
@@ -68,18 +68,9 @@ struct KeyScale {   // listed keys: one set each
 // and the D / 16 x 4 accumulators of row c, dimensions (4 g + r) D/16 + e.
 template <int D>
 struct RowState {
-    float m, l;
+    float m, over, l;
     at_f32x4 o[D / 16];
 };
-
-template <int D>
-__device__ __forceinline__ void rescale(RowState<D>& st, float m_new) {
-    const float f = __builtin_amdgcn_exp2f(st.m - m_new);
-    st.l *= f;
-#pragma unroll
-    for (int e = 0; e < D / 16; ++e) st.o[e] *= f;
-    st.m = m_new;
-}
 
 // Word w of the lane's value bytes as matrix operands: operand e holds byte
 // 4 w + e of its 8 keys.
@@ -126,11 +117,11 @@ __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const
     at_f16x8 p[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        float y[8], top = kNoRef;
+        float y[8], top = -INFINITY;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[4 * a + i] = __builtin_fmaf(s[mt][a][i], hs[a].c(i), hs[a].lv(i));
+            for (int i = 0; i < 4; ++i) y[4 * a + i] = __builtin_fmaf(s[mt][a][i], hs[a].c(i), hs[a].lv(i) - st[mt].m);
         if (masked) {
 #pragma unroll
             for (int a = 0; a < 2; ++a)
@@ -139,13 +130,25 @@ __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
-        if (__any(top > st[mt].m + kSlack)) rescale<D>(st[mt], fmaxf(st[mt].m, max_groups(top)));
+        if (__any(top > st[mt].over)) {
+            const float up = max_groups(top);
+            const bool move = up > st[mt].over;
+            const float d = move ? up : 0.0f;
+            const float f = st[mt].over == kSlack ? __builtin_amdgcn_exp2f(-d) : 1.0f;   // (nothing to scale at the first move)
+            st[mt].m += d;
+            st[mt].over = move ? kSlack : st[mt].over;
+            st[mt].l *= f;
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) st[mt].o[e] *= f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] -= d;
+        }
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
-                const float p0 = __builtin_amdgcn_exp2f(y[4 * a + i] - st[mt].m);
-                const float p1 = __builtin_amdgcn_exp2f(y[4 * a + i + 1] - st[mt].m);
+                const float p0 = __builtin_amdgcn_exp2f(y[4 * a + i]);
+                const float p1 = __builtin_amdgcn_exp2f(y[4 * a + i + 1]);
                 st[mt].l = __builtin_fmaf(p0, hs[a].iv(i), st[mt].l);
                 st[mt].l = __builtin_fmaf(p1, hs[a].iv(i + 1), st[mt].l);
                 const at_f32x2 pp{p0, p1};
@@ -187,7 +190,7 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
                 *reinterpret_cast<at_f32x4*>(so + (wave * 16 + c) * kStride + (4 * g + r) * (D / 16) + e) =
                     at_f32x4{st[mt].o[e][r], st[mt].o[e + 1][r], st[mt].o[e + 2][r], st[mt].o[e + 3][r]};
         if (g == 0) {
-            sm[(wave * 16 + c) * 2] = st[mt].m;
+            sm[(wave * 16 + c) * 2] = l > 0.0f ? st[mt].m : kNoRef;
             sm[(wave * 16 + c) * 2 + 1] = l;
         }
         __syncthreads();
@@ -366,7 +369,8 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     for (int mt = 0; mt < MT; ++mt) {
         row[mt] = row_of(mt * 16 + c);
         pos[mt] = row[mt] < 0 ? -1 : sr.pos0 + (f0 + mt * 16 + c) / a.G;
-        st[mt].m = kNoRef;
+        st[mt].m = 0.0f;
+        st[mt].over = -INFINITY;
         st[mt].l = 0.0f;
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) st[mt].o[e] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -587,7 +591,8 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         row[mt] = row_of(mt * 16 + c);
-        st[mt].m = kNoRef;
+        st[mt].m = 0.0f;
+        st[mt].over = -INFINITY;
         st[mt].l = 0.0f;
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) st[mt].o[e] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};

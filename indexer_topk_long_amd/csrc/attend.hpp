@@ -91,8 +91,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, at_bf16x2));
 }
 
-constexpr float kNoRef = -1e30f;     // reference before the first visible key
-constexpr float kSlack = 8.0f;       // scores may pass the reference by 2^8: weights up to 256 in fp16
+// Running softmax of a row: weights are 2^(y - m).  The reference m moves only
+// when a score passes it by more than kSlack (weights up to 256 in fp16), or
+// at the row's first visible key: until then m is 0 and `over`, the excess
+// that moves it, is -infinity.
+constexpr float kSlack = 8.0f;
+constexpr float kNoRef = -1e30f;     // reference of a part that saw no key
 
 // 8 e4m3 bytes as bf16, exact
 __device__ __forceinline__ at_bf16x8 bf16_of(uint32_t a, uint32_t b) {

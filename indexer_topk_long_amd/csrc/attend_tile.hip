@@ -155,13 +155,14 @@ __device__ __forceinline__ void pipelined(Read read, Use use) {
 // holds row c, of its accumulators the dimensions 32 t + 8 (r / 4) + 4 g + r % 4.
 template <int D>
 struct WaveState {
-    float m, l;
+    float m, over, l;
     at_f32x16 o[D / 32];
 };
 
-// 64 keys of a stage against the wave's rows.  scale(hb, i): constants of the
-// lane's keys 4 i .. 4 i + 3 of half hb (i < 4), as at_f32x4 c, lv, iv;
-// mask(hb, y): hides keys the lane's row does not see.
+// 64 keys of a stage against the wave's rows.  scale(hb, i, m, c, lv):
+// constants of the lane's keys 4 i .. 4 i + 3 of half hb (i < 4), lv less m;
+// scale.inverse: their 1 / vs; mask(hb, y): hides keys the lane's row does not
+// see.
 template <int D, class Scale, class Mask>
 __device__ __forceinline__ void step_keys(const Stage<D>& s, const at_bf16x8 (&q)[D / 16], WaveState<D>& st, Scale scale,
                                           Mask mask) {
@@ -175,13 +176,13 @@ __device__ __forceinline__ void step_keys(const Stage<D>& s, const at_bf16x8 (&q
             x[n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[n >> 1], x[n & 1], 0, 0, 0);
         });
     // scores relative to the reference
-    float top = kNoRef;
+    float top = -INFINITY;
 #pragma unroll
     for (int hb = 0; hb < 2; ++hb) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             at_f32x4 cc, lv;
-            scale(hb, i, cc, lv);
+            scale(hb, i, st.m, cc, lv);
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[hb][4 * i + r] = __builtin_fmaf(x[hb][4 * i + r], cc[r], lv[r]);
         }
@@ -189,12 +190,18 @@ __device__ __forceinline__ void step_keys(const Stage<D>& s, const at_bf16x8 (&q
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, x[hb][r]);
     }
-    if (__any(top > st.m + kSlack)) {
-        const float m = fmaxf(st.m, max_halves(top)), f = __builtin_amdgcn_exp2f(st.m - m);
+    if (__any(top > st.over)) {
+        const float up = max_halves(top);
+        const bool move = up > st.over;
+        const float d = move ? up : 0.0f;
+        const float f = st.over == kSlack ? __builtin_amdgcn_exp2f(-d) : 1.0f;   // (nothing to scale at the first move)
+        st.m += d;
+        st.over = move ? kSlack : st.over;
         st.l *= f;
 #pragma unroll
         for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
-        st.m = m;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[0][r] -= d, x[1][r] -= d;
     }
     at_f16x8 p[4];
 #pragma unroll
@@ -205,8 +212,8 @@ __device__ __forceinline__ void step_keys(const Stage<D>& s, const at_bf16x8 (&q
             scale.inverse(hb, i, iv);
 #pragma unroll
             for (int r = 0; r < 4; r += 2) {
-                const float p0 = __builtin_amdgcn_exp2f(x[hb][4 * i + r] - st.m);
-                const float p1 = __builtin_amdgcn_exp2f(x[hb][4 * i + r + 1] - st.m);
+                const float p0 = __builtin_amdgcn_exp2f(x[hb][4 * i + r]);
+                const float p1 = __builtin_amdgcn_exp2f(x[hb][4 * i + r + 1]);
                 st.l = __builtin_fmaf(p0, iv[r], st.l);
                 st.l = __builtin_fmaf(p1, iv[r + 1], st.l);
                 const at_f32x2 pp{p0, p1};
@@ -246,7 +253,8 @@ __device__ __forceinline__ void begin_rows(const AttendArgs& a, int64_t row, at_
         if (row >= 0) w = *reinterpret_cast<const at_u32x4*>(a.q + row * D + 16 * j + 8 * g);
         q[j] = __builtin_bit_cast(at_bf16x8, w);
     }
-    st.m = kNoRef;
+    st.m = 0.0f;
+    st.over = -INFINITY;
     st.l = 0.0f;
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
@@ -285,7 +293,7 @@ __device__ __forceinline__ void end_rows(const AttendArgs& a, int64_t row, const
             *reinterpret_cast<at_f32x4*>(part + (size_t)r * D + 32 * t + 8 * i + 4 * g) =
                 at_f32x4{st.o[t][4 * i], st.o[t][4 * i + 1], st.o[t][4 * i + 2], st.o[t][4 * i + 3]};
     if (g == 0) {
-        part[(size_t)kRows * D + 2 * r] = st.m;
+        part[(size_t)kRows * D + 2 * r] = l > 0.0f ? st.m : kNoRef;
         part[(size_t)kRows * D + 2 * r + 1] = l;
     }
 }
@@ -332,10 +340,11 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttendArgs& a, int pos_lo, i
 
 struct DenseScale {
     const at_f32x4* s;   // the stage's four pages: c, lv, iv
-    __device__ __forceinline__ void operator()(int hb, int i, at_f32x4& c, at_f32x4& lv) const {
+    __device__ __forceinline__ void operator()(int hb, int i, float m, at_f32x4& c, at_f32x4& lv) const {
         const at_f32x4 x = s[2 * hb + (i >> 1)];
+        const float y = x[1] - m;
         c = at_f32x4{x[0], x[0], x[0], x[0]};
-        lv = at_f32x4{x[1], x[1], x[1], x[1]};
+        lv = at_f32x4{y, y, y, y};
     }
     __device__ __forceinline__ void inverse(int hb, int i, at_f32x4& iv) const {
         const float x = s[2 * hb + (i >> 1)][2];
@@ -573,9 +582,10 @@ struct ListScale {
     const Ring* r;
     int at, g;   // the step's place in the ring, the lane's half
     __device__ __forceinline__ int key(int hb, int i) const { return at + 32 * hb + 8 * i + 4 * g; }
-    __device__ __forceinline__ void operator()(int hb, int i, at_f32x4& c, at_f32x4& lv) const {
+    __device__ __forceinline__ void operator()(int hb, int i, float m, at_f32x4& c, at_f32x4& lv) const {
         c = *reinterpret_cast<const at_f32x4*>(r->c + key(hb, i));
         lv = *reinterpret_cast<const at_f32x4*>(r->lv + key(hb, i));
+        lv = at_f32x4{lv[0] - m, lv[1] - m, lv[2] - m, lv[3] - m};
     }
     __device__ __forceinline__ void inverse(int hb, int i, at_f32x4& iv) const {
         iv = *reinterpret_cast<const at_f32x4*>(r->iv + key(hb, i));
