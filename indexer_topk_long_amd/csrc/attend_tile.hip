@@ -42,31 +42,37 @@ __device__ __forceinline__ float sum_halves(float x) {
     return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+// A stage of LDS: keys [64][D] bf16, then values [D][64] fp16.  16-byte chunk
+// x of a row lies at chunk x ^ swizzle(row), so that the 16 lanes of one LDS
+// cycle (256 bytes) touch all banks: 16 consecutive rows when read, 2 or 4 key
+// rows and 16 value rows 4 apart when written.  A 256-byte row (keys at
+// D = 128) takes its number; of 128-byte rows two fill the banks, and pairs
+// take theirs.  Rows are whole numbers of 128 bytes, so within a row a chunk
+// is exchanged by one XOR on the byte offset.
 template <int D>
-struct Stage {
-    uint16_t k[kKeys * D];
-    uint16_t v[D * kKeys];
-    at_f32x4 scale[kKeys / 16];   // dense: c, lv, iv of each 16 keys' page
-};
+constexpr int kStageBytes = 4 * kKeys * D;
+template <int D>
+constexpr int kValuesAt = 2 * kKeys * D;
 struct Ring {                     // listed keys, resolved
     int32_t row[2 * kRing];       // cache row of the unit's head, -1: no key
     uint32_t mask[2 * kRing];     // rows that see it
     float c[2 * kRing], lv[2 * kRing], iv[2 * kRing];
 };
-template <int D, bool LIST>
-struct Lds {
-    Stage<D> st[2];
-    Ring ring[LIST ? 1 : 0];
-};
-
-// Swizzles: key rows by their low bits; value rows so that both 8 consecutive
-// rows (reads) and 8 rows 4 apart (writes) get different chunks.
-template <int D>
-__device__ __forceinline__ int k_at(int key, int chunk) {
-    return key * D + ((chunk ^ (key & 7)) << 3);
+__device__ __forceinline__ uint8_t* lds() {
+    extern __shared__ at_u32x4 lds_words[];
+    return reinterpret_cast<uint8_t*>(lds_words);
 }
-__device__ __forceinline__ int v_at(int d, int chunk) {
-    return d * kKeys + ((chunk ^ ((d & 7) ^ ((d >> 3) & 3))) << 3);
+template <int D>
+__device__ __forceinline__ int key_swizzle(int key) {
+    return D == 128 ? key & 15 : (key >> 1) & 7;
+}
+__device__ __forceinline__ int val_swizzle(int d) { return ((d >> 1) & 7) ^ ((d >> 4) & 1); }
+// An offset that the compiler does not see through: what is derived from it is
+// formed again in every step, by an XOR each, and not kept in registers over
+// the loop.
+__device__ __forceinline__ int per_step(int off) {
+    asm volatile("" : "+v"(off));
+    return off;
 }
 
 // The thread's part of a step's bytes.  D = 128: every thread takes two
@@ -97,58 +103,34 @@ struct Raw {
     uint32_t v[8];
 };
 
+// The conversions of a step's bytes into the stage at LDS offset `stage`, in
+// four equal parts (i = 0 .. 3) that the matrix instructions of the step
+// before are issued between.
 template <int D>
-__device__ __forceinline__ void store_stage(const Part<D>& p, const Raw& r, Stage<D>& s) {
-    if (p.keys) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int key = p.key + 32 * x;
-            *reinterpret_cast<at_bf16x8*>(s.k + k_at<D>(key, 2 * p.piece)) = bf16_of(r.k[x][0], r.k[x][1]);
-            *reinterpret_cast<at_bf16x8*>(s.k + k_at<D>(key, 2 * p.piece + 1)) = bf16_of(r.k[x][2], r.k[x][3]);
-        }
+__device__ __forceinline__ void store_stage(const Part<D>& p, const Raw& r, int stage, int i) {
+    if (i < 2) {
+        if (!p.keys) return;
+        // rows key and key + 32, chunks 2 piece and 2 piece + 1
+        const int at = per_step(p.key * (2 * D) + (((2 * p.piece) ^ key_swizzle<D>(p.key)) << 4)) + stage;
+        *reinterpret_cast<at_bf16x8*>(lds() + at + i * (64 * D)) = bf16_of(r.k[i][0], r.k[i][1]);
+        *reinterpret_cast<at_bf16x8*>(lds() + (at ^ 16) + i * (64 * D)) = bf16_of(r.k[i][2], r.k[i][3]);
+        return;
     }
-    if (p.vals) {
-        at_f16x8 o[4];
+    if (!p.vals) return;
+    const int e = 2 * (i - 2);   // bytes e and e + 1 of the patch: value rows 4 dq + e and the next
+    at_f16x8 o0, o1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = __builtin_amdgcn_perm(r.v[2 * i + 1], r.v[2 * i], 0x05010400u);
-            const uint32_t hi = __builtin_amdgcn_perm(r.v[2 * i + 1], r.v[2 * i], 0x07030602u);
-            const at_f16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
-            const at_f16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
-            const at_f16x2 x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
-            const at_f16x2 x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
-            o[0][2 * i] = x0[0], o[0][2 * i + 1] = x0[1];
-            o[1][2 * i] = x1[0], o[1][2 * i + 1] = x1[1];
-            o[2][2 * i] = x2[0], o[2][2 * i + 1] = x2[1];
-            o[3][2 * i] = x3[0], o[3][2 * i + 1] = x3[1];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<at_f16x8*>(s.v + v_at(4 * p.dq + e, p.chunk)) = o[e];
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t w = __builtin_amdgcn_perm(r.v[2 * j + 1], r.v[2 * j], e ? 0x07030602u : 0x05010400u);
+        const at_f16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
+        const at_f16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true);
+        o0[2 * j] = x0[0], o0[2 * j + 1] = x0[1];
+        o1[2 * j] = x1[0], o1[2 * j + 1] = x1[1];
     }
-}
-
-// N matrix instructions whose LDS operands are read kAhead at a time, one
-// batch ahead of their use.  The scheduling barriers hold the order: left
-// alone, the compiler keeps one operand and waits for LDS before every
-// instruction.
-constexpr int kAhead = 2;
-template <int N, class V, class Read, class Use>
-__device__ __forceinline__ void pipelined(Read read, Use use) {
-    V f[2][kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) f[0][i] = read(i);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 0; n < N / kAhead; ++n) {
-        if (n + 1 < N / kAhead) {
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) f[(n + 1) & 1][i] = read((n + 1) * kAhead + i);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) use(n * kAhead + i, f[n & 1][i]);
-        __builtin_amdgcn_sched_barrier(0);
-    }
+    const int at = per_step(p.dq * 512 + ((p.chunk ^ val_swizzle(4 * p.dq)) << 4)) + stage + kValuesAt<D>;
+    const int pair = at ^ ((e >> 1) << 4);   // both rows' chunk
+    *reinterpret_cast<at_f16x8*>(lds() + pair + e * 128) = o0;
+    *reinterpret_cast<at_f16x8*>(lds() + pair + (e + 1) * 128) = o1;
 }
 
 // Running state of a wave's 32 rows: lane (c, g) = (lane % 32, lane / 32)
@@ -159,78 +141,144 @@ struct WaveState {
     at_f32x16 o[D / 32];
 };
 
-// 64 keys of a stage against the wave's rows.  scale(hb, i, m, c, lv):
-// constants of the lane's keys 4 i .. 4 i + 3 of half hb (i < 4), lv less m;
-// scale.inverse: their 1 / vs; mask(hb, y): hides keys the lane's row does not
-// see.
-template <int D, class Scale, class Mask>
-__device__ __forceinline__ void step_keys(const Stage<D>& s, const at_bf16x8 (&q)[D / 16], WaveState<D>& st, Scale scale,
-                                          Mask mask) {
+// 64 keys of a stage against the wave's rows, in two halves of 32.
+//
+// A wave issues in order, and a matrix instruction keeps its unit busy for 8
+// issue slots: the vector work of one half is written between the matrix
+// instructions of the other, and the next stage's conversions between those
+// of the last product (about 8 vector instructions each).  The scheduling
+// barriers hold that order; left alone, the compiler puts each product in one
+// run, and both waves of a SIMD then wait for the same unit in turn.
+//   scores 0 | scores 1 with weights of 0 | values 0 with weights of 1 | values 1 with fill
+// LDS operands are read kAhead instructions before their use.
+//
+// scale(hb, i, m, c, lv): constants of the lane's keys 4 i .. 4 i + 3 of half
+// hb (i < 4), lv less m; scale.inverse: their 1 / vs.  mask.each(hb, i, y)
+// hides keys among four, mask.late(hb, x) among all 16 where it says so.
+constexpr int kAhead = 4;
+template <int D, class Scale, class Mask, class Fill>
+__device__ __forceinline__ void step_keys(int stage, const at_bf16x8 (&q)[D / 16], WaveState<D>& st, Scale scale,
+                                          Mask mask, Fill fill) {
     const int lane = threadIdx.x & 63, c = lane & 31, g = lane >> 5;
-    at_f32x16 x[2];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) x[0][r] = x[1][r] = 0.0f;
-    pipelined<D / 8, at_bf16x8>(   // n = 2 j + hb
-        [&](int n) { return *reinterpret_cast<const at_bf16x8*>(s.k + k_at<D>(32 * (n & 1) + c, (n & ~1) + g)); },
-        [&](int n, const at_bf16x8& kf) {
-            x[n & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[n >> 1], x[n & 1], 0, 0, 0);
-        });
-    // scores relative to the reference
-    float top = -INFINITY;
-#pragma unroll
-    for (int hb = 0; hb < 2; ++hb) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            at_f32x4 cc, lv;
-            scale(hb, i, st.m, cc, lv);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[hb][4 * i + r] = __builtin_fmaf(x[hb][4 * i + r], cc[r], lv[r]);
-        }
-        mask(hb, x[hb]);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, x[hb][r]);
-    }
-    if (__any(top > st.over)) {
-        const float up = max_halves(top);
-        const bool move = up > st.over;
-        const float d = move ? up : 0.0f;
-        const float f = st.over == kSlack ? __builtin_amdgcn_exp2f(-d) : 1.0f;   // (nothing to scale at the first move)
-        st.m += d;
-        st.over = move ? kSlack : st.over;
-        st.l *= f;
-#pragma unroll
-        for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[0][r] -= d, x[1][r] -= d;
-    }
+    constexpr int N = D / 16;   // matrix instructions of a product of one half
+    at_f32x16 x0, x1;
     at_f16x8 p[4];
+    // operand n of the 4 N: keys n = N hb + j, then values n = 2 N + N hb + (D / 32) w + t
+    at_u32x4 frag[kAhead];
+    const int k0 = per_step(c * (2 * D) + ((g ^ key_swizzle<D>(c)) << 4)) + stage;
+    const int v0 = per_step(c * 128 + ((g ^ val_swizzle(c)) << 4)) + stage + kValuesAt<D>;
+    auto fetch = [&](int n) {
+        if (n >= 4 * N) return;
+        const int w = (n - 2 * N) / (D / 32), t = (n - 2 * N) % (D / 32);
+        // key row 32 hb + c, chunk 2 j + g; value row 32 t + c, chunk 2 w + g
+        const int at = n < 2 * N ? (k0 ^ (32 * (n % N))) + 64 * D * (n / N) : (v0 ^ (32 * w)) + 4096 * t;
+        frag[n % kAhead] = *reinterpret_cast<const at_u32x4*>(lds() + at);
+    };
 #pragma unroll
-    for (int hb = 0; hb < 2; ++hb)
+    for (int i = 0; i < kAhead; ++i) fetch(i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            at_f32x4 iv;
-            scale.inverse(hb, i, iv);
+    for (int r = 0; r < 16; ++r) x0[r] = x1[r] = 0.0f;
+    auto score = [&](int n) {
+        at_f32x16& x = n < N ? x0 : x1;
+        x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(at_bf16x8, frag[n % kAhead]), q[n % N], x, 0, 0, 0);
+        fetch(n + kAhead);
+    };
+    auto value = [&](int n) {
+        const int w = n / (D / 32), t = n % (D / 32);
+        st.o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(at_f16x8, frag[n % kAhead]), p[w], st.o[t], 0, 0, 0);
+        fetch(2 * N + n + kAhead);
+    };
+    float top = -INFINITY;
+    auto relative = [&](int hb, at_f32x16& x, int i) {   // scores of four keys relative to the reference
+        at_f32x4 cc, lv;
+        scale(hb, i, st.m, cc, lv);
 #pragma unroll
-            for (int r = 0; r < 4; r += 2) {
-                const float p0 = __builtin_amdgcn_exp2f(x[hb][4 * i + r]);
-                const float p1 = __builtin_amdgcn_exp2f(x[hb][4 * i + r + 1]);
-                st.l = __builtin_fmaf(p0, iv[r], st.l);
-                st.l = __builtin_fmaf(p1, iv[r + 1], st.l);
-                const at_f32x2 pp{p0, p1};
-                const at_f16x2 ph = __builtin_convertvector(pp, at_f16x2);
-                p[2 * hb + (i >> 1)][4 * (i & 1) + r] = ph[0];
-                p[2 * hb + (i >> 1)][4 * (i & 1) + r + 1] = ph[1];
+        for (int r = 0; r < 4; ++r) x[4 * i + r] = __builtin_fmaf(x[4 * i + r], cc[r], lv[r]);
+        mask.each(hb, i, x);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, x[4 * i + r]);
+    };
+    auto settle = [&](int hb, at_f32x16& x) {   // moves the reference where a score passes it by too much
+        if (mask.late(hb, x)) {
+            top = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, x[r]);
+        }
+        if (__any(top > st.over)) {
+            const float up = max_halves(top);
+            const bool move = up > st.over;
+            const float d = move ? up : 0.0f;
+            const float f = st.over == kSlack ? __builtin_amdgcn_exp2f(-d) : 1.0f;   // (nothing to scale at the first move)
+            st.m += d;
+            st.over = move ? kSlack : st.over;
+            st.l *= f;
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] -= d;
+            if (hb == 1) {   // half 0's weights, part of whose product is still to come
+                const _Float16 fh = (_Float16)f;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) p[0][r] *= fh, p[1][r] *= fh;
             }
         }
-    pipelined<D / 8, at_f16x8>(    // n = (D / 32) w + t
-        [&](int n) {
-            const int w = n / (D / 32), t = n % (D / 32);
-            return *reinterpret_cast<const at_f16x8*>(s.v + v_at(32 * t + c, 2 * w + g));
-        },
-        [&](int n, const at_f16x8& vf) {
-            const int w = n / (D / 32), t = n % (D / 32);
-            st.o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[w], st.o[t], 0, 0, 0);
-        });
+        top = -INFINITY;
+    };
+    auto weights = [&](int hb, const at_f32x16& x, int i) {   // of four keys
+        at_f32x4 iv;
+        scale.inverse(hb, i, iv);
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+            const float a = __builtin_amdgcn_exp2f(x[4 * i + r]), b = __builtin_amdgcn_exp2f(x[4 * i + r + 1]);
+            st.l = __builtin_fmaf(a, iv[r], st.l);
+            st.l = __builtin_fmaf(b, iv[r + 1], st.l);
+            const at_f32x2 ab{a, b};
+            const at_f16x2 h = __builtin_convertvector(ab, at_f16x2);
+            p[2 * hb + (i >> 1)][4 * (i & 1) + r] = h[0];
+            p[2 * hb + (i >> 1)][4 * (i & 1) + r + 1] = h[1];
+        }
+    };
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        score(n);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int n = 0; n < N / 2; ++n) {
+        score(N + n);
+#pragma unroll
+        for (int i = 0; i < 8 / N; ++i) relative(0, x0, n * (8 / N) + i);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    settle(0, x0);
+#pragma unroll
+    for (int n = 0; n < N / 2; ++n) {
+        score(N + N / 2 + n);
+#pragma unroll
+        for (int i = 0; i < 8 / N; ++i) weights(0, x0, n * (8 / N) + i);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int n = 0; n < N / 2; ++n) {
+        value(n);
+#pragma unroll
+        for (int i = 0; i < 8 / N; ++i) relative(1, x1, n * (8 / N) + i);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    settle(1, x1);
+#pragma unroll
+    for (int n = 0; n < N / 2; ++n) {
+        value(N / 2 + n);
+#pragma unroll
+        for (int i = 0; i < 8 / N; ++i) weights(1, x1, n * (8 / N) + i);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        value(N + n);
+        if (n % (N / 4) == 0) fill(n / (N / 4));
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 // The unit's rows, flattened (row, head) from f0 to f1: row r0 + f / G, head
@@ -338,23 +386,30 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttendArgs& a, int pos_lo, i
     return k;
 }
 
+// Constants of a step's four pages, in scalar registers.  (Named, not an
+// array: an indexed array ends up in scratch memory, and the wait for it is a
+// wait for every load in flight.)
+struct StepScales {
+    PageScale s0, s1, s2, s3;
+    __device__ __forceinline__ PageScale get(int i) const { return i == 0 ? s0 : i == 1 ? s1 : i == 2 ? s2 : s3; }
+};
 struct DenseScale {
-    const at_f32x4* s;   // the stage's four pages: c, lv, iv
+    const StepScales& s;
     __device__ __forceinline__ void operator()(int hb, int i, float m, at_f32x4& c, at_f32x4& lv) const {
-        const at_f32x4 x = s[2 * hb + (i >> 1)];
-        const float y = x[1] - m;
-        c = at_f32x4{x[0], x[0], x[0], x[0]};
+        const PageScale x = s.get(2 * hb + (i >> 1));
+        const float y = x.lv_ - m;
+        c = at_f32x4{x.c_, x.c_, x.c_, x.c_};
         lv = at_f32x4{y, y, y, y};
     }
     __device__ __forceinline__ void inverse(int hb, int i, at_f32x4& iv) const {
-        const float x = s[2 * hb + (i >> 1)][2];
+        const float x = s.get(2 * hb + (i >> 1)).iv_;
         iv = at_f32x4{x, x, x, x};
     }
 };
 
 template <int D>
 __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& sr, int b, const UnitRows& u,
-                                           const KeyTiles& kt, int t0, int t1, Lds<D, false>& ls, float* part) {
+                                           const KeyTiles& kt, int t0, int t1, float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
     const int fw = u.f0 + 32 * wave;                      // the wave's rows [fw, fw1)
@@ -371,14 +426,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     const int page = 1 << a.c.page_shift;
     const Part<D> p;
     auto key0_of = [&](int t) { return (t < kt.sink_tiles ? t : kt.win_tile0 + t - kt.sink_tiles) * kKeys; };
-    // pages of a step's four 16-key groups; a lane holds one of the next 16 steps'
-    // (named, not an array: an array copied from step to step stays in scratch
-    // memory, and the wait for it is a wait for every load in flight)
-    struct Ids {
-        int p0, p1, p2, p3;
-        __device__ __forceinline__ int get(int i) const { return i == 0 ? p0 : i == 1 ? p1 : i == 2 ? p2 : p3; }
-        __device__ __forceinline__ bool all() const { return (p0 | p1 | p2 | p3) >= 0; }
-    };
+    // a lane holds the page of one 16-key group of the next 16 steps
     PageLanes pl;
     auto lane_key = [&](int block) {
         const int t = t0 + 16 * block + (lane >> 2);
@@ -386,85 +434,98 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     };
     // (a page with no visible key is not looked at: its scale and bytes may be anything)
     auto seen = [&](int key) { return (key < kt.hi) & ((key + 15 >= kt.lo) | (key < a.n_sink)); };
-    auto cache_row = [&](const Ids& x, int key0, int grp, int key) -> size_t {   // grp: key / 16 of the step
-        return (((size_t)max(x.get(grp), 0) * a.c.Hkv + u.h) << a.c.page_shift) + ((key0 + key) & (page - 1));
-    };
+    // What later needs to know of a step's four pages: bit i is set when keys
+    // 16 i .. of the step have a page and are looked at.
     Raw raw;
-    auto load = [&](int t, Ids& x) {
-        const int n = t - t0, key0 = key0_of(t);
+    auto load = [&](int t) -> int {
+        const int n = t - t0, key0 = key0_of(t), at = 4 * (n % 16);
         if (n % 16 == 0) pl.turn(table, a, u.h, n / 16, lane_key, seen);
-        const int at = 4 * (n % 16);
-        x = Ids{pl.page(at), pl.page(at + 1), pl.page(at + 2), pl.page(at + 3)};
-        if (p.keys) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-                raw.k[y] = *reinterpret_cast<const at_u32x4*>(
-                    a.c.k + cache_row(x, key0, (p.key + 32 * y) >> 4, p.key + 32 * y) * D + 16 * p.piece);
+        const int p0 = pl.page(at), p1 = pl.page(at + 1), p2 = pl.page(at + 2), p3 = pl.page(at + 3);
+        auto page_of = [&](int grp) { return grp == 0 ? p0 : grp == 1 ? p1 : grp == 2 ? p2 : p3; };
+        // byte offset in the cache of key 16 grp of the step: scalar
+        auto base = [&](int grp) -> size_t {
+            return ((((size_t)max(page_of(grp), 0) * a.c.Hkv + u.h) << a.c.page_shift) + ((key0 + 16 * grp) & (page - 1))) * D;
+        };
+        if (p.keys) {   // a wave's pieces lie in one group, and in the second one on
+            const int grp = D == 128 ? wave >> 1 : wave & 1;
+            const int off = (p.key & 15) * D + 16 * p.piece;
+            raw.k[0] = *reinterpret_cast<const at_u32x4*>(a.c.k + base(grp) + off);
+            raw.k[1] = *reinterpret_cast<const at_u32x4*>(a.c.k + base(grp + 2) + off);
         }
-        if (p.vals) {
-            const uint8_t* v = a.c.v + cache_row(x, key0, p.chunk >> 1, p.val_key(0)) * D + 4 * p.dq;
+        if (p.vals) {   // D = 128: a wave's patches lie in one group; D = 64: in one a half wave
+            const int off = (p.val_key(0) & 15) * D + 4 * p.dq;
+            const uint8_t* v = D == 128 ? a.c.v + base(wave) + off
+                                        : a.c.v + (lane < 32 ? base(2 * (wave & 1)) : base(2 * (wave & 1) + 1)) + off;
 #pragma unroll
             for (int i = 0; i < 8; ++i) raw.v[i] = *reinterpret_cast<const uint32_t*>(v + (p.val_key(i) - p.val_key(0)) * D);
         }
+        return (p0 >= 0 ? 1 : 0) | (p1 >= 0 ? 2 : 0) | (p2 >= 0 ? 4 : 0) | (p3 >= 0 ? 8 : 0);
     };
-    auto seen_by_all = [&](int key0, const Ids& x, int lo, int hi) {   // every key of the step by rows at lo .. hi
-        return x.all() && key0 + kKeys - 1 <= lo &&
-               key0 + kKeys <= kt.hi && (a.window <= 0 || key0 > hi - a.window || key0 + kKeys <= a.n_sink);
+    auto seen_by_all = [&](int key0, int ok, int lo, int hi) {   // every key of the step by rows at lo .. hi
+        return ok == 15 && key0 + kKeys - 1 <= lo && key0 + kKeys <= kt.hi &&
+               (a.window <= 0 || key0 > hi - a.window || key0 + kKeys <= a.n_sink);
     };
-    auto store = [&](int t, const Ids& x, Stage<D>& s) {
+    // what a step's bytes need before they are converted
+    auto settle_raw = [&](int t, int pages) {
         const int key0 = key0_of(t);
-        const bool clean = x.all() && key0 + kKeys <= kt.hi &&
-                           (key0 >= kt.lo || key0 + kKeys <= a.n_sink);
-        if (!clean) {
-            // bytes of keys that no row sees may be NaN: their weights are 0, so the values must be finite
+        if (pages == 15 && key0 + kKeys <= kt.hi && (key0 >= kt.lo || key0 + kKeys <= a.n_sink)) return;
+        // bytes of keys that no row sees may be NaN: their weights are 0, so the values must be finite
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int key = key0 + p.val_key(i);
-                const bool ok = (x.get(p.chunk >> 1) >= 0) & (key < kt.hi) & ((key >= kt.lo) | (key < a.n_sink));
-                raw.v[i] = ok ? raw.v[i] : 0u;
-            }
-        }
-        store_stage<D>(p, raw, s);
-        const int n = t - t0;
-        if (wave == 0) {   // (before the loads of step t + 1, which may turn the lanes)
-            if (n % 16 == 0) pl.scales(a.c2);
-            if ((lane >> 2) == n % 16) s.scale[lane & 3] = at_f32x4{pl.s.c_, pl.s.lv_, pl.s.iv_, 0.0f};
+        for (int i = 0; i < 8; ++i) {
+            const int key = key0 + p.val_key(i);
+            const bool ok = ((pages >> (p.chunk >> 1)) & 1) & (key < kt.hi) & ((key >= kt.lo) | (key < a.n_sink));
+            raw.v[i] = ok ? raw.v[i] : 0u;
         }
     };
-    auto step = [&](int t, const Ids& x, const Stage<D>& s) {
-        const int key0 = key0_of(t);
-        if (fw >= fw1 || key0 > pos_hi) return;   // no row of the wave sees a key of it
-        if (a.window > 0 && key0 + kKeys - 1 <= max(pos_lo, 0) - a.window && key0 >= a.n_sink) return;
-        const bool all = seen_by_all(key0, x, pos_lo, pos_hi);
-        step_keys<D>(s, q, st, DenseScale{s.scale}, [&](int hb, at_f32x16& y) {
-            if (all) return;
+    struct Mask {
+        int pages;
+        bool none;                  // no key of the step is hidden
+        int key, last, from, n_sink;   // the lane's first key; its row sees keys up to last, behind from or below n_sink
+        __device__ __forceinline__ void each(int, int, at_f32x16&) const {}
+        __device__ __forceinline__ bool late(int hb, at_f32x16& y) const {
+            if (none) return false;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int key = key0 + 32 * hb + 8 * (r >> 2) + 4 * g + (r & 3);
-                const bool ok = (x.get(2 * hb + (r >> 3)) >= 0) & (key <= pos) & (key < kt.hi) &
-                                ((key > from) | (key < a.n_sink));
-                y[r] = ok ? y[r] : -INFINITY;
+            for (int i = 0; i < 4; ++i) {
+                // by signs, not by 16 compares at once: their results would fill the scalar registers
+                const int end = (pages >> (2 * hb + (i >> 1))) & 1 ? last : -1;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int k = key + 32 * hb + 8 * i + r;
+                    const uint32_t hide = (uint32_t)(min(end - k, max(k - from - 1, n_sink - 1 - k)) >> 31);
+                    y[4 * i + r] = __uint_as_float((~hide & __float_as_uint(y[4 * i + r])) | (hide & 0xff800000u));
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-        });
+            return true;
+        }
+    };
+    auto step = [&](int t, int pages, int stage, auto fill) {
+        const int n = t - t0, key0 = key0_of(t), at = 4 * (n % 16);
+        if (n % 16 == 0) pl.scales(a.c2);
+        // (a wave none of whose rows sees the step goes through it too: a way
+        // around would give its accumulators two places, and cost 70 spills)
+        const StepScales sc{pl.scale(at), pl.scale(at + 1), pl.scale(at + 2), pl.scale(at + 3)};
+        step_keys<D>(stage, q, st, DenseScale{sc},
+                     Mask{pages, seen_by_all(key0, pages, pos_lo, pos_hi), key0 + 4 * g, min(pos, kt.hi - 1), from, a.n_sink}, fill);
     };
 
     // step t computes from one stage while t + 1 is written to the other and
     // t + 2 is on its way
     if (t0 < t1) {
-        Ids now, next, far;
         pl.read(table, a, 0, lane_key);
-        load(t0, now);
-        store(t0, now, ls.st[0]);
-        next = far = now;
-        if (t0 + 1 < t1) load(t0 + 1, next);
+        int now = load(t0), next = 0;
+        settle_raw(t0, now);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_stage<D>(p, raw, 0, i);
+        if (t0 + 1 < t1) next = load(t0 + 1);
         __syncthreads();
         for (int t = t0; t < t1; ++t) {
             const int x = (t - t0) & 1;
-            if (t + 1 < t1) store(t + 1, next, ls.st[x ^ 1]);
-            if (t + 2 < t1) load(t + 2, far);
-            step(t, now, ls.st[x]);
+            // (past the last step the conversions write a stage that nothing reads)
+            if (t + 1 < t1) settle_raw(t + 1, next);
+            step(t, now, x * kStageBytes<D>, [&](int i) { store_stage<D>(p, raw, (x ^ 1) * kStageBytes<D>, i); });
             now = next;
-            next = far;
+            if (t + 2 < t1) next = load(t + 2);
             __syncthreads();
         }
     }
@@ -480,8 +541,12 @@ struct Crossing {
 };
 struct ScanLds {
     int64_t wave[kThreads / 64];
-    int64_t at;   // place of sequence b, which the workgroup's range begins in
-    int b;
+};
+// Where a workgroup stands on the line.  It lives in LDS and is read again for
+// every unit: in registers over a unit's loop it would cost that loop spills.
+struct Place {
+    int64_t at, first;   // on the line: the place reached, and where sequence b begins
+    int b, h, i;         // sequence, head, row tile
 };
 __device__ __forceinline__ int64_t scan_256(int64_t x, ScanLds& ls, int64_t& sum) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -509,8 +574,6 @@ __device__ __forceinline__ int64_t line_of(const AttendArgs& a, int b) {
 
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attend_tile_kernel(AttendArgs a) {
-    extern __shared__ at_u32x4 sh[];
-    Lds<D, false>& ls = *reinterpret_cast<Lds<D, false>*>(sh);
     __shared__ ScanLds sc;
     int64_t total = 0, sum;
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += kThreads) {
@@ -522,57 +585,64 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_kernel(AttendArgs a) 
     // line, so that the row tiles of one head read its keys through one L2.
     const int n8 = gridDim.x / 8;
     const int me = (int)blockIdx.x < 8 * n8 ? (blockIdx.x % 8) * n8 + blockIdx.x / 8 : (int)blockIdx.x;
-    int64_t at = me * per;
-    const int64_t end = min(at + per, total);
+    const int64_t begin = me * per, end = min(begin + per, total);
     Crossing* crossing = reinterpret_cast<Crossing*>(a.head) + me;
     if (threadIdx.x == 0) crossing->n = 0;
-    if (at >= end) return;
+    if (begin >= end) return;
+    __shared__ Place place;
     int64_t before = 0;
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += kThreads) {
         const int64_t w = line_of(a, b0 + threadIdx.x), x = before + scan_256(w, sc, sum);
-        if (x - w <= at && at < x) sc.b = b0 + threadIdx.x, sc.at = x - w;
+        if (x - w <= begin && begin < x) {   // the sequence that the range begins in
+            const SeqLine s = seq_line(a, b0 + threadIdx.x);
+            const int64_t off = begin - (x - w), head = s.before(s.tiles);
+            const int h = (int)(off / head);
+            int lo = 0, hi = s.tiles - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (s.before(mid) <= off - h * head)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            place = Place{begin, x - w, b0 + (int)threadIdx.x, h, lo};
+        }
         before += uniform(sum);
-        if (at < before) break;
+        if (begin < before) break;
     }
     __syncthreads();
-    int b = uniform(sc.b);
-    int64_t first = uniform(sc.at);
-    SeqLine s = seq_line(a, b);
     while (true) {
-        const int64_t per_head = s.before(s.tiles);
-        int h = uniform((int)((at - first) / per_head));
-        const int64_t off = at - first - h * per_head;
-        int i = 0, hi = s.tiles - 1;   // the row tile that holds off
-        while (i < hi) {
-            const int mid = (i + hi + 1) >> 1;
-            if (s.before(mid) <= off)
-                i = mid;
-            else
-                hi = mid - 1;
-        }
-        for (; h < a.c.Hkv && at < end; ++h, i = 0)
-            for (; i < s.tiles && at < end; ++i) {
-                const int64_t us = first + h * per_head + s.before(i), cost = s.cost(i);
-                UnitRows u;
-                u.r0 = s.sr.r0;
-                u.h = h;
-                u.f0 = i * kRows;
-                u.f1 = min(u.f0 + kRows, (s.sr.r1 - s.sr.r0) * a.G);
-                const KeyTiles kt = key_tiles(a, s.sr.pos0 + uniform(u.f0 / a.G), s.sr.pos0 + uniform((u.f1 - 1) / a.G));
-                // a step belongs to the range that its first key lies in
-                const int64_t k0 = at - us, k1 = min(end - us, cost);
-                const int t0 = (int)((k0 + kKeys - 1) / kKeys), t1 = (int)((k1 + kKeys - 1) / kKeys);
-                const bool whole = k0 == 0 && k1 == cost;
-                float* part = whole ? nullptr : a.part + (2 * (int64_t)me + (at == me * per ? 0 : 1)) * part_floats<D>();
-                dense_unit<D>(a, s.sr, b, u, kt, t0, min(t1, kt.tiles), ls, part);
-                if (k0 == 0 && k1 < cost && threadIdx.x == 0)
-                    *crossing = Crossing{(int)((us + cost - 1) / per) - me + 1, 2 * me + (at == me * per ? 0 : 1), u};
-                at = us + k1;
+        const int b = uniform(place.b), h = uniform(place.h), i = uniform(place.i);
+        const int64_t at = uniform(place.at);
+        const SeqLine s = seq_line(a, b);
+        const int64_t us = uniform(place.first) + h * s.before(s.tiles) + s.before(i), cost = s.cost(i);
+        UnitRows u;
+        u.r0 = s.sr.r0;
+        u.h = h;
+        u.f0 = i * kRows;
+        u.f1 = min(u.f0 + kRows, (s.sr.r1 - s.sr.r0) * a.G);
+        // a step belongs to the range that its first key lies in
+        const int64_t k0 = at - us, k1 = min(end - us, cost);
+        float* part = nullptr;
+        if (k0 > 0 || k1 < cost) part = a.part + (2 * (int64_t)me + (at == begin ? 0 : 1)) * part_floats<D>();
+        if (k0 == 0 && k1 < cost && threadIdx.x == 0)
+            *crossing = Crossing{(int)((us + cost - 1) / per) - me + 1, 2 * me + (at == begin ? 0 : 1), u};
+        __syncthreads();
+        if (threadIdx.x == 0) {   // the next unit
+            Place n{us + k1, place.first, b, h, i + 1};
+            if (n.i == s.tiles) n.i = 0, ++n.h;
+            if (n.h == a.c.Hkv) {
+                n.h = 0;
+                n.first += a.c.Hkv * s.before(s.tiles);
+                n.b = n.at < end ? n.b + 1 : n.b;
+                while (n.at < end && seq_line(a, n.b).tiles == 0) ++n.b;
             }
-        if (at >= end) return;
-        first += a.c.Hkv * per_head;
-        do s = seq_line(a, ++b);
-        while (s.tiles == 0);
+            place = n;
+        }
+        const KeyTiles kt = key_tiles(a, s.sr.pos0 + uniform(u.f0 / a.G), s.sr.pos0 + uniform((u.f1 - 1) / a.G));
+        dense_unit<D>(a, s.sr, b, u, kt, (int)((k0 + kKeys - 1) / kKeys), min((int)((k1 + kKeys - 1) / kKeys), kt.tiles), part);
+        __syncthreads();
+        if (uniform(place.at) >= end) return;
     }
 }
 
@@ -596,9 +666,7 @@ struct ListScale {
 // are the group's list, cut into a.splits.
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArgs a) {
-    extern __shared__ at_u32x4 sh[];
-    Lds<D, true>& ls = *reinterpret_cast<Lds<D, true>*>(sh);
-    Ring& ring = ls.ring[0];
+    Ring& ring = *reinterpret_cast<Ring*>(lds() + 2 * kStageBytes<D>);
     const int ht = (a.group * a.G + kRows - 1) / kRows;   // row tiles of a group
     UnitRows u;
     u.h = uniform((int)(blockIdx.x % a.c.Hkv));
@@ -646,9 +714,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArg
     auto entry_page = [&]() {
         en.pid = -1;
         if (en.s >= 0 && en.s < end) en.pid = a.bt.table[en.s >> a.c.page_shift];
-        if (en.pid >= a.c.n_pages) en.pid = -1;
     };
     auto entry_scale = [&]() {
+        if (en.pid >= a.c.n_pages) en.pid = -1;
         const size_t at = (size_t)max(en.pid, 0) * a.c.Hkv + u.h;
         en.ks = en.pid >= 0 ? a.c.ks[at] : 1.0f;
         en.vs = en.pid >= 0 ? a.c.vs[at] : 1.0f;
@@ -686,28 +754,29 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArg
             }
         }
     };
-    auto store = [&](Stage<D>& s) {
+    auto settle_raw = [&]() {
         if (__any(none != 0)) {   // bytes behind no key may be NaN
 #pragma unroll
             for (int i = 0; i < 8; ++i) raw.v[i] = (none >> i) & 1u ? 0u : raw.v[i];
         }
-        store_stage<D>(p, raw, s);
     };
-    auto step = [&](int t, const Stage<D>& s) {
-        if (fw >= u.f1) return;
-        const int at = (t * kKeys) & (2 * kRing - 1);
-        step_keys<D>(s, q, st, ListScale{&ring, at, g}, [&](int hb, at_f32x16& y) {
+    struct Mask {
+        const Ring& ring;
+        int at, g, qi;
+        __device__ __forceinline__ void each(int hb, int i, at_f32x16& y) const {
+            const at_i32x4 m = *reinterpret_cast<const at_i32x4*>(ring.mask + at + 32 * hb + 8 * i + 4 * g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const at_i32x4 m = *reinterpret_cast<const at_i32x4*>(ring.mask + at + 32 * hb + 8 * i + 4 * g);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    // the row's bit over the whole word selects the score or -inf
-                    const uint32_t see = (uint32_t)__builtin_amdgcn_sbfe(m[r], qi, 1);
-                    y[4 * i + r] = __uint_as_float((see & __float_as_uint(y[4 * i + r])) | (~see & 0xff800000u));
-                }
+            for (int r = 0; r < 4; ++r) {
+                // the row's bit over the whole word selects the score or -infinity
+                const uint32_t see = (uint32_t)__builtin_amdgcn_sbfe(m[r], qi, 1);
+                y[4 * i + r] = __uint_as_float((see & __float_as_uint(y[4 * i + r])) | (~see & 0xff800000u));
             }
-        });
+        }
+        __device__ __forceinline__ bool late(int, at_f32x16&) const { return false; }
+    };
+    auto step = [&](int t, int stage, auto fill) {
+        const int at = (t * kKeys) & (2 * kRing - 1);
+        step_keys<D>(stage, q, st, ListScale{&ring, at, g}, Mask{ring, at, g, qi}, fill);
     };
 
     const int steps = (e1 - e0 + kKeys - 1) / kKeys;
@@ -720,18 +789,20 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArg
         entry_load(1);
         __syncthreads();
         load(0);
-        store(ls.st[0]);
+        settle_raw();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_stage<D>(p, raw, 0, i);
         if (steps > 1) load(1);
         __syncthreads();
         // a chunk's entries are read in the last two steps of the chunk two
         // before it, and resolved in the first two of the one before it
         for (int t = 0; t < steps; ++t) {
             const int x = t & 1, ph = t % kPer, chunk = t / kPer;
-            if (t + 1 < steps) store(ls.st[x ^ 1]);
-            if (t + 2 < steps) load(t + 2);
             if (ph == 0) entry_page();
-            step(t, ls.st[x]);
+            if (t + 1 < steps) settle_raw();
+            step(t, x * kStageBytes<D>, [&](int i) { store_stage<D>(p, raw, (x ^ 1) * kStageBytes<D>, i); });
             if (ph == 0) entry_scale();
+            if (t + 2 < steps) load(t + 2);
             if (ph == 1) entry_store(chunk + 1);
             if (ph == 2) entry_load(chunk + 2);
             __syncthreads();
@@ -793,7 +864,7 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attend_tile_list_join_kerne
 
 template <int D, bool LIST>
 hipError_t launch_d(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
-    constexpr size_t lds = sizeof(Lds<D, LIST>);
+    constexpr size_t lds = 2 * kStageBytes<D> + (LIST ? sizeof(Ring) : 0);
     const void* fn = LIST ? reinterpret_cast<const void*>(attend_tile_list_kernel<D>)
                           : reinterpret_cast<const void*>(attend_tile_kernel<D>);
     if (lds > 65536)
