@@ -1,5 +1,6 @@
 """Build the gfx950 HIP libraries in-tree: indexer_topk_long_amd/_lib/liblitetopk.so (the
-fused Indexer-TopK) and indexer_topk_long_amd/_lib/libltkpeak.so (the achievable-peak
+fused Indexer-TopK and the paged cache's operators), ltk_bind.so (the Python entry of the
+latter) and indexer_topk_long_amd/_lib/libltkpeak.so (the achievable-peak
 microbenchmarks the benchmark reports beside the vendor peaks).
 
     python -m indexer_topk_long_amd.build [-v]
@@ -22,6 +23,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "liblitetopk.so"
 PEAK_SRC = os.path.join(PKG, "peak", "peak.hip")
 PEAK_LIB = "libltkpeak.so"
+BIND_SRC = os.path.join(CSRC, "attend_bind.cpp")
+BIND_LIB = "ltk_bind.so"
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -41,6 +44,29 @@ def hipcc() -> str:
 
 def lib_path() -> str:
     return os.path.join(OUT_DIR, LIB_NAME)
+
+
+def bind_path() -> str:
+    return os.path.join(OUT_DIR, BIND_LIB)
+
+
+def _compile_bind(verbose: bool) -> str:
+    """The Python entry of the paged cache's operators: host code against torch's headers."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD_DIR, "attend_bind.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", "/opt/rocm/include", "-isystem",
+           sysconfig.get_paths()["include"], "-c", BIND_SRC, "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}{r.stderr}")
+    return obj
 
 
 def peak_lib_path() -> str:
@@ -66,8 +92,10 @@ def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(OUT_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, 8)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 2, 8)) as ex:
+        bind = ex.submit(_compile_bind, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs + [PEAK_SRC]))
+        bind_obj = bind.result()
     peak_obj = objs.pop()
     for out, inputs in ((lib_path(), objs), (peak_lib_path(), [peak_obj])):
         tmp = out + ".tmp"
@@ -76,6 +104,14 @@ def build(verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
         os.replace(tmp, out)
+    tmp = bind_path() + ".tmp"
+    import torch   # its libraries are in the process before this one is loaded: no path to them is kept
+    r = subprocess.run(["g++", "-shared", "-o", tmp, bind_obj, "-L", OUT_DIR, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN", "-L",
+                        os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+                        "-lc10_hip"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, bind_path())
     return lib_path()
 
 

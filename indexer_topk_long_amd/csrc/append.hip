@@ -149,11 +149,18 @@ __device__ __forceinline__ void rotate_item(float (&lo)[VEC], float (&hi)[VEC], 
     }
 }
 
+// With few rows (decode) a page's items keep 8 threads a row busy, each with
+// VEC sines in turn: then all threads form the rows' sines together, through
+// LDS (append-decode-batch, 96 rows: 10.1 -> 6.4 us; more rows fill the
+// threads as they are).
+constexpr int kShareRows = 4;
+
 // One page, one key/value head, keys or values.  NT threads, NI items each:
 // NT * NI >= page * D / (2 VEC).
 template <int D, int VEC, int NT, int NI>
 __device__ __forceinline__ void append_page(const AppendArgs& a, int unit, int h, bool is_v) {
     __shared__ float s_max[NT / 64];
+    __shared__ double s_cs[kShareRows][D / 2][2];
     constexpr int kItems = D / (2 * VEC);
     const int tid = threadIdx.x, page = 1 << a.c.page_shift;
     const int b = unit_seq(a.bt, unit, a.T, 1, page, 2);
@@ -166,13 +173,8 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int unit, int h
     if (p0 >= end) return;
     const int p1 = min(end, (P + 1) << a.c.page_shift), rows = p1 - p0;
     const int pid = a.bt.table[(size_t)b * a.bt.max_pages + P];
-    if (pid < 0 || pid >= a.c.n_pages) return;
-    const size_t tile = (size_t)pid * a.c.Hkv + h;            // the page's and head's tile
-    float* scale = (is_v ? a.c.vs : a.c.ks) + tile;
-    uint8_t* dst = (is_v ? a.c.v : a.c.k) + ((tile << a.c.page_shift) * D);
     const uint16_t* src = is_v ? a.v : a.k;
     const int slot0 = p0 & (page - 1);
-    const float old = slot0 > 0 ? *scale : 0.0f;
     const int rot = is_v ? 0 : a.rot;
 
     float lo[NI][VEC], hi[NI][VEC];
@@ -189,6 +191,20 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int unit, int h
             load_bf16<VEC>(p + it.hi, hi[n]);
         }
     }
+    const bool share = rows <= kShareRows && rot > 0;
+    if (share) {
+        for (int i = tid; i < rows * (rot / 2); i += NT) {
+            const int r = i / (rot / 2), f = i - r * (rot / 2);
+            sincospi(2.0 * turns(p0 + r, a.inv_freq[f]), &s_cs[r][f][1], &s_cs[r][f][0]);
+        }
+        __syncthreads();
+    }
+    // (the page id is first needed here: rows and sines do not wait for it)
+    if (pid < 0 || pid >= a.c.n_pages) return;
+    const size_t tile = (size_t)pid * a.c.Hkv + h;            // the page's and head's tile
+    float* scale = (is_v ? a.c.vs : a.c.ks) + tile;
+    uint8_t* dst = (is_v ? a.c.v : a.c.k) + ((tile << a.c.page_shift) * D);
+    const float old = slot0 > 0 ? *scale : 0.0f;
 #pragma unroll
     for (int n = 0; n < NI; ++n) {
         const int w = n * NT + tid, r = w / kItems;
@@ -196,7 +212,12 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int unit, int h
         if (r < rows && it.freq >= 0) {
             double c[VEC], s[VEC];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sincospi(2.0 * turns(p0 + r, a.inv_freq[it.freq + j]), &s[j], &c[j]);
+            for (int j = 0; j < VEC; ++j) {
+                if (share)
+                    c[j] = s_cs[r][it.freq + j][0], s[j] = s_cs[r][it.freq + j][1];
+                else
+                    sincospi(2.0 * turns(p0 + r, a.inv_freq[it.freq + j]), &s[j], &c[j]);
+            }
             rotate_item<VEC, double>(lo[n], hi[n], c, s, a.interleaved);
         }
 #pragma unroll
@@ -247,16 +268,7 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a, int blk) {
     const int64_t row64 = w / kItems / hb;
     if (row64 >= a.T) return;
     const int row = (int)row64;
-    // the row's sequence: the last one that begins at or before it and is not empty
-    int lo = 0, hi = a.bt.n_seq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu_at(a.bt, mid, a.T) <= row)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    const SeqRows sr = seq_rows(a.bt, lo, a.T);
+    const SeqRows sr = seq_rows(a.bt, row_seq(a.bt, row, a.T), a.T);
     if (row < sr.r0 || row >= sr.r1) return;
     const int pos = sr.pos0 + (row - sr.r0);
     const Item it = item_of<VEC>(i, a.rot, a.interleaved);
@@ -331,7 +343,11 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& bt, int D, const ui
     a.rot = rot;
     a.interleaved = interleaved;
     a.units = (int)unit_bound(bt.n_seq, T, 1, 1 << c.page_shift, 2);
+    // a thread's sines serve up to 8 heads while the threads left still fill the
+    // card (append-chunk-8k: 107 us with 1, 83 with 2, 76 with 4, 74 with 8, 80
+    // with 16; append-decode-batch: 10.0 us with 1, 12.3 with 8)
     a.heads_per = 1;
+    while (a.heads_per < 8 && (int64_t)T * Hq * (D / 16) / (2 * a.heads_per) >= 1 << 18) a.heads_per *= 2;
     // rot / 2 (half-split pairs) and rot (the border) in whole vectors
     if (rot % 16 == 0) return D == 64 ? launch_vec<64, 8>(a, st) : launch_vec<128, 8>(a, st);
     if (rot % 8 == 0) return D == 64 ? launch_vec<64, 4>(a, st) : launch_vec<128, 4>(a, st);

@@ -558,14 +558,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
     if constexpr (PACKED) {
         pos = max(a.bt.len[0], 0) - a.T + t;
     } else {
-        int hi = a.bt.n_seq - 1;
-        while (b < hi) {
-            const int mid = (b + hi + 1) >> 1;
-            if (cu_at(a.bt, mid, a.T) <= t)
-                b = mid;
-            else
-                hi = mid - 1;
-        }
+        b = uniform(row_seq(a.bt, t, a.T));
         const SeqRows sr = seq_rows(a.bt, b, a.T);
         if (t < sr.r0 || t >= sr.r1) return;
         pos = sr.pos0 + (t - sr.r0);
@@ -719,14 +712,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     int slot_step = 1;
     if constexpr (KIND == LTK_ATTEND) {
         const DenseHead* hd = reinterpret_cast<const DenseHead*>(a.head);
-        int b = 0, hi = a.bt.n_seq - 1;
-        while (b < hi) {
-            const int mid = (b + hi + 1) >> 1;
-            if (cu_at(a.bt, mid, a.T) <= t)
-                b = mid;
-            else
-                hi = mid - 1;
-        }
+        const int b = uniform(row_seq(a.bt, t, a.T));
         const SeqWork w = seq_work<MT>(a, b);
         if (t < w.sr.r0 || t >= w.sr.r1) return;
         const int64_t per = hd->per;

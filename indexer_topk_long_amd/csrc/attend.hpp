@@ -59,11 +59,40 @@ __device__ __forceinline__ SeqRows seq_rows(const KvBatch& bt, int b, int T) {
 __device__ __forceinline__ int unit_first(const KvBatch& bt, int b, int T, int mul, int per, int extra) {
     return (int)((int64_t)cu_at(bt, b, T) * mul / per) + extra * b;
 }
+// Both searches try the sequence that an even batch would give first (one
+// round of loads instead of log2(n_seq) dependent ones) and its neighbours.
 __device__ __forceinline__ int unit_seq(const KvBatch& bt, int u, int T, int mul, int per, int extra) {
-    int lo = 0, hi = bt.n_seq - 1;
+    const int last = bt.n_seq - 1;
+    if (last <= 0) return 0;
+    const int64_t all = (int64_t)T * mul / per + (int64_t)extra * bt.n_seq;
+    const int g = min((int)((int64_t)u * bt.n_seq / max(all, (int64_t)1)), last);
+    const int f0 = unit_first(bt, max(g - 1, 0), T, mul, per, extra), f1 = unit_first(bt, g, T, mul, per, extra);
+    const int f2 = unit_first(bt, min(g + 1, last), T, mul, per, extra);
+    const int f3 = unit_first(bt, min(g + 2, last), T, mul, per, extra);
+    if (g > 0 && f0 <= u && u < f1) return g - 1;
+    if (f1 <= u && (g == last || u < f2)) return g;
+    if (g < last && f2 <= u && (g + 1 == last || u < f3)) return g + 1;
+    int lo = 0, hi = last;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (unit_first(bt, mid, T, mul, per, extra) <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+// The sequence of a row: the last one that begins at or before it (so not an
+// empty one, where the row is in any).
+__device__ __forceinline__ int row_seq(const KvBatch& bt, int row, int T) {
+    const int last = bt.n_seq - 1;
+    if (last <= 0) return 0;
+    const int g = min((int)((int64_t)row * bt.n_seq / max(T, 1)), last);
+    if (cu_at(bt, g, T) <= row && row < cu_at(bt, g + 1, T)) return g;
+    int lo = 0, hi = last;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu_at(bt, mid, T) <= row)
             lo = mid;
         else
             hi = mid - 1;

@@ -11,7 +11,30 @@ import indexer_topk_long_amd as ltk
 from indexer_topk_long_amd import attention as A
 from indexer_topk_long_amd import build as B
 
+_p, _i, _f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
 OK, EINVAL, EUNSUP, EWS = 0, -1, -2, -3
+
+
+class CCache(ctypes.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("n_pages", _i), ("n_kv_heads", _i),
+                ("page_size", _i), ("head_dim", _i)]
+
+
+class CBatch(ctypes.Structure):
+    _fields_ = [("page_table", _p), ("cu", _p), ("kv_len", _p), ("n_seq", _i), ("max_pages", _i)]
+
+
+def _fn(name):
+    f = getattr(ltk.library(), name)
+    f.restype = ctypes.c_int
+    f.argtypes = [ctypes.POINTER(CCache), ctypes.POINTER(CBatch)] + {
+        "litetopk_kv_append": [_p, _p, _p, _i, _i, _p, _i, _i, _p, _p],
+        "litetopk_attend": [_p, _i, _i, _f, _i, _i, _p, _p, ctypes.c_size_t, _p],
+        "litetopk_attend_selected": [_p, _i, _i, _p, _i, _f, _p, _p, ctypes.c_size_t, _p],
+        "litetopk_attend_packed": [_p, _i, _i, _p, _p, _p, _i, _i, _f, _p, _p, ctypes.c_size_t, _p]}[name]
+    return f
+
+
 P, MIS = 0x10000, 0x10004          # aligned and misaligned fake device addresses, never dereferenced
 
 
@@ -39,8 +62,8 @@ def test_header_is_c_and_matches_binding_layout(tmp_path):
     exe = tmp_path / "probe"
     subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", B.INCLUDE, str(src), "-o", str(exe)], check=True)
     got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
-    assert got == [ctypes.sizeof(A._CCache), A._CCache.n_pages.offset, ctypes.sizeof(A._CBatch),
-                   A._CBatch.n_seq.offset]
+    assert got == [ctypes.sizeof(CCache), CCache.n_pages.offset, ctypes.sizeof(CBatch),
+                   CBatch.n_seq.offset]
 
 
 def _cb(kw):
@@ -48,7 +71,7 @@ def _cb(kw):
     b = dict(page_table=P, cu=P, kv_len=P, n_seq=3, max_pages=50)
     for d in (c, b):
         d.update({x: kw.pop(x) for x in list(kw) if x in d})
-    return A._CCache(*c.values()), A._CBatch(*b.values())
+    return CCache(*c.values()), CBatch(*b.values())
 
 
 CACHE_ERRORS = [
@@ -68,7 +91,7 @@ def _append(**kw):
     c, b = _cb(kw)
     a = dict(kp=P, vp=P, q=P, T=4, Hq=8, f=P, rot=64, il=0, qo=P)
     a.update(kw)
-    return A._fn("litetopk_kv_append")(ctypes.byref(c), ctypes.byref(b), a["kp"], a["vp"], a["q"], a["T"], a["Hq"],
+    return _fn("litetopk_kv_append")(ctypes.byref(c), ctypes.byref(b), a["kp"], a["vp"], a["q"], a["T"], a["Hq"],
                                        a["f"], a["rot"], a["il"], a["qo"], None)
 
 
@@ -92,10 +115,10 @@ def _attend(kind, **kw):
     head = (ctypes.byref(c), ctypes.byref(b), a["q"], a["T"], a["Hq"])
     tail = (a["out"], a["ws"], a["wsb"], None)
     if kind == "attend":
-        return A._fn("litetopk_attend")(*head, a["scale"], a["window"], a["sink"], *tail)
+        return _fn("litetopk_attend")(*head, a["scale"], a["window"], a["sink"], *tail)
     if kind == "selected":
-        return A._fn("litetopk_attend_selected")(*head, a["idx"], a["topk"], a["scale"], *tail)
-    return A._fn("litetopk_attend_packed")(*head, a["shared"], a["masks"], a["lens"], a["group"], a["cap"], a["scale"],
+        return _fn("litetopk_attend_selected")(*head, a["idx"], a["topk"], a["scale"], *tail)
+    return _fn("litetopk_attend_packed")(*head, a["shared"], a["masks"], a["lens"], a["group"], a["cap"], a["scale"],
                                            *tail)
 
 
@@ -126,7 +149,7 @@ def test_packed_argument_errors(kw, code):
 
 
 def test_null_structs_are_refused():
-    f = A._fn("litetopk_attend")
+    f = _fn("litetopk_attend")
     c, b = _cb({})
     assert f(None, ctypes.byref(b), P, 4, 8, 0.1, 0, 0, P, P, 1 << 30, None) == EINVAL
     assert f(ctypes.byref(c), None, P, 4, 8, 0.1, 0, 0, P, P, 1 << 30, None) == EINVAL
