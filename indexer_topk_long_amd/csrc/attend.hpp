@@ -213,8 +213,9 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& bt, int D, const ui
 // Launch of an attend call, fixed by its sizes alone so that the workspace
 // size and the call agree.
 struct AttendPlan {
-    bool tile;         // the kernels of attend_tile.hip (128 rows a unit), else those of attend.hip
+    bool tile;         // the kernels of attend_tile.hip, else those of attend.hip
     int mt;            // attend.hip: 16-row tiles per unit
+    int waves;         // attend_tile.hip: 32 rows each
     int64_t blocks;
     int splits;
     bool join;         // units may be cut: partial rows and a joining launch

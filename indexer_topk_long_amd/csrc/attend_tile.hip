@@ -27,11 +27,14 @@ namespace {
 typedef float at_f32x16 __attribute__((ext_vector_type(16)));
 typedef int at_i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kRows = 128;      // (row, head) pairs of a unit
 constexpr int kKeys = 64;       // keys of a step
-constexpr int kThreads = 256;
+// A workgroup of NW waves takes 32 NW (row, head) pairs.
+template <int NW>
+constexpr int kRows = 32 * NW;
+constexpr int kListWaves = 4;   // packed lists: 128 pairs a unit
 constexpr int kRing = 256;      // list entries resolved together (one a thread), two such chunks in LDS
 constexpr int kMinKeys = 4 * kKeys;   // least keys of a workgroup's range
+constexpr int kWide = 512;            // rows a sequence from which a unit has 256
 
 __device__ __forceinline__ float max_halves(float x) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -75,21 +78,24 @@ __device__ __forceinline__ int per_step(int off) {
     return off;
 }
 
-// The thread's part of a step's bytes.  D = 128: every thread takes two
-// 16-byte key pieces and one value patch (8 keys x 4 bytes).  D = 64: waves 2
-// and 3 take the keys, waves 0 and 1 the values.
-template <int D>
+// The thread's part of a step's bytes: two 16-byte key pieces, one value patch
+// (8 keys x 4 bytes), or both.  256 threads can hold the patches of D = 128 and
+// half as many pieces: four waves take both there.  At D = 64, and with eight
+// waves, the first waves take the values and the next the keys; waves w and
+// w + 4 share a SIMD, so with eight waves every SIMD has the same work.
+template <int D, int NW>
 struct Part {
-    static constexpr bool kSplit = D == 64;
-    static constexpr int kPieces = D / 16;   // 16-byte pieces of a key row
+    static constexpr int kPatches = 2 * D;            // threads that take a value patch, and as many key pieces
+    static constexpr bool kBoth = 64 * NW < 2 * kPatches;
+    static constexpr int kPieces = D / 16;            // 16-byte pieces of a key row
     bool keys, vals;
     int key, piece;          // key pieces: rows key and key + 32
     int chunk, dq;           // value patch: 8 keys of chunk, dimensions 4 dq ..
     __device__ __forceinline__ Part() {
         const int tid = threadIdx.x;
-        keys = !kSplit || tid >= 128;
-        vals = !kSplit || tid < 128;
-        const int i = kSplit ? (tid & 127) : tid;
+        vals = kBoth || tid < kPatches;
+        keys = kBoth || (tid >= kPatches && tid < 2 * kPatches);
+        const int i = tid & (kPatches - 1);
         key = i / kPieces, piece = i % kPieces;
         chunk = i / (D / 4), dq = i % (D / 4);
     }
@@ -98,22 +104,26 @@ struct Part {
         return 16 * (chunk >> 1) + 4 * (chunk & 1) + (i & 3) + ((i & 4) << 1);
     }
 };
+// Where a thread takes either, both share the same registers.
+template <bool BOTH>
 struct Raw {
-    at_u32x4 k[2];
-    uint32_t v[8];
+    at_u32x4 w[BOTH ? 4 : 2];
+    __device__ __forceinline__ at_u32x4& k(int i) { return w[i]; }
+    __device__ __forceinline__ uint32_t v(int i) const { return w[(BOTH ? 2 : 0) + i / 4][i % 4]; }
+    __device__ __forceinline__ void set_v(int i, uint32_t x) { w[(BOTH ? 2 : 0) + i / 4][i % 4] = x; }
 };
 
 // The conversions of a step's bytes into the stage at LDS offset `stage`, in
 // four equal parts (i = 0 .. 3) that the matrix instructions of the step
 // before are issued between.
-template <int D>
-__device__ __forceinline__ void store_stage(const Part<D>& p, const Raw& r, int stage, int i) {
+template <int D, int NW>
+__device__ __forceinline__ void store_stage(const Part<D, NW>& p, Raw<Part<D, NW>::kBoth>& r, int stage, int i) {
     if (i < 2) {
         if (!p.keys) return;
         // rows key and key + 32, chunks 2 piece and 2 piece + 1
         const int at = per_step(p.key * (2 * D) + (((2 * p.piece) ^ key_swizzle<D>(p.key)) << 4)) + stage;
-        *reinterpret_cast<at_bf16x8*>(lds() + at + i * (64 * D)) = bf16_of(r.k[i][0], r.k[i][1]);
-        *reinterpret_cast<at_bf16x8*>(lds() + (at ^ 16) + i * (64 * D)) = bf16_of(r.k[i][2], r.k[i][3]);
+        *reinterpret_cast<at_bf16x8*>(lds() + at + i * (64 * D)) = bf16_of(r.k(i)[0], r.k(i)[1]);
+        *reinterpret_cast<at_bf16x8*>(lds() + (at ^ 16) + i * (64 * D)) = bf16_of(r.k(i)[2], r.k(i)[3]);
         return;
     }
     if (!p.vals) return;
@@ -121,7 +131,7 @@ __device__ __forceinline__ void store_stage(const Part<D>& p, const Raw& r, int 
     at_f16x8 o0, o1;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const uint32_t w = __builtin_amdgcn_perm(r.v[2 * j + 1], r.v[2 * j], e ? 0x07030602u : 0x05010400u);
+        const uint32_t w = __builtin_amdgcn_perm(r.v(2 * j + 1), r.v(2 * j), e ? 0x07030602u : 0x05010400u);
         const at_f16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
         const at_f16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true);
         o0[2 * j] = x0[0], o0[2 * j + 1] = x0[1];
@@ -311,12 +321,12 @@ __device__ __forceinline__ void begin_rows(const AttendArgs& a, int64_t row, at_
 }
 
 // Rows written as bf16 where the workgroup saw all of their keys (part ==
-// NULL), else as a part: [kRows][D] floats, then [kRows] (m, l).
-template <int D>
+// NULL), else as a part: [32 NW][D] floats, then [32 NW] (m, l).
+template <int D, int NW>
 constexpr int part_floats() {
-    return kRows * (D + 2);
+    return kRows<NW> * (D + 2);
 }
-template <int D>
+template <int D, int NW>
 __device__ __forceinline__ void end_rows(const AttendArgs& a, int64_t row, const WaveState<D>& st, float* part) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
     const float l = sum_halves(st.l);
@@ -341,8 +351,8 @@ __device__ __forceinline__ void end_rows(const AttendArgs& a, int64_t row, const
             *reinterpret_cast<at_f32x4*>(part + (size_t)r * D + 32 * t + 8 * i + 4 * g) =
                 at_f32x4{st.o[t][4 * i], st.o[t][4 * i + 1], st.o[t][4 * i + 2], st.o[t][4 * i + 3]};
     if (g == 0) {
-        part[(size_t)kRows * D + 2 * r] = l > 0.0f ? st.m : kNoRef;
-        part[(size_t)kRows * D + 2 * r + 1] = l;
+        part[(size_t)kRows<NW> * D + 2 * r] = l > 0.0f ? st.m : kNoRef;
+        part[(size_t)kRows<NW> * D + 2 * r + 1] = l;
     }
 }
 
@@ -358,12 +368,13 @@ struct SeqLine {
     __device__ __forceinline__ int64_t cost(int i) const { return A + i * Q; }
     __device__ __forceinline__ int64_t before(int i) const { return i * A + Q * ((int64_t)i * (i - 1) / 2); }
 };
+template <int NW>
 __device__ __forceinline__ SeqLine seq_line(const AttendArgs& a, int b) {
     SeqLine s;
     s.sr = seq_rows(a.bt, b, a.T);
     const int n = s.sr.r1 - s.sr.r0;
-    s.tiles = (int)(((int64_t)n * a.G + kRows - 1) / kRows);
-    s.Q = uniform((kRows + a.G - 1) / a.G);
+    s.tiles = (int)(((int64_t)n * a.G + kRows<NW> - 1) / kRows<NW>);
+    s.Q = uniform((kRows<NW> + a.G - 1) / a.G);
     const int64_t cap = (int64_t)a.bt.max_pages << a.c.page_shift;
     s.A = max(min((int64_t)s.sr.pos0 + 1 + s.Q, cap), (int64_t)1);
     // a window's rows see at most the sinks, the window and the tiles' borders
@@ -407,7 +418,7 @@ struct DenseScale {
     }
 };
 
-template <int D>
+template <int D, int NW>
 __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& sr, int b, const UnitRows& u,
                                            const KeyTiles& kt, int t0, int t1, float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -424,7 +435,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 
     const int32_t* table = a.bt.table + (size_t)b * a.bt.max_pages;
     const int page = 1 << a.c.page_shift;
-    const Part<D> p;
+    const Part<D, NW> p;
     auto key0_of = [&](int t) { return (t < kt.sink_tiles ? t : kt.win_tile0 + t - kt.sink_tiles) * kKeys; };
     // a lane holds the page of one 16-key group of the next 16 steps
     PageLanes pl;
@@ -436,8 +447,8 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     auto seen = [&](int key) { return (key < kt.hi) & ((key + 15 >= kt.lo) | (key < a.n_sink)); };
     // What later needs to know of a step's four pages: bit i is set when keys
     // 16 i .. of the step have a page and are looked at.
-    Raw raw;
-    auto load = [&](int t) -> int {
+    using Bytes = Raw<Part<D, NW>::kBoth>;
+    auto load = [&](int t, Bytes& raw) -> int {
         const int n = t - t0, key0 = key0_of(t), at = 4 * (n % 16);
         if (n % 16 == 0) pl.turn(table, a, u.h, n / 16, lane_key, seen);
         const int p0 = pl.page(at), p1 = pl.page(at + 1), p2 = pl.page(at + 2), p3 = pl.page(at + 3);
@@ -447,17 +458,17 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
             return ((((size_t)max(page_of(grp), 0) * a.c.Hkv + u.h) << a.c.page_shift) + ((key0 + 16 * grp) & (page - 1))) * D;
         };
         if (p.keys) {   // a wave's pieces lie in one group, and in the second one on
-            const int grp = D == 128 ? wave >> 1 : wave & 1;
+            const int grp = D == 128 ? (wave & 3) >> 1 : wave & 1;
             const int off = (p.key & 15) * D + 16 * p.piece;
-            raw.k[0] = *reinterpret_cast<const at_u32x4*>(a.c.k + base(grp) + off);
-            raw.k[1] = *reinterpret_cast<const at_u32x4*>(a.c.k + base(grp + 2) + off);
+            raw.k(0) = *reinterpret_cast<const at_u32x4*>(a.c.k + base(grp) + off);
+            raw.k(1) = *reinterpret_cast<const at_u32x4*>(a.c.k + base(grp + 2) + off);
         }
         if (p.vals) {   // D = 128: a wave's patches lie in one group; D = 64: in one a half wave
             const int off = (p.val_key(0) & 15) * D + 4 * p.dq;
-            const uint8_t* v = D == 128 ? a.c.v + base(wave) + off
+            const uint8_t* v = D == 128 ? a.c.v + base(wave & 3) + off
                                         : a.c.v + (lane < 32 ? base(2 * (wave & 1)) : base(2 * (wave & 1) + 1)) + off;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) raw.v[i] = *reinterpret_cast<const uint32_t*>(v + (p.val_key(i) - p.val_key(0)) * D);
+            for (int i = 0; i < 8; ++i) raw.set_v(i, *reinterpret_cast<const uint32_t*>(v + (p.val_key(i) - p.val_key(0)) * D));
         }
         return (p0 >= 0 ? 1 : 0) | (p1 >= 0 ? 2 : 0) | (p2 >= 0 ? 4 : 0) | (p3 >= 0 ? 8 : 0);
     };
@@ -466,7 +477,8 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
                (a.window <= 0 || key0 > hi - a.window || key0 + kKeys <= a.n_sink);
     };
     // what a step's bytes need before they are converted
-    auto settle_raw = [&](int t, int pages) {
+    auto settle_raw = [&](int t, int pages, Bytes& raw) {
+        if (!p.vals) return;
         const int key0 = key0_of(t);
         if (pages == 15 && key0 + kKeys <= kt.hi && (key0 >= kt.lo || key0 + kKeys <= a.n_sink)) return;
         // bytes of keys that no row sees may be NaN: their weights are 0, so the values must be finite
@@ -474,7 +486,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
         for (int i = 0; i < 8; ++i) {
             const int key = key0 + p.val_key(i);
             const bool ok = ((pages >> (p.chunk >> 1)) & 1) & (key < kt.hi) & ((key >= kt.lo) | (key < a.n_sink));
-            raw.v[i] = ok ? raw.v[i] : 0u;
+            raw.set_v(i, ok ? raw.v(i) : 0u);
         }
     };
     struct Mask {
@@ -510,26 +522,44 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     };
 
     // step t computes from one stage while t + 1 is written to the other and
-    // t + 2 is on its way
+    // the loads of t + 2 are on their way; where a thread's bytes take 8
+    // registers, those of t + 3 too
     if (t0 < t1) {
+        constexpr bool kDeep = !Part<D, NW>::kBoth;
+        Bytes ra, rb;
         pl.read(table, a, 0, lane_key);
-        int now = load(t0), next = 0;
-        settle_raw(t0, now);
+        int now = load(t0, ra), next = 0, after = 0;
+        settle_raw(t0, now, ra);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store_stage<D>(p, raw, 0, i);
-        if (t0 + 1 < t1) next = load(t0 + 1);
+        for (int i = 0; i < 4; ++i) store_stage<D, NW>(p, ra, 0, i);
+        if (t0 + 1 < t1) next = load(t0 + 1, ra);
+        if (kDeep && t0 + 2 < t1) after = load(t0 + 2, rb);
         __syncthreads();
-        for (int t = t0; t < t1; ++t) {
-            const int x = (t - t0) & 1;
+        auto body = [&](int t, int x, Bytes& raw) {   // raw: the bytes of t + 1
             // (past the last step the conversions write a stage that nothing reads)
-            if (t + 1 < t1) settle_raw(t + 1, next);
-            step(t, now, x * kStageBytes<D>, [&](int i) { store_stage<D>(p, raw, (x ^ 1) * kStageBytes<D>, i); });
+            if (t + 1 < t1) settle_raw(t + 1, next, raw);
+            step(t, now, x * kStageBytes<D>, [&](int i) { store_stage<D, NW>(p, raw, (x ^ 1) * kStageBytes<D>, i); });
             now = next;
-            if (t + 2 < t1) next = load(t + 2);
+            if (kDeep) {
+                next = after;
+                if (t + 3 < t1) after = load(t + 3, raw);
+            } else if (t + 2 < t1) {
+                next = load(t + 2, raw);
+            }
             __syncthreads();
+        };
+        if constexpr (kDeep) {
+            for (int t = t0;; t += 2) {
+                body(t, 0, ra);
+                if (t + 1 >= t1) break;
+                body(t + 1, 1, rb);
+                if (t + 2 >= t1) break;
+            }
+        } else {
+            for (int t = t0; t < t1; ++t) body(t, (t - t0) & 1, ra);
         }
     }
-    end_rows<D>(a, row, st, part);
+    end_rows<D, NW>(a, row, st, part);
 }
 
 // What a workgroup leaves to join, in the workspace: the unit that began in
@@ -539,8 +569,9 @@ struct Crossing {
     int n, slot;   // n == 0: none
     UnitRows u;
 };
+template <int NW>
 struct ScanLds {
-    int64_t wave[kThreads / 64];
+    int64_t wave[NW];
 };
 // Where a workgroup stands on the line.  It lives in LDS and is read again for
 // every unit: in registers over a unit's loop it would cost that loop spills.
@@ -548,7 +579,8 @@ struct Place {
     int64_t at, first;   // on the line: the place reached, and where sequence b begins
     int b, h, i;         // sequence, head, row tile
 };
-__device__ __forceinline__ int64_t scan_256(int64_t x, ScanLds& ls, int64_t& sum) {
+template <int NW>
+__device__ __forceinline__ int64_t scan_block(int64_t x, ScanLds<NW>& ls, int64_t& sum) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -560,24 +592,25 @@ __device__ __forceinline__ int64_t scan_256(int64_t x, ScanLds& ls, int64_t& sum
     __syncthreads();
     sum = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) {
+    for (int w = 0; w < NW; ++w) {
         if (w < wave) x += ls.wave[w];
         sum += ls.wave[w];
     }
     return x;
 }
+template <int NW>
 __device__ __forceinline__ int64_t line_of(const AttendArgs& a, int b) {
     if (b >= a.bt.n_seq) return 0;
-    const SeqLine s = seq_line(a, b);
+    const SeqLine s = seq_line<NW>(a, b);
     return s.before(s.tiles) * a.c.Hkv;
 }
 
-template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attend_tile_kernel(AttendArgs a) {
-    __shared__ ScanLds sc;
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
+    __shared__ ScanLds<NW> sc;
     int64_t total = 0, sum;
-    for (int b0 = 0; b0 < a.bt.n_seq; b0 += kThreads) {
-        scan_256(line_of(a, b0 + threadIdx.x), sc, sum);
+    for (int b0 = 0; b0 < a.bt.n_seq; b0 += 64 * NW) {
+        scan_block<NW>(line_of<NW>(a, b0 + threadIdx.x), sc, sum);
         total += uniform(sum);
     }
     const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kMinKeys);
@@ -591,10 +624,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_kernel(AttendArgs a) 
     if (begin >= end) return;
     __shared__ Place place;
     int64_t before = 0;
-    for (int b0 = 0; b0 < a.bt.n_seq; b0 += kThreads) {
-        const int64_t w = line_of(a, b0 + threadIdx.x), x = before + scan_256(w, sc, sum);
+    for (int b0 = 0; b0 < a.bt.n_seq; b0 += 64 * NW) {
+        const int64_t w = line_of<NW>(a, b0 + threadIdx.x), x = before + scan_block<NW>(w, sc, sum);
         if (x - w <= begin && begin < x) {   // the sequence that the range begins in
-            const SeqLine s = seq_line(a, b0 + threadIdx.x);
+            const SeqLine s = seq_line<NW>(a, b0 + threadIdx.x);
             const int64_t off = begin - (x - w), head = s.before(s.tiles);
             const int h = (int)(off / head);
             int lo = 0, hi = s.tiles - 1;
@@ -614,17 +647,17 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_kernel(AttendArgs a) 
     while (true) {
         const int b = uniform(place.b), h = uniform(place.h), i = uniform(place.i);
         const int64_t at = uniform(place.at);
-        const SeqLine s = seq_line(a, b);
+        const SeqLine s = seq_line<NW>(a, b);
         const int64_t us = uniform(place.first) + h * s.before(s.tiles) + s.before(i), cost = s.cost(i);
         UnitRows u;
         u.r0 = s.sr.r0;
         u.h = h;
-        u.f0 = i * kRows;
-        u.f1 = min(u.f0 + kRows, (s.sr.r1 - s.sr.r0) * a.G);
+        u.f0 = i * kRows<NW>;
+        u.f1 = min(u.f0 + kRows<NW>, (s.sr.r1 - s.sr.r0) * a.G);
         // a step belongs to the range that its first key lies in
         const int64_t k0 = at - us, k1 = min(end - us, cost);
         float* part = nullptr;
-        if (k0 > 0 || k1 < cost) part = a.part + (2 * (int64_t)me + (at == begin ? 0 : 1)) * part_floats<D>();
+        if (k0 > 0 || k1 < cost) part = a.part + (2 * (int64_t)me + (at == begin ? 0 : 1)) * part_floats<D, NW>();
         if (k0 == 0 && k1 < cost && threadIdx.x == 0)
             *crossing = Crossing{(int)((us + cost - 1) / per) - me + 1, 2 * me + (at == begin ? 0 : 1), u};
         __syncthreads();
@@ -635,12 +668,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_kernel(AttendArgs a) 
                 n.h = 0;
                 n.first += a.c.Hkv * s.before(s.tiles);
                 n.b = n.at < end ? n.b + 1 : n.b;
-                while (n.at < end && seq_line(a, n.b).tiles == 0) ++n.b;
+                while (n.at < end && seq_line<NW>(a, n.b).tiles == 0) ++n.b;
             }
             place = n;
         }
         const KeyTiles kt = key_tiles(a, s.sr.pos0 + uniform(u.f0 / a.G), s.sr.pos0 + uniform((u.f1 - 1) / a.G));
-        dense_unit<D>(a, s.sr, b, u, kt, (int)((k0 + kKeys - 1) / kKeys), min((int)((k1 + kKeys - 1) / kKeys), kt.tiles), part);
+        dense_unit<D, NW>(a, s.sr, b, u, kt, (int)((k0 + kKeys - 1) / kKeys), min((int)((k1 + kKeys - 1) / kKeys), kt.tiles), part);
         __syncthreads();
         if (uniform(place.at) >= end) return;
     }
@@ -665,9 +698,10 @@ struct ListScale {
 // A unit is 128 (row, head) pairs of one group and key/value head; its keys
 // are the group's list, cut into a.splits.
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArgs a) {
+__global__ __launch_bounds__(64 * kListWaves, 2) void attend_tile_list_kernel(AttendArgs a) {
+    constexpr int NW = kListWaves;
     Ring& ring = *reinterpret_cast<Ring*>(lds() + 2 * kStageBytes<D>);
-    const int ht = (a.group * a.G + kRows - 1) / kRows;   // row tiles of a group
+    const int ht = (a.group * a.G + kRows<NW> - 1) / kRows<NW>;   // row tiles of a group
     UnitRows u;
     u.h = uniform((int)(blockIdx.x % a.c.Hkv));
     int rest = uniform((int)(blockIdx.x / a.c.Hkv));
@@ -675,8 +709,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArg
     rest = uniform(rest / ht);
     const int split = uniform(rest % a.splits), grp = uniform(rest / a.splits);
     u.r0 = grp * a.group;
-    u.f0 = tile * kRows;
-    u.f1 = min(u.f0 + kRows, min(a.group, a.T - u.r0) * a.G);
+    u.f0 = tile * kRows<NW>;
+    u.f1 = min(u.f0 + kRows<NW>, min(a.group, a.T - u.r0) * a.G);
     if (u.f0 >= u.f1) return;
     const int n = min(max(a.lens[grp], 0), a.cap);
     const int per = uniform(((n + kKeys - 1) / kKeys + a.splits - 1) / a.splits * kKeys);
@@ -731,15 +765,15 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArg
         ring.mask[at] = m;
         ring.c[at] = ps.c_, ring.lv[at] = ps.lv_, ring.iv[at] = ps.iv_;
     };
-    const Part<D> p;
-    Raw raw;
+    const Part<D, NW> p;
+    Raw<Part<D, NW>::kBoth> raw;
     uint32_t none = 0;   // bit i: the patch's i-th key is no key
     auto load = [&](int t) {
         const int at = (t * kKeys) & (2 * kRing - 1);
         if (p.keys) {
 #pragma unroll
             for (int y = 0; y < 2; ++y)
-                raw.k[y] = *reinterpret_cast<const at_u32x4*>(a.c.k + (size_t)max(ring.row[at + p.key + 32 * y], 0) * D +
+                raw.k(y) = *reinterpret_cast<const at_u32x4*>(a.c.k + (size_t)max(ring.row[at + p.key + 32 * y], 0) * D +
                                                               16 * p.piece);
         }
         if (p.vals) {
@@ -750,14 +784,14 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArg
             for (int i = 0; i < 8; ++i) {
                 const int r = i < 4 ? r0[i & 3] : r1[i & 3];
                 none |= r < 0 ? 1u << i : 0u;
-                raw.v[i] = *reinterpret_cast<const uint32_t*>(a.c.v + (size_t)max(r, 0) * D + 4 * p.dq);
+                raw.set_v(i, *reinterpret_cast<const uint32_t*>(a.c.v + (size_t)max(r, 0) * D + 4 * p.dq));
             }
         }
     };
     auto settle_raw = [&]() {
         if (__any(none != 0)) {   // bytes behind no key may be NaN
 #pragma unroll
-            for (int i = 0; i < 8; ++i) raw.v[i] = (none >> i) & 1u ? 0u : raw.v[i];
+            for (int i = 0; i < 8; ++i) raw.set_v(i, (none >> i) & 1u ? 0u : raw.v(i));
         }
     };
     struct Mask {
@@ -791,7 +825,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArg
         load(0);
         settle_raw();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store_stage<D>(p, raw, 0, i);
+        for (int i = 0; i < 4; ++i) store_stage<D, NW>(p, raw, 0, i);
         if (steps > 1) load(1);
         __syncthreads();
         // a chunk's entries are read in the last two steps of the chunk two
@@ -800,7 +834,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArg
             const int x = t & 1, ph = t % kPer, chunk = t / kPer;
             if (ph == 0) entry_page();
             if (t + 1 < steps) settle_raw();
-            step(t, x * kStageBytes<D>, [&](int i) { store_stage<D>(p, raw, (x ^ 1) * kStageBytes<D>, i); });
+            step(t, x * kStageBytes<D>, [&](int i) { store_stage<D, NW>(p, raw, (x ^ 1) * kStageBytes<D>, i); });
             if (ph == 0) entry_scale();
             if (t + 2 < steps) load(t + 2);
             if (ph == 1) entry_store(chunk + 1);
@@ -809,14 +843,14 @@ __global__ __launch_bounds__(kThreads, 2) void attend_tile_list_kernel(AttendArg
         }
     }
     const int64_t slot = (((int64_t)grp * ht + tile) * a.c.Hkv + u.h) * a.splits + split;
-    end_rows<D>(a, row, st, used > 1 ? a.part + slot * part_floats<D>() : nullptr);
+    end_rows<D, NW>(a, row, st, used > 1 ? a.part + slot * part_floats<D, NW>() : nullptr);
 }
 
 // ------------------------------------------------------- joining the parts
 
 // Sum of n parts of one row by D / 4 lanes: part i at slot0 (i == 0) or
 // slot1 + (i - 1) step.
-template <int D>
+template <int D, int NW>
 __device__ __forceinline__ void join_row(const AttendArgs& a, int64_t row, int at, int n, int64_t slot0, int64_t slot1,
                                          int step) {
     const int lane = threadIdx.x % (D / 4);
@@ -824,8 +858,8 @@ __device__ __forceinline__ void join_row(const AttendArgs& a, int64_t row, int a
     at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-        const float* p = a.part + (i == 0 ? slot0 : slot1 + (int64_t)(i - 1) * step) * part_floats<D>();
-        const float mi = p[kRows * D + at * 2], li = p[kRows * D + at * 2 + 1];
+        const float* p = a.part + (i == 0 ? slot0 : slot1 + (int64_t)(i - 1) * step) * part_floats<D, NW>();
+        const float mi = p[kRows<NW> * D + at * 2], li = p[kRows<NW> * D + at * 2 + 1];
         const at_f32x4 x = *reinterpret_cast<const at_f32x4*>(p + at * D + 4 * lane);
         const float mn = fmaxf(m, mi), f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(mi - mn);
         l = l * f0 + li * f1;
@@ -839,46 +873,52 @@ __device__ __forceinline__ void join_row(const AttendArgs& a, int64_t row, int a
 
 constexpr int kJoinRows = 8;   // rows of a joining workgroup
 
-template <int D>
+template <int D, int NW>
 __global__ __launch_bounds__(kJoinRows * D / 4) void attend_tile_join_kernel(AttendArgs a) {
     const Crossing x = reinterpret_cast<const Crossing*>(a.head)[blockIdx.x];
     const int at = blockIdx.y * kJoinRows + threadIdx.x / (D / 4);
     const int64_t row = x.n > 0 ? out_row(a, x.u, x.u.f0 + at) : -1;
-    if (row >= 0) join_row<D>(a, row, at, x.n, x.slot, 2 * ((int64_t)blockIdx.x + 1), 2);
+    if (row >= 0) join_row<D, NW>(a, row, at, x.n, x.slot, 2 * ((int64_t)blockIdx.x + 1), 2);
 }
 
 template <int D>
 __global__ __launch_bounds__(kJoinRows * D / 4) void attend_tile_list_join_kernel(AttendArgs a) {
+    constexpr int NW = kListWaves;
     const int64_t r = (int64_t)blockIdx.x * kJoinRows + threadIdx.x / (D / 4);   // row * Hq + head
     if (r >= (int64_t)a.T * a.Hq) return;
     const int t = (int)(r / a.Hq), head = (int)(r % a.Hq), h = head / a.G;
-    const int grp = t / a.group, ht = (a.group * a.G + kRows - 1) / kRows;
+    const int grp = t / a.group, ht = (a.group * a.G + kRows<NW> - 1) / kRows<NW>;
     const int n = min(max(a.lens[grp], 0), a.cap);
     const int per = ((n + kKeys - 1) / kKeys + a.splits - 1) / a.splits * kKeys;
     const int used = per > 0 ? (n + per - 1) / per : 1;
     if (used <= 1) return;
     const int f = (t % a.group) * a.G + (head - h * a.G);
-    const int64_t slot0 = (((int64_t)grp * ht + f / kRows) * a.c.Hkv + h) * a.splits;
-    join_row<D>(a, r, f % kRows, used, slot0, slot0 + 1, 1);
+    const int64_t slot0 = (((int64_t)grp * ht + f / kRows<NW>) * a.c.Hkv + h) * a.splits;
+    join_row<D, NW>(a, r, f % kRows<NW>, used, slot0, slot0 + 1, 1);
 }
 
-template <int D, bool LIST>
-hipError_t launch_d(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
-    constexpr size_t lds = 2 * kStageBytes<D> + (LIST ? sizeof(Ring) : 0);
-    const void* fn = LIST ? reinterpret_cast<const void*>(attend_tile_list_kernel<D>)
-                          : reinterpret_cast<const void*>(attend_tile_kernel<D>);
-    if (lds > 65536)
-        (void)hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if constexpr (LIST)
-        attend_tile_list_kernel<D><<<(unsigned)p.blocks, kThreads, lds, st>>>(a);
-    else
-        attend_tile_kernel<D><<<(unsigned)p.blocks, kThreads, lds, st>>>(a);
-    constexpr int threads = kJoinRows * D / 4;
-    if (p.join && LIST)
-        attend_tile_list_join_kernel<D>
-            <<<(unsigned)(((int64_t)a.T * a.Hq + kJoinRows - 1) / kJoinRows), threads, 0, st>>>(a);
-    else if (p.join)
-        attend_tile_join_kernel<D><<<dim3((unsigned)p.blocks, kRows / kJoinRows), threads, 0, st>>>(a);
+hipError_t allow_lds(const void* fn, size_t bytes) {
+    return bytes > 65536 ? hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : hipSuccess;
+}
+
+template <int D, int NW>
+hipError_t launch_dense(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
+    attend_tile_kernel<D, NW><<<(unsigned)p.blocks, 64 * NW, 2 * kStageBytes<D>, st>>>(a);
+    if (p.join)
+        attend_tile_join_kernel<D, NW>
+            <<<dim3((unsigned)p.blocks, kRows<NW> / kJoinRows), kJoinRows * D / 4, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_list(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
+    constexpr size_t bytes = 2 * kStageBytes<D> + sizeof(Ring);
+    const hipError_t e = allow_lds(reinterpret_cast<const void*>(attend_tile_list_kernel<D>), bytes);
+    if (e != hipSuccess) return e;
+    attend_tile_list_kernel<D><<<(unsigned)p.blocks, 64 * kListWaves, bytes, st>>>(a);
+    if (p.join)
+        attend_tile_list_join_kernel<D><<<(unsigned)(((int64_t)a.T * a.Hq + kJoinRows - 1) / kJoinRows),
+                                          kJoinRows * D / 4, 0, st>>>(a);
     return hipGetLastError();
 }
 
@@ -888,29 +928,34 @@ AttendPlan attend_tile_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, 
     AttendPlan p{};
     p.tile = true;
     const int G = Hq / Hkv;
-    const size_t part = (size_t)kRows * (D + 2) * sizeof(float);
     if (kind == LTK_ATTEND) {
-        const int64_t units = ((int64_t)T * G / kRows + n_seq) * Hkv;
+        // 256 rows a workgroup, one on a CU, where the sequences fill them
+        p.waves = (int64_t)T * G >= kWide * (int64_t)std::max(n_seq, 1) ? 8 : 4;
+        const int rows = 32 * p.waves;
+        const int64_t units = ((int64_t)T * G / rows + n_seq) * Hkv;
         const int64_t most = (units * (entries + kKeys) + kMinKeys - 1) / kMinKeys;
-        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, 512));   // two a CU
+        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, 2048 / p.waves));   // eight waves a CU
         p.join = p.blocks > 1;
         p.head_bytes = (sizeof(Crossing) * (size_t)p.blocks + 255) / 256 * 256;
-        p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * part : 0);
+        p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * rows * (D + 2) * sizeof(float) : 0);
         return p;
     }
-    const int64_t units = (int64_t)((T + group - 1) / group) * ((group * G + kRows - 1) / kRows) * Hkv;
+    p.waves = kListWaves;
+    constexpr int rows = kRows<kListWaves>;
+    const int64_t units = (int64_t)((T + group - 1) / group) * ((group * G + rows - 1) / rows) * Hkv;
     const int64_t most = (entries + kKeys - 1) / kKeys;
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 512 / std::max<int64_t>(units, 1)));
     p.blocks = units * p.splits;
     p.join = p.splits > 1;
-    p.ws_bytes = std::max<size_t>(256, p.join ? (size_t)p.blocks * part : 0);
+    p.ws_bytes = std::max<size_t>(256, p.join ? (size_t)p.blocks * rows * (D + 2) * sizeof(float) : 0);
     return p;
 }
 
 hipError_t launch_attend_tile(int kind, int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
     if (p.blocks > 0x7fffffff) return hipErrorInvalidValue;
-    if (kind == LTK_ATTEND) return D == 64 ? launch_d<64, false>(p, a, st) : launch_d<128, false>(p, a, st);
-    return D == 64 ? launch_d<64, true>(p, a, st) : launch_d<128, true>(p, a, st);
+    if (kind != LTK_ATTEND) return D == 64 ? launch_list<64>(p, a, st) : launch_list<128>(p, a, st);
+    if (p.waves == 8) return D == 64 ? launch_dense<64, 8>(p, a, st) : launch_dense<128, 8>(p, a, st);
+    return D == 64 ? launch_dense<64, 4>(p, a, st) : launch_dense<128, 4>(p, a, st);
 }
 
 }  // namespace ltk
