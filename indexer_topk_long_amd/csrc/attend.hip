@@ -102,15 +102,16 @@ __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const
                                           bool masked, int g, Mask mask) {
     at_f32x4 s[MT][2];
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
+    for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) s[mt][a] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < D / 32; ++j) {
+        const at_bf16x8 k0 = bf16_of(t.k[0][j / 2][2 * (j % 2)], t.k[0][j / 2][2 * (j % 2) + 1]);
+        const at_bf16x8 k1 = bf16_of(t.k[1][j / 2][2 * (j % 2)], t.k[1][j / 2][2 * (j % 2) + 1]);
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-            const at_bf16x8 kf = bf16_of(t.k[a][j / 2][2 * (j % 2)], t.k[a][j / 2][2 * (j % 2) + 1]);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                s[mt][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, query(mt, j), s[mt][a], 0, 0, 0);
+        for (int mt = 0; mt < MT; ++mt) {
+            const at_bf16x8 qf = query(mt, j);
+            s[mt][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf, s[mt][0], 0, 0, 0);
+            s[mt][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf, s[mt][1], 0, 0, 0);
         }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -237,7 +238,7 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
 
 template <int D, int MT>
 constexpr int waves_per_simd() {
-    return MT == 4 ? (D == 64 ? 2 : 1) : MT == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 3 : 2);
+    return MT == 1 && D == 64 ? 3 : 2;
 }
 
 template <int D, int MT>
@@ -301,6 +302,14 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int b) {
 constexpr int kPlanSeqs = 64 * kWaves;   // sequences looked at together
 struct PlanLds {
     int64_t wave[kWaves];
+};
+
+// Where a workgroup stands: the place reached on the line, and the sequence
+// there with its own place.  It lives in LDS and is read again for every unit:
+// in registers over a unit's loop it would cost that loop spills.
+struct Place {
+    int64_t at, first;
+    int b;
 };
 
 // Work of sequence b (0 past the batch).
@@ -482,52 +491,59 @@ template <int D, int MT>
 __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend_kernel(AttendArgs a) {
     extern __shared__ float sh[];
     __shared__ PlanLds ls;
-    __shared__ int64_t s_at;   // place of sequence s_b on the line
-    __shared__ int s_b;
+    __shared__ Place place;
     DenseHead* head = reinterpret_cast<DenseHead*>(a.head);
-    // the total, then the sequence that this workgroup's range begins in
-    int64_t total = 0, sum;
+    // the total, then the sequence that this workgroup's range begins in; one
+    // look at up to kPlanSeqs sequences serves both
+    int64_t total = 0, sum, w0 = 0, x0 = 0;
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += kPlanSeqs) {
-        const int64_t w = work_of<MT>(a, b0 + threadIdx.x), x = block_scan(w, ls, sum);
-        if (blockIdx.x == 0 && b0 + (int)threadIdx.x < a.bt.n_seq) head->first[b0 + threadIdx.x] = total + x - w;
+        w0 = work_of<MT>(a, b0 + threadIdx.x);
+        x0 = total + (a.bt.n_seq > 1 ? block_scan(w0, ls, sum) : (sum = work_of<MT>(a, 0)));
+        if (blockIdx.x == 0 && b0 + (int)threadIdx.x < a.bt.n_seq) head->first[b0 + threadIdx.x] = x0 - w0;
         total += uniform(sum);
     }
     const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)a.min_per);
     if (blockIdx.x == 0 && threadIdx.x == 0) head->total = total, head->per = per;
-    int64_t at = (int64_t)blockIdx.x * per;
-    const int64_t end = min(at + per, total);
-    if (at >= end) return;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.bt.n_seq; b0 += kPlanSeqs) {
-        const int64_t w = work_of<MT>(a, b0 + threadIdx.x), x = before + block_scan(w, ls, sum);
-        if (x - w <= at && at < x) s_b = b0 + threadIdx.x, s_at = x - w;
-        before += uniform(sum);
-        if (at < before) break;
+    const int64_t begin = (int64_t)blockIdx.x * per, end = min(begin + per, total);
+    if (begin >= end) return;
+    if (a.bt.n_seq <= kPlanSeqs) {
+        if (x0 - w0 <= begin && begin < x0) place = Place{begin, x0 - w0, (int)threadIdx.x};
+    } else {
+        int64_t before = 0;
+        for (int b0 = 0; b0 < a.bt.n_seq; b0 += kPlanSeqs) {
+            const int64_t w = work_of<MT>(a, b0 + threadIdx.x), x = before + block_scan(w, ls, sum);
+            if (x - w <= begin && begin < x) place = Place{begin, x - w, b0 + (int)threadIdx.x};
+            before += uniform(sum);
+            if (begin < before) break;
+        }
     }
     __syncthreads();
-    int b = uniform(s_b);
-    int64_t first = uniform(s_at);
-    SeqWork w = seq_work<MT>(a, b);
     while (true) {
-        const int units = w.row_tiles * a.c.Hkv;
-        int u = uniform((int)((at - first) / w.tiles));
-        for (; u < units && at < end; ++u) {
-            const int64_t us = first + (int64_t)u * w.tiles;   // the unit's place
-            const int h = uniform(u / w.row_tiles), f0 = (u - h * w.row_tiles) * 16 * MT;
-            const int f1 = min(f0 + 16 * MT, (w.sr.r1 - w.sr.r0) * a.G);
-            const KeyRange32 kr = key_range(a, w.sr.pos0 + uniform(f0 / a.G), w.sr.pos0 + uniform((f1 - 1) / a.G));
-            const int t0 = (int)(at - us), t1 = (int)min(end - us, (int64_t)w.tiles);
-            const bool whole = t0 == 0 && t1 == w.tiles;
-            const bool begins = at == (int64_t)blockIdx.x * per;
-            float* part = whole ? nullptr : a.part + ((int64_t)blockIdx.x * 2 + (begins ? 0 : 1)) * part_floats<D, MT>();
-            dense_unit<D, MT>(a, w.sr, b, h, f0, f1, kr, t0, min(t1, kr.tiles), sh, part);
-            at = us + t1;
-            __syncthreads();   // finish() has read its LDS
+        const int b = uniform(place.b);
+        const int64_t at = uniform(place.at), first = uniform(place.first);
+        const SeqWork w = seq_work<MT>(a, b);
+        const int units = w.row_tiles * a.c.Hkv, u = uniform((int)((at - first) / w.tiles));
+        const int64_t us = first + (int64_t)u * w.tiles;   // the unit's place
+        const int h = uniform(u / w.row_tiles), f0 = (u - h * w.row_tiles) * 16 * MT;
+        const int f1 = min(f0 + 16 * MT, (w.sr.r1 - w.sr.r0) * a.G);
+        const KeyRange32 kr = key_range(a, w.sr.pos0 + uniform(f0 / a.G), w.sr.pos0 + uniform((f1 - 1) / a.G));
+        const int t0 = (int)(at - us), t1 = (int)min(end - us, (int64_t)w.tiles);
+        float* part = nullptr;
+        if (t0 > 0 || t1 < w.tiles)
+            part = a.part + ((int64_t)blockIdx.x * 2 + (at == begin ? 0 : 1)) * part_floats<D, MT>();
+        __syncthreads();
+        if (threadIdx.x == 0) {   // the next unit
+            Place n{us + t1, first, b};
+            if (u + 1 == units && n.at < end) {
+                n.first += (int64_t)units * w.tiles;
+                do ++n.b;
+                while (seq_work<MT>(a, n.b).row_tiles == 0);
+            }
+            place = n;
         }
-        if (at >= end) return;
-        first += (int64_t)units * w.tiles;
-        do w = seq_work<MT>(a, ++b);
-        while (w.row_tiles == 0);
+        dense_unit<D, MT>(a, w.sr, b, h, f0, f1, kr, t0, min(t1, kr.tiles), sh, part);
+        __syncthreads();   // finish() has read its LDS
+        if (uniform(place.at) >= end) return;
     }
 }
 
@@ -787,9 +803,7 @@ hipError_t launch(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
 
 template <int KIND, int D>
 hipError_t launch_rows(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
-    if (p.mt == 1) return launch<KIND, D, 1>(p, a, st);
-    if (p.mt == 2) return launch<KIND, D, 2>(p, a, st);
-    return launch<KIND, D, 4>(p, a, st);
+    return p.mt == 1 ? launch<KIND, D, 1>(p, a, st) : launch<KIND, D, 2>(p, a, st);
 }
 
 template <int KIND>
@@ -806,23 +820,27 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
         return attend_tile_plan(kind, T, Hq, Hkv, D, n_seq, entries, group);
     const size_t part = (size_t)(D + 2) * 16 * sizeof(float);   // of 16 rows
     if (kind == LTK_ATTEND) {
-        // rows that share keys: 16, 32 or 64 to a workgroup
-        const int64_t shared = (int64_t)T * G / std::max(n_seq, 1);
-        p.mt = shared > 32 ? 4 : shared > 16 ? 2 : 1;
+        // Rows that share keys: 16 or 32 to a unit.  (64 rows in one unit read
+        // the cache once but leave one wave on a SIMD: attend-specdecode-1m took
+        // 529 us so, and 507 us as two units of 32 whose ranges run side by side
+        // and meet in L2; with units of 16, 760 us.)
+        p.mt = (int64_t)T * G > 16 * (int64_t)std::max(n_seq, 1) ? 2 : 1;
         // one range of key tiles a workgroup
         const int64_t units = ((int64_t)T * G / (16 * p.mt) + n_seq) * Hkv, tiles = (entries + kTile - 1) / kTile;
         const int64_t most = (units * tiles + kMinPer - 1) / kMinPer;
-        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, p.mt == 4 ? 256 : 1024));
+        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, p.mt == 2 ? 512 : 1024));
         p.join = p.blocks > 1;
         p.head_bytes = (sizeof(DenseHead) + (size_t)n_seq * 8 + 255) / 256 * 256;
         p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * p.mt * part : 0);
         return p;
     }
-    p.mt = G > 32 ? 4 : G > 16 ? 2 : 1;
+    p.mt = G > 16 ? 2 : 1;
     const int64_t units = (int64_t)T * ((G + 16 * p.mt - 1) / (16 * p.mt)) * Hkv;
-    // about 1,024 workgroups (four per CU), each with at least one 32-key tile per wave
+    // Lists are cut only while the units leave CUs with less than two workgroups,
+    // each part at least one 32-key tile a wave (selected-specdecode-batch, 580
+    // units: 54 us whole, 68 us cut in two and joined).
     const int64_t most = std::max<int64_t>(1, (entries + kTile * kWaves - 1) / (kTile * kWaves));
-    p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, 1024 / std::max<int64_t>(units, 1)));
+    p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, 512 / std::max<int64_t>(units, 1)));
     p.blocks = units * p.splits;
     p.join = p.splits > 1;
     p.ws_bytes = std::max<size_t>(256, p.join ? (size_t)p.blocks * p.mt * part : 0);

@@ -608,9 +608,10 @@ __device__ __forceinline__ int64_t line_of(const AttendArgs& a, int b) {
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
     __shared__ ScanLds<NW> sc;
-    int64_t total = 0, sum;
+    int64_t total = 0, sum, w0 = 0, x0 = 0;   // one look at up to 64 NW sequences gives the total and the place
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += 64 * NW) {
-        scan_block<NW>(line_of<NW>(a, b0 + threadIdx.x), sc, sum);
+        w0 = line_of<NW>(a, b0 + threadIdx.x);
+        x0 = total + (a.bt.n_seq > 1 ? scan_block<NW>(w0, sc, sum) : (sum = line_of<NW>(a, 0)));
         total += uniform(sum);
     }
     const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kMinKeys);
@@ -625,10 +626,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
     __shared__ Place place;
     int64_t before = 0;
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += 64 * NW) {
-        const int64_t w = line_of<NW>(a, b0 + threadIdx.x), x = before + scan_block<NW>(w, sc, sum);
-        if (x - w <= begin && begin < x) {   // the sequence that the range begins in
+        if (a.bt.n_seq > 64 * NW) {
+            w0 = line_of<NW>(a, b0 + threadIdx.x);
+            x0 = before + scan_block<NW>(w0, sc, sum);
+            before += uniform(sum);
+        }
+        if (x0 - w0 <= begin && begin < x0) {   // the sequence that the range begins in
             const SeqLine s = seq_line<NW>(a, b0 + threadIdx.x);
-            const int64_t off = begin - (x - w), head = s.before(s.tiles);
+            const int64_t off = begin - (x0 - w0), head = s.before(s.tiles);
             const int h = (int)(off / head);
             int lo = 0, hi = s.tiles - 1;
             while (lo < hi) {
@@ -638,9 +643,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
                 else
                     hi = mid - 1;
             }
-            place = Place{begin, x - w, b0 + (int)threadIdx.x, h, lo};
+            place = Place{begin, x0 - w0, b0 + (int)threadIdx.x, h, lo};
         }
-        before += uniform(sum);
         if (begin < before) break;
     }
     __syncthreads();
