@@ -41,10 +41,12 @@ from .attention import (  # noqa: F401
     kv_append,
 )
 from .prefill import next_sample, prefill_chunked, prefill_workspace_bytes  # noqa: F401
+from .sparse import sparse_step  # noqa: F401
 
 __all__ = [
     "score_select", "retrieve", "unfused_score_select", "workspace_bytes", "strerror", "device_check",
     "Opts", "Stats", "LtkError", "next_sample", "prefill_chunked", "library", "exported_symbols",
     "dsa_pack", "dsa_gather", "prefill_workspace_bytes", "score_select_static", "unfused_retrieve",
     "kv_append", "attend", "attend_selected", "attend_packed", "attend_workspace_bytes",
+    "sparse_step",
 ]

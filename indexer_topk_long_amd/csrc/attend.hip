@@ -816,7 +816,13 @@ hipError_t launch_kind(int D, const AttendPlan& p, const AttendArgs& a, hipStrea
 AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group) {
     AttendPlan p{};
     const int G = Hq / Hkv;
-    if (kind == LTK_ATTEND ? (int64_t)T * G > 64 * (int64_t)std::max(n_seq, 1) : kind == LTK_ATTEND_PACKED && group > 1)
+    // The tile kernels from 65 rows a sequence and head, or four rows a group.
+    // (Hq 64, Hkv 8, D 128, against these kernels: one sequence of 131,072
+    // tokens, 64 rows 117 against 76 us, 96 rows 107 against 136, 512 rows 339
+    // against 399; 32 sequences of 2,048 tokens, 72 rows 67 against 99, 256 rows
+    // 91 against 250.  Packed, 512 rows of 1,024 keys: groups of two 217 against
+    // 159 us, of four 119 against 156, of 16 60 against 176.)
+    if (kind == LTK_ATTEND ? (int64_t)T * G > 64 * (int64_t)std::max(n_seq, 1) : kind == LTK_ATTEND_PACKED && group >= 4)
         return attend_tile_plan(kind, T, Hq, Hkv, D, n_seq, entries, group);
     const size_t part = (size_t)(D + 2) * 16 * sizeof(float);   // of 16 rows
     if (kind == LTK_ATTEND) {

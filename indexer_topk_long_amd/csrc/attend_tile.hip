@@ -17,6 +17,7 @@
 // 8 pieces each touch all banks.  Two stages of LDS (64 KB at D = 128), global
 // loads two steps ahead, one barrier a step, two workgroups on a CU.
 #include <algorithm>
+#include <atomic>
 
 #include "attend.hpp"
 
@@ -34,7 +35,11 @@ constexpr int kRows = 32 * NW;
 constexpr int kListWaves = 4;   // packed lists: 128 pairs a unit
 constexpr int kRing = 256;      // list entries resolved together (one a thread), two such chunks in LDS
 constexpr int kMinKeys = 4 * kKeys;   // least keys of a workgroup's range
-constexpr int kWide = 512;            // rows a sequence from which a unit has 256
+// Rows a sequence from which a unit has 256 (Hq 64, Hkv 8, D 128; units of 128
+// against 256: one sequence of 131,072 tokens, 128 rows a head 111 against 158
+// us, 256 rows 194 against 174, 1,024 rows 640 against 596; 32 sequences of
+// 2,048 tokens, 128 rows 68 against 83, 256 rows 115 against 91).
+constexpr int kWide = 256;
 
 __device__ __forceinline__ float max_halves(float x) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -562,11 +567,13 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     end_rows<D, NW>(a, row, st, part);
 }
 
-// What a workgroup leaves to join, in the workspace: the unit that began in
-// its range and goes on in those behind it.  Its parts are the workgroup's
-// (slot), then the first ones of the n - 1 workgroups that follow.
+// A unit cut over n > 1 workgroups, as each of them notes it in the workspace
+// for the join: [0] where it takes a later part of the unit (at the start of
+// its range), [1] where it takes the first (at its end).  The parts are in the
+// first one's slot, then in the slots 2 w of the workgroups w behind it.
 struct Crossing {
-    int n, slot;   // n == 0: none
+    int n, i;           // parts (0: none), and which of them is this workgroup's
+    int slot, behind;   // slot of the first part, and the workgroup of the second
     UnitRows u;
 };
 template <int NW>
@@ -616,12 +623,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
     }
     const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kMinKeys);
     // Workgroups go to the eight XCDs in turn: each XCD takes a stretch of the
-    // line, so that the row tiles of one head read its keys through one L2.
-    const int n8 = gridDim.x / 8;
+    // n8 ranges that hold work (so that the row tiles of one head read its keys
+    // through one L2); the numbers behind those are the other workgroups'.
+    const int n8 = (int)((total + 8 * per - 1) / (8 * per));
     const int me = (int)blockIdx.x < 8 * n8 ? (blockIdx.x % 8) * n8 + blockIdx.x / 8 : (int)blockIdx.x;
     const int64_t begin = me * per, end = min(begin + per, total);
-    Crossing* crossing = reinterpret_cast<Crossing*>(a.head) + me;
-    if (threadIdx.x == 0) crossing->n = 0;
+    Crossing* crossing = reinterpret_cast<Crossing*>(a.head) + 2 * (int64_t)me;
+    if (threadIdx.x == 0) crossing[0].n = crossing[1].n = 0;
     if (begin >= end) return;
     __shared__ Place place;
     int64_t before = 0;
@@ -662,8 +670,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
         const int64_t k0 = at - us, k1 = min(end - us, cost);
         float* part = nullptr;
         if (k0 > 0 || k1 < cost) part = a.part + (2 * (int64_t)me + (at == begin ? 0 : 1)) * part_floats<D, NW>();
-        if (k0 == 0 && k1 < cost && threadIdx.x == 0)
-            *crossing = Crossing{(int)((us + cost - 1) / per) - me + 1, 2 * me + (at == begin ? 0 : 1), u};
+        if (part && threadIdx.x == 0) {
+            const int w0 = (int)(us / per), w1 = (int)((us + cost - 1) / per);
+            crossing[k0 > 0 ? 0 : 1] = Crossing{w1 - w0 + 1, me - w0, 2 * w0 + (us == w0 * per ? 0 : 1), w0 + 1, u};
+        }
         __syncthreads();
         if (threadIdx.x == 0) {   // the next unit
             Place n{us + k1, place.first, b, h, i + 1};
@@ -852,44 +862,86 @@ __global__ __launch_bounds__(64 * kListWaves, 2) void attend_tile_list_kernel(At
 
 // ------------------------------------------------------- joining the parts
 
-// Sum of n parts of one row by D / 4 lanes: part i at slot0 (i == 0) or
-// slot1 + (i - 1) step.
+constexpr int kJoinRows = 8;   // lane groups (D / 4 lanes, a row's dimensions) of a joining workgroup
+
+struct RowSum {
+    float m, l;
+    at_f32x4 o;
+};
+__device__ __forceinline__ void add_part(RowSum& s, float m, float l, const at_f32x4& o) {
+    const float mn = fmaxf(s.m, m), f0 = __builtin_amdgcn_exp2f(s.m - mn), f1 = __builtin_amdgcn_exp2f(m - mn);
+    s.l = s.l * f0 + l * f1;
+    s.o = s.o * f0 + o * f1;
+    s.m = mn;
+}
+// Parts i0, i0 + step, .. below n of row `at` of a unit: part i at slot0
+// (i == 0) or slot1 + (i - 1) slot_step.
 template <int D, int NW>
-__device__ __forceinline__ void join_row(const AttendArgs& a, int64_t row, int at, int n, int64_t slot0, int64_t slot1,
-                                         int step) {
+__device__ __forceinline__ RowSum sum_parts(const AttendArgs& a, int at, int i0, int step, int n, int64_t slot0,
+                                            int64_t slot1, int slot_step) {
     const int lane = threadIdx.x % (D / 4);
-    float m = kNoRef, l = 0.0f;
-    at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
+    RowSum s{kNoRef, 0.0f, at_f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float* p = a.part + (i == 0 ? slot0 : slot1 + (int64_t)(i - 1) * step) * part_floats<D, NW>();
-        const float mi = p[kRows<NW> * D + at * 2], li = p[kRows<NW> * D + at * 2 + 1];
-        const at_f32x4 x = *reinterpret_cast<const at_f32x4*>(p + at * D + 4 * lane);
-        const float mn = fmaxf(m, mi), f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(mi - mn);
-        l = l * f0 + li * f1;
-        o = o * f0 + x * f1;
-        m = mn;
+    for (int i = i0; i < n; i += step) {
+        const float* p = a.part + (i == 0 ? slot0 : slot1 + (int64_t)(i - 1) * slot_step) * part_floats<D, NW>();
+        add_part(s, p[kRows<NW> * D + at * 2], p[kRows<NW> * D + at * 2 + 1],
+                 *reinterpret_cast<const at_f32x4*>(p + at * D + 4 * lane));
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    *reinterpret_cast<at_u32x2*>(a.out + row * D + 4 * lane) =
-        at_u32x2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+    return s;
+}
+template <int D>
+__device__ __forceinline__ void write_row(const AttendArgs& a, int64_t row, const RowSum& s) {
+    const float inv = s.l > 0.0f ? 1.0f / s.l : 0.0f;
+    *reinterpret_cast<at_u32x2*>(a.out + row * D + 4 * (threadIdx.x % (D / 4))) =
+        at_u32x2{pack_bf16(s.o[0] * inv, s.o[1] * inv), pack_bf16(s.o[2] * inv, s.o[3] * inv)};
+}
+// One row by all lane groups, each every kJoinRows-th part.
+template <int D, int NW>
+__device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t row, int at, int n, int64_t slot0, int64_t slot1,
+                                          int slot_step) {
+    __shared__ float s_ml[kJoinRows][2];
+    __shared__ float s_o[kJoinRows][D + 4];
+    const int grp = threadIdx.x / (D / 4), lane = threadIdx.x % (D / 4);
+    const RowSum s = sum_parts<D, NW>(a, at, grp, kJoinRows, n, slot0, slot1, slot_step);
+    __syncthreads();
+    *reinterpret_cast<at_f32x4*>(&s_o[grp][4 * lane]) = s.o;
+    if (lane == 0) s_ml[grp][0] = s.m, s_ml[grp][1] = s.l;
+    __syncthreads();
+    if (grp != 0 || row < 0) return;
+    RowSum all{kNoRef, 0.0f, at_f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+    for (int w = 0; w < kJoinRows; ++w)
+        add_part(all, s_ml[w][0], s_ml[w][1], *reinterpret_cast<const at_f32x4*>(&s_o[w][4 * lane]));
+    write_row<D>(a, row, all);
 }
 
-constexpr int kJoinRows = 8;   // rows of a joining workgroup
-
+// The workgroups (w, 0 .. kRows / kJoinRows - 1) stand for workgroup w of the
+// main launch: those of a cut unit's n workgroups share its rows, so that many
+// parts have many hands.
 template <int D, int NW>
 __global__ __launch_bounds__(kJoinRows * D / 4) void attend_tile_join_kernel(AttendArgs a) {
-    const Crossing x = reinterpret_cast<const Crossing*>(a.head)[blockIdx.x];
-    const int at = blockIdx.y * kJoinRows + threadIdx.x / (D / 4);
-    const int64_t row = x.n > 0 ? out_row(a, x.u, x.u.f0 + at) : -1;
-    if (row >= 0) join_row<D, NW>(a, row, at, x.n, x.slot, 2 * ((int64_t)blockIdx.x + 1), 2);
+    const int grp = threadIdx.x / (D / 4);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const Crossing x = reinterpret_cast<const Crossing*>(a.head)[2 * (int64_t)blockIdx.x + e];
+        if (x.n <= 1) continue;
+        // kRows rows over n * kRows / kJoinRows workgroups
+        const int id = x.i * gridDim.y + blockIdx.y;
+        const int r0 = id * kJoinRows / x.n, r1 = (id + 1) * kJoinRows / x.n;
+        const int64_t slot1 = 2 * (int64_t)x.behind;
+        if (x.n < kJoinRows) {
+            const int at = r0 + grp;
+            const int64_t row = at < r1 ? out_row(a, x.u, x.u.f0 + at) : -1;
+            if (row >= 0) write_row<D>(a, row, sum_parts<D, NW>(a, at, 0, 1, x.n, x.slot, slot1, 2));
+        } else if (r0 < r1) {   // one row
+            join_wide<D, NW>(a, out_row(a, x.u, x.u.f0 + r0), r0, x.n, x.slot, slot1, 2);
+        }
+    }
 }
 
 template <int D>
 __global__ __launch_bounds__(kJoinRows * D / 4) void attend_tile_list_join_kernel(AttendArgs a) {
     constexpr int NW = kListWaves;
-    const int64_t r = (int64_t)blockIdx.x * kJoinRows + threadIdx.x / (D / 4);   // row * Hq + head
-    if (r >= (int64_t)a.T * a.Hq) return;
+    const int64_t r = blockIdx.x;   // row * Hq + head
     const int t = (int)(r / a.Hq), head = (int)(r % a.Hq), h = head / a.G;
     const int grp = t / a.group, ht = (a.group * a.G + kRows<NW> - 1) / kRows<NW>;
     const int n = min(max(a.lens[grp], 0), a.cap);
@@ -898,11 +950,7 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attend_tile_list_join_kerne
     if (used <= 1) return;
     const int f = (t % a.group) * a.G + (head - h * a.G);
     const int64_t slot0 = (((int64_t)grp * ht + f / kRows<NW>) * a.c.Hkv + h) * a.splits;
-    join_row<D, NW>(a, r, f % kRows<NW>, used, slot0, slot0 + 1, 1);
-}
-
-hipError_t allow_lds(const void* fn, size_t bytes) {
-    return bytes > 65536 ? hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : hipSuccess;
+    join_wide<D, NW>(a, r, f % kRows<NW>, used, slot0, slot0 + 1, 1);
 }
 
 template <int D, int NW>
@@ -917,12 +965,22 @@ hipError_t launch_dense(const AttendPlan& p, const AttendArgs& a, hipStream_t st
 template <int D>
 hipError_t launch_list(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
     constexpr size_t bytes = 2 * kStageBytes<D> + sizeof(Ring);
-    const hipError_t e = allow_lds(reinterpret_cast<const void*>(attend_tile_list_kernel<D>), bytes);
-    if (e != hipSuccess) return e;
+    if constexpr (bytes > 65536) {   // asked for once per device
+        static std::atomic<uint64_t> allowed;
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess) return e;
+        const uint64_t bit = 1ull << (dev & 63);
+        if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) & bit)) {
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(attend_tile_list_kernel<D>),
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+            if (e != hipSuccess) return e;
+            allowed.fetch_or(bit, std::memory_order_relaxed);
+        }
+    }
     attend_tile_list_kernel<D><<<(unsigned)p.blocks, 64 * kListWaves, bytes, st>>>(a);
     if (p.join)
-        attend_tile_list_join_kernel<D><<<(unsigned)(((int64_t)a.T * a.Hq + kJoinRows - 1) / kJoinRows),
-                                          kJoinRows * D / 4, 0, st>>>(a);
+        attend_tile_list_join_kernel<D><<<(unsigned)((int64_t)a.T * a.Hq), kJoinRows * D / 4, 0, st>>>(a);
     return hipGetLastError();
 }
 
@@ -938,9 +996,10 @@ AttendPlan attend_tile_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, 
         const int rows = 32 * p.waves;
         const int64_t units = ((int64_t)T * G / rows + n_seq) * Hkv;
         const int64_t most = (units * (entries + kKeys) + kMinKeys - 1) / kMinKeys;
-        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, 2048 / p.waves));   // eight waves a CU
-        p.join = p.blocks > 1;
-        p.head_bytes = (sizeof(Crossing) * (size_t)p.blocks + 255) / 256 * 256;
+        // eight waves a CU; whole rounds of the XCDs
+        p.blocks = (std::max<int64_t>(1, std::min<int64_t>(most, 2048 / p.waves)) + 7) / 8 * 8;
+        p.join = true;
+        p.head_bytes = (2 * sizeof(Crossing) * (size_t)p.blocks + 255) / 256 * 256;
         p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * rows * (D + 2) * sizeof(float) : 0);
         return p;
     }
