@@ -254,16 +254,23 @@ constexpr size_t finish_lds() {
 // Dense work is cut evenly over the workgroups whatever the sequences'
 // lengths are.  Sequence b has units (key/value head, row tile): its rows
 // times the G heads of a key/value head, flattened as (row, head), 16 MT a
-// tile; each unit counts tiles_of(b) key tiles, those its last row sees.  The
-// tiles of all units of all sequences lie on one line, and workgroup w takes
-// [w per, (w + 1) per) of it, across unit borders.  A unit that lies in one
-// workgroup's range is written at once; the parts of the others are joined by
-// attend_join_kernel.  A workgroup leaves at most two such parts: of the unit
-// its range begins in, and of the one that goes on past its end.
+// tile; each counts kUnitTiles for what a unit costs whatever it reads, then
+// its key tiles, those its last row sees.  All units of all sequences lie on
+// one line, and workgroup w takes [w per, (w + 1) per) of it, across unit
+// borders.  A unit whose tiles lie in one workgroup's range is written at once;
+// the parts of the others are joined by attend_join_kernel.  A workgroup leaves
+// at most two parts: a later one of the unit its range begins in (slot 2 w),
+// and the first one of the unit that goes on past its end (slot 2 w + 1).
+//
+// (Without the unit's own cost, 480 units of one tile each went eight to a
+// workgroup, one after the other: 60 us.)
+constexpr int kUnitTiles = 8;
+constexpr int kWhole = 32;   // units of up to this cost are not cut further than the card needs
 struct SeqWork {
     SeqRows sr;
     int tiles;       // key tiles per unit, at least 1 (a unit that sees nothing is one empty tile)
     int row_tiles;
+    __device__ __forceinline__ int64_t cost() const { return (int64_t)kUnitTiles + tiles; }
 };
 
 // Key tiles of the rows at positions pos_lo .. pos_hi: [0, sink_tiles) and
@@ -302,6 +309,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int b) {
 constexpr int kPlanSeqs = 64 * kWaves;   // sequences looked at together
 struct PlanLds {
     int64_t wave[kWaves];
+    int largest;   // cost of the largest unit, up to kWhole + 1
 };
 
 // Where a workgroup stands: the place reached on the line, and the sequence
@@ -317,7 +325,7 @@ template <int MT>
 __device__ __forceinline__ int64_t work_of(const AttendArgs& a, int b) {
     if (b >= a.bt.n_seq) return 0;
     const SeqWork w = seq_work<MT>(a, b);
-    return (int64_t)w.tiles * w.row_tiles * a.c.Hkv;
+    return w.cost() * w.row_tiles * a.c.Hkv;
 }
 
 // Inclusive scan over the workgroup's threads; total of all in `sum`.
@@ -495,14 +503,19 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
     DenseHead* head = reinterpret_cast<DenseHead*>(a.head);
     // the total, then the sequence that this workgroup's range begins in; one
     // look at up to kPlanSeqs sequences serves both
+    if (threadIdx.x == 0) ls.largest = 0;
+    __syncthreads();
     int64_t total = 0, sum, w0 = 0, x0 = 0;
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += kPlanSeqs) {
         w0 = work_of<MT>(a, b0 + threadIdx.x);
         x0 = total + (a.bt.n_seq > 1 ? block_scan(w0, ls, sum) : (sum = work_of<MT>(a, 0)));
+        if (w0 > 0) atomicMax(&ls.largest, (int)min(seq_work<MT>(a, b0 + threadIdx.x).cost(), (int64_t)kWhole + 1));
         if (blockIdx.x == 0 && b0 + (int)threadIdx.x < a.bt.n_seq) head->first[b0 + threadIdx.x] = x0 - w0;
         total += uniform(sum);
     }
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)a.min_per);
+    __syncthreads();
+    const int largest = uniform(ls.largest);
+    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(largest <= kWhole ? largest : kMinPer));
     if (blockIdx.x == 0 && threadIdx.x == 0) head->total = total, head->per = per;
     const int64_t begin = (int64_t)blockIdx.x * per, end = min(begin + per, total);
     if (begin >= end) return;
@@ -522,26 +535,28 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
         const int b = uniform(place.b);
         const int64_t at = uniform(place.at), first = uniform(place.first);
         const SeqWork w = seq_work<MT>(a, b);
-        const int units = w.row_tiles * a.c.Hkv, u = uniform((int)((at - first) / w.tiles));
-        const int64_t us = first + (int64_t)u * w.tiles;   // the unit's place
+        const int units = w.row_tiles * a.c.Hkv, u = uniform((int)((at - first) / w.cost()));
+        const int64_t us = first + u * w.cost(), tile0 = us + kUnitTiles;   // places of the unit and of its first tile
+        const int64_t stop = min(end, us + w.cost());
         const int h = uniform(u / w.row_tiles), f0 = (u - h * w.row_tiles) * 16 * MT;
         const int f1 = min(f0 + 16 * MT, (w.sr.r1 - w.sr.r0) * a.G);
-        const KeyRange32 kr = key_range(a, w.sr.pos0 + uniform(f0 / a.G), w.sr.pos0 + uniform((f1 - 1) / a.G));
-        const int t0 = (int)(at - us), t1 = (int)min(end - us, (int64_t)w.tiles);
+        const int t0 = (int)max(at - tile0, (int64_t)0), t1 = (int)max(stop - tile0, (int64_t)0);
         float* part = nullptr;
-        if (t0 > 0 || t1 < w.tiles)
-            part = a.part + ((int64_t)blockIdx.x * 2 + (at == begin ? 0 : 1)) * part_floats<D, MT>();
+        if (t0 > 0 || t1 < w.tiles) part = a.part + ((int64_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * part_floats<D, MT>();
         __syncthreads();
         if (threadIdx.x == 0) {   // the next unit
-            Place n{us + t1, first, b};
-            if (u + 1 == units && n.at < end) {
-                n.first += (int64_t)units * w.tiles;
+            Place n{stop, first, b};
+            if (u + 1 == units && stop == us + w.cost() && stop < end) {
+                n.first += units * w.cost();
                 do ++n.b;
                 while (seq_work<MT>(a, n.b).row_tiles == 0);
             }
             place = n;
         }
-        dense_unit<D, MT>(a, w.sr, b, h, f0, f1, kr, t0, min(t1, kr.tiles), sh, part);
+        if (t0 < t1) {   // (else the range ends before the unit's first tile)
+            const KeyRange32 kr = key_range(a, w.sr.pos0 + uniform(f0 / a.G), w.sr.pos0 + uniform((f1 - 1) / a.G));
+            dense_unit<D, MT>(a, w.sr, b, h, f0, f1, kr, t0, min(t1, kr.tiles), sh, part);
+        }
         __syncthreads();   // finish() has read its LDS
         if (uniform(place.at) >= end) return;
     }
@@ -733,12 +748,11 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
         if (t < w.sr.r0 || t >= w.sr.r1) return;
         const int64_t per = hd->per;
         const int f = (t - w.sr.r0) * a.G + g;
-        const int64_t us = hd->first[b] + ((int64_t)h * w.row_tiles + f / RT) * w.tiles;
-        const int64_t w0 = us / per, w1 = (us + w.tiles - 1) / per;
+        const int64_t tile0 = hd->first[b] + ((int64_t)h * w.row_tiles + f / RT) * w.cost() + kUnitTiles;
+        const int64_t w0 = tile0 / per, w1 = (tile0 + w.tiles - 1) / per;
         used = (int)(w1 - w0) + 1;
         at = f % RT;
-        // every part but the first begins its workgroup's range
-        slot0 = 2 * w0 + (us == w0 * per ? 0 : 1);
+        slot0 = 2 * w0 + 1;
         slot1 = 2 * (w0 + 1);
         slot_step = 2;
     } else {
@@ -833,7 +847,7 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
         p.mt = (int64_t)T * G > 16 * (int64_t)std::max(n_seq, 1) ? 2 : 1;
         // one range of key tiles a workgroup
         const int64_t units = ((int64_t)T * G / (16 * p.mt) + n_seq) * Hkv, tiles = (entries + kTile - 1) / kTile;
-        const int64_t most = (units * tiles + kMinPer - 1) / kMinPer;
+        const int64_t most = (units * (tiles + kUnitTiles) + kMinPer - 1) / kMinPer;
         p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, p.mt == 2 ? 512 : 1024));
         p.join = p.blocks > 1;
         p.head_bytes = (sizeof(DenseHead) + (size_t)n_seq * 8 + 255) / 256 * 256;
@@ -855,7 +869,6 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
 
 hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, void* ws, hipStream_t st) {
     a.splits = p.splits;
-    a.min_per = kMinPer;
     a.head = ws;
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.head_bytes);
     if (p.tile) return launch_attend_tile(kind, D, p, a, st);

@@ -163,8 +163,7 @@ struct AttendArgs {
     const int32_t* lens;     // packed
     int cap, group;
     int splits;              // list kinds: key splits per unit
-    int min_per;             // attend: least key tiles of a workgroup's range
-    void* head;              // attend: the plan for the join
+    void* head;              // attend: what the join needs to know
     float* part;             // partial rows and their statistics
 };
 

@@ -35,6 +35,8 @@ constexpr int kRows = 32 * NW;
 constexpr int kListWaves = 4;   // packed lists: 128 pairs a unit
 constexpr int kRing = 256;      // list entries resolved together (one a thread), two such chunks in LDS
 constexpr int kMinKeys = 4 * kKeys;   // least keys of a workgroup's range
+constexpr int kUnitKeys = 4 * kKeys;  // what a unit costs whatever it reads
+constexpr int kWhole = 16 * kKeys;    // units of up to this cost are not cut further than the card needs
 // Rows a sequence from which a unit has 256 (Hq 64, Hkv 8, D 128; units of 128
 // against 256: one sequence of 131,072 tokens, 128 rows a head 111 against 158
 // us, 256 rows 194 against 174, 1,024 rows 640 against 596; 32 sequences of
@@ -363,15 +365,16 @@ __device__ __forceinline__ void end_rows(const AttendArgs& a, int64_t row, const
 
 // ------------------------------------------------------------ dense keys
 
-// Work is cut evenly as in attend.hip, here on a line of keys: the unit of
-// row tile i counts A + i Q keys, at least as many as its last row sees, so
-// that a sequence's prefix sums have a closed form.
+// Work is cut evenly as in attend.hip, here on a line of keys: the unit of row
+// tile i counts kUnitKeys for itself and then A + i Q keys, at least as many as
+// its last row sees, so that a sequence's prefix sums have a closed form.
 struct SeqLine {
     SeqRows sr;
     int tiles;       // row tiles
     int64_t A, Q;
-    __device__ __forceinline__ int64_t cost(int i) const { return A + i * Q; }
-    __device__ __forceinline__ int64_t before(int i) const { return i * A + Q * ((int64_t)i * (i - 1) / 2); }
+    __device__ __forceinline__ int64_t keys(int i) const { return A + i * Q; }
+    __device__ __forceinline__ int64_t cost(int i) const { return kUnitKeys + keys(i); }
+    __device__ __forceinline__ int64_t before(int i) const { return i * (kUnitKeys + A) + Q * ((int64_t)i * (i - 1) / 2); }
 };
 template <int NW>
 __device__ __forceinline__ SeqLine seq_line(const AttendArgs& a, int b) {
@@ -579,6 +582,7 @@ struct Crossing {
 template <int NW>
 struct ScanLds {
     int64_t wave[NW];
+    int largest;   // cost of the largest unit, up to kWhole + 1
 };
 // Where a workgroup stands on the line.  It lives in LDS and is read again for
 // every unit: in registers over a unit's loop it would cost that loop spills.
@@ -615,13 +619,21 @@ __device__ __forceinline__ int64_t line_of(const AttendArgs& a, int b) {
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
     __shared__ ScanLds<NW> sc;
+    if (threadIdx.x == 0) sc.largest = 0;
+    __syncthreads();
     int64_t total = 0, sum, w0 = 0, x0 = 0;   // one look at up to 64 NW sequences gives the total and the place
     for (int b0 = 0; b0 < a.bt.n_seq; b0 += 64 * NW) {
         w0 = line_of<NW>(a, b0 + threadIdx.x);
         x0 = total + (a.bt.n_seq > 1 ? scan_block<NW>(w0, sc, sum) : (sum = line_of<NW>(a, 0)));
+        if (w0 > 0) {
+            const SeqLine s = seq_line<NW>(a, b0 + threadIdx.x);
+            atomicMax(&sc.largest, (int)min(s.cost(s.tiles - 1), (int64_t)kWhole + 1));
+        }
         total += uniform(sum);
     }
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kMinKeys);
+    __syncthreads();
+    const int largest = uniform(sc.largest);
+    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(largest <= kWhole ? largest : kMinKeys));
     // Workgroups go to the eight XCDs in turn: each XCD takes a stretch of the
     // n8 ranges that hold work (so that the row tiles of one head read its keys
     // through one L2); the numbers behind those are the other workgroups'.
@@ -660,34 +672,40 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
         const int b = uniform(place.b), h = uniform(place.h), i = uniform(place.i);
         const int64_t at = uniform(place.at);
         const SeqLine s = seq_line<NW>(a, b);
-        const int64_t us = uniform(place.first) + h * s.before(s.tiles) + s.before(i), cost = s.cost(i);
+        const int64_t us = uniform(place.first) + h * s.before(s.tiles) + s.before(i);
+        const int64_t key0 = us + kUnitKeys, keys = s.keys(i), stop = min(end, us + s.cost(i));
         UnitRows u;
         u.r0 = s.sr.r0;
         u.h = h;
         u.f0 = i * kRows<NW>;
         u.f1 = min(u.f0 + kRows<NW>, (s.sr.r1 - s.sr.r0) * a.G);
         // a step belongs to the range that its first key lies in
-        const int64_t k0 = at - us, k1 = min(end - us, cost);
+        const int64_t k0 = max(at - key0, (int64_t)0), k1 = max(stop - key0, (int64_t)0);
         float* part = nullptr;
-        if (k0 > 0 || k1 < cost) part = a.part + (2 * (int64_t)me + (at == begin ? 0 : 1)) * part_floats<D, NW>();
-        if (part && threadIdx.x == 0) {
-            const int w0 = (int)(us / per), w1 = (int)((us + cost - 1) / per);
-            crossing[k0 > 0 ? 0 : 1] = Crossing{w1 - w0 + 1, me - w0, 2 * w0 + (us == w0 * per ? 0 : 1), w0 + 1, u};
+        if (k0 > 0 || k1 < keys) part = a.part + (2 * (int64_t)me + (k0 == 0 ? 1 : 0)) * part_floats<D, NW>();
+        if (part && k0 < k1 && threadIdx.x == 0) {
+            const int w0 = (int)(key0 / per), w1 = (int)((key0 + keys - 1) / per);
+            crossing[k0 > 0 ? 0 : 1] = Crossing{w1 - w0 + 1, me - w0, 2 * w0 + 1, w0 + 1, u};
         }
         __syncthreads();
         if (threadIdx.x == 0) {   // the next unit
-            Place n{us + k1, place.first, b, h, i + 1};
-            if (n.i == s.tiles) n.i = 0, ++n.h;
-            if (n.h == a.c.Hkv) {
-                n.h = 0;
-                n.first += a.c.Hkv * s.before(s.tiles);
-                n.b = n.at < end ? n.b + 1 : n.b;
-                while (n.at < end && seq_line<NW>(a, n.b).tiles == 0) ++n.b;
+            Place n{stop, place.first, b, h, i};
+            if (stop == us + s.cost(i)) {
+                if (++n.i == s.tiles) n.i = 0, ++n.h;
+                if (n.h == a.c.Hkv) {
+                    n.h = 0;
+                    n.first += a.c.Hkv * s.before(s.tiles);
+                    n.b = n.at < end ? n.b + 1 : n.b;
+                    while (n.at < end && seq_line<NW>(a, n.b).tiles == 0) ++n.b;
+                }
             }
             place = n;
         }
-        const KeyTiles kt = key_tiles(a, s.sr.pos0 + uniform(u.f0 / a.G), s.sr.pos0 + uniform((u.f1 - 1) / a.G));
-        dense_unit<D, NW>(a, s.sr, b, u, kt, (int)((k0 + kKeys - 1) / kKeys), min((int)((k1 + kKeys - 1) / kKeys), kt.tiles), part);
+        if (k0 < k1) {   // (else the range ends before the unit's first key)
+            const KeyTiles kt = key_tiles(a, s.sr.pos0 + uniform(u.f0 / a.G), s.sr.pos0 + uniform((u.f1 - 1) / a.G));
+            dense_unit<D, NW>(a, s.sr, b, u, kt, (int)((k0 + kKeys - 1) / kKeys),
+                              min((int)((k1 + kKeys - 1) / kKeys), kt.tiles), part);
+        }
         __syncthreads();
         if (uniform(place.at) >= end) return;
     }
@@ -995,7 +1013,7 @@ AttendPlan attend_tile_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, 
         p.waves = (int64_t)T * G >= kWide * (int64_t)std::max(n_seq, 1) ? 8 : 4;
         const int rows = 32 * p.waves;
         const int64_t units = ((int64_t)T * G / rows + n_seq) * Hkv;
-        const int64_t most = (units * (entries + kKeys) + kMinKeys - 1) / kMinKeys;
+        const int64_t most = (units * (entries + kKeys + kUnitKeys) + kMinKeys - 1) / kMinKeys;
         // eight waves a CU; whole rounds of the XCDs
         p.blocks = (std::max<int64_t>(1, std::min<int64_t>(most, 2048 / p.waves)) + 7) / 8 * 8;
         p.join = true;
