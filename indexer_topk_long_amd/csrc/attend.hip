@@ -26,7 +26,7 @@
 // four lane groups are joined once at the end.
 #include <algorithm>
 
-#include "attend.hpp"
+#include "attend_join.hpp"
 
 namespace ltk {
 
@@ -172,8 +172,8 @@ __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const
 }
 
 // The waves' states joined through LDS, then the unit's rows written: bf16
-// rows where this workgroup saw all of the unit's keys (part == NULL), else
-// fp32 partial rows: [16 MT] rows of D floats, then [16 MT] (m, l).
+// rows where this workgroup saw all of the unit's keys (part == NULL), else a
+// part.
 template <int D, int MT, class Row>
 __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT], float* sh, float* part, Row row_of) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
@@ -242,11 +242,6 @@ constexpr int waves_per_simd() {
 }
 
 template <int D, int MT>
-constexpr int part_floats() {
-    return 16 * MT * (D + 2);
-}
-
-template <int D, int MT>
 constexpr size_t finish_lds() {
     return (size_t)(kWaves * 16 * (D + 4) + kWaves * 16 * 2) * 4;
 }
@@ -258,7 +253,7 @@ constexpr size_t finish_lds() {
 // its key tiles, those its last row sees.  All units of all sequences lie on
 // one line, and workgroup w takes [w per, (w + 1) per) of it, across unit
 // borders.  A unit whose tiles lie in one workgroup's range is written at once;
-// the parts of the others are joined by attend_join_kernel.  A workgroup leaves
+// the parts of the others are joined by a second launch.  A workgroup leaves
 // at most two parts: a later one of the unit its range begins in (slot 2 w),
 // and the first one of the unit that goes on past its end (slot 2 w + 1).
 //
@@ -488,19 +483,11 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     finish<D, MT>(a, st, sh, part, row_of);
 }
 
-// Header of the workspace of a dense call, written by workgroup 0 for the
-// join: the line's total and share, then each sequence's place on it.
-struct DenseHead {
-    int64_t total, per;
-    int64_t first[];   // [n_seq]
-};
-
 template <int D, int MT>
 __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend_kernel(AttendArgs a) {
     extern __shared__ float sh[];
     __shared__ PlanLds ls;
     __shared__ Place place;
-    DenseHead* head = reinterpret_cast<DenseHead*>(a.head);
     // the total, then the sequence that this workgroup's range begins in; one
     // look at up to kPlanSeqs sequences serves both
     if (threadIdx.x == 0) ls.largest = 0;
@@ -510,14 +497,14 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
         w0 = work_of<MT>(a, b0 + threadIdx.x);
         x0 = total + (a.bt.n_seq > 1 ? block_scan(w0, ls, sum) : (sum = work_of<MT>(a, 0)));
         if (w0 > 0) atomicMax(&ls.largest, (int)min(seq_work<MT>(a, b0 + threadIdx.x).cost(), (int64_t)kWhole + 1));
-        if (blockIdx.x == 0 && b0 + (int)threadIdx.x < a.bt.n_seq) head->first[b0 + threadIdx.x] = x0 - w0;
         total += uniform(sum);
     }
     __syncthreads();
     const int largest = uniform(ls.largest);
     const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(largest <= kWhole ? largest : kMinPer));
-    if (blockIdx.x == 0 && threadIdx.x == 0) head->total = total, head->per = per;
     const int64_t begin = (int64_t)blockIdx.x * per, end = min(begin + per, total);
+    Crossing* crossing = reinterpret_cast<Crossing*>(a.head) + 2 * (int64_t)blockIdx.x;
+    if (threadIdx.x == 0) crossing[0].n = crossing[1].n = 0;
     if (begin >= end) return;
     if (a.bt.n_seq <= kPlanSeqs) {
         if (x0 - w0 <= begin && begin < x0) place = Place{begin, x0 - w0, (int)threadIdx.x};
@@ -542,7 +529,11 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
         const int f1 = min(f0 + 16 * MT, (w.sr.r1 - w.sr.r0) * a.G);
         const int t0 = (int)max(at - tile0, (int64_t)0), t1 = (int)max(stop - tile0, (int64_t)0);
         float* part = nullptr;
-        if (t0 > 0 || t1 < w.tiles) part = a.part + ((int64_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * part_floats<D, MT>();
+        if (t0 > 0 || t1 < w.tiles) part = a.part + ((int64_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * part_floats<D, 16 * MT>();
+        if (part && t0 < t1 && threadIdx.x == 0) {
+            const int w0 = (int)(tile0 / per), w1 = (int)((tile0 + w.tiles - 1) / per);
+            crossing[t0 > 0 ? 0 : 1] = Crossing{w1 - w0 + 1, (int)blockIdx.x - w0, 2 * w0 + 1, w0 + 1, {w.sr.r0, f0, f1, h}};
+        }
         __syncthreads();
         if (threadIdx.x == 0) {   // the next unit
             Place n{stop, first, b};
@@ -724,81 +715,26 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend
     }
     __syncthreads();   // the list is done with: finish() reuses its LDS
     const int64_t slot = (((int64_t)t * ht + tile) * a.c.Hkv + h) * a.splits + split;
-    finish<D, MT>(a, st, sh, used > 1 ? a.part + slot * part_floats<D, MT>() : nullptr, row_of);
+    finish<D, MT>(a, st, sh, used > 1 ? a.part + slot * part_floats<D, 16 * MT>() : nullptr, row_of);
 }
 
 // ------------------------------------------------------- joining the splits
 
-// One workgroup per query row and head: 256 threads = 256 / (D / 4) groups
-// that take splits in turn, then one sum over the groups.
-template <int D, int MT, int KIND>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
-    constexpr int RT = 16 * MT, kLanes = D / 4, kGroups = 256 / kLanes;
-    __shared__ float s_o[kGroups][D + 4];
-    __shared__ float s_ml[kGroups][2];
+// One workgroup per query row and head.
+template <int D, int MT, bool PACKED>
+__global__ __launch_bounds__(kJoinRows * D / 4) void attend_list_join_kernel(AttendArgs a) {
+    constexpr int RT = 16 * MT;
     const int64_t r = blockIdx.x;   // row * Hq + head
     const int t = (int)(r / a.Hq), head = (int)(r % a.Hq), h = head / a.G, g = head - h * a.G;
-    int used, at;                  // parts of the row's unit, and the row in it
-    int64_t slot0, slot1;          // the first part's slot, and the second's (the others follow it by slot_step)
-    int slot_step = 1;
-    if constexpr (KIND == LTK_ATTEND) {
-        const DenseHead* hd = reinterpret_cast<const DenseHead*>(a.head);
-        const int b = uniform(row_seq(a.bt, t, a.T));
-        const SeqWork w = seq_work<MT>(a, b);
-        if (t < w.sr.r0 || t >= w.sr.r1) return;
-        const int64_t per = hd->per;
-        const int f = (t - w.sr.r0) * a.G + g;
-        const int64_t tile0 = hd->first[b] + ((int64_t)h * w.row_tiles + f / RT) * w.cost() + kUnitTiles;
-        const int64_t w0 = tile0 / per, w1 = (tile0 + w.tiles - 1) / per;
-        used = (int)(w1 - w0) + 1;
-        at = f % RT;
-        slot0 = 2 * w0 + 1;
-        slot1 = 2 * (w0 + 1);
-        slot_step = 2;
-    } else {
-        if constexpr (KIND == LTK_ATTEND_SELECTED) {
-            if (t < cu_at(a.bt, 0, a.T) || t >= cu_at(a.bt, a.bt.n_seq, a.T)) return;
-        }
-        const int ht = (a.G + RT - 1) / RT;
-        const int n = KIND == LTK_ATTEND_PACKED ? min(max(a.lens[t / a.group], 0), a.cap) : a.cap;
-        const int per = (n + a.splits - 1) / a.splits;
-        used = (n + per - 1) / max(per, 1);
-        slot0 = (((int64_t)t * ht + g / RT) * a.c.Hkv + h) * a.splits;
-        slot1 = slot0 + 1;
-        at = g % RT;
+    if constexpr (!PACKED) {
+        if (t < cu_at(a.bt, 0, a.T) || t >= cu_at(a.bt, a.bt.n_seq, a.T)) return;
     }
+    const int ht = (a.G + RT - 1) / RT;
+    const int n = PACKED ? min(max(a.lens[t / a.group], 0), a.cap) : a.cap;
+    const int per = (n + a.splits - 1) / a.splits, used = (n + per - 1) / max(per, 1);
     if (used <= 1) return;   // written by its only workgroup
-    const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-    float m = kNoRef, l = 0.0f;
-    at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = grp; s < used; s += kGroups) {
-        const float* p = a.part + (s == 0 ? slot0 : slot1 + (int64_t)(s - 1) * slot_step) * part_floats<D, MT>();
-        const float ms = p[RT * D + at * 2], lsum = p[RT * D + at * 2 + 1];
-        const at_f32x4 x = *reinterpret_cast<const at_f32x4*>(p + at * D + 4 * lane);
-        const float mn = fmaxf(m, ms), f0 = __builtin_amdgcn_exp2f(m - mn), f1 = __builtin_amdgcn_exp2f(ms - mn);
-        l = l * f0 + lsum * f1;
-        o = o * f0 + x * f1;
-        m = mn;
-    }
-    *reinterpret_cast<at_f32x4*>(&s_o[grp][4 * lane]) = o;
-    if (lane == 0) s_ml[grp][0] = m, s_ml[grp][1] = l;
-    __syncthreads();
-    if (grp != 0) return;
-    float mm = kNoRef;
-#pragma unroll
-    for (int w = 0; w < kGroups; ++w) mm = fmaxf(mm, s_ml[w][0]);
-    float sum = 0.0f;
-    at_f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < kGroups; ++w) {
-        const float f = __builtin_amdgcn_exp2f(s_ml[w][0] - mm);
-        sum = __builtin_fmaf(f, s_ml[w][1], sum);
-        const at_f32x4 x = *reinterpret_cast<const at_f32x4*>(&s_o[w][4 * lane]);
-        acc = acc + x * f;
-    }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    *reinterpret_cast<at_u32x2*>(a.out + r * D + 4 * lane) =
-        at_u32x2{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
+    const int64_t slot0 = (((int64_t)t * ht + g / RT) * a.c.Hkv + h) * a.splits;
+    join_wide<D, RT>(a, r, g % RT, used, slot0, slot0 + 1, 1);
 }
 
 template <int KIND, int D, int MT>
@@ -807,11 +743,13 @@ hipError_t launch(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
     if (p.blocks > 0x7fffffff || rows > 0x7fffffff) return hipErrorInvalidValue;
     if constexpr (KIND == LTK_ATTEND) {
         attend_kernel<D, MT><<<(unsigned)p.blocks, 64 * kWaves, finish_lds<D, MT>(), st>>>(a);
+        if (p.join) launch_join<D, 16 * MT>(p, a, st);
     } else {
         constexpr size_t lds = std::max(finish_lds<D, MT>(), sizeof(ListLds));
-        attend_list_kernel<D, MT, KIND == LTK_ATTEND_PACKED><<<(unsigned)p.blocks, 64 * kWaves, lds, st>>>(a);
+        constexpr bool packed = KIND == LTK_ATTEND_PACKED;
+        attend_list_kernel<D, MT, packed><<<(unsigned)p.blocks, 64 * kWaves, lds, st>>>(a);
+        if (p.join) attend_list_join_kernel<D, MT, packed><<<(unsigned)rows, kJoinRows * D / 4, 0, st>>>(a);
     }
-    if (p.join) attend_join_kernel<D, MT, KIND><<<(unsigned)rows, 256, 0, st>>>(a);
     return hipGetLastError();
 }
 
@@ -850,7 +788,7 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
         const int64_t most = (units * (tiles + kUnitTiles) + kMinPer - 1) / kMinPer;
         p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, p.mt == 2 ? 512 : 1024));
         p.join = p.blocks > 1;
-        p.head_bytes = (sizeof(DenseHead) + (size_t)n_seq * 8 + 255) / 256 * 256;
+        p.head_bytes = crossing_bytes(p.blocks);
         p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * p.mt * part : 0);
         return p;
     }

@@ -19,7 +19,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "attend.hpp"
+#include "attend_join.hpp"
 
 namespace ltk {
 
@@ -37,11 +37,15 @@ constexpr int kRing = 256;      // list entries resolved together (one a thread)
 constexpr int kMinKeys = 4 * kKeys;   // least keys of a workgroup's range
 constexpr int kUnitKeys = 4 * kKeys;  // what a unit costs whatever it reads
 constexpr int kWhole = 16 * kKeys;    // units of up to this cost are not cut further than the card needs
-// Rows a sequence from which a unit has 256 (Hq 64, Hkv 8, D 128; units of 128
-// against 256: one sequence of 131,072 tokens, 128 rows a head 111 against 158
-// us, 256 rows 194 against 174, 1,024 rows 640 against 596; 32 sequences of
-// 2,048 tokens, 128 rows 68 against 83, 256 rows 115 against 91).
+// Units have 256 rows, of eight waves, from this many rows a sequence and this
+// many (row, head) pairs times keys of the table, else 128.  (Hq 64, Hkv 8,
+// D 128, units of 128 against 256: one sequence of 131,072 tokens, 128 rows a
+// head 111 against 158 us, 256 rows 194 against 174, 1,024 rows 640 against
+// 596; 32 sequences of 2,048 tokens, 128 rows 68 against 83, 256 rows 115
+// against 91.  Hq 32, one sequence with 512 tokens of queries: 512 tokens 38
+// against 46 us, 2,048 51 against 54, 8,192 107 against 105.)
 constexpr int kWide = 256;
+constexpr int64_t kWideWork = (int64_t)1 << 25;
 
 __device__ __forceinline__ float max_halves(float x) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -298,17 +302,6 @@ __device__ __forceinline__ void step_keys(int stage, const at_bf16x8 (&q)[D / 16
     }
 }
 
-// The unit's rows, flattened (row, head) from f0 to f1: row r0 + f / G, head
-// h G + f % G.
-struct UnitRows {
-    int r0, f0, f1, h;
-};
-__device__ __forceinline__ int64_t out_row(const AttendArgs& a, const UnitRows& u, int f) {
-    if (f >= u.f1) return -1;
-    const int i = f / a.G;
-    return (int64_t)(u.r0 + i) * a.Hq + u.h * a.G + (f - i * a.G);
-}
-
 template <int D>
 __device__ __forceinline__ void begin_rows(const AttendArgs& a, int64_t row, at_bf16x8 (&q)[D / 16], WaveState<D>& st) {
     const int g = (threadIdx.x & 63) >> 5;
@@ -328,11 +321,7 @@ __device__ __forceinline__ void begin_rows(const AttendArgs& a, int64_t row, at_
 }
 
 // Rows written as bf16 where the workgroup saw all of their keys (part ==
-// NULL), else as a part: [32 NW][D] floats, then [32 NW] (m, l).
-template <int D, int NW>
-constexpr int part_floats() {
-    return kRows<NW> * (D + 2);
-}
+// NULL), else as a part.
 template <int D, int NW>
 __device__ __forceinline__ void end_rows(const AttendArgs& a, int64_t row, const WaveState<D>& st, float* part) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
@@ -387,7 +376,7 @@ __device__ __forceinline__ SeqLine seq_line(const AttendArgs& a, int b) {
     s.A = max(min((int64_t)s.sr.pos0 + 1 + s.Q, cap), (int64_t)1);
     // a window's rows see at most the sinks, the window and the tiles' borders
     const int64_t win = (int64_t)a.n_sink + a.window + s.Q + 1 + 3 * kKeys;
-    if (a.window > 0 && win < s.A) s.A = win, s.Q = 0;
+    if (a.window > 0 && 2 * win < 2 * s.A + s.Q * (s.tiles - 1)) s.A = win, s.Q = 0;   // where that is less in all
     return s;
 }
 
@@ -570,15 +559,6 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     end_rows<D, NW>(a, row, st, part);
 }
 
-// A unit cut over n > 1 workgroups, as each of them notes it in the workspace
-// for the join: [0] where it takes a later part of the unit (at the start of
-// its range), [1] where it takes the first (at its end).  The parts are in the
-// first one's slot, then in the slots 2 w of the workgroups w behind it.
-struct Crossing {
-    int n, i;           // parts (0: none), and which of them is this workgroup's
-    int slot, behind;   // slot of the first part, and the workgroup of the second
-    UnitRows u;
-};
 template <int NW>
 struct ScanLds {
     int64_t wave[NW];
@@ -682,7 +662,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
         // a step belongs to the range that its first key lies in
         const int64_t k0 = max(at - key0, (int64_t)0), k1 = max(stop - key0, (int64_t)0);
         float* part = nullptr;
-        if (k0 > 0 || k1 < keys) part = a.part + (2 * (int64_t)me + (k0 == 0 ? 1 : 0)) * part_floats<D, NW>();
+        if (k0 > 0 || k1 < keys) part = a.part + (2 * (int64_t)me + (k0 == 0 ? 1 : 0)) * part_floats<D, kRows<NW>>();
         if (part && k0 < k1 && threadIdx.x == 0) {
             const int w0 = (int)(key0 / per), w1 = (int)((key0 + keys - 1) / per);
             crossing[k0 > 0 ? 0 : 1] = Crossing{w1 - w0 + 1, me - w0, 2 * w0 + 1, w0 + 1, u};
@@ -875,86 +855,10 @@ __global__ __launch_bounds__(64 * kListWaves, 2) void attend_tile_list_kernel(At
         }
     }
     const int64_t slot = (((int64_t)grp * ht + tile) * a.c.Hkv + u.h) * a.splits + split;
-    end_rows<D, NW>(a, row, st, used > 1 ? a.part + slot * part_floats<D, NW>() : nullptr);
+    end_rows<D, NW>(a, row, st, used > 1 ? a.part + slot * part_floats<D, kRows<NW>>() : nullptr);
 }
 
 // ------------------------------------------------------- joining the parts
-
-constexpr int kJoinRows = 8;   // lane groups (D / 4 lanes, a row's dimensions) of a joining workgroup
-
-struct RowSum {
-    float m, l;
-    at_f32x4 o;
-};
-__device__ __forceinline__ void add_part(RowSum& s, float m, float l, const at_f32x4& o) {
-    const float mn = fmaxf(s.m, m), f0 = __builtin_amdgcn_exp2f(s.m - mn), f1 = __builtin_amdgcn_exp2f(m - mn);
-    s.l = s.l * f0 + l * f1;
-    s.o = s.o * f0 + o * f1;
-    s.m = mn;
-}
-// Parts i0, i0 + step, .. below n of row `at` of a unit: part i at slot0
-// (i == 0) or slot1 + (i - 1) slot_step.
-template <int D, int NW>
-__device__ __forceinline__ RowSum sum_parts(const AttendArgs& a, int at, int i0, int step, int n, int64_t slot0,
-                                            int64_t slot1, int slot_step) {
-    const int lane = threadIdx.x % (D / 4);
-    RowSum s{kNoRef, 0.0f, at_f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll 4
-    for (int i = i0; i < n; i += step) {
-        const float* p = a.part + (i == 0 ? slot0 : slot1 + (int64_t)(i - 1) * slot_step) * part_floats<D, NW>();
-        add_part(s, p[kRows<NW> * D + at * 2], p[kRows<NW> * D + at * 2 + 1],
-                 *reinterpret_cast<const at_f32x4*>(p + at * D + 4 * lane));
-    }
-    return s;
-}
-template <int D>
-__device__ __forceinline__ void write_row(const AttendArgs& a, int64_t row, const RowSum& s) {
-    const float inv = s.l > 0.0f ? 1.0f / s.l : 0.0f;
-    *reinterpret_cast<at_u32x2*>(a.out + row * D + 4 * (threadIdx.x % (D / 4))) =
-        at_u32x2{pack_bf16(s.o[0] * inv, s.o[1] * inv), pack_bf16(s.o[2] * inv, s.o[3] * inv)};
-}
-// One row by all lane groups, each every kJoinRows-th part.
-template <int D, int NW>
-__device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t row, int at, int n, int64_t slot0, int64_t slot1,
-                                          int slot_step) {
-    __shared__ float s_ml[kJoinRows][2];
-    __shared__ float s_o[kJoinRows][D + 4];
-    const int grp = threadIdx.x / (D / 4), lane = threadIdx.x % (D / 4);
-    const RowSum s = sum_parts<D, NW>(a, at, grp, kJoinRows, n, slot0, slot1, slot_step);
-    __syncthreads();
-    *reinterpret_cast<at_f32x4*>(&s_o[grp][4 * lane]) = s.o;
-    if (lane == 0) s_ml[grp][0] = s.m, s_ml[grp][1] = s.l;
-    __syncthreads();
-    if (grp != 0 || row < 0) return;
-    RowSum all{kNoRef, 0.0f, at_f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
-    for (int w = 0; w < kJoinRows; ++w)
-        add_part(all, s_ml[w][0], s_ml[w][1], *reinterpret_cast<const at_f32x4*>(&s_o[w][4 * lane]));
-    write_row<D>(a, row, all);
-}
-
-// The workgroups (w, 0 .. kRows / kJoinRows - 1) stand for workgroup w of the
-// main launch: those of a cut unit's n workgroups share its rows, so that many
-// parts have many hands.
-template <int D, int NW>
-__global__ __launch_bounds__(kJoinRows * D / 4) void attend_tile_join_kernel(AttendArgs a) {
-    const int grp = threadIdx.x / (D / 4);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const Crossing x = reinterpret_cast<const Crossing*>(a.head)[2 * (int64_t)blockIdx.x + e];
-        if (x.n <= 1) continue;
-        // kRows rows over n * kRows / kJoinRows workgroups
-        const int id = x.i * gridDim.y + blockIdx.y;
-        const int r0 = id * kJoinRows / x.n, r1 = (id + 1) * kJoinRows / x.n;
-        const int64_t slot1 = 2 * (int64_t)x.behind;
-        if (x.n < kJoinRows) {
-            const int at = r0 + grp;
-            const int64_t row = at < r1 ? out_row(a, x.u, x.u.f0 + at) : -1;
-            if (row >= 0) write_row<D>(a, row, sum_parts<D, NW>(a, at, 0, 1, x.n, x.slot, slot1, 2));
-        } else if (r0 < r1) {   // one row
-            join_wide<D, NW>(a, out_row(a, x.u, x.u.f0 + r0), r0, x.n, x.slot, slot1, 2);
-        }
-    }
-}
 
 template <int D>
 __global__ __launch_bounds__(kJoinRows * D / 4) void attend_tile_list_join_kernel(AttendArgs a) {
@@ -968,15 +872,13 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attend_tile_list_join_kerne
     if (used <= 1) return;
     const int f = (t % a.group) * a.G + (head - h * a.G);
     const int64_t slot0 = (((int64_t)grp * ht + f / kRows<NW>) * a.c.Hkv + h) * a.splits;
-    join_wide<D, NW>(a, r, f % kRows<NW>, used, slot0, slot0 + 1, 1);
+    join_wide<D, kRows<NW>>(a, r, f % kRows<NW>, used, slot0, slot0 + 1, 1);
 }
 
 template <int D, int NW>
 hipError_t launch_dense(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
     attend_tile_kernel<D, NW><<<(unsigned)p.blocks, 64 * NW, 2 * kStageBytes<D>, st>>>(a);
-    if (p.join)
-        attend_tile_join_kernel<D, NW>
-            <<<dim3((unsigned)p.blocks, kRows<NW> / kJoinRows), kJoinRows * D / 4, 0, st>>>(a);
+    if (p.join) launch_join<D, kRows<NW>>(p, a, st);
     return hipGetLastError();
 }
 
@@ -1009,15 +911,15 @@ AttendPlan attend_tile_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, 
     p.tile = true;
     const int G = Hq / Hkv;
     if (kind == LTK_ATTEND) {
-        // 256 rows a workgroup, one on a CU, where the sequences fill them
-        p.waves = (int64_t)T * G >= kWide * (int64_t)std::max(n_seq, 1) ? 8 : 4;
+        const bool wide = (int64_t)T * G >= kWide * (int64_t)std::max(n_seq, 1) && (double)T * Hq * (double)entries >= (double)kWideWork;
+        p.waves = wide ? 8 : 4;
         const int rows = 32 * p.waves;
         const int64_t units = ((int64_t)T * G / rows + n_seq) * Hkv;
         const int64_t most = (units * (entries + kKeys + kUnitKeys) + kMinKeys - 1) / kMinKeys;
         // eight waves a CU; whole rounds of the XCDs
         p.blocks = (std::max<int64_t>(1, std::min<int64_t>(most, 2048 / p.waves)) + 7) / 8 * 8;
         p.join = true;
-        p.head_bytes = (2 * sizeof(Crossing) * (size_t)p.blocks + 255) / 256 * 256;
+        p.head_bytes = crossing_bytes(p.blocks);
         p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * rows * (D + 2) * sizeof(float) : 0);
         return p;
     }
