@@ -1,0 +1,208 @@
+"""The paged e4m3 cache's attention where work is cut, joined and planned on
+the device: many sequences, many parts of one unit, tables shorter than the
+sequences, shared pages, captured calls, and the sparse step as a whole."""
+import pytest
+
+from tests.attend_ref import make_batch, make_cache, poison, ref_append, ref_attend, ref_packed
+from tests.gpu_util import say
+from tests.test_gpu_attend import _attend_case, _dev, _gen, _lists, _within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B,rows,G,Hkv,max_pages", [
+    (600, [0, 1, 2], 4, 2, 4),         # few rows a sequence
+    (300, [0, 3, 9], 16, 1, 4),        # more than 64 a head: units of 128
+    (560, [4, 0, 8, 4, 4], 64, 1, 24),   # 256 a head: units of 256
+])
+def test_more_sequences_than_one_look(lib, B, rows, G, Hkv, max_pages):
+    """Batches whose sequences the kernels look at in several portions, empty ones among them."""
+    import torch
+    rows = [rows[b % len(rows)] for b in range(B)]
+    lens = [r + (7 * b) % 41 for b, r in enumerate(rows)]
+    say("sequences", B, sum(rows), G, Hkv)
+    g = _gen(61)
+    table, cu, n, pages = make_batch(g, rows, lens, 16, max_pages=max_pages)
+    cache = make_cache(g, pages, Hkv, 16, 64)
+    poison(cache, table, lens, 16)
+    q = torch.randn(sum(rows), Hkv * G, 64, generator=g).bfloat16()
+    a = (q.cuda(), _dev(*cache), *_dev(table, cu, n))
+    out = lib.attend(*a)
+    ref, tol, _ = ref_attend(q, cache, table, cu, n, 0.125)
+    _within(out, ref, tol, f"{B} sequences")
+    assert torch.equal(out, lib.attend(*a))
+    idx = _lists(_gen(62), rows, lens, 20)
+    ref, tol, _ = ref_attend(q, cache, table, cu, n, 0.125, idx=idx)
+    _within(lib.attend_selected(*a, idx.cuda()), ref, tol, f"{B} sequences, selected")
+
+
+@pytest.mark.parametrize("T,L,G,D,window,sinks", [
+    (1, 20000, 4, 64, 0, 0), (1, 20000, 20, 128, 0, 0), (20, 20000, 8, 64, 0, 0), (70, 9000, 4, 128, 0, 0),
+    (40, 9000, 8, 128, 5000, 33), (1, 20000, 3, 128, 9000, 7),
+])
+def test_one_unit_in_many_parts(lib, T, L, G, D, window, sinks):
+    import torch
+    say("parts", T, L, G, D, window, sinks)
+    cache, table, cu, n, q = _attend_case([T], [L], 1, G, 64, D, 63)
+    a = (q.cuda(), _dev(*cache), *_dev(table, cu, n))
+    out = lib.attend(*a, window=window, n_sink=sinks)
+    ref, tol, _ = ref_attend(q, cache, table, cu, n, D ** -0.5, window, sinks)
+    _within(out, ref, tol, "parts")
+    assert torch.equal(out, lib.attend(*a, window=window, n_sink=sinks))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [576, 16384])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 5), (3, 70)])
+def test_chunks_over_holes_and_short_tables(lib, D, cap, window, sinks):
+    """Many rows: pages missing in the middle, tokens past the table or a table far wider than the tokens (units of 128
+    and of 256 rows), freed pages before the window, rows before cu[0] and behind cu[B]."""
+    import torch
+    page, Hkv, G = 16, 2, 8
+    rows, lens = [260, 0, 77], [700, 5, 500]
+    g = _gen(64)
+    table, cu, n, pages = make_batch(g, rows, lens, page, max_pages=cap // page)
+    table[0, 7], table[0, 20:22], table[2, 3] = -1, torch.tensor([pages, 2 ** 31 - 1]).int(), -2 ** 31
+    if window:
+        table[0, 5:15] = -5              # positions 80 .. 239: behind every row's window (and the sinks)
+    cache = make_cache(g, pages, Hkv, page, D)
+    poison(cache, table, lens, page)
+    T = sum(rows) + 5
+    q = torch.randn(T, Hkv * G, D, generator=g).bfloat16()
+    cu = cu + 2
+    out = torch.full((T, Hkv * G, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    say("chunk", D, cap, window, sinks)
+    lib.attend(q.cuda(), _dev(*cache), *_dev(table, cu, n), window=window, n_sink=sinks, out=out)
+    ref, tol, written = ref_attend(q, cache, table, cu, n, D ** -0.5, window, sinks)
+    assert bool((out.cpu()[~written] == 9).all()) and int(written.sum()) == 337
+    _within(out.cpu()[written], ref[written], tol[written], "chunk")
+
+
+def test_scales_and_sharp_softmax_of_chunks(lib):
+    """Many rows with scales that are no powers of two, scores in the hundreds, and value scales far apart."""
+    import torch
+    for D, pow2, qs in ((64, False, 60.0), (128, True, 40.0)):
+        cache, table, cu, n, q = _attend_case([150], [400], 2, 4, 16, D, 65, pow2, qs)
+        cache[3][table[0].long()] *= torch.exp2(torch.linspace(-40, 40, 25).round())[:, None]
+        out = lib.attend(q.cuda(), _dev(*cache), *_dev(table, cu, n), window=300, n_sink=2)
+        ref, tol, _ = ref_attend(q, cache, table, cu, n, D ** -0.5, 300, 2)
+        _within(out, ref, tol, f"D {D}")
+
+
+def test_shared_pages_and_equal_sequences(lib):
+    """Two sequences that share their first pages, and two that are the same."""
+    import torch
+    page, D, Hkv, G = 32, 128, 2, 4
+    g = _gen(66)
+    table, cu, n, pages = make_batch(g, [3, 90, 90], [200, 190, 190], page)
+    table[1, :3] = table[0, :3]
+    table[2] = table[1]
+    cache = make_cache(g, pages, Hkv, page, D)
+    q = torch.randn(183, Hkv * G, D, generator=g).bfloat16()
+    q[93:] = q[3:93]
+    out = lib.attend(q.cuda(), _dev(*cache), *_dev(table, cu, n))
+    ref, tol, _ = ref_attend(q, cache, table, cu, n, D ** -0.5)
+    _within(out, ref, tol, "shared")
+
+
+def test_one_workspace_for_calls_of_many_kinds(lib):
+    """A workspace used by calls of other kinds and sizes before, on one stream, as it is left."""
+    import torch
+    import indexer_topk_long_amd as ltk
+    g = _gen(67)
+    cases = [([1], [9000], 1, 4, 64, 128), ([200], [900], 2, 8, 64, 128), ([1, 1], [50, 3000], 2, 2, 64, 64),
+             ([300], [300], 1, 8, 64, 64)]
+    built = [_attend_case(*c, seed=68 + i) for i, c in enumerate(cases)]
+    need = max(ltk.attend_workspace_bytes(0, q.shape[0], q.shape[1], c[0].shape[1], q.shape[2], table.shape[0],
+                                          table.shape[1] * 64) for c, table, cu, n, q in built)
+    ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda")
+    args = [(q.cuda(), _dev(*c), *_dev(t, cu, n)) for c, t, cu, n, q in built]
+    want = [lib.attend(*a) for a in args]
+    graphs = []
+    for a in args:      # captured over the same workspace
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            o = lib.attend(*a, workspace=ws)
+        graphs.append((gr, o))
+    for turn in range(3):
+        for i in (0, 1, 2, 3, 1, 0, 3, 2):
+            assert torch.equal(lib.attend(*args[i], workspace=ws), want[i]), (turn, i)
+            graphs[i][1].zero_()
+            graphs[i][0].replay()
+            assert torch.equal(graphs[i][1], want[i]), (turn, i)
+
+
+def test_chunk_and_packed_captured_and_replayed(lib):
+    """Lengths, rows' starts, lists and their lengths change in place between replays."""
+    import torch
+    g = _gen(69)
+    page, D, Hkv, G, T, group, cap = 16, 64, 2, 8, 64, 16, 300
+    table, _, _, pages = make_batch(g, [T], [900], page)
+    cache = make_cache(g, pages, Hkv, page, D)
+    dc, dt = _dev(*cache), table.cuda()
+    q = torch.randn(T, Hkv * G, D, generator=g).bfloat16().cuda()
+    cu, n = torch.tensor([0, T]).int().cuda(), torch.tensor([T]).int().cuda()
+    shared = torch.zeros(4, cap, dtype=torch.int32, device="cuda")
+    masks, lens = torch.zeros_like(shared).view(torch.uint32), torch.zeros(4, dtype=torch.int32, device="cuda")
+    run = lambda: (lib.attend(q, dc, dt, cu, n, window=200, n_sink=3), lib.attend(q, dc, dt, cu, n),
+                   lib.attend_packed(q, dc, dt, n, shared, masks, lens, group))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run()
+    for i, L in enumerate((64, 900, 333, 10, 512)):
+        n.fill_(L)
+        cu.copy_(torch.tensor([i, T - i]).int())
+        shared.copy_(torch.stack([torch.randperm(900, generator=g)[:cap] for _ in range(4)]).int())
+        masks.view(torch.int32).copy_(torch.randint(0, 1 << 16, (4, cap), generator=g).int())
+        lens.copy_(torch.tensor([cap, 0, 1, 37 * i]).int())
+        for o in outs:
+            o.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        want = run()
+        torch.cuda.synchronize()
+        for o, w, sl in zip(got, want, (slice(i, T - i), slice(i, T - i), slice(0, T))):
+            assert torch.equal(o[sl], w[sl]), i
+        ref, tol, written = ref_attend(q.cpu(), cache, table, cu.cpu(), n.cpu(), 0.125)
+        _within(got[1].cpu()[written], ref[written], tol[written], f"length {L}")
+        ref, tol = ref_packed(q.cpu(), cache, table, n.cpu(), shared.cpu(), masks.cpu(), lens.cpu(), group, 0.125)
+        _within(got[2], ref, tol, f"packed, length {L}")
+
+
+@pytest.mark.parametrize("T,Hkv,topk", [(0, 2, 40), (1, 2, 40), (9, 1, 64), (520, 4, 100), (700, 2, 33)])
+def test_sparse_step(lib, T, Hkv, topk):
+    """Append, select and attend in one call, on a stream of its own: few rows on their own lists, long chunks packed."""
+    import torch
+    import indexer_topk_long_amd as ltk
+    g = _gen(70)
+    page, D, G, L, H = 32, 64, 2, 900, 4
+    table, cu, n, pages = make_batch(g, [T], [L], page)
+    cache = make_cache(g, pages, Hkv, page, D)
+    k, v = (torch.randn(T, Hkv, D, generator=g).bfloat16() for _ in range(2))
+    q = torch.randn(T, Hkv * G, D, generator=g).bfloat16()
+    f = 10000.0 ** (-torch.arange(32, dtype=torch.float64) / 32)
+    iq, ik = torch.randn(T, H, D, generator=g).bfloat16(), torch.randn(L, D, generator=g).bfloat16()
+    w = torch.rand(T, H, generator=g)
+    want = ref_append(k, v, cache, table, cu, n, f, False)
+    dc = _dev(*cache)
+    dev = _dev(q, k, v, table, n, iq, ik, w, f)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out, idx = ltk.sparse_step(dev[0], dev[1], dev[2], dc, dev[3], dev[4], dev[5], dev[6], dev[7], topk, inv_freq=dev[8])
+    side.synchronize()
+    assert out.shape == q.shape and idx.shape == (T, topk)
+    for a, b in zip(dc, want):
+        assert torch.equal(a.cpu().view(torch.uint8), b.view(torch.uint8))
+    if T == 0:
+        return
+    pos = torch.arange(L - T, L, dtype=torch.int32, device="cuda")
+    assert torch.equal(idx.sort(1)[0], ltk.score_select(dev[5], dev[6], dev[7], pos, topk).sort(1)[0])
+    qr = lib.kv_append(dev[1], dev[2], dc, dev[3], *_dev(cu, n, f), q=dev[0]).cpu()   # the same rows again: the same cache
+    ref, tol, _ = ref_attend(qr, want, table, cu, n, D ** -0.5, idx=idx.cpu())
+    _within(out, ref, tol, f"{T} rows")
