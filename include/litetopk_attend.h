@@ -26,7 +26,15 @@
  *  - rows outside every sequence (at or past cu[n_seq]) are not written;
  *  - a list entry outside [0, kv_len) or after the row's position is no key.
  * Bytes and scales that hold no key of the sequence may be anything (NaN
- * included); everything else must be finite, scales also normal and > 0.
+ * included); everything else must be finite, scales also within
+ * 2^-100 .. 2^100.
+ *
+ * Sums, softmax statistics and partial rows are fp32, products of bf16 and
+ * fp16 operands (the cache's bytes convert exactly).  A key's weight times its
+ * value scale is rounded to fp16 relative to the row's largest such product:
+ * 2^-11 of itself, or 2^-25 of the largest where it is below fp16's normal
+ * range (2^-14 of it).  Results do not depend on timing: the same call gives
+ * the same bits.
  */
 #ifndef LITETOPK_ATTEND_H
 #define LITETOPK_ATTEND_H
@@ -107,7 +115,7 @@ size_t litetopk_attend_workspace_bytes(int32_t kind, int32_t T, int32_t Hq, int3
  * window > 0 only those with s > p - window or s < n_sink.
  *
  *  q, out  [T, Hq, head_dim] bf16, Hq a multiple of n_kv_heads
- *  scale   finite
+ *  scale   finite, also times log2(e)
  *  window  >= 0 (0: no window); n_sink >= 0 (no effect without a window) */
 int litetopk_attend(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void* q, int32_t T, int32_t Hq,
                     float scale, int32_t window, int32_t n_sink, void* out, void* ws, size_t ws_bytes, void* stream);

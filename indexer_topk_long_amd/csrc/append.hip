@@ -342,7 +342,9 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& bt, int D, const ui
     a.Hq = Hq;
     a.rot = rot;
     a.interleaved = interleaved;
-    a.units = (int)unit_bound(bt.n_seq, T, 1, 1 << c.page_shift, 2);
+    const int64_t units = unit_bound(bt.n_seq, T, 1, 1 << c.page_shift, 2);
+    if (units > 0x7fffffff) return hipErrorInvalidValue;
+    a.units = (int)units;
     // a thread's sines serve up to 8 heads while the threads left still fill the
     // card (append-chunk-8k: 107 us with 1, 83 with 2, 76 with 4, 74 with 8, 80
     // with 16; append-decode-batch: 10.0 us with 1, 12.3 with 8)

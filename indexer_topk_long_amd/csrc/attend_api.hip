@@ -51,7 +51,6 @@ int attend_args(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void
     int st = check_cache(cache, batch, T, need_cu, a.c, a.bt);
     if (st != LTK_OK) return st;
     if ((st = check_heads(T, Hq, cache->n_kv_heads)) != LTK_OK) return st;
-    if (!isfinite(scale)) return LTK_EINVAL;
     if (T > 0 && (!q || !out || !ws)) return LTK_EINVAL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return LTK_EINVAL;
     a.q = static_cast<const uint16_t*>(q);
@@ -60,7 +59,7 @@ int attend_args(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void
     a.Hq = Hq;
     a.G = Hq / cache->n_kv_heads;
     a.c2 = scale * 1.4426950408889634f;
-    return LTK_OK;
+    return isfinite(a.c2) ? LTK_OK : LTK_EINVAL;
 }
 
 }  // namespace

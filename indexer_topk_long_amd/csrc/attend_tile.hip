@@ -425,7 +425,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     const int pos_lo = sr.pos0 + uniform(fw / a.G), pos_hi = sr.pos0 + uniform((max(fw1, 1) - 1) / a.G);
     const int64_t row = out_row(a, u, fw + c);
     const int pos = row < 0 ? -1 : sr.pos0 + (fw + c) / a.G;
-    const int from = a.window > 0 ? max(pos, 0) - a.window : -1;   // the lane's row sees keys behind it, and the sinks
+    const int from = a.window > 0 ? max(max(pos, 0) - a.window, -1) : -1;   // the lane's row sees keys behind it, and the sinks
     at_bf16x8 q[D / 16];
     WaveState<D> st;
     begin_rows<D>(a, row, q, st);

@@ -192,3 +192,8 @@ def test_binding_refuses_what_the_kernels_could_not_read():
         ltk.attend(q, (k.float(), k, s, s), table, cu, n)
     with pytest.raises(ValueError, match=r"cache k must be"):
         ltk.attend(q, (k[0], k, s, s), table, cu, n)
+
+
+@pytest.mark.parametrize("kind", ["attend", "selected", "packed"])
+def test_a_score_scale_that_overflows_in_base_2_is_refused(kind):
+    assert _attend(kind, scale=3.0e38) == EINVAL
