@@ -18,6 +18,12 @@
 // rows of the call that fall into the page), so the page's largest magnitude
 // is a workgroup reduction and each row is read once, kept in registers and
 // written once.  The workgroups behind those rotate the queries.
+//
+// Bound by the bytes where rows are many: 8,192 rows of 64 query and 8
+// key/value heads, D = 128 (319 MB read and written) take 77 us, 4.1 TB/s of
+// the 5.0 that a large copy reaches.  Bound by the chain page id, scale, sines,
+// reduction, store where they are few: one row takes 4.6 us, 96 rows of as many
+// sequences 8 us.
 #include <algorithm>
 
 #include "attend.hpp"
@@ -151,8 +157,8 @@ __device__ __forceinline__ void rotate_item(float (&lo)[VEC], float (&hi)[VEC], 
 
 // With few rows (decode) a page's items keep 8 threads a row busy, each with
 // VEC sines in turn: then all threads form the rows' sines together, through
-// LDS (append-decode-batch, 96 rows: 10.1 -> 6.4 us; more rows fill the
-// threads as they are).
+// LDS (96 sequences of one row, 32 query heads, pages of 16: 10.1 -> 8 us; more
+// rows fill the threads as they are).
 constexpr int kShareRows = 4;
 
 // One page, one key/value head, keys or values.  NT threads, NI items each:
@@ -346,8 +352,8 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& bt, int D, const ui
     if (units > 0x7fffffff) return hipErrorInvalidValue;
     a.units = (int)units;
     // a thread's sines serve up to 8 heads while the threads left still fill the
-    // card (append-chunk-8k: 107 us with 1, 83 with 2, 76 with 4, 74 with 8, 80
-    // with 16; append-decode-batch: 10.0 us with 1, 12.3 with 8)
+    // card (8,192 rows of 64 heads, D = 128: 107 us with 1, 83 with 2, 76 with 4,
+    // 74 with 8, 80 with 16; 96 rows of 32 heads: 10.0 us with 1, 12.3 with 8)
     a.heads_per = 1;
     while (a.heads_per < 8 && (int64_t)T * Hq * (D / 16) / (2 * a.heads_per) >= 1 << 18) a.heads_per *= 2;
     // rot / 2 (half-split pairs) and rot (the border) in whole vectors

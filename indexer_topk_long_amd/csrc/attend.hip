@@ -24,6 +24,18 @@
 // Softmax statistics stay in the lane: m moves only when a score passes it by
 // 8, so most tiles need no exchange between lanes; the weights' sums of the
 // four lane groups are joined once at the end.
+//
+// Two tiles a wave, one in use and one on its way: 8 KB a tile at D = 128, and
+// with two waves a SIMD 64 KB a CU on their way, which covers the latency of
+// memory.  64 decoding sequences of up to 16,384 tokens (64 heads on 8, D = 128,
+// 1.11 GB of cache) take 207 us, 5.4 TB/s, as a stream of reads would; the join
+// adds 6.  Eight rows over 1,048,576 tokens (2.15 GB) take 500 to 540 us, 4.0 to
+// 4.3 TB/s: each byte is converted for two units of 32 rows, and conversions,
+// exponentials and matrix instructions fill the issue slots.  145 rows on lists
+// of 2,048 keys each (four key/value heads) take 54 us, 4.9 TB/s of the lists'
+// keys.  The smallest calls
+// (one row, 4,096 tokens) take 6.6 us and 3.9 for the join: launches and the
+// chain length, page id, keys, values.
 #include <algorithm>
 
 #include "attend_join.hpp"
@@ -236,6 +248,9 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
     }
 }
 
+// Two waves hold the registers of a tile on its way beside one in use; 64
+// dimensions and 16 rows fit three.  (Three at D = 128 and 16 rows spilled: 64
+// decoding sequences of up to 16,384 tokens 264 against 218 us.)
 template <int D, int MT>
 constexpr int waves_per_simd() {
     return MT == 1 && D == 64 ? 3 : 2;
@@ -779,9 +794,9 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
     const size_t part = (size_t)(D + 2) * 16 * sizeof(float);   // of 16 rows
     if (kind == LTK_ATTEND) {
         // Rows that share keys: 16 or 32 to a unit.  (64 rows in one unit read
-        // the cache once but leave one wave on a SIMD: attend-specdecode-1m took
-        // 529 us so, and 507 us as two units of 32 whose ranges run side by side
-        // and meet in L2; with units of 16, 760 us.)
+        // the cache once but leave one wave on a SIMD: eight rows of 64 heads on
+        // 8 over 1,048,576 tokens took 529 us so, and 507 us as two units of 32
+        // whose ranges run side by side and meet in L2; with units of 16, 760.)
         p.mt = (int64_t)T * G > 16 * (int64_t)std::max(n_seq, 1) ? 2 : 1;
         // one range of key tiles a workgroup
         const int64_t units = ((int64_t)T * G / (16 * p.mt) + n_seq) * Hkv, tiles = (entries + kTile - 1) / kTile;
@@ -795,8 +810,8 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
     p.mt = G > 16 ? 2 : 1;
     const int64_t units = (int64_t)T * ((G + 16 * p.mt - 1) / (16 * p.mt)) * Hkv;
     // Lists are cut only while the units leave CUs with less than two workgroups,
-    // each part at least one 32-key tile a wave (selected-specdecode-batch, 580
-    // units: 54 us whole, 68 us cut in two and joined).
+    // each part at least one 32-key tile a wave (580 units of 2,048 keys,
+    // D = 128: 54 us whole, 68 us cut in two and joined).
     const int64_t most = std::max<int64_t>(1, (entries + kTile * kWaves - 1) / (kTile * kWaves));
     p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, 512 / std::max<int64_t>(units, 1)));
     p.blocks = units * p.splits;
