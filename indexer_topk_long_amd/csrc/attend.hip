@@ -251,10 +251,7 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
 // Two waves hold the registers of a tile on its way beside one in use; 64
 // dimensions and 16 rows fit three.  (Three at D = 128 and 16 rows spilled: 64
 // decoding sequences of up to 16,384 tokens 264 against 218 us.)
-template <int D, int MT>
-constexpr int waves_per_simd() {
-    return MT == 1 && D == 64 ? 3 : 2;
-}
+constexpr int waves_per_simd(int D, int MT) { return MT == 1 && D == 64 ? 3 : 2; }
 
 template <int D, int MT>
 constexpr size_t finish_lds() {
@@ -499,7 +496,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 }
 
 template <int D, int MT>
-__global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_kernel(AttendArgs a) {
     extern __shared__ float sh[];
     __shared__ PlanLds ls;
     __shared__ Place place;
@@ -581,7 +578,7 @@ struct ListLds {
 // 16 MT heads); its list is idx[row], or with PACKED the entries of the row's
 // group whose mask holds the row's bit.
 template <int D, int MT, bool PACKED>
-__global__ __launch_bounds__(64 * kWaves, (waves_per_simd<D, MT>())) void attend_list_kernel(AttendArgs a) {
+__global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_list_kernel(AttendArgs a) {
     extern __shared__ float sh[];
     ListLds& ls = *reinterpret_cast<ListLds*>(sh);
     __shared__ int s_cnt[kWaves];
@@ -798,10 +795,14 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
         // 8 over 1,048,576 tokens took 529 us so, and 507 us as two units of 32
         // whose ranges run side by side and meet in L2; with units of 16, 760.)
         p.mt = (int64_t)T * G > 16 * (int64_t)std::max(n_seq, 1) ? 2 : 1;
-        // one range of key tiles a workgroup
+        // One range of key tiles a workgroup, and as many workgroups as run at
+        // once.  (64 heads on 8, D = 128, twice as many against that: one row
+        // over 65,536 tokens 37 against 33 us, 16 rows of as many sequences of up
+        // to 4,096 30 against 25, 256 rows 223 against 215; D = 64, 200 rows of 32
+        // heads, sequences of up to 3,000: 1,024 workgroups 81 us, 768 69, 512 76.)
         const int64_t units = ((int64_t)T * G / (16 * p.mt) + n_seq) * Hkv, tiles = (entries + kTile - 1) / kTile;
         const int64_t most = (units * (tiles + kUnitTiles) + kMinPer - 1) / kMinPer;
-        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, p.mt == 2 ? 512 : 1024));
+        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, 256 * waves_per_simd(D, p.mt)));
         p.join = p.blocks > 1;
         p.head_bytes = crossing_bytes(p.blocks);
         p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * p.mt * part : 0);
