@@ -135,7 +135,7 @@ int litetopk_attend_selected(const ltk_kv_cache* cache, const ltk_kv_batch* batc
  *  shared  [ceil(T / group), cap] int32 distinct positions per group
  *  masks   [ceil(T / group), cap] uint32; lens [ceil(T / group)] int32
  *          (clamped to [0, cap])
- *  group   1 .. 32; cap 1 .. 2^26 */
+ *  group   1 .. 32, group * Hq / n_kv_heads <= 2^30; cap 1 .. 2^26 */
 int litetopk_attend_packed(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void* q, int32_t T,
                            int32_t Hq, const int32_t* shared, const uint32_t* masks, const int32_t* lens,
                            int32_t group, int32_t cap, float scale, void* out, void* ws, size_t ws_bytes,

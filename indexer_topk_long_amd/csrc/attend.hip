@@ -1,6 +1,6 @@
 // attend.hip -- attention over the paged e4m3 cache for few rows per key on
-// gfx950 (decode, speculative decode, selected keys): bound by reading the
-// cache once.
+// gfx950 (decode, speculative decode, selected keys, packed groups of few
+// rows): bound by reading the cache once.
 //
 // For a query row q and the keys s it sees, with page scales ks and vs,
 //   y_s = scale log2(e) ks (q . k_s) + log2(vs)
@@ -104,14 +104,14 @@ __device__ __forceinline__ void value_operands(const KvTile<D>& t, int w, at_f16
 }
 
 // One 32-key tile against MT x 16 query rows.  query(mt, j) is operand j of
-// row tile mt; mask(mt, key) says whether the lane's row of tile mt sees key
-// (0..31) of the tile, asked only where `masked` (the same in all lanes).
+// row tile mt; mask(mt, a, i) says whether the lane's row of tile mt sees key
+// 16 a + 4 g + i of the tile, asked only where `masked` (the same in all lanes).
 //
 // The scheduling barriers keep the parts apart: left alone, the compiler
 // converts all of a tile's bytes first and holds 64 registers of operands.
 template <int D, int MT, class Query, class Scale, class Mask>
 __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const Scale (&hs)[2], RowState<D> (&st)[MT],
-                                          bool masked, int g, Mask mask) {
+                                          bool masked, Mask mask) {
     at_f32x4 s[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -139,7 +139,7 @@ __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const
 #pragma unroll
             for (int a = 0; a < 2; ++a)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[4 * a + i] = mask(mt, 16 * a + 4 * g + i) ? y[4 * a + i] : -INFINITY;
+                for (int i = 0; i < 4; ++i) y[4 * a + i] = mask(mt, a, i) ? y[4 * a + i] : -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
@@ -466,10 +466,10 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
                     for (int j = 0; j < D / 64; ++j) t.v[4 * x + i][j] = ok ? t.v[4 * x + i][j] : 0u;
                 }
         }
-        tile_step<D, MT>(t, query, hs, st, !whole, g, [&](int mt, int k) {
-            const int key = w.key0 + k;
+        tile_step<D, MT>(t, query, hs, st, !whole, [&](int mt, int x, int i) {
+            const int key = w.key0 + 16 * x + 4 * g + i;
             const int from = a.window > 0 ? max(pos[mt], 0) - a.window : -1;
-            return ((k < 16 ? w.pid[0] : w.pid[1]) >= 0) & (key <= pos[mt]) & (key < kr.hi) &
+            return (w.pid[x] >= 0) & (key <= pos[mt]) & (key < kr.hi) &
                    ((key > from) | (key < a.n_sink));
         });
     };
@@ -565,59 +565,71 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_k
     }
 }
 
-// --------------------------------------------------- listed keys (one row)
+// ------------------------------------------------------------ listed keys
 
-// One entry of the staged list: row of the cache for the unit's head, and the
-// constants of its page.
+// Entries of the staged list: rows of the cache for the unit's head, the
+// constants of their pages, and (packed) the group's rows that see them.
 struct ListLds {
     int32_t row[kListChunk];
     float c[kListChunk], lv[kListChunk], iv[kListChunk];
+    uint32_t mask[kListChunk];
 };
 
-// A unit is one row of the call (all heads of one key/value head, in tiles of
-// 16 MT heads); its list is idx[row], or with PACKED the entries of the row's
-// group whose mask holds the row's bit.
+// (row, head) pairs of a group that share a list, and the units of 16 MT they
+// make: a group is one row with a list of its own, or `group` rows of a packed
+// list.
+__host__ __device__ __forceinline__ int list_tiles(int group, int G, int RT) { return (group * G + RT - 1) / RT; }
+
+// A unit is 16 MT (row, head) pairs of one group and key/value head, flattened
+// as elsewhere; its list is idx[row], or with PACKED the group's entries that
+// one of the unit's rows sees.
 template <int D, int MT, bool PACKED>
 __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_list_kernel(AttendArgs a) {
     extern __shared__ float sh[];
     ListLds& ls = *reinterpret_cast<ListLds*>(sh);
     __shared__ int s_cnt[kWaves];
     constexpr int RT = 16 * MT;
-    const int h = uniform((int)(blockIdx.x % a.c.Hkv));
+    const int group = PACKED ? a.group : 1;
+    UnitRows u;
+    u.h = uniform((int)(blockIdx.x % a.c.Hkv));
     int rest = uniform((int)(blockIdx.x / a.c.Hkv));
     const int split = uniform(rest % a.splits);
     rest = uniform(rest / a.splits);
-    const int ht = (a.G + RT - 1) / RT, tile = uniform(rest % ht), t = uniform(rest / ht);
-    int b = 0, pos;
+    const int ht = list_tiles(group, a.G, RT), tile = uniform(rest % ht), grp = uniform(rest / ht);
+    u.r0 = grp * group;
+    u.f0 = tile * RT;
+    u.f1 = min(u.f0 + RT, min(group, a.T - u.r0) * a.G);
+    if (u.f0 >= u.f1) return;
+    int b = 0, pos0;   // position of row u.r0
     if constexpr (PACKED) {
-        pos = max(a.bt.len[0], 0) - a.T + t;
+        pos0 = max(a.bt.len[0], 0) - a.T + u.r0;
     } else {
-        b = uniform(row_seq(a.bt, t, a.T));
+        b = uniform(row_seq(a.bt, u.r0, a.T));
         const SeqRows sr = seq_rows(a.bt, b, a.T);
-        if (t < sr.r0 || t >= sr.r1) return;
-        pos = sr.pos0 + (t - sr.r0);
+        if (u.r0 < sr.r0 || u.r0 >= sr.r1) return;
+        pos0 = sr.pos0 + (u.r0 - sr.r0);
     }
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int grp = PACKED ? uniform(t / a.group) : 0, bit = PACKED ? t - grp * a.group : 0;
-    const int32_t* list = a.list + (size_t)(PACKED ? grp : t) * a.cap;
+    const int32_t* list = a.list + (size_t)grp * a.cap;
     const uint32_t* masks = PACKED ? a.masks + (size_t)grp * a.cap : nullptr;
     const int n = PACKED ? min(max(a.lens[grp], 0), a.cap) : a.cap;
     const int per = uniform((n + a.splits - 1) / a.splits);
     const int e0 = split * per, e1 = min(e0 + per, n);
     if (split > 0 && e0 >= e1) return;
     const int used = max((n + per - 1) / max(per, 1), 1);
+    const int i0 = uniform(u.f0 / a.G), i1 = uniform((u.f1 - 1) / a.G);   // the unit's first and last row in the group
+    const uint32_t rows = (~0u << i0) & (~0u >> (31 - i1));
 
-    auto row_of = [&](int r) -> int64_t {
-        const int head = tile * RT + r;
-        return head < a.G ? (int64_t)t * a.Hq + h * a.G + head : -1;
-    };
+    auto row_of = [&](int r) -> int64_t { return out_row(a, u, u.f0 + r); };
     at_bf16x8 q[MT][D / 32];
     int64_t row[MT];
+    int qi[MT];   // the lane's row in the group
     RowState<D> st[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         row[mt] = row_of(mt * 16 + c);
+        qi[mt] = row[mt] < 0 ? 0 : (u.f0 + mt * 16 + c) / a.G;
         st[mt].m = 0.0f;
         st[mt].over = -INFINITY;
         st[mt].l = 0.0f;
@@ -628,7 +640,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
     auto query = [&](int mt, int j) { return q[mt][j]; };
     const int32_t* table = a.bt.table + (size_t)b * a.bt.max_pages;
     const int page = 1 << a.c.page_shift;
-    const int end = min(max(pos + 1, 0), a.bt.max_pages << a.c.page_shift);   // keys the row may see
+    const int end = min(max(pos0 + i1 + 1, 0), a.bt.max_pages << a.c.page_shift);   // keys the unit's rows may see
 
     auto load = [&](KvTile<D>& x, int at) {
 #pragma unroll
@@ -658,8 +670,16 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
             hs[z].lv_ = *reinterpret_cast<const at_f32x4*>(ls.lv + k);
             hs[z].iv_ = *reinterpret_cast<const at_f32x4*>(ls.iv + k);
         }
-        // (padded entries repeat the last key)
-        tile_step<D, MT>(x, query, hs, st, at + kTile > cnt, g, [&](int, int k) { return at + k < cnt; });
+        // (padded entries repeat the last key; packed, they have no rows; a unit of one row sees every other entry)
+        if constexpr (PACKED) {
+            const at_u32x4 m0 = *reinterpret_cast<const at_u32x4*>(ls.mask + at + 4 * g);
+            const at_u32x4 m1 = *reinterpret_cast<const at_u32x4*>(ls.mask + at + 16 + 4 * g);
+            tile_step<D, MT>(x, query, hs, st, i1 > i0 || at + kTile > cnt,
+                             [&](int mt, int z, int i) { return (((z == 0 ? m0 : m1)[i] >> qi[mt]) & 1u) != 0; });
+        } else {
+            tile_step<D, MT>(x, query, hs, st, at + kTile > cnt,
+                             [&](int, int z, int i) { return at + 16 * z + 4 * g + i < cnt; });
+        }
     };
 
     for (int c0 = e0; c0 < e1; c0 += kListChunk) {
@@ -670,9 +690,15 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
         for (int s0 = c0; s0 < c1; s0 += 64 * kWaves) {
             const int e = s0 + threadIdx.x;
             int s = -1;
+            uint32_t m = rows;
             if (e < c1) {
                 s = list[e];
-                if (PACKED && !((masks[e] >> bit) & 1u)) s = -1;
+                if constexpr (PACKED) {   // rows at or after the key only
+                    const int later = s - pos0;
+                    m &= masks[e];
+                    if (later > 0) m &= later < 32 ? ~0u << later : 0u;
+                    if (m == 0u) s = -1;
+                }
             }
             int pid = -1;
             if (s >= 0 && s < end) {
@@ -690,10 +716,11 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
             }
             if (pid >= 0) {
                 const int at = base + __popcll(have & ((1ull << lane) - 1ull));
-                const size_t pg = (size_t)pid * a.c.Hkv + h;
+                const size_t pg = (size_t)pid * a.c.Hkv + u.h;
                 ls.row[at] = (int)((pg << a.c.page_shift) + (s & (page - 1)));
                 const PageScale ps = page_scale(a.c2, a.c.ks[pg], a.c.vs[pg]);
                 ls.c[at] = ps.c_, ls.lv[at] = ps.lv_, ls.iv[at] = ps.iv_;
+                if constexpr (PACKED) ls.mask[at] = m;
             }
             __syncthreads();
         }
@@ -704,6 +731,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
             const int at = cnt + threadIdx.x;
             ls.row[at] = ls.row[cnt - 1];
             ls.c[at] = ls.c[cnt - 1], ls.lv[at] = ls.lv[cnt - 1], ls.iv[at] = ls.iv[cnt - 1];
+            ls.mask[at] = 0u;
         }
         __syncthreads();
         KvTile<D> ta, tb;
@@ -726,7 +754,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
         }
     }
     __syncthreads();   // the list is done with: finish() reuses its LDS
-    const int64_t slot = (((int64_t)t * ht + tile) * a.c.Hkv + h) * a.splits + split;
+    const int64_t slot = (((int64_t)grp * ht + tile) * a.c.Hkv + u.h) * a.splits + split;
     finish<D, MT>(a, st, sh, used > 1 ? a.part + slot * part_floats<D, 16 * MT>() : nullptr, row_of);
 }
 
@@ -741,12 +769,13 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attend_list_join_kernel(Att
     if constexpr (!PACKED) {
         if (t < cu_at(a.bt, 0, a.T) || t >= cu_at(a.bt, a.bt.n_seq, a.T)) return;
     }
-    const int ht = (a.G + RT - 1) / RT;
-    const int n = PACKED ? min(max(a.lens[t / a.group], 0), a.cap) : a.cap;
+    const int group = PACKED ? a.group : 1, grp = t / group, ht = list_tiles(group, a.G, RT);
+    const int n = PACKED ? min(max(a.lens[grp], 0), a.cap) : a.cap;
     const int per = (n + a.splits - 1) / a.splits, used = (n + per - 1) / max(per, 1);
     if (used <= 1) return;   // written by its only workgroup
-    const int64_t slot0 = (((int64_t)t * ht + g / RT) * a.c.Hkv + h) * a.splits;
-    join_wide<D, RT>(a, r, g % RT, used, slot0, slot0 + 1, 1);
+    const int f = (t - grp * group) * a.G + g;
+    const int64_t slot0 = (((int64_t)grp * ht + f / RT) * a.c.Hkv + h) * a.splits;
+    join_wide<D, RT>(a, r, f % RT, used, slot0, slot0 + 1, 1);
 }
 
 template <int KIND, int D, int MT>
@@ -780,13 +809,16 @@ hipError_t launch_kind(int D, const AttendPlan& p, const AttendArgs& a, hipStrea
 AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group) {
     AttendPlan p{};
     const int G = Hq / Hkv;
-    // The tile kernels from 65 rows a sequence and head, or four rows a group.
-    // (Hq 64, Hkv 8, D 128, against these kernels: one sequence of 131,072
-    // tokens, 64 rows 117 against 76 us, 96 rows 107 against 136, 512 rows 339
-    // against 399; 32 sequences of 2,048 tokens, 72 rows 67 against 99, 256 rows
-    // 91 against 250.  Packed, 512 rows of 1,024 keys: groups of two 217 against
-    // 159 us, of four 119 against 156, of 16 60 against 176.)
-    if (kind == LTK_ATTEND ? (int64_t)T * G > 64 * (int64_t)std::max(n_seq, 1) : kind == LTK_ATTEND_PACKED && group >= 4)
+    // The tile kernels from 65 rows a sequence and head, or 97 (row, head) pairs
+    // a group.  (Hq 64, Hkv 8, D 128, against these kernels: one sequence of
+    // 131,072 tokens, 64 rows 117 against 76 us, 96 rows 107 against 136, 512
+    // rows 339 against 399; 32 sequences of 2,048 tokens, 72 rows 67 against 99,
+    // 256 rows 91 against 250.  Packed, 512 rows of 1,024 keys, groups of four
+    // rows, 32 pairs, 116 against 59 us, of eight 75 against 66, of 12 89 against
+    // 74, of 16 97 against 85; 2,048 rows of 2,048 keys in groups of 16, 128
+    // pairs, 464 against 667; at D 64, 1,024 rows in groups of 16 80 against 97.)
+    if (kind == LTK_ATTEND ? (int64_t)T * G > 64 * (int64_t)std::max(n_seq, 1)
+                           : kind == LTK_ATTEND_PACKED && group * G > 96)
         return attend_tile_plan(kind, T, Hq, Hkv, D, n_seq, entries, group);
     const size_t part = (size_t)(D + 2) * 16 * sizeof(float);   // of 16 rows
     if (kind == LTK_ATTEND) {
@@ -808,8 +840,9 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
         p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * p.mt * part : 0);
         return p;
     }
-    p.mt = G > 16 ? 2 : 1;
-    const int64_t units = (int64_t)T * ((G + 16 * p.mt - 1) / (16 * p.mt)) * Hkv;
+    if (kind == LTK_ATTEND_SELECTED) group = 1;
+    p.mt = group * G > 16 ? 2 : 1;
+    const int64_t units = (int64_t)((T + group - 1) / group) * list_tiles(group, G, 16 * p.mt) * Hkv;
     // Lists are cut only while the units leave CUs with less than two workgroups,
     // each part at least one 32-key tile a wave (580 units of 2,048 keys,
     // D = 128: 54 us whole, 68 us cut in two and joined).

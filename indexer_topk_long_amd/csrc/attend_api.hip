@@ -34,6 +34,9 @@ int check_heads(int32_t T, int32_t Hq, int32_t Hkv) {
     return (int64_t)T * Hq > 0x7fffffff ? LTK_EINVAL : LTK_OK;
 }
 
+// A group's (row, head) pairs of a key/value head, which the kernels number.
+bool group_fits(int32_t group, int32_t Hq, int32_t Hkv) { return (int64_t)group * (Hq / Hkv) <= 1 << 30; }
+
 int run_attend(int kind, const ltk_kv_cache* cache, AttendArgs& a, int64_t entries, void* ws, size_t ws_bytes,
                void* stream) {
     const AttendPlan p = attend_plan(kind, a.T, a.Hq, a.c.Hkv, cache->head_dim, a.bt.n_seq, entries, a.group);
@@ -92,7 +95,7 @@ size_t litetopk_attend_workspace_bytes(int32_t kind, int32_t T, int32_t Hq, int3
                                        int32_t n_seq, int64_t entries, int32_t group) {
     if (kind < LTK_ATTEND || kind > LTK_ATTEND_PACKED || T < 0 || n_kv_heads < 1 || Hq < 1 || Hq % n_kv_heads != 0 ||
         n_seq < 0 || entries < 1 || entries > 0x7fffffff || (int64_t)T * Hq > 0x7fffffff ||
-        (head_dim != 64 && head_dim != 128) || (kind == LTK_ATTEND_PACKED && (group < 1 || group > 32)))
+        (head_dim != 64 && head_dim != 128) || (kind == LTK_ATTEND_PACKED && (group < 1 || group > 32 || !group_fits(group, Hq, n_kv_heads))))
         return 0;
     return attend_plan(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries, group).ws_bytes;
 }
@@ -128,6 +131,7 @@ int litetopk_attend_packed(const ltk_kv_cache* cache, const ltk_kv_batch* batch,
     const int st = attend_args(cache, batch, q, T, Hq, scale, out, ws, false, a);
     if (st != LTK_OK) return st;
     if (batch->n_seq != 1 || group < 1 || group > 32 || cap < 1 || cap > (1 << 26)) return LTK_EINVAL;
+    if (!group_fits(group, Hq, cache->n_kv_heads)) return LTK_EINVAL;
     if (T > 0 && (!shared || !masks || !lens)) return LTK_EINVAL;
     a.list = shared;
     a.masks = masks;

@@ -197,3 +197,9 @@ def test_binding_refuses_what_the_kernels_could_not_read():
 @pytest.mark.parametrize("kind", ["attend", "selected", "packed"])
 def test_a_score_scale_that_overflows_in_base_2_is_refused(kind):
     assert _attend(kind, scale=3.0e38) == EINVAL
+
+
+def test_a_group_of_more_pairs_than_are_numbered_is_refused():
+    assert _attend("packed", n_seq=1, T=1, Hq=1 << 28, group=32) == EINVAL
+    with pytest.raises(ltk.LtkError):
+        ltk.attend_workspace_bytes(2, 1, 1 << 28, 4, 128, 1, 64, 32)

@@ -174,6 +174,33 @@ def test_chunk_and_packed_captured_and_replayed(lib):
         _within(got[2], ref, tol, f"packed, length {L}")
 
 
+@pytest.mark.parametrize("G,group,D", [(1, 32, 64), (5, 7, 128), (4, 24, 64), (7, 14, 128), (12, 9, 64), (16, 8, 128),
+                                       (3, 32, 128), (40, 2, 64)])
+def test_packed_groups_over_odd_lists(lib, G, group, D):
+    """Groups of few and of many (row, head) pairs, the last one not full: holes in the table, keys after some rows of a
+    group, repeated entries, lengths past cap, bits of rows that are not there, rows that select nothing, long lists."""
+    import torch
+    T, L, cap = 3 * group - 1, 2600, 2500
+    cache, table, cu, n, q = _attend_case([T], [L], 2, G, 16, D, 71)
+    table[0, 4], table[0, 100] = -1, 2 ** 31 - 1
+    poison(cache, torch.where(table == 2 ** 31 - 1, -1, table), [L], 16)
+    g = _gen(72)
+    shared = torch.stack([torch.randperm(L + 20, generator=g)[:cap] for _ in range(3)]).int()
+    shared[:, 5], shared[1, 9], shared[2, 11] = -3, 2 ** 31 - 1, shared[2, 10]
+    shared[:, 40:40 + T // 2] = torch.arange(L - T, L - T + T // 2).int()      # the rows themselves
+    masks = torch.randint(0, 1 << 32, (3, cap), generator=g)
+    masks[0] &= ~1                                  # the first row selects nothing
+    masks = masks.to(torch.uint32)
+    lens = torch.tensor([cap + 50, 33, cap]).int()
+    a = (q.cuda(), _dev(*cache), *_dev(table, n, shared, masks, lens), group)
+    say("packed", G, group, D)
+    out = lib.attend_packed(*a)
+    ref, tol = ref_packed(q, cache, table, n, shared, masks, lens, group, D ** -0.5)
+    assert bool((out[0] == 0).all())
+    _within(out, ref, tol, "odd lists")
+    assert torch.equal(out, lib.attend_packed(*a))
+
+
 @pytest.mark.parametrize("T,Hkv,topk", [(0, 2, 40), (1, 2, 40), (9, 1, 64), (520, 4, 100), (700, 2, 33)])
 def test_sparse_step(lib, T, Hkv, topk):
     """Append, select and attend in one call, on a stream of its own: few rows on their own lists, long chunks packed."""
