@@ -817,7 +817,14 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
     // rows, 32 pairs, 116 against 59 us, of eight 75 against 66, of 12 89 against
     // 74, of 16 97 against 85; 2,048 rows of 2,048 keys in groups of 16, 128
     // pairs, 464 against 667; at D 64, 1,024 rows in groups of 16 80 against 97.)
-    if (kind == LTK_ATTEND ? (int64_t)T * G > 64 * (int64_t)std::max(n_seq, 1)
+    // Dense calls of fewer (row, head) pairs times keys of the table than
+    // kTileWork stay here too: units of 32 rows fill the card where those of 128
+    // do not.  (Hq 32, Hkv 8, one sequence's first 512 tokens, 2^23: 20 against 38
+    // us; Hq 64, 128 rows after 1,920 tokens, 2^24: 31 against 46; Hq 32, 512 rows
+    // after 1,536, 2^25: 57 against 49, eight sequences of 128 rows and 1,024
+    // tokens, 2^25: 97 against 48.)
+    constexpr int64_t kTileWork = (int64_t)1 << 24;
+    if (kind == LTK_ATTEND ? (int64_t)T * G > 64 * (int64_t)std::max(n_seq, 1) && (int64_t)T * Hq * entries > kTileWork
                            : kind == LTK_ATTEND_PACKED && group * G > 96)
         return attend_tile_plan(kind, T, Hq, Hkv, D, n_seq, entries, group);
     const size_t part = (size_t)(D + 2) * 16 * sizeof(float);   // of 16 rows

@@ -55,8 +55,8 @@ constexpr int kWhole = 16 * kKeys;    // units of up to this cost are not cut fu
 // D 128, units of 128 against 256: one sequence of 131,072 tokens, 128 rows a
 // head 111 against 158 us, 256 rows 194 against 174, 1,024 rows 640 against
 // 596; 32 sequences of 2,048 tokens, 128 rows 68 against 83, 256 rows 115
-// against 91.  Hq 32, one sequence with 512 tokens of queries: 512 tokens 38
-// against 46 us, 2,048 51 against 54, 8,192 107 against 105.)
+// against 91.  Hq 32, one sequence with 512 rows: 2,048 tokens 51 against 54 us,
+// 8,192 107 against 105.)
 constexpr int kWide = 256;
 constexpr int64_t kWideWork = (int64_t)1 << 25;
 
@@ -924,7 +924,7 @@ AttendPlan attend_tile_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, 
     p.tile = true;
     const int G = Hq / Hkv;
     if (kind == LTK_ATTEND) {
-        const bool wide = (int64_t)T * G >= kWide * (int64_t)std::max(n_seq, 1) && (double)T * Hq * (double)entries >= (double)kWideWork;
+        const bool wide = (int64_t)T * G >= kWide * (int64_t)std::max(n_seq, 1) && (int64_t)T * Hq * entries >= kWideWork;
         p.waves = wide ? 8 : 4;
         const int rows = 32 * p.waves;
         const int64_t units = ((int64_t)T * G / rows + n_seq) * Hkv;

@@ -5,14 +5,40 @@ import pytest
 
 from tests.attend_ref import make_batch, make_cache, poison, ref_append, ref_attend, ref_packed
 from tests.gpu_util import say
-from tests.test_gpu_attend import _attend_case, _dev, _gen, _lists, _within
+from tests.test_gpu_attend import ATTEND, _attend_case, _dev, _gen, _lists, _within
 
 pytestmark = pytest.mark.gpu
 
 
+def _widen(table, page, T, Hq, log2_work):
+    """The table with room for so many tokens that (row, head) pairs times them pass 2^log2_work: past 2^24 calls of many
+    rows take units of 128 rows, past 2^25 of 256."""
+    import torch
+    more = (2 ** log2_work // (T * Hq) + 1 + page) // page - table.shape[1]
+    return torch.nn.functional.pad(table, (0, max(more, 0)), value=-1)
+
+
+@pytest.mark.parametrize("log2_work", [24, 25])
+@pytest.mark.parametrize("case", [c for c in ATTEND if sum(c[0]) * c[3] > 64 * len(c[0])] +
+                         [([9, 300], [5000, 300], 2, 16, 64, 64, 0, 0), ([65], [65], 1, 1, 16, 128, 0, 0),
+                          ([33, 33], [0, 900], 3, 7, 32, 128, 80, 3), ([400], [100], 1, 2, 16, 64, 0, 0)],
+                         ids=lambda c: f"{c[0]}_{c[1]}_h{c[2]}x{c[3]}_p{c[4]}_d{c[5]}_w{c[6]}s{c[7]}")
+def test_many_rows_in_large_units(lib, case, log2_work):
+    import torch
+    rows, lens, Hkv, G, page, D, window, sinks = case
+    say("attend", case, log2_work)
+    cache, table, cu, n, q = _attend_case(rows, lens, Hkv, G, page, D, 60)
+    table = _widen(table, page, sum(rows), Hkv * G, log2_work)
+    a = (q.cuda(), _dev(*cache), *_dev(table, cu, n))
+    out = lib.attend(*a, window=window, n_sink=sinks)
+    ref, tol, _ = ref_attend(q, cache, table, cu, n, D ** -0.5, window, sinks)
+    _within(out, ref, tol, "attend")
+    assert torch.equal(out, lib.attend(*a, window=window, n_sink=sinks))
+
+
 @pytest.mark.parametrize("B,rows,G,Hkv,max_pages", [
     (600, [0, 1, 2], 4, 2, 4),         # few rows a sequence
-    (300, [0, 3, 9], 16, 1, 4),        # more than 64 a head: units of 128
+    (300, [0, 3, 9], 16, 1, 64),       # more than 64 a head: units of 128
     (560, [4, 0, 8, 4, 4], 64, 1, 24),   # 256 a head: units of 256
 ])
 def test_more_sequences_than_one_look(lib, B, rows, G, Hkv, max_pages):
@@ -38,6 +64,7 @@ def test_more_sequences_than_one_look(lib, B, rows, G, Hkv, max_pages):
 
 @pytest.mark.parametrize("T,L,G,D,window,sinks", [
     (1, 20000, 4, 64, 0, 0), (1, 20000, 20, 128, 0, 0), (20, 20000, 8, 64, 0, 0), (70, 9000, 4, 128, 0, 0),
+    (130, 20000, 8, 64, 0, 0), (110, 20000, 16, 128, 0, 0),   # units of 128 rows, of 256
     (40, 9000, 8, 128, 5000, 33), (1, 20000, 3, 128, 9000, 7),
 ])
 def test_one_unit_in_many_parts(lib, T, L, G, D, window, sinks):
@@ -52,11 +79,11 @@ def test_one_unit_in_many_parts(lib, T, L, G, D, window, sinks):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("cap", [576, 16384])
+@pytest.mark.parametrize("cap", [576, 4096, 16384])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (100, 5), (3, 70)])
 def test_chunks_over_holes_and_short_tables(lib, D, cap, window, sinks):
-    """Many rows: pages missing in the middle, tokens past the table or a table far wider than the tokens (units of 128
-    and of 256 rows), freed pages before the window, rows before cu[0] and behind cu[B]."""
+    """Many rows: pages missing in the middle, tokens past the table or a table far wider than the tokens (units of 32,
+    of 128 and of 256 rows), freed pages before the window, rows before cu[0] and behind cu[B]."""
     import torch
     page, Hkv, G = 16, 2, 8
     rows, lens = [260, 0, 77], [700, 5, 500]
@@ -84,9 +111,10 @@ def test_scales_and_sharp_softmax_of_chunks(lib):
     for D, pow2, qs in ((64, False, 60.0), (128, True, 40.0)):
         cache, table, cu, n, q = _attend_case([150], [400], 2, 4, 16, D, 65, pow2, qs)
         cache[3][table[0].long()] *= torch.exp2(torch.linspace(-40, 40, 25).round())[:, None]
-        out = lib.attend(q.cuda(), _dev(*cache), *_dev(table, cu, n), window=300, n_sink=2)
-        ref, tol, _ = ref_attend(q, cache, table, cu, n, D ** -0.5, 300, 2)
-        _within(out, ref, tol, f"D {D}")
+        for t in (table, _widen(table, 16, 150, 8, 24), _widen(table, 16, 150, 8, 25)):
+            out = lib.attend(q.cuda(), _dev(*cache), *_dev(t, cu, n), window=300, n_sink=2)
+            ref, tol, _ = ref_attend(q, cache, t, cu, n, D ** -0.5, 300, 2)
+            _within(out, ref, tol, f"D {D}")
 
 
 def test_shared_pages_and_equal_sequences(lib):
@@ -113,6 +141,8 @@ def test_one_workspace_for_calls_of_many_kinds(lib):
     cases = [([1], [9000], 1, 4, 64, 128), ([200], [900], 2, 8, 64, 128), ([1, 1], [50, 3000], 2, 2, 64, 64),
              ([300], [300], 1, 8, 64, 64)]
     built = [_attend_case(*c, seed=68 + i) for i, c in enumerate(cases)]
+    built = [(c, _widen(t, 64, q.shape[0], q.shape[1], 24 + i % 2) if i in (1, 3) else t, cu, n, q)
+             for i, (c, t, cu, n, q) in enumerate(built)]
     need = max(ltk.attend_workspace_bytes(0, q.shape[0], q.shape[1], c[0].shape[1], q.shape[2], table.shape[0],
                                           table.shape[1] * 64) for c, table, cu, n, q in built)
     ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda")
@@ -138,6 +168,7 @@ def test_chunk_and_packed_captured_and_replayed(lib):
     g = _gen(69)
     page, D, Hkv, G, T, group, cap = 16, 64, 2, 8, 64, 16, 300
     table, _, _, pages = make_batch(g, [T], [900], page)
+    table = _widen(table, page, T, Hkv * G, 24)
     cache = make_cache(g, pages, Hkv, page, D)
     dc, dt = _dev(*cache), table.cuda()
     q = torch.randn(T, Hkv * G, D, generator=g).bfloat16().cuda()
