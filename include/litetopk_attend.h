@@ -26,8 +26,8 @@
  *  - rows outside every sequence (at or past cu[n_seq]) are not written;
  *  - a list entry outside [0, kv_len) or after the row's position is no key.
  * Bytes and scales that hold no key of the sequence may be anything (NaN
- * included); everything else must be finite, scales also within
- * 2^-100 .. 2^100.
+ * included); everything else must be finite, scales also within 2^-64 .. 2^64,
+ * the range that the append writes (the ends of it may meet in one sequence).
  *
  * Sums, softmax statistics and partial rows are fp32, products of bf16 and
  * fp16 operands (the cache's bytes convert exactly).  A key's weight times its

@@ -7,7 +7,8 @@
 //   out = sum_s 2^(y_s - m) vbyte_s / sum_s 2^(y_s - m) / vs,
 // one pass with a running reference m: moving the value scale into the
 // exponent keeps the weights 2^(y - m) within fp16 whatever the scales are,
-// and the divisor takes it out again.
+// and the divisor takes it out again (for scales below kSmallScale by an
+// exponential of its own).
 //
 // A wave takes 32 keys at a time and reads them straight into matrix-core
 // operands; no key or value passes through LDS:
@@ -106,12 +107,13 @@ __device__ __forceinline__ void value_operands(const KvTile<D>& t, int w, at_f16
 // One 32-key tile against MT x 16 query rows.  query(mt, j) is operand j of
 // row tile mt; mask(mt, a, i) says whether the lane's row of tile mt sees key
 // 16 a + 4 g + i of the tile, asked only where `masked` (the same in all lanes).
+// `small`: the tile may hold keys of small value scales (the same in all lanes).
 //
 // The scheduling barriers keep the parts apart: left alone, the compiler
 // converts all of a tile's bytes first and holds 64 registers of operands.
 template <int D, int MT, class Query, class Scale, class Mask>
 __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const Scale (&hs)[2], RowState<D> (&st)[MT],
-                                          bool masked, Mask mask) {
+                                          bool masked, bool small, Mask mask) {
     at_f32x4 s[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -147,14 +149,20 @@ __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const
             const float up = max_groups(top);
             const bool move = up > st[mt].over;
             const float d = move ? up : 0.0f;
-            const float f = st[mt].over == kSlack ? __builtin_amdgcn_exp2f(-d) : 1.0f;   // (nothing to scale at the first move)
+            const float e = st[mt].over == kSlack ? -d : 0.0f, f = __builtin_amdgcn_exp2f(e);   // (nothing to scale at the first move)
             st[mt].m += d;
             st[mt].over = move ? kSlack : st[mt].over;
-            st[mt].l *= f;
+            st[mt].l = scaled(st[mt].l, e);
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) st[mt].o[e] *= f;
+            for (int t = 0; t < D / 16; ++t) st[mt].o[t] *= f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] -= d;
+        }
+        if (small) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st[mt].l += small_share(y[4 * a + i], hs[a].lv(i), hs[a].iv(i));
         }
 #pragma unroll
         for (int a = 0; a < 2; ++a)
@@ -217,8 +225,8 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
         for (int e = 0; e < D / 16; ++e) o[e] = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            const float f = __builtin_amdgcn_exp2f(sm[(w * 16 + r) * 2] - m);
-            sum = __builtin_fmaf(f, sm[(w * 16 + r) * 2 + 1], sum);
+            const float d = sm[(w * 16 + r) * 2] - m, f = __builtin_amdgcn_exp2f(d);
+            sum += scaled(sm[(w * 16 + r) * 2 + 1], d);
             const float* src = so + (w * 16 + r) * kStride + d0;
 #pragma unroll
             for (int e = 0; e < D / 16; ++e) o[e] = __builtin_fmaf(f, src[e], o[e]);
@@ -466,7 +474,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
                     for (int j = 0; j < D / 64; ++j) t.v[4 * x + i][j] = ok ? t.v[4 * x + i][j] : 0u;
                 }
         }
-        tile_step<D, MT>(t, query, hs, st, !whole, [&](int mt, int x, int i) {
+        tile_step<D, MT>(t, query, hs, st, !whole, is_small(hs[0]) || is_small(hs[1]), [&](int mt, int x, int i) {
             const int key = w.key0 + 16 * x + 4 * g + i;
             const int from = a.window > 0 ? max(pos[mt], 0) - a.window : -1;
             return (w.pid[x] >= 0) & (key <= pos[mt]) & (key < kr.hi) &
@@ -588,6 +596,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
     extern __shared__ float sh[];
     ListLds& ls = *reinterpret_cast<ListLds*>(sh);
     __shared__ int s_cnt[kWaves];
+    __shared__ int s_small;   // the staged list holds keys of small value scales
     constexpr int RT = 16 * MT;
     const int group = PACKED ? a.group : 1;
     UnitRows u;
@@ -661,7 +670,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
             }
         }
     };
-    auto step = [&](KvTile<D>& x, int at, int cnt) {
+    auto step = [&](KvTile<D>& x, int at, int cnt, bool small) {
         KeyScale hs[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
@@ -674,10 +683,10 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
         if constexpr (PACKED) {
             const at_u32x4 m0 = *reinterpret_cast<const at_u32x4*>(ls.mask + at + 4 * g);
             const at_u32x4 m1 = *reinterpret_cast<const at_u32x4*>(ls.mask + at + 16 + 4 * g);
-            tile_step<D, MT>(x, query, hs, st, i1 > i0 || at + kTile > cnt,
+            tile_step<D, MT>(x, query, hs, st, i1 > i0 || at + kTile > cnt, small,
                              [&](int mt, int z, int i) { return (((z == 0 ? m0 : m1)[i] >> qi[mt]) & 1u) != 0; });
         } else {
-            tile_step<D, MT>(x, query, hs, st, at + kTile > cnt,
+            tile_step<D, MT>(x, query, hs, st, at + kTile > cnt, small,
                              [&](int, int z, int i) { return at + 16 * z + 4 * g + i < cnt; });
         }
     };
@@ -687,6 +696,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
         const int c1 = min(c0 + kListChunk, e1);
         int cnt = 0;
         __syncthreads();   // the previous chunk has been read
+        if (threadIdx.x == 0) s_small = 0;
         for (int s0 = c0; s0 < c1; s0 += 64 * kWaves) {
             const int e = s0 + threadIdx.x;
             int s = -1;
@@ -720,6 +730,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
                 ls.row[at] = (int)((pg << a.c.page_shift) + (s & (page - 1)));
                 const PageScale ps = page_scale(a.c2, a.c.ks[pg], a.c.vs[pg]);
                 ls.c[at] = ps.c_, ls.lv[at] = ps.lv_, ls.iv[at] = ps.iv_;
+                if (is_small(ps)) s_small = 1;
                 if constexpr (PACKED) ls.mask[at] = m;
             }
             __syncthreads();
@@ -734,6 +745,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
             ls.mask[at] = 0u;
         }
         __syncthreads();
+        const bool small = uniform(s_small) != 0;
         KvTile<D> ta, tb;
         int at = wave * kTile;
         constexpr int kStep = kWaves * kTile;
@@ -742,12 +754,12 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
             while (true) {
                 const bool more = at + kStep < cnt;
                 if (more) load(tb, at + kStep);
-                step(ta, at, cnt);
+                step(ta, at, cnt, small);
                 if (!more) break;
                 at += kStep;
                 const bool more2 = at + kStep < cnt;
                 if (more2) load(ta, at + kStep);
-                step(tb, at, cnt);
+                step(tb, at, cnt, small);
                 if (!more2) break;
                 at += kStep;
             }

@@ -136,8 +136,16 @@ __device__ __forceinline__ at_bf16x8 bf16_of(uint32_t a, uint32_t b) {
     return at_bf16x8{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
 }
 
-// Constants of a key: scale log2(e) ks, log2(vs), 1 / vs.  Dense tiles have
-// one set per half (a page holds at least 16 keys), listed keys one each.
+// Keys whose value scale is below this have their share of the divisor formed
+// by an exponential of its own, 2^((y - m) - log2(vs)), and not as 2^(y - m)
+// times 1 / vs: beside a value scale of up to 2^64, a weight that matters to the
+// divisor can lie below fp32's range (2^-126) in the first form.  A key at or
+// above it whose weight falls below that range is at most 2^-38 of the divisor.
+constexpr float kSmallScale = 0x1p-24f;
+
+// Constants of a key: scale log2(e) ks, log2(vs), 1 / vs (0 for a small scale).
+// Dense tiles have one set per half (a page holds at least 16 keys), listed keys
+// one each.
 struct PageScale {
     float c_, lv_, iv_;
     __device__ __forceinline__ float c(int) const { return c_; }
@@ -147,7 +155,18 @@ struct PageScale {
 // v_log_f32 is base 2; both it and v_rcp_f32 are exact on powers of two and
 // within 1 ulp elsewhere.
 __device__ __forceinline__ PageScale page_scale(float c2, float ks, float vs) {
-    return PageScale{c2 * ks, __builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs)};
+    return PageScale{c2 * ks, __builtin_amdgcn_logf(vs), vs >= kSmallScale ? __builtin_amdgcn_rcpf(vs) : 0.0f};
+}
+__device__ __forceinline__ bool is_small(const PageScale& s) { return __float_as_uint(s.iv_) == 0u; }
+// The divisor's share of a key of a small scale, for y relative to the row's reference.
+__device__ __forceinline__ float small_share(float y, float lv, float iv) {
+    return iv == 0.0f ? __builtin_amdgcn_exp2f(y - lv) : 0.0f;
+}
+// x 2^d for a divisor x: d can pass the range of one factor (scales 2^128 apart)
+// where the product is one that counts.
+__device__ __forceinline__ float scaled(float x, float d) {
+    const float h = __builtin_amdgcn_exp2f(0.5f * d);
+    return x * h * h;
 }
 
 struct AttendArgs {

@@ -49,7 +49,7 @@ struct RowSum {
 };
 __device__ __forceinline__ void add_part(RowSum& s, float m, float l, const at_f32x4& o) {
     const float mn = fmaxf(s.m, m), f0 = __builtin_amdgcn_exp2f(s.m - mn), f1 = __builtin_amdgcn_exp2f(m - mn);
-    s.l = s.l * f0 + l * f1;
+    s.l = scaled(s.l, s.m - mn) + scaled(l, m - mn);
     s.o = s.o * f0 + o * f1;
     s.m = mn;
 }

@@ -84,6 +84,7 @@ struct Ring {                     // listed keys, resolved
     int32_t row[2 * kRing];       // cache row of the unit's head, -1: no key
     uint32_t mask[2 * kRing];     // rows that see it
     float c[2 * kRing], lv[2 * kRing], iv[2 * kRing];
+    int small[2 * kRing / kKeys];   // of a step's keys, some have small value scales
 };
 __device__ __forceinline__ uint8_t* lds() {
     extern __shared__ at_u32x4 lds_words[];
@@ -187,7 +188,8 @@ struct WaveState {
 // LDS operands are read kAhead instructions before their use.
 //
 // scale(hb, i, m, c, lv): constants of the lane's keys 4 i .. 4 i + 3 of half
-// hb (i < 4), lv less m; scale.inverse: their 1 / vs.  mask.each(hb, i, y)
+// hb (i < 4), lv less m; scale.inverse: their 1 / vs; scale.small(hb): some of
+// the half's value scales may be small (the same in all lanes).  mask.each(hb, i, y)
 // hides keys among four, mask.late(hb, x) among all 16 where it says so.
 constexpr int kAhead = 4;
 template <int D, class Scale, class Mask, class Fill>
@@ -242,10 +244,10 @@ __device__ __forceinline__ void step_keys(int stage, const at_bf16x8 (&q)[D / 16
             const float up = max_halves(top);
             const bool move = up > st.over;
             const float d = move ? up : 0.0f;
-            const float f = st.over == kSlack ? __builtin_amdgcn_exp2f(-d) : 1.0f;   // (nothing to scale at the first move)
+            const float e = st.over == kSlack ? -d : 0.0f, f = __builtin_amdgcn_exp2f(e);   // (nothing to scale at the first move)
             st.m += d;
             st.over = move ? kSlack : st.over;
-            st.l *= f;
+            st.l = scaled(st.l, e);
 #pragma unroll
             for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
 #pragma unroll
@@ -254,6 +256,16 @@ __device__ __forceinline__ void step_keys(int stage, const at_bf16x8 (&q)[D / 16
                 const _Float16 fh = (_Float16)f;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) p[0][r] *= fh, p[1][r] *= fh;
+            }
+        }
+        if (scale.small(hb)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                at_f32x4 cc, lv, iv;
+                scale(hb, i, 0.0f, cc, lv);
+                scale.inverse(hb, i, iv);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) st.l += small_share(x[4 * i + r], lv[r], iv[r]);
             }
         }
         top = -INFINITY;
@@ -426,6 +438,7 @@ struct DenseScale {
         const float x = s.get(2 * hb + (i >> 1)).iv_;
         iv = at_f32x4{x, x, x, x};
     }
+    __device__ __forceinline__ bool small(int hb) const { return is_small(s.get(2 * hb)) || is_small(s.get(2 * hb + 1)); }
 };
 
 template <int D, int NW>
@@ -718,6 +731,7 @@ struct ListScale {
     __device__ __forceinline__ void inverse(int hb, int i, at_f32x4& iv) const {
         iv = *reinterpret_cast<const at_f32x4*>(r->iv + key(hb, i));
     }
+    __device__ __forceinline__ bool small(int) const { return uniform(r->small[at / kKeys]) != 0; }
 };
 
 // A unit is 128 (row, head) pairs of one group and key/value head; its keys
@@ -789,6 +803,8 @@ __global__ __launch_bounds__(64 * kListWaves, 2) void attend_tile_list_kernel(At
         ring.row[at] = en.pid >= 0 ? (int)((((size_t)en.pid * a.c.Hkv + u.h) << a.c.page_shift) + (en.s & (page - 1))) : -1;
         ring.mask[at] = m;
         ring.c[at] = ps.c_, ring.lv[at] = ps.lv_, ring.iv[at] = ps.iv_;
+        const bool small = __any(is_small(ps));   // (a wave resolves the 64 entries of one step)
+        if (lane == 0) ring.small[at / kKeys] = small;
     };
     const Part<D, NW> p;
     Raw<Part<D, NW>::kBoth> raw;
