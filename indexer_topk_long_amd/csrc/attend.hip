@@ -107,13 +107,13 @@ __device__ __forceinline__ void value_operands(const KvTile<D>& t, int w, at_f16
 // One 32-key tile against MT x 16 query rows.  query(mt, j) is operand j of
 // row tile mt; mask(mt, a, i) says whether the lane's row of tile mt sees key
 // 16 a + 4 g + i of the tile, asked only where `masked` (the same in all lanes).
-// `small`: the tile may hold keys of small value scales (the same in all lanes).
+// `small`, not 0: the tile may hold keys of small value scales (the same in all lanes).
 //
 // The scheduling barriers keep the parts apart: left alone, the compiler
 // converts all of a tile's bytes first and holds 64 registers of operands.
 template <int D, int MT, class Query, class Scale, class Mask>
 __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const Scale (&hs)[2], RowState<D> (&st)[MT],
-                                          bool masked, bool small, Mask mask) {
+                                          bool masked, uint32_t small, Mask mask) {
     at_f32x4 s[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -145,24 +145,24 @@ __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
-        if (__any(top > st[mt].over)) {
+        if ((__ballot(top > st[mt].over) | small) != 0) {   // (one branch for both)
             const float up = max_groups(top);
             const bool move = up > st[mt].over;
             const float d = move ? up : 0.0f;
-            const float e = st[mt].over == kSlack ? -d : 0.0f, f = __builtin_amdgcn_exp2f(e);   // (nothing to scale at the first move)
+            const Factor by(st[mt].over == kSlack ? -d : 0.0f);   // (nothing to scale at the first move)
             st[mt].m += d;
             st[mt].over = move ? kSlack : st[mt].over;
-            st[mt].l = scaled(st[mt].l, e);
+            st[mt].l = by.divisor(st[mt].l);
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t) st[mt].o[t] *= f;
+            for (int e = 0; e < D / 16; ++e) st[mt].o[e] *= by.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] -= d;
-        }
-        if (small) {
+            if (small != 0) {
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+                for (int a = 0; a < 2; ++a)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) st[mt].l += small_share(y[4 * a + i], hs[a].lv(i), hs[a].iv(i));
+                    for (int i = 0; i < 4; ++i) st[mt].l += small_share(y[4 * a + i], hs[a].lv(i), hs[a].iv(i));
+            }
         }
 #pragma unroll
         for (int a = 0; a < 2; ++a)
@@ -225,11 +225,11 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
         for (int e = 0; e < D / 16; ++e) o[e] = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            const float d = sm[(w * 16 + r) * 2] - m, f = __builtin_amdgcn_exp2f(d);
-            sum += scaled(sm[(w * 16 + r) * 2 + 1], d);
+            const Factor by(sm[(w * 16 + r) * 2] - m);
+            sum += by.divisor(sm[(w * 16 + r) * 2 + 1]);
             const float* src = so + (w * 16 + r) * kStride + d0;
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) o[e] = __builtin_fmaf(f, src[e], o[e]);
+            for (int e = 0; e < D / 16; ++e) o[e] = __builtin_fmaf(by.f, src[e], o[e]);
         }
         const int64_t row = row_of(mt * 16 + r);   // row * Hq + head, -1 past the unit
         if (row < 0) continue;
@@ -452,10 +452,12 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
             }
         }
     };
+    uint32_t small = 0;
     auto scales = [&](PageScale (&hs)[2], int n) {   // before the loads of step n + 1, which may turn the lanes
         if (n % 32 == 0) pl.scales(a.c2);
         hs[0] = pl.scale(2 * (n % 32));
         hs[1] = pl.scale(2 * (n % 32) + 1);
+        small = pl.any_small(2 * (n % 32), 2);
         __builtin_amdgcn_sched_barrier(0);
     };
     auto step = [&](KvTile<D>& t, const Where& w, const PageScale (&hs)[2]) {
@@ -474,7 +476,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
                     for (int j = 0; j < D / 64; ++j) t.v[4 * x + i][j] = ok ? t.v[4 * x + i][j] : 0u;
                 }
         }
-        tile_step<D, MT>(t, query, hs, st, !whole, is_small(hs[0]) || is_small(hs[1]), [&](int mt, int x, int i) {
+        tile_step<D, MT>(t, query, hs, st, !whole, small, [&](int mt, int x, int i) {
             const int key = w.key0 + 16 * x + 4 * g + i;
             const int from = a.window > 0 ? max(pos[mt], 0) - a.window : -1;
             return (w.pid[x] >= 0) & (key <= pos[mt]) & (key < kr.hi) &
@@ -505,7 +507,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 
 template <int D, int MT>
 __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_kernel(AttendArgs a) {
-    extern __shared__ float sh[];
+    extern __shared__ __attribute__((aligned(16))) float sh[];
     __shared__ PlanLds ls;
     __shared__ Place place;
     // the total, then the sequence that this workgroup's range begins in; one
@@ -593,7 +595,7 @@ __host__ __device__ __forceinline__ int list_tiles(int group, int G, int RT) { r
 // one of the unit's rows sees.
 template <int D, int MT, bool PACKED>
 __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_list_kernel(AttendArgs a) {
-    extern __shared__ float sh[];
+    extern __shared__ __attribute__((aligned(16))) float sh[];
     ListLds& ls = *reinterpret_cast<ListLds*>(sh);
     __shared__ int s_cnt[kWaves];
     __shared__ int s_small;   // the staged list holds keys of small value scales
@@ -670,7 +672,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
             }
         }
     };
-    auto step = [&](KvTile<D>& x, int at, int cnt, bool small) {
+    auto step = [&](KvTile<D>& x, int at, int cnt, uint32_t small) {
         KeyScale hs[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
@@ -745,7 +747,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_l
             ls.mask[at] = 0u;
         }
         __syncthreads();
-        const bool small = uniform(s_small) != 0;
+        const uint32_t small = uniform(s_small);
         KvTile<D> ta, tb;
         int at = wave * kTile;
         constexpr int kStep = kWaves * kTile;

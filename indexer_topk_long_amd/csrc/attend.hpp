@@ -162,12 +162,14 @@ __device__ __forceinline__ bool is_small(const PageScale& s) { return __float_as
 __device__ __forceinline__ float small_share(float y, float lv, float iv) {
     return iv == 0.0f ? __builtin_amdgcn_exp2f(y - lv) : 0.0f;
 }
-// x 2^d for a divisor x: d can pass the range of one factor (scales 2^128 apart)
-// where the product is one that counts.
-__device__ __forceinline__ float scaled(float x, float d) {
-    const float h = __builtin_amdgcn_exp2f(0.5f * d);
-    return x * h * h;
-}
+// 2^d as the square of h = 2^(d / 2).  A divisor is scaled by h twice: d can pass
+// the range of one factor (value scales 2^128 apart) where the product is one
+// that counts.
+struct Factor {
+    float h, f;
+    explicit __device__ __forceinline__ Factor(float d) : h(__builtin_amdgcn_exp2f(0.5f * d)), f(h * h) {}
+    __device__ __forceinline__ float divisor(float x) const { return x * h * h; }
+};
 
 struct AttendArgs {
     KvCache c;
@@ -195,6 +197,7 @@ struct PageLanes {
     int id, ahead;      // checked ids of this block (-1: no page, or no key of it is seen); the next block's as read
     float ks, vs;       // as read
     PageScale s;
+    uint64_t small;     // lanes whose group's value scale is small
 
     // key_of(block): first key of the lane's group, < 0 past the end.
     template <class KeyOf>
@@ -213,7 +216,13 @@ struct PageLanes {
         ks = 1.0f, vs = 1.0f;
         if (id >= 0) ks = a.c.ks[tile], vs = a.c.vs[tile];
     }
-    __device__ __forceinline__ void scales(float c2) { s = page_scale(c2, ks, vs); }
+    __device__ __forceinline__ void scales(float c2) {
+        s = page_scale(c2, ks, vs);
+        small = __ballot(is_small(s));
+    }
+    __device__ __forceinline__ uint32_t any_small(int lane, int groups) const {
+        return (uint32_t)(small >> lane) & ((1u << groups) - 1u);
+    }
     __device__ __forceinline__ int page(int lane) const { return __builtin_amdgcn_readlane(id, lane); }
     __device__ __forceinline__ PageScale scale(int lane) const {
         return PageScale{lane_of(s.c_, lane), lane_of(s.lv_, lane), lane_of(s.iv_, lane)};

@@ -48,10 +48,11 @@ struct RowSum {
     at_f32x4 o;
 };
 __device__ __forceinline__ void add_part(RowSum& s, float m, float l, const at_f32x4& o) {
-    const float mn = fmaxf(s.m, m), f0 = __builtin_amdgcn_exp2f(s.m - mn), f1 = __builtin_amdgcn_exp2f(m - mn);
-    s.l = scaled(s.l, s.m - mn) + scaled(l, m - mn);
-    s.o = s.o * f0 + o * f1;
-    s.m = mn;
+    const bool up = m > s.m;   // the sum so far is scaled, else the part
+    const Factor by(up ? s.m - m : m - s.m);
+    s.l = up ? by.divisor(s.l) + l : s.l + by.divisor(l);
+    s.o = s.o * (up ? by.f : 1.0f) + o * (up ? 1.0f : by.f);
+    s.m = up ? m : s.m;
 }
 // Parts i0, i0 + step, .. below n of row `at` of a unit: part i at slot0
 // (i == 0) or slot1 + (i - 1) slot_step.
@@ -88,8 +89,14 @@ __device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t row, int 
     __syncthreads();
     if (grp != 0 || row < 0) return;
     RowSum all{kNoRef, 0.0f, at_f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
-    for (int w = 0; w < kJoinRows; ++w)
-        add_part(all, s_ml[w][0], s_ml[w][1], *reinterpret_cast<const at_f32x4*>(&s_o[w][4 * lane]));
+#pragma unroll
+    for (int w = 0; w < kJoinRows; ++w) all.m = fmaxf(all.m, s_ml[w][0]);
+#pragma unroll
+    for (int w = 0; w < kJoinRows; ++w) {
+        const Factor by(s_ml[w][0] - all.m);
+        all.l += by.divisor(s_ml[w][1]);
+        all.o += *reinterpret_cast<const at_f32x4*>(&s_o[w][4 * lane]) * by.f;
+    }
     write_row<D>(a, row, all);
 }
 

@@ -188,8 +188,8 @@ struct WaveState {
 // LDS operands are read kAhead instructions before their use.
 //
 // scale(hb, i, m, c, lv): constants of the lane's keys 4 i .. 4 i + 3 of half
-// hb (i < 4), lv less m; scale.inverse: their 1 / vs; scale.small(hb): some of
-// the half's value scales may be small (the same in all lanes).  mask.each(hb, i, y)
+// hb (i < 4), lv less m; scale.inverse: their 1 / vs; scale.small(hb), not 0:
+// some of the half's value scales may be small (the same in all lanes).  mask.each(hb, i, y)
 // hides keys among four, mask.late(hb, x) among all 16 where it says so.
 constexpr int kAhead = 4;
 template <int D, class Scale, class Mask, class Fill>
@@ -240,32 +240,33 @@ __device__ __forceinline__ void step_keys(int stage, const at_bf16x8 (&q)[D / 16
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, x[r]);
         }
-        if (__any(top > st.over)) {
+        const uint32_t small = scale.small(hb);
+        if ((__ballot(top > st.over) | small) != 0) {   // (one branch for both)
             const float up = max_halves(top);
             const bool move = up > st.over;
             const float d = move ? up : 0.0f;
-            const float e = st.over == kSlack ? -d : 0.0f, f = __builtin_amdgcn_exp2f(e);   // (nothing to scale at the first move)
+            const Factor by(st.over == kSlack ? -d : 0.0f);   // (nothing to scale at the first move)
             st.m += d;
             st.over = move ? kSlack : st.over;
-            st.l = scaled(st.l, e);
+            st.l = by.divisor(st.l);
 #pragma unroll
-            for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
+            for (int t = 0; t < D / 32; ++t) st.o[t] *= by.f;
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[r] -= d;
             if (hb == 1) {   // half 0's weights, part of whose product is still to come
-                const _Float16 fh = (_Float16)f;
+                const _Float16 fh = (_Float16)by.f;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) p[0][r] *= fh, p[1][r] *= fh;
             }
-        }
-        if (scale.small(hb)) {
+            if (small != 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                at_f32x4 cc, lv, iv;
-                scale(hb, i, 0.0f, cc, lv);
-                scale.inverse(hb, i, iv);
+                for (int i = 0; i < 4; ++i) {
+                    at_f32x4 cc, lv, iv;
+                    scale(hb, i, 0.0f, cc, lv);
+                    scale.inverse(hb, i, iv);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) st.l += small_share(x[4 * i + r], lv[r], iv[r]);
+                    for (int r = 0; r < 4; ++r) st.l += small_share(x[4 * i + r], lv[r], iv[r]);
+                }
             }
         }
         top = -INFINITY;
@@ -424,6 +425,7 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttendArgs& a, int pos_lo, i
 // wait for every load in flight.)
 struct StepScales {
     PageScale s0, s1, s2, s3;
+    uint32_t small;   // bit i: the value scale of page i is small
     __device__ __forceinline__ PageScale get(int i) const { return i == 0 ? s0 : i == 1 ? s1 : i == 2 ? s2 : s3; }
 };
 struct DenseScale {
@@ -438,7 +440,7 @@ struct DenseScale {
         const float x = s.get(2 * hb + (i >> 1)).iv_;
         iv = at_f32x4{x, x, x, x};
     }
-    __device__ __forceinline__ bool small(int hb) const { return is_small(s.get(2 * hb)) || is_small(s.get(2 * hb + 1)); }
+    __device__ __forceinline__ uint32_t small(int hb) const { return s.small >> (2 * hb) & 3u; }
 };
 
 template <int D, int NW>
@@ -539,7 +541,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
         if (n % 16 == 0) pl.scales(a.c2);
         // (a wave none of whose rows sees the step goes through it too: a way
         // around would give its accumulators two places, and cost 70 spills)
-        const StepScales sc{pl.scale(at), pl.scale(at + 1), pl.scale(at + 2), pl.scale(at + 3)};
+        const StepScales sc{pl.scale(at), pl.scale(at + 1), pl.scale(at + 2), pl.scale(at + 3), pl.any_small(at, 4)};
         step_keys<D>(stage, q, st, DenseScale{sc},
                      Mask{pages, seen_by_all(key0, pages, pos_lo, pos_hi), key0 + 4 * g, min(pos, kt.hi - 1), from, a.n_sink}, fill);
     };
@@ -721,7 +723,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
 
 struct ListScale {
     const Ring* r;
-    int at, g;   // the step's place in the ring, the lane's half
+    int at, g, some;   // the step's place in the ring, the lane's half, the step's ring.small
     __device__ __forceinline__ int key(int hb, int i) const { return at + 32 * hb + 8 * i + 4 * g; }
     __device__ __forceinline__ void operator()(int hb, int i, float m, at_f32x4& c, at_f32x4& lv) const {
         c = *reinterpret_cast<const at_f32x4*>(r->c + key(hb, i));
@@ -731,7 +733,7 @@ struct ListScale {
     __device__ __forceinline__ void inverse(int hb, int i, at_f32x4& iv) const {
         iv = *reinterpret_cast<const at_f32x4*>(r->iv + key(hb, i));
     }
-    __device__ __forceinline__ bool small(int) const { return uniform(r->small[at / kKeys]) != 0; }
+    __device__ __forceinline__ uint32_t small(int) const { return uniform(some); }
 };
 
 // A unit is 128 (row, head) pairs of one group and key/value head; its keys
@@ -851,7 +853,7 @@ __global__ __launch_bounds__(64 * kListWaves, 2) void attend_tile_list_kernel(At
     };
     auto step = [&](int t, int stage, auto fill) {
         const int at = (t * kKeys) & (2 * kRing - 1);
-        step_keys<D>(stage, q, st, ListScale{&ring, at, g}, Mask{ring, at, g, qi}, fill);
+        step_keys<D>(stage, q, st, ListScale{&ring, at, g, ring.small[at / kKeys]}, Mask{ring, at, g, qi}, fill);
     };
 
     const int steps = (e1 - e0 + kKeys - 1) / kKeys;
