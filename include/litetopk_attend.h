@@ -33,8 +33,9 @@
  * fp16 operands (the cache's bytes convert exactly).  A key's weight times its
  * value scale is rounded to fp16 relative to the row's largest such product:
  * 2^-11 of itself, or 2^-25 of the largest where it is below fp16's normal
- * range (2^-14 of it).  Results do not depend on timing: the same call gives
- * the same bits.
+ * range (2^-14 of it).  With many rows a key, some are rounded twice (a larger
+ * product met in the same 64 keys): 2^-10, or 2^-24 of the largest.  Results do
+ * not depend on timing: the same call gives the same bits.
  */
 #ifndef LITETOPK_ATTEND_H
 #define LITETOPK_ATTEND_H

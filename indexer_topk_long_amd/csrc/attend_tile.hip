@@ -253,10 +253,9 @@ __device__ __forceinline__ void step_keys(int stage, const at_bf16x8 (&q)[D / 16
             for (int t = 0; t < D / 32; ++t) st.o[t] *= by.f;
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[r] -= d;
-            if (hb == 1) {   // half 0's weights, part of whose product is still to come
-                const _Float16 fh = (_Float16)by.f;
+            if (hb == 1) {   // half 0's weights whose product is still to come: by the fp32 factor, rounded to fp16 again
 #pragma unroll
-                for (int r = 0; r < 8; ++r) p[0][r] *= fh, p[1][r] *= fh;
+                for (int r = 0; r < 8; ++r) p[1][r] = (_Float16)((float)p[1][r] * by.f);
             }
             if (small != 0) {
 #pragma unroll

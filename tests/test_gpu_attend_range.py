@@ -116,3 +116,73 @@ def test_value_scales_at_the_ends_of_their_range_packed(lib, T, L, G, D, group, 
         out = lib.attend_packed(q.cuda(), _dev(*cache), *_dev(table, n, shared, masks, lens), group, scale=math.log(2.0))
         ref, tol = _sums(cache, table, small, T, L, G, 0, shift)
         _within(out, ref, tol, f"{order}, shift {shift}")
+
+
+# ----------------------------------- a reference that moves in a step's second half
+
+# A late key's score in base 2, as the two bytes (sixteenths) that make it.
+LATE = [(224, 4), (256, 8), (288, 4), (320, 8), (352, 4)]
+
+
+def _late_reference(T, Hkv, G, D, late, tail):
+    """64 keys of score 0; then 64 of which 16 .. 31 score 7 to 7.9 and have large values, and one of the second half
+    scores 14 to 22 and has the value 0; then `tail` keys of score 0 and value 0.  All scores in base 2."""
+    import torch
+    g = _gen(84)
+    L = 128 + tail
+    table, cu, n, pages = make_batch(g, [T], [L], 64, spare=0)
+    k, v = torch.zeros(L, Hkv, D), torch.zeros(L, Hkv, D)
+    k[80:96, :, 0] = 112.0
+    k[80:96, :, 1] = torch.randint(0, 15, (16, Hkv), generator=g).float()
+    k[104, :, 0], k[104, :, 1] = late
+    v[80:96] = 256.0 + 16 * torch.randint(0, 12, (16, Hkv, D), generator=g)
+    v = v.to(torch.float8_e4m3fn).float()      # the values that the bytes stand for
+    score = (k[..., 0] + k[..., 1]).double() / 16
+    cache = [torch.zeros(pages, Hkv, 64, D) for _ in range(2)]
+    for dst, src in zip(cache, (k, v)):
+        for p in range(-(-L // 64)):
+            x = src[64 * p:64 * p + 64].transpose(0, 1)
+            dst[int(table[0, p]), :, :x.shape[1]] = x
+    cache = [x.to(torch.float8_e4m3fn) for x in cache] + [torch.full((pages, Hkv), 1.0 / 16), torch.ones(pages, Hkv)]
+    q = torch.zeros(T, Hkv * G, D)
+    q[..., :2] = 1.0
+    w = torch.exp2(score)
+
+    def ref(see):
+        """Rows that see the keys below see [T].  Off by half a step of bf16, two roundings of a weight to fp16, the
+        scores' error E, n additions, and twice 2^-25 of the largest weight for each of the 16 values."""
+        W = w.cumsum(0)[see - 1]
+        out = ((w[..., None] * v.double()).cumsum(0)[see - 1] / W[..., None])
+        size = float(score.max()) * math.log(2.0)
+        E = (D + 4) * 2.0 ** -24 * size + 8 * 2.0 ** -24 * (size + 64) + 2.0 ** -22
+        tol = (2.0 ** -8 + 2.0 ** -10 + 2 * E + L * 2.0 ** -23) * out
+        tol = tol + 16 * 2.0 ** -24 * E4M3_MAX * (w.max() / W)[..., None]
+        return out.repeat_interleave(G, 1), tol.repeat_interleave(G, 1)
+    return tuple(cache), table, cu, n, q.bfloat16(), ref
+
+
+@pytest.mark.parametrize("late", LATE, ids=lambda x: str(sum(x) / 16))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("log2_work", [24, 25])
+def test_weights_before_a_late_reference(lib, D, late, log2_work):
+    import torch
+    T, G = 80, 4
+    cache, table, cu, n, q, ref = _late_reference(T, 2, G, D, late, T)
+    say("late reference", D, late, log2_work)
+    out = lib.attend(q.cuda(), _dev(*cache), *_dev(_widen(table, 64, T, 2 * G, log2_work), cu, n), scale=math.log(2.0))
+    _within(out, *ref(torch.arange(128, 128 + T) + 1), f"late reference, {sum(late) / 16}")
+
+
+@pytest.mark.parametrize("late", LATE, ids=lambda x: str(sum(x) / 16))
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_before_a_late_reference_packed(lib, D, late):
+    """Enough groups that their lists are not cut."""
+    import torch
+    T, G, group = 1024, 8, 16
+    cache, table, cu, n, q, ref = _late_reference(T, 8, G, D, late, T)
+    shared = torch.arange(128).repeat(T // group, 1).int()
+    masks = torch.full(shared.shape, -1, dtype=torch.int32).view(torch.uint32)
+    lens = torch.full((T // group,), 128, dtype=torch.int32)
+    say("late reference, packed", D, late)
+    out = lib.attend_packed(q.cuda(), _dev(*cache), *_dev(table, n, shared, masks, lens), group, scale=math.log(2.0))
+    _within(out, *ref(torch.full((T,), 128)), f"late reference, packed, {sum(late) / 16}")
