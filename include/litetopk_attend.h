@@ -98,7 +98,8 @@ typedef enum {
  * |x| <= 448 s for every token of the page.  When the rows join a page that
  * already holds tokens of the sequence, its scale never falls; if it grows,
  * the bytes of the tokens before the rows are rounded again to the new scale
- * (exact except for e4m3 subnormals).  A page written from its first slot
+ * (exact for a power of two, except for e4m3 subnormals).  A page begun with a
+ * scale that is no power of two keeps it until it grows.  A page written from its first slot
  * starts a new scale.  Slots behind the last row are left as they are.
  * No page may receive rows from two sequences in one call. */
 int litetopk_kv_append(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void* k, const void* v,

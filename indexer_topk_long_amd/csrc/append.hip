@@ -72,6 +72,22 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(sat(c), sat(d), w, true);
 }
 
+// x c and x / s (s > 0) in fp32 rounded to odd: an inexact result whose last bit
+// is 0 moves to its neighbour on the exact value's side.  Rounding that to e4m3
+// gives the exact value rounded once.
+__device__ __forceinline__ float to_odd(float y, float rest, bool away) {   // rest: exact value less y (its sign)
+    const uint32_t b = __float_as_uint(y);
+    return rest == 0.0f || (b & 1u) ? y : __uint_as_float(away ? b + 1u : b - 1u);
+}
+__device__ __forceinline__ float product_to_odd(float x, float c) {   // c > 0
+    const float y = x * c, rest = __builtin_fmaf(x, c, -y);
+    return to_odd(y, rest, (rest < 0.0f) == (x < 0.0f));
+}
+__device__ __forceinline__ float quotient_to_odd(float x, float s) {
+    const float y = x / s, rest = __builtin_fmaf(-y, s, x);
+    return to_odd(y, rest, (rest < 0.0f) == (x < 0.0f));
+}
+
 // VEC bf16 values
 template <int VEC>
 __device__ __forceinline__ void load_bf16(const uint16_t* p, float (&x)[VEC]) {
@@ -240,19 +256,28 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int unit, int h
     const float now = fmaxf(need, old);
     if (tid == 0 && now != old) *scale = now;
     if (slot0 > 0 && now > old) {   // the page's earlier tokens move to the grown scale
-        const float f = old / now;
+        const float f = old / now;   // exact: a scale that grows is a power of two
         for (int i = tid; i < slot0 * (D / 16); i += NT) {
             at_u32x4 w = reinterpret_cast<const at_u32x4*>(dst)[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const auto x = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], false);
                 const auto y = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[j], true);
-                w[j] = pack_e4m3(x[0] * f, x[1] * f, y[0] * f, y[1] * f);
+                w[j] = pack_e4m3(product_to_odd(x[0], f), product_to_odd(x[1], f), product_to_odd(y[0], f),
+                                 product_to_odd(y[1], f));
             }
             reinterpret_cast<at_u32x4*>(dst)[i] = w;
         }
     }
-    const float inv = 1.0f / now;
+    // scales written here are powers of two; a page begun by another writer may keep another one
+    const bool pow2 = (__float_as_uint(now) & 0x7fffffu) == 0u;
+    if (!pow2) {
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) lo[n][j] = quotient_to_odd(lo[n][j], now), hi[n][j] = quotient_to_odd(hi[n][j], now);
+    }
+    const float inv = pow2 ? 1.0f / now : 1.0f;
 #pragma unroll
     for (int n = 0; n < NI; ++n) {
         const int w = n * NT + tid, r = w / kItems;
