@@ -48,13 +48,14 @@ struct AppendArgs {
 
 // p * f in turns, reduced to [-1/2, 1/2]
 __device__ __forceinline__ double turns(int p, double f) {
-    constexpr double kInv2Pi = 0.15915494309189535, kInv2PiLo = -9.8393416157117e-18;
+    constexpr double kInv2Pi = 0.15915494309189535, kInv2PiLo = -9.839338337591243e-18;
     const double r = f * kInv2Pi;
     const double re = __builtin_fma(f, kInv2Pi, -r) + f * kInv2PiLo;
     const double x = (double)p;
     const double t = x * r;
     const double te = __builtin_fma(x, r, -t) + x * re;
-    return (t - __builtin_rint(t)) + te;
+    const double y = (t - __builtin_rint(t)) + te;   // te passes a turn where t passes 2^52
+    return y - __builtin_rint(y);
 }
 
 // Least power of two s (as its exponent) with amax <= 448 s, in [-64, 64].

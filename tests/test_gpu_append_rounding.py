@@ -111,3 +111,45 @@ def test_tokens_of_a_page_whose_other_scale_grows(lib):
         for slot in range(3):
             d = (got[:, slot] != want) & ((got[:, slot] | want) != 0x80)
             assert not d.any(), f"{int(d.sum())} of {d.numel()} bytes differ"
+
+
+def _pi():
+    """pi to 70 digits: 16 atan(1/5) - 4 atan(1/239)."""
+    def atan_inv(n, one):
+        t = s = one // n
+        k = 1
+        while t:
+            t //= n * n
+            k += 2
+            s += -t // k if k % 4 == 3 else t // k
+        return s
+    one = 10 ** 80
+    return Fraction(16 * atan_inv(5, one) - 4 * atan_inv(239, one), one)
+
+
+@pytest.mark.parametrize("pos,f", [(1048575, 3.0 ** 33), (2 ** 31 - 20, 3.0 ** 26), (777777, 2.0 ** 50 + 1), (999, 5.0 ** 22)])
+def test_rotation_by_many_turns(lib, pos, f):
+    """Angles of up to 2^72 radians: 1 / 2pi takes both words of its constant.  The reduced angle is off by the third
+    word (2^-109 of the angle in turns) and the products' roundings (2^-35 turns): neither reaches a byte's border here
+    nor a bf16's half step."""
+    import math
+    import torch
+    g = _gen(93)
+    pi, D, page = _pi(), 64, 16
+    assert abs(float(pi) - math.pi) < 1e-15
+    freq = torch.tensor([f / (i + 1) for i in range(32)], dtype=torch.float64)
+    turns = [(pos * Fraction(x) / (2 * pi)) % 1 for x in freq.tolist()]
+    ang = torch.tensor([float(2 * pi * t) for t in turns], dtype=torch.float64)
+    x = torch.randn(1, 2, D, generator=g).bfloat16()
+    lo, hi = x.double()[..., :32], x.double()[..., 32:]
+    ref = torch.cat([lo * ang.cos() - hi * ang.sin(), hi * ang.cos() + lo * ang.sin()], -1)
+    zero = torch.zeros(1, 2, page, D, dtype=torch.uint8)
+    cache = _dev(zero.view(torch.float8_e4m3fn), zero.clone().view(torch.float8_e4m3fn), torch.ones(1, 2), torch.ones(1, 2))
+    table = torch.zeros(1, pos // page + 1, dtype=torch.int32)
+    say("turns", pos, f)
+    q = lib.kv_append(*_dev(x, x), cache, *_dev(table, torch.tensor([0, 1]).int(), torch.tensor([pos + 1]).int(), freq, x))
+    tol = 2.0 ** -8 * ref.abs() + 4 * 2.0 ** -24 * 2 * x.double().abs().amax(-1, keepdim=True)
+    assert ((q.cpu().double() - ref).abs() <= tol).all()
+    s = cache[2].cpu().double()[0][:, None]
+    want = (ref[0] / s).float().clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(cache[0].cpu().view(torch.uint8)[0, :, pos % page], want)
