@@ -8,6 +8,9 @@ using namespace ltk;
 
 namespace {
 
+// Positions of a table: key offsets past a tile's end stay in 32 bits.
+constexpr int64_t kMaxTokens = 0x7fffffff - 127;
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1; }
@@ -20,7 +23,7 @@ int check_cache(const ltk_kv_cache* c, const ltk_kv_batch* b, int32_t T, bool ne
     const int sh = page_shift(c->page_size);
     if (sh < 0) return LTK_EUNSUPPORTED;
     constexpr int64_t kMost = 0x7fffffff;
-    if ((int64_t)c->n_pages * c->n_kv_heads > (kMost >> sh) || b->max_pages > (kMost >> sh)) return LTK_EINVAL;
+    if ((int64_t)c->n_pages * c->n_kv_heads > (kMost >> sh) || b->max_pages > (kMaxTokens >> sh)) return LTK_EINVAL;
     if (!c->k || !c->v || !c->k_scale || !c->v_scale || !aligned16(c->k) || !aligned16(c->v)) return LTK_EINVAL;
     if (T > 0 && b->n_seq > 0 && (!b->page_table || !b->kv_len || (need_cu && !b->cu))) return LTK_EINVAL;
     kc = KvCache{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scale, c->v_scale,
@@ -94,7 +97,7 @@ int litetopk_kv_append(const ltk_kv_cache* cache, const ltk_kv_batch* batch, con
 size_t litetopk_attend_workspace_bytes(int32_t kind, int32_t T, int32_t Hq, int32_t n_kv_heads, int32_t head_dim,
                                        int32_t n_seq, int64_t entries, int32_t group) {
     if (kind < LTK_ATTEND || kind > LTK_ATTEND_PACKED || T < 0 || n_kv_heads < 1 || Hq < 1 || Hq % n_kv_heads != 0 ||
-        n_seq < 0 || entries < 1 || entries > 0x7fffffff || (int64_t)T * Hq > 0x7fffffff ||
+        n_seq < 0 || entries < 1 || entries > kMaxTokens || (int64_t)T * Hq > 0x7fffffff ||
         (head_dim != 64 && head_dim != 128) || (kind == LTK_ATTEND_PACKED && (group < 1 || group > 32 || !group_fits(group, Hq, n_kv_heads))))
         return 0;
     return attend_plan(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries, group).ws_bytes;
