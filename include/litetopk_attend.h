@@ -15,7 +15,7 @@
  * Attention of the row at position p over the keys s it sees, per query head:
  *   x_s = scale * (q . k_s)     out = sum_s exp(x_s) v_s / sum_s exp(x_s)
  * A row that sees no key gets zeros.  Query head h reads key/value head
- * h / (Hq / n_kv_heads).
+ * h / (Hq / n_kv_heads).  T * Hq <= 2^31 - 256.
  *
  * Conventions: those of litetopk.h (device pointers, caller-owned memory,
  * asynchronous on `stream`, errors before anything is enqueued).  q, k, v and

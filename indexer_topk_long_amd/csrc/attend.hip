@@ -588,7 +588,7 @@ struct ListLds {
 // (row, head) pairs of a group that share a list, and the units of 16 MT they
 // make: a group is one row with a list of its own, or `group` rows of a packed
 // list.
-__host__ __device__ __forceinline__ int list_tiles(int group, int G, int RT) { return (group * G + RT - 1) / RT; }
+__host__ __device__ __forceinline__ int list_tiles(int group, int G, int RT) { return (group * G + RT - 1) / RT; }   // (group G <= 2^31 - 256)
 
 // A unit is 16 MT (row, head) pairs of one group and key/value head, flattened
 // as elsewhere; its list is idx[row], or with PACKED the group's entries that
@@ -863,7 +863,7 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
     }
     if (kind == LTK_ATTEND_SELECTED) group = 1;
     p.mt = group * G > 16 ? 2 : 1;
-    const int64_t units = (int64_t)((T + group - 1) / group) * list_tiles(group, G, 16 * p.mt) * Hkv;
+    const int64_t units = ((int64_t)T + group - 1) / group * list_tiles(group, G, 16 * p.mt) * Hkv;
     // Lists are cut only while the units leave CUs with less than two workgroups,
     // each part at least one 32-key tile a wave (580 units of 2,048 keys,
     // D = 128: 54 us whole, 68 us cut in two and joined).

@@ -10,6 +10,8 @@ namespace {
 
 // Positions of a table: key offsets past a tile's end stay in 32 bits.
 constexpr int64_t kMaxTokens = 0x7fffffff - 127;
+// Rows times query heads: a unit's rows past the last one stay in 32 bits.
+constexpr int64_t kMaxRows = 0x7fffffff - 255;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -34,7 +36,7 @@ int check_cache(const ltk_kv_cache* c, const ltk_kv_batch* b, int32_t T, bool ne
 
 int check_heads(int32_t T, int32_t Hq, int32_t Hkv) {
     if (Hq < 1 || Hq % Hkv != 0) return LTK_EINVAL;
-    return (int64_t)T * Hq > 0x7fffffff ? LTK_EINVAL : LTK_OK;
+    return (int64_t)T * Hq > kMaxRows ? LTK_EINVAL : LTK_OK;
 }
 
 // A group's (row, head) pairs of a key/value head, which the kernels number.
@@ -97,7 +99,7 @@ int litetopk_kv_append(const ltk_kv_cache* cache, const ltk_kv_batch* batch, con
 size_t litetopk_attend_workspace_bytes(int32_t kind, int32_t T, int32_t Hq, int32_t n_kv_heads, int32_t head_dim,
                                        int32_t n_seq, int64_t entries, int32_t group) {
     if (kind < LTK_ATTEND || kind > LTK_ATTEND_PACKED || T < 0 || n_kv_heads < 1 || Hq < 1 || Hq % n_kv_heads != 0 ||
-        n_seq < 0 || entries < 1 || entries > kMaxTokens || (int64_t)T * Hq > 0x7fffffff ||
+        n_seq < 0 || entries < 1 || entries > kMaxTokens || (int64_t)T * Hq > kMaxRows ||
         (head_dim != 64 && head_dim != 128) || (kind == LTK_ATTEND_PACKED && (group < 1 || group > 32 || !group_fits(group, Hq, n_kv_heads))))
         return 0;
     return attend_plan(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries, group).ws_bytes;

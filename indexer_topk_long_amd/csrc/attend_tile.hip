@@ -955,7 +955,7 @@ AttendPlan attend_tile_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, 
     }
     p.waves = kListWaves;
     constexpr int rows = kRows<kListWaves>;
-    const int64_t units = (int64_t)((T + group - 1) / group) * ((group * G + rows - 1) / rows) * Hkv;
+    const int64_t units = ((int64_t)T + group - 1) / group * ((group * G + rows - 1) / rows) * Hkv;
     const int64_t most = (entries + kKeys - 1) / kKeys;
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 512 / std::max<int64_t>(units, 1)));
     p.blocks = units * p.splits;

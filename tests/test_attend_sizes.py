@@ -18,3 +18,31 @@ def test_tables_whose_last_tile_passes_32_bits(kind, page):
     with pytest.raises(ltk.LtkError):
         ltk.attend_workspace_bytes(0, 4, 8, 4, 128, 1, (most + 1) * page)
     assert ltk.attend_workspace_bytes(0, 4, 8, 4, 128, 1, most * page) >= 256
+
+
+MOST = 2 ** 31 - 256      # rows times query heads
+
+
+@pytest.mark.parametrize("kind", ["append", "attend", "selected", "packed"])
+@pytest.mark.parametrize("T,Hq", [(MOST + 1, 1), (1, MOST + 1), (MOST // 8 + 1, 8)])
+def test_rows_times_heads_past_32_bits(kind, T, Hq):
+    n_seq = dict(n_seq=1) if kind == "packed" else {}
+    call = _append if kind == "append" else lambda **kw: _attend(kind, **kw)
+    assert call(T=T, Hq=Hq, n_kv_heads=1, **n_seq) == EINVAL
+    if kind != "append":
+        with pytest.raises(ltk.LtkError):
+            ltk.attend_workspace_bytes(["attend", "selected", "packed"].index(kind), T, Hq, 1, 128, 1, 64, 1)
+
+
+@pytest.mark.parametrize("kind,group", [(0, 0), (1, 0), (2, 1), (2, 32)])
+@pytest.mark.parametrize("T,Hq,Hkv", [(MOST, 1, 1), (MOST - 31, 1, 1), (1 << 20, 1 << 10, 1 << 10), (1 << 10, 1 << 20, 1)])
+def test_workspaces_of_the_largest_calls(kind, group, T, Hq, Hkv):
+    """Sizes whose sums pass 32 bits on the way: a refusal or a size that can be one (a few thousand parts of at most 256
+    rows of 130 floats, and what the join reads)."""
+    if kind == 2 and group * (Hq // Hkv) > 1 << 30:
+        return
+    try:
+        n = ltk.attend_workspace_bytes(kind, T, Hq, Hkv, 128, 1, 2048, group)
+    except ltk.LtkError:
+        return
+    assert 256 <= n <= 2048 * 256 * 130 * 4
