@@ -25,6 +25,10 @@
  *    rows are not written there and its keys are not seen;
  *  - rows outside every sequence (at or past cu[n_seq]) are not written;
  *  - a list entry outside [0, kv_len) or after the row's position is no key.
+ * Calls that would launch 2^32 threads are refused (LTK_EINVAL): selected and
+ * packed ones launch 256 for 16 or more (row, head) pairs of a list and key/value
+ * head.
+ *
  * Bytes and scales that hold no key of the sequence may be anything (NaN
  * included); everything else must be finite, scales also within 2^-64 .. 2^64,
  * the range that the append writes (the ends of it may meet in one sequence).

@@ -42,7 +42,6 @@ struct AppendArgs {
     const double* inv_freq;
     int T, Hq, rot, interleaved;
     int units;       // pages that can receive rows, upper bound
-    int q_blocks;
     int heads_per;   // query heads per thread
 };
 
@@ -333,35 +332,53 @@ __global__ __launch_bounds__(NT) void kv_append_kernel(AppendArgs a) {
     }
 }
 
+// Threads of a workgroup for items of VEC elements.
+constexpr int append_threads(int D, int vec, int page) {
+    const int items = page * D / (2 * vec), most = vec == 1 ? 1024 : 256;   // single elements: more threads, not more registers
+    return items < 64 ? 64 : (items > most ? most : items);
+}
+
 template <int D, int VEC, int PAGE>
-hipError_t launch_page(AppendArgs& a, hipStream_t st) {
-    constexpr int kItems = PAGE * D / (2 * VEC);
-    constexpr int kMost = VEC == 1 ? 1024 : 256;   // single elements: more threads, not more registers
-    constexpr int NT = kItems < 64 ? 64 : (kItems > kMost ? kMost : kItems);
-    constexpr int NI = (kItems + NT - 1) / NT;
-    const int64_t kv_blocks = (int64_t)a.units * a.c.Hkv * 2;
-    const int64_t hb = (a.Hq + a.heads_per - 1) / a.heads_per;
-    const int64_t q_blocks = a.q ? ((int64_t)a.T * hb * (D / (2 * VEC)) + NT - 1) / NT : 0;
-    if (kv_blocks + q_blocks > 0x7fffffff) return hipErrorInvalidValue;
-    kv_append_kernel<D, VEC, NT, NI><<<(unsigned)(kv_blocks + q_blocks), NT, 0, st>>>(a);
+hipError_t launch_page(const AppendArgs& a, unsigned blocks, hipStream_t st) {
+    constexpr int NT = append_threads(D, VEC, PAGE);
+    constexpr int NI = (PAGE * D / (2 * VEC) + NT - 1) / NT;
+    kv_append_kernel<D, VEC, NT, NI><<<blocks, NT, 0, st>>>(a);
     return hipGetLastError();
 }
 
 template <int D, int VEC>
-hipError_t launch_vec(AppendArgs& a, hipStream_t st) {
+hipError_t launch_vec(const AppendArgs& a, unsigned blocks, hipStream_t st) {
     switch (a.c.page_shift) {
-        case 4: return launch_page<D, VEC, 16>(a, st);
-        case 5: return launch_page<D, VEC, 32>(a, st);
-        case 6: return launch_page<D, VEC, 64>(a, st);
-        default: return launch_page<D, VEC, 128>(a, st);
+        case 4: return launch_page<D, VEC, 16>(a, blocks, st);
+        case 5: return launch_page<D, VEC, 32>(a, blocks, st);
+        case 6: return launch_page<D, VEC, 64>(a, blocks, st);
+        default: return launch_page<D, VEC, 128>(a, blocks, st);
     }
 }
 
 }  // namespace
 
-hipError_t launch_kv_append(const KvCache& c, const KvBatch& bt, int D, const uint16_t* k, const uint16_t* v,
-                            const uint16_t* q, int T, int Hq, const double* inv_freq, int rot, int interleaved,
-                            uint16_t* q_out, hipStream_t st) {
+AppendPlan append_plan(int T, int Hq, int Hkv, int D, int n_seq, int page, int rot, bool queries) {
+    AppendPlan p{};
+    // rot / 2 (half-split pairs) and rot (the border) in whole vectors
+    p.vec = rot % 16 == 0 ? 8 : rot % 8 == 0 ? 4 : 1;
+    // a thread's sines serve up to 8 heads while the threads left still fill the
+    // card (8,192 rows of 64 heads, D = 128: 107 us with 1, 83 with 2, 76 with 4,
+    // 74 with 8, 80 with 16; 96 rows of 32 heads: 10.0 us with 1, 12.3 with 8)
+    p.heads_per = 1;
+    while (p.heads_per < 8 && (int64_t)T * Hq * (D / 16) / (2 * p.heads_per) >= 1 << 18) p.heads_per *= 2;
+    const int nt = append_threads(D, p.vec, page);
+    const int64_t units = unit_bound(n_seq, T, 1, page, 2), hb = (Hq + p.heads_per - 1) / p.heads_per;
+    if (units > 0x7fffffff) return p;   // (fits: false)
+    p.units = (int)units;
+    p.blocks = units * Hkv * 2 + (queries ? ((int64_t)T * hb * (D / (2 * p.vec)) + nt - 1) / nt : 0);
+    p.fits = grid_fits(p.blocks, nt);
+    return p;
+}
+
+hipError_t launch_kv_append(const AppendPlan& p, const KvCache& c, const KvBatch& bt, int D, const uint16_t* k,
+                            const uint16_t* v, const uint16_t* q, int T, int Hq, const double* inv_freq, int rot,
+                            int interleaved, uint16_t* q_out, hipStream_t st) {
     AppendArgs a{};
     a.c = c;
     a.bt = bt;
@@ -374,18 +391,12 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& bt, int D, const ui
     a.Hq = Hq;
     a.rot = rot;
     a.interleaved = interleaved;
-    const int64_t units = unit_bound(bt.n_seq, T, 1, 1 << c.page_shift, 2);
-    if (units > 0x7fffffff) return hipErrorInvalidValue;
-    a.units = (int)units;
-    // a thread's sines serve up to 8 heads while the threads left still fill the
-    // card (8,192 rows of 64 heads, D = 128: 107 us with 1, 83 with 2, 76 with 4,
-    // 74 with 8, 80 with 16; 96 rows of 32 heads: 10.0 us with 1, 12.3 with 8)
-    a.heads_per = 1;
-    while (a.heads_per < 8 && (int64_t)T * Hq * (D / 16) / (2 * a.heads_per) >= 1 << 18) a.heads_per *= 2;
-    // rot / 2 (half-split pairs) and rot (the border) in whole vectors
-    if (rot % 16 == 0) return D == 64 ? launch_vec<64, 8>(a, st) : launch_vec<128, 8>(a, st);
-    if (rot % 8 == 0) return D == 64 ? launch_vec<64, 4>(a, st) : launch_vec<128, 4>(a, st);
-    return D == 64 ? launch_vec<64, 1>(a, st) : launch_vec<128, 1>(a, st);
+    a.units = p.units;
+    a.heads_per = p.heads_per;
+    const unsigned blocks = (unsigned)p.blocks;
+    if (p.vec == 8) return D == 64 ? launch_vec<64, 8>(a, blocks, st) : launch_vec<128, 8>(a, blocks, st);
+    if (p.vec == 4) return D == 64 ? launch_vec<64, 4>(a, blocks, st) : launch_vec<128, 4>(a, blocks, st);
+    return D == 64 ? launch_vec<64, 1>(a, blocks, st) : launch_vec<128, 1>(a, blocks, st);
 }
 
 }  // namespace ltk

@@ -45,7 +45,7 @@ namespace ltk {
 
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;            // (256 threads: AttendPlan::fits)
 constexpr int kTile = 32;            // keys per wave step
 constexpr int kMinPer = 2 * kWaves;  // least key tiles of a workgroup's range: two per wave
 constexpr int kListChunk = 2048;     // list entries staged in LDS at a time
@@ -795,7 +795,6 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attend_list_join_kernel(Att
 template <int KIND, int D, int MT>
 hipError_t launch(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.T * a.Hq;
-    if (p.blocks > 0x7fffffff || rows > 0x7fffffff) return hipErrorInvalidValue;
     if constexpr (KIND == LTK_ATTEND) {
         attend_kernel<D, MT><<<(unsigned)p.blocks, 64 * kWaves, finish_lds<D, MT>(), st>>>(a);
         if (p.join) launch_join<D, 16 * MT>(p, a, st);

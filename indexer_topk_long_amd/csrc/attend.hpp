@@ -232,10 +232,19 @@ struct PageLanes {
     }
 };
 
-hipError_t launch_kv_append(const KvCache& c, const KvBatch& bt, int D, const uint16_t* k, const uint16_t* v,
-                            const uint16_t* q, int T, int Hq, const double* inv_freq, int rot, int interleaved,
-                            uint16_t* q_out, hipStream_t st);
+// A launch has fewer than 2^32 threads.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= (int64_t)0xffffffff / threads; }
 
+// Launch of an append, fixed by its sizes.
+struct AppendPlan {
+    int vec, heads_per, units;
+    int64_t blocks;
+    bool fits;
+};
+AppendPlan append_plan(int T, int Hq, int Hkv, int D, int n_seq, int page, int rot, bool queries);
+hipError_t launch_kv_append(const AppendPlan& p, const KvCache& c, const KvBatch& bt, int D, const uint16_t* k,
+                            const uint16_t* v, const uint16_t* q, int T, int Hq, const double* inv_freq, int rot,
+                            int interleaved, uint16_t* q_out, hipStream_t st);
 
 // Launch of an attend call, fixed by its sizes alone so that the workspace
 // size and the call agree.
@@ -247,6 +256,7 @@ struct AttendPlan {
     int splits;
     bool join;         // units may be cut: partial rows and a joining launch
     size_t head_bytes, ws_bytes;
+    bool fits() const { return grid_fits(blocks, tile ? 64 * waves : 256); }
 };
 // `group` is the packed kind's (else 0).
 AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group);

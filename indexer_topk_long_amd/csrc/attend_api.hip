@@ -45,6 +45,7 @@ bool group_fits(int32_t group, int32_t Hq, int32_t Hkv) { return (int64_t)group 
 int run_attend(int kind, const ltk_kv_cache* cache, AttendArgs& a, int64_t entries, void* ws, size_t ws_bytes,
                void* stream) {
     const AttendPlan p = attend_plan(kind, a.T, a.Hq, a.c.Hkv, cache->head_dim, a.bt.n_seq, entries, a.group);
+    if (!p.fits()) return LTK_EINVAL;
     if (ws_bytes < p.ws_bytes) return LTK_EWORKSPACE;
     if (a.T == 0 || a.bt.n_seq == 0) return LTK_OK;
     const int st = litetopk_device_check();
@@ -88,9 +89,12 @@ int litetopk_kv_append(const ltk_kv_cache* cache, const ltk_kv_batch* batch, con
     if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || ((uintptr_t)inv_freq & 7u))
         return LTK_EINVAL;
     if (T == 0 || kb.n_seq == 0) return LTK_OK;
+    if (!q) Hq = 1;
+    const AppendPlan p = append_plan(T, Hq, kc.Hkv, cache->head_dim, kb.n_seq, cache->page_size, rot_dim, q != nullptr);
+    if (!p.fits) return LTK_EINVAL;
     if ((st = litetopk_device_check()) != LTK_OK) return st;
-    if (launch_kv_append(kc, kb, cache->head_dim, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
-                         static_cast<const uint16_t*>(q), T, q ? Hq : 1, inv_freq, rot_dim, interleaved != 0,
+    if (launch_kv_append(p, kc, kb, cache->head_dim, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
+                         static_cast<const uint16_t*>(q), T, Hq, inv_freq, rot_dim, interleaved != 0,
                          static_cast<uint16_t*>(q_out), static_cast<hipStream_t>(stream)) != hipSuccess)
         return LTK_EHIP;
     return LTK_OK;
@@ -102,7 +106,8 @@ size_t litetopk_attend_workspace_bytes(int32_t kind, int32_t T, int32_t Hq, int3
         n_seq < 0 || entries < 1 || entries > kMaxTokens || (int64_t)T * Hq > kMaxRows ||
         (head_dim != 64 && head_dim != 128) || (kind == LTK_ATTEND_PACKED && (group < 1 || group > 32 || !group_fits(group, Hq, n_kv_heads))))
         return 0;
-    return attend_plan(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries, group).ws_bytes;
+    const AttendPlan p = attend_plan(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries, group);
+    return p.fits() ? p.ws_bytes : 0;
 }
 
 int litetopk_attend(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void* q, int32_t T, int32_t Hq,

@@ -965,7 +965,6 @@ AttendPlan attend_tile_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, 
 }
 
 hipError_t launch_attend_tile(int kind, int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
-    if (p.blocks > 0x7fffffff) return hipErrorInvalidValue;
     if (kind != LTK_ATTEND) return D == 64 ? launch_list<64>(p, a, st) : launch_list<128>(p, a, st);
     if (p.waves == 8) return D == 64 ? launch_dense<64, 8>(p, a, st) : launch_dense<128, 8>(p, a, st);
     return D == 64 ? launch_dense<64, 4>(p, a, st) : launch_dense<128, 4>(p, a, st);

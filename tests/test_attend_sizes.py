@@ -3,7 +3,7 @@ number is refused as an argument error, before any device call."""
 import pytest
 
 import indexer_topk_long_amd as ltk
-from tests.test_attend_abi import EINVAL, _append, _attend
+from tests.test_attend_abi import EINVAL, EWS, _append, _attend
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
@@ -46,3 +46,27 @@ def test_workspaces_of_the_largest_calls(kind, group, T, Hq, Hkv):
     except ltk.LtkError:
         return
     assert 256 <= n <= 2048 * 256 * 130 * 4
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n_seq=1 << 30),                                       # pages that can receive rows: 2 n_seq + ..
+    dict(n_seq=1 << 21, n_kv_heads=8, Hq=8),                   # .. times heads, keys and values: 2^25 workgroups of 256
+    dict(T=1 << 28, Hq=4, n_kv_heads=4, page_size=16),         # 2^24 pages
+    dict(T=1 << 24, Hq=64, n_kv_heads=4, rot=2, n_seq=1),      # queries in single elements: 2^24 workgroups of 1,024
+])
+def test_appends_of_more_workgroups_than_a_launch_has(kw):
+    assert _append(n_pages=4, **kw) == EINVAL
+
+
+@pytest.mark.parametrize("kind,few,many", [
+    ("selected", dict(T=(1 << 21) - 1, Hq=8, n_kv_heads=8), dict(T=1 << 21, Hq=8, n_kv_heads=8)),
+    ("selected", dict(T=(1 << 20) - 1, Hq=64, n_kv_heads=1), dict(T=1 << 23, Hq=64, n_kv_heads=1)),
+    ("packed", dict(T=(1 << 24) - 1, Hq=1, n_kv_heads=1, group=1, n_seq=1), dict(T=1 << 24, Hq=1, n_kv_heads=1, group=1, n_seq=1)),
+])
+def test_lists_of_more_workgroups_than_a_launch_has(kind, few, many):
+    """Refused as an argument error; the next smaller call gets as far as its (too small) workspace."""
+    assert _attend(kind, wsb=0, **few) == EWS
+    assert _attend(kind, wsb=0, **many) == EINVAL
+    kw = dict(group=0, **many) if kind == "selected" else many
+    with pytest.raises(ltk.LtkError):
+        ltk.attend_workspace_bytes(1 if kind == "selected" else 2, kw["T"], kw["Hq"], kw["n_kv_heads"], 128, 1, 64, kw["group"])
