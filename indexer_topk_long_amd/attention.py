@@ -8,7 +8,9 @@ cu[b] .. cu[b+1]-1 of the call, at the last positions of its kv_len[b] tokens.
 
 Tensors are contiguous and on the cache's device; calls run on that device's
 current stream.  Wrong types raise TypeError, wrong shapes or places
-ValueError, and what the library refuses LtkError.
+ValueError, and what the library refuses LtkError.  The operators compute no
+gradients: a tensor that requires grad (while grad mode is on) or carries a
+tangent raises RuntimeError.
 """
 from __future__ import annotations
 

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -54,6 +55,16 @@ constexpr Kind kBf16{at::kBFloat16, "torch.bfloat16"}, kFp8{at::kFloat8_e4m3fn, 
     kF32{at::kFloat, "torch.float32"}, kF64{at::kDouble, "torch.float64"}, kI32{at::kInt, "torch.int32"},
     kU32{at::kUInt32, "torch.uint32"};
 
+// The operators compute no gradients: a result would silently be detached from
+// a tensor that autograd follows, backward or forward.
+void without_grad(const at::Tensor& t, const char* name) {
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        refuse(PyExc_RuntimeError, std::string(name) + " requires grad: the paged cache's operators are forward only "
+                                                       "(call them under torch.no_grad(), or detach it)");
+    if (t.unsafeGetTensorImpl()->_fw_grad(0, t).defined())   // (read in place: as an operator it goes through the dispatcher)
+        refuse(PyExc_RuntimeError, std::string(name) + " carries a tangent: the paged cache's operators are forward only");
+}
+
 // A contiguous device tensor of this type and shape (-1: any size), on the
 // cache's device where dev >= 0.
 const at::Tensor& tensor(PyObject* o, const char* name, Kind kind, std::initializer_list<int64_t> want, int dev) {
@@ -69,6 +80,7 @@ const at::Tensor& tensor(PyObject* o, const char* name, Kind kind, std::initiali
         for (int64_t n : want) w += (w.empty() ? "" : ", ") + (n < 0 ? std::string("*") : std::to_string(n));
         refuse(PyExc_ValueError, std::string(name) + " must be [" + w + "], got " + shape_text(got));
     }
+    without_grad(t, name);
     if (!t.is_cuda() || !t.is_contiguous())
         refuse(PyExc_ValueError, std::string(name) + " must be a contiguous device tensor");
     if (dev >= 0 && t.get_device() != dev)

@@ -70,3 +70,17 @@ def test_lists_of_more_workgroups_than_a_launch_has(kind, few, many):
     kw = dict(group=0, **many) if kind == "selected" else many
     with pytest.raises(ltk.LtkError):
         ltk.attend_workspace_bytes(1 if kind == "selected" else 2, kw["T"], kw["Hq"], kw["n_kv_heads"], 128, 1, 64, kw["group"])
+
+
+def test_a_cache_that_autograd_follows_is_refused():
+    import torch
+    i32 = torch.int32
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.float8_e4m3fn)
+    s = torch.ones(4, 2)
+    batch = torch.zeros(1, 4, dtype=i32), torch.tensor([0, 1], dtype=i32), torch.ones(1, dtype=i32)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    followed = k.clone().requires_grad_()
+    with pytest.raises(RuntimeError, match="cache k requires grad"):
+        ltk.attend(q, (followed, k, s, s), *batch)
+    with torch.no_grad(), pytest.raises(ValueError, match="device tensor"):     # the next check
+        ltk.attend(q, (followed, k, s, s), *batch)

@@ -1,0 +1,51 @@
+"""The paged cache's operators under autograd: they are forward only."""
+import pytest
+
+from tests.test_gpu_attend import _attend_case, _dev, _lists, _gen
+
+pytestmark = pytest.mark.gpu
+
+
+def _calls(lib):
+    """Per entry: its name, and the call with q (kv_append: k, v and q) taken from a dict."""
+    import torch
+    cache, table, cu, n, q = _attend_case([6], [90], 2, 4, 16, 64, 85)
+    dc, (dt, dcu, dn) = _dev(*cache), _dev(table, cu, n)
+    idx = _lists(_gen(86), [6], [90], 20).cuda()
+    sh, m, ln = lib.dsa_pack(idx, 90, 3)
+    k = torch.randn(6, 2, 64, generator=_gen(87)).bfloat16()
+    t = dict(q=q.cuda(), k=k.cuda(), v=k.cuda(), k_scale=dc[2], v_scale=dc[3], out=torch.empty_like(q).cuda(),
+             inv_freq=torch.ones(32, dtype=torch.float64, device="cuda"))
+    c = lambda x: (dc[0], dc[1], x["k_scale"], x["v_scale"])
+    return t, {
+        "kv_append": (("k", "v", "q", "k_scale", "v_scale", "inv_freq", "out"), lambda x: lib.kv_append(
+            x["k"], x["v"], c(x), dt, dcu, dn, x["inv_freq"], x["q"], q_out=x["out"])),
+        "attend": (("q", "k_scale", "v_scale", "out"), lambda x: lib.attend(x["q"], c(x), dt, dcu, dn, out=x["out"])),
+        "attend_selected": (("q", "out"), lambda x: lib.attend_selected(x["q"], c(x), dt, dcu, dn, idx, out=x["out"])),
+        "attend_packed": (("q", "out"), lambda x: lib.attend_packed(x["q"], c(x), dt, dn, sh, m, ln, 3, out=x["out"])),
+    }
+
+
+@pytest.mark.parametrize("entry", ["kv_append", "attend", "attend_selected", "attend_packed"])
+def test_tensors_that_autograd_follows_are_refused(lib, entry):
+    import torch
+    import torch.autograd.forward_ad as fwd
+    t, calls = _calls(lib)
+    names, call = calls[entry]
+    before = [x.clone() for x in t.values()]
+    for name in names:
+        x = dict(t)
+        x[name] = t[name].clone().requires_grad_()
+        with pytest.raises(RuntimeError, match="requires grad"):
+            call(x)
+        with fwd.dual_level():
+            x[name] = fwd.make_dual(t[name].clone(), torch.ones_like(t[name]))
+            with pytest.raises(RuntimeError, match="tangent"), torch.no_grad():
+                call(x)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(before, t.values()))   # nothing ran
+    want = call(t).clone()
+    with torch.no_grad():      # a followed tensor as an input is welcome here
+        got = call({**t, "q": t["q"].clone().requires_grad_()})
+    assert torch.equal(got, want) and not got.requires_grad
+    with torch.inference_mode():
+        assert torch.equal(call({**t, "q": t["q"].clone()}), want)
