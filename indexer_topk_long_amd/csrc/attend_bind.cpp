@@ -65,6 +65,12 @@ void without_grad(const at::Tensor& t, const char* name) {
         refuse(PyExc_RuntimeError, std::string(name) + " carries a tangent: the paged cache's operators are forward only");
 }
 
+// After a call has written a tensor in place: autograd sees that what it saved
+// of it has changed.  (Inference tensors count no versions.)
+void in_place(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // A contiguous device tensor of this type and shape (-1: any size), on the
 // cache's device where dev >= 0.
 const at::Tensor& tensor(PyObject* o, const char* name, Kind kind, std::initializer_list<int64_t> want, int dev) {
@@ -104,6 +110,10 @@ int32_t size32(int64_t n, const char* name) {
 struct Cache {
     ltk_kv_cache c;
     int dev;
+    PyObject* tensors[4];   // borrowed
+    void written() const {
+        for (PyObject* o : tensors) in_place(THPVariable_Unpack(o));
+    }
 };
 Cache cache_of(PyObject* o) {
     PyObject** e = PyTuple_Check(o) ? &PyTuple_GET_ITEM(o, 0) : nullptr;
@@ -115,6 +125,7 @@ Cache cache_of(PyObject* o) {
     const auto s = k.sizes();
     Cache r;
     r.dev = dev;
+    for (int i = 0; i < 4; ++i) r.tensors[i] = e[i];
     r.c.k = k.data_ptr();
     r.c.v = tensor(e[1], "cache v", kFp8, {s[0], s[1], s[2], s[3]}, dev).data_ptr();
     r.c.k_scale = static_cast<float*>(tensor(e[2], "k_scale", kF32, {s[0], s[1]}, dev).data_ptr());
@@ -220,6 +231,7 @@ struct Call {
     PyObject* result(int rc, const char* where, PyObject* out_o) {
         if (rc != LTK_OK) failed(rc, where);
         if (own_out) return THPVariable_Wrap(out);
+        in_place(out);
         Py_INCREF(out_o);
         return out_o;
     }
@@ -276,8 +288,10 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const On on(cache.dev);
         const int rc = litetopk_kv_append(&c, &b, k.data_ptr(), v.data_ptr(), q, T, Hq, f, rot, interleaved, q_out, on.stream);
         if (rc != LTK_OK) failed(rc, "litetopk_kv_append");
+        cache.written();
         if (q_o == Py_None) Py_RETURN_NONE;
         if (qo_o == Py_None) return THPVariable_Wrap(qo);
+        in_place(qo);
         Py_INCREF(qo_o);
         return qo_o;
     });

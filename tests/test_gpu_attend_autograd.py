@@ -49,3 +49,31 @@ def test_tensors_that_autograd_follows_are_refused(lib, entry):
     assert torch.equal(got, want) and not got.requires_grad
     with torch.inference_mode():
         assert torch.equal(call({**t, "q": t["q"].clone()}), want)
+
+
+def test_what_is_written_in_place_counts_versions(lib):
+    """The cache and given outputs, so that a backward pass which saved one of them before notices."""
+    import torch
+    t, calls = _calls(lib)
+    versions = lambda: {name: x._version for name, x in t.items()}
+    v0 = versions()
+    calls["attend"][1](t)
+    v1 = versions()
+    assert v1["out"] > v0["out"] and all(v1[n] == v0[n] for n in t if n != "out")
+    x = torch.ones(1, device="cuda", requires_grad=True)
+    y = (x * t["k_scale"]).sum()                     # saves the scales
+    calls["kv_append"][1](t)
+    v2 = versions()
+    assert all(v2[n] > v1[n] for n in ("out", "k_scale", "v_scale")) and v2["q"] == v1["q"] and v2["k"] == v1["k"]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    for entry in ("attend_selected", "attend_packed"):
+        before = t["out"]._version
+        calls[entry][1](t)
+        assert t["out"]._version > before
+    with torch.inference_mode():                     # no versions there
+        inf = {n: a.clone() for n, a in t.items()}
+        for _, call in calls.values():
+            call(inf)
+    for _, call in calls.values():
+        call(inf)                                    # .. nor outside it, of its tensors
