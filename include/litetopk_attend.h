@@ -111,8 +111,10 @@ int litetopk_kv_append(const ltk_kv_cache* cache, const ltk_kv_batch* batch, con
                        const void* q, int32_t T, int32_t Hq, const double* inv_freq, int32_t rot_dim,
                        int32_t interleaved, void* q_out, void* stream);
 
-/* Bytes of workspace an attend call of `kind` needs (at least 256; 0 for
- * invalid sizes).  `entries` bounds the keys a row reads: max_pages *
+/* Bytes of workspace that suffice for an attend call of `kind` and for every call
+ * of it with no more rows, sequences and entries and the same heads and group (at
+ * least 256; 0 for invalid sizes).  Smaller calls may need more than larger ones:
+ * their work is cut into more parts.  `entries` bounds the keys a row reads: max_pages *
  * page_size (attend), topk (selected) or cap (packed); `group` is the packed
  * call's (ignored otherwise). */
 size_t litetopk_attend_workspace_bytes(int32_t kind, int32_t T, int32_t Hq, int32_t n_kv_heads, int32_t head_dim,

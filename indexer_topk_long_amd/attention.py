@@ -78,7 +78,8 @@ def attend_packed(q, cache, page_table, kv_len, shared, masks, lens, group: int,
 
 def attend_workspace_bytes(kind: int, T: int, Hq: int, n_kv_heads: int, head_dim: int, n_seq: int,
                            entries: int, group: int = 0) -> int:
-    """Workspace bytes of an attend call (litetopk_attend_workspace_bytes)."""
+    """Workspace bytes that suffice for an attend call and for all with no more
+    rows, sequences and entries (litetopk_attend_workspace_bytes)."""
     f = library().litetopk_attend_workspace_bytes
     f.restype, f.argtypes = _c_sz, [_c_i32] * 6 + [_c_i64, _c_i32]
     n = f(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries, group)

@@ -588,7 +588,7 @@ struct ListLds {
 // (row, head) pairs of a group that share a list, and the units of 16 MT they
 // make: a group is one row with a list of its own, or `group` rows of a packed
 // list.
-__host__ __device__ __forceinline__ int list_tiles(int group, int G, int RT) { return (group * G + RT - 1) / RT; }   // (group G <= 2^31 - 256)
+__host__ __device__ __forceinline__ int list_tiles(int group, int G, int RT) { return (group * G + RT - 1) / RT; }
 
 // A unit is 16 MT (row, head) pairs of one group and key/value head, flattened
 // as elsewhere; its list is idx[row], or with PACKED the group's entries that
@@ -819,8 +819,57 @@ hipError_t launch_kind(int D, const AttendPlan& p, const AttendArgs& a, hipStrea
 
 }  // namespace
 
-AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group) {
+namespace {
+
+constexpr size_t part_bytes(int D) { return (size_t)(D + 2) * 16 * sizeof(float); }   // of 16 rows
+
+// attend_kernel with units of 16 mt rows; `units` bounds their number.
+AttendPlan few_rows_plan(int mt, int64_t units, int D, int64_t entries) {
     AttendPlan p{};
+    p.mt = mt;
+    // One range of key tiles a workgroup, and as many workgroups as run at
+    // once.  (64 heads on 8, D = 128, twice as many against that: one row
+    // over 65,536 tokens 37 against 33 us, 16 rows of as many sequences of up
+    // to 4,096 30 against 25, 256 rows 223 against 215; D = 64, 200 rows of 32
+    // heads, sequences of up to 3,000: 1,024 workgroups 81 us, 768 69, 512 76.)
+    const int64_t tiles = (entries + kTile - 1) / kTile;
+    const int64_t most = (units * (tiles + kUnitTiles) + kMinPer - 1) / kMinPer;
+    p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, 256 * waves_per_simd(D, mt)));
+    p.join = p.blocks > 1;
+    p.head_bytes = crossing_bytes(p.blocks);
+    p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * mt * part_bytes(D) : 0);
+    return p;
+}
+
+// Lists of `pairs` (row, head) pairs each: packed groups of many pairs go to the
+// tile kernels, attend_list_kernel takes the others.
+AttendPlan list_plan(bool packed, int64_t groups, int64_t pairs, int Hkv, int D, int64_t entries) {
+    if (packed && pairs > 96) return attend_tile_list_plan(groups, pairs, Hkv, D, entries);
+    AttendPlan p{};
+    p.mt = pairs > 16 ? 2 : 1;
+    const int64_t units = groups * ((pairs + 16 * p.mt - 1) / (16 * p.mt)) * Hkv;
+    // Lists are cut only while the units leave CUs with less than two workgroups,
+    // each part at least one 32-key tile a wave (580 units of 2,048 keys,
+    // D = 128: 54 us whole, 68 us cut in two and joined).
+    const int64_t most = std::max<int64_t>(1, (entries + kTile * kWaves - 1) / (kTile * kWaves));
+    p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, 512 / std::max<int64_t>(units, 1)));
+    p.blocks = units * p.splits;
+    p.join = p.splits > 1;
+    p.ws_bytes = std::max<size_t>(256, p.join ? (size_t)p.blocks * p.mt * part_bytes(D) : 0);
+    return p;
+}
+
+// Dense calls of fewer (row, head) pairs times keys of the table than this stay
+// with attend_kernel: units of 32 rows fill the card where those of 128 do not.
+// (Hq 32, Hkv 8, one sequence's first 512 tokens, 2^23: 20 against 38 us; Hq 64,
+// 128 rows after 1,920 tokens, 2^24: 31 against 46; Hq 32, 512 rows after 1,536,
+// 2^25: 57 against 49, eight sequences of 128 rows and 1,024 tokens, 2^25: 97
+// against 48.)
+constexpr int64_t kTileWork = (int64_t)1 << 24;
+
+}  // namespace
+
+AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group) {
     const int G = Hq / Hkv;
     // The tile kernels from 65 rows a sequence and head, or 97 (row, head) pairs
     // a group.  (Hq 64, Hkv 8, D 128, against these kernels: one sequence of
@@ -830,48 +879,47 @@ AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64
     // rows, 32 pairs, 116 against 59 us, of eight 75 against 66, of 12 89 against
     // 74, of 16 97 against 85; 2,048 rows of 2,048 keys in groups of 16, 128
     // pairs, 464 against 667; at D 64, 1,024 rows in groups of 16 80 against 97.)
-    // Dense calls of fewer (row, head) pairs times keys of the table than
-    // kTileWork stay here too: units of 32 rows fill the card where those of 128
-    // do not.  (Hq 32, Hkv 8, one sequence's first 512 tokens, 2^23: 20 against 38
-    // us; Hq 64, 128 rows after 1,920 tokens, 2^24: 31 against 46; Hq 32, 512 rows
-    // after 1,536, 2^25: 57 against 49, eight sequences of 128 rows and 1,024
-    // tokens, 2^25: 97 against 48.)
-    constexpr int64_t kTileWork = (int64_t)1 << 24;
-    if (kind == LTK_ATTEND ? (int64_t)T * G > 64 * (int64_t)std::max(n_seq, 1) && (int64_t)T * Hq * entries > kTileWork
-                           : kind == LTK_ATTEND_PACKED && group * G > 96)
-        return attend_tile_plan(kind, T, Hq, Hkv, D, n_seq, entries, group);
-    const size_t part = (size_t)(D + 2) * 16 * sizeof(float);   // of 16 rows
-    if (kind == LTK_ATTEND) {
-        // Rows that share keys: 16 or 32 to a unit.  (64 rows in one unit read
-        // the cache once but leave one wave on a SIMD: eight rows of 64 heads on
-        // 8 over 1,048,576 tokens took 529 us so, and 507 us as two units of 32
-        // whose ranges run side by side and meet in L2; with units of 16, 760.)
-        p.mt = (int64_t)T * G > 16 * (int64_t)std::max(n_seq, 1) ? 2 : 1;
-        // One range of key tiles a workgroup, and as many workgroups as run at
-        // once.  (64 heads on 8, D = 128, twice as many against that: one row
-        // over 65,536 tokens 37 against 33 us, 16 rows of as many sequences of up
-        // to 4,096 30 against 25, 256 rows 223 against 215; D = 64, 200 rows of 32
-        // heads, sequences of up to 3,000: 1,024 workgroups 81 us, 768 69, 512 76.)
-        const int64_t units = ((int64_t)T * G / (16 * p.mt) + n_seq) * Hkv, tiles = (entries + kTile - 1) / kTile;
-        const int64_t most = (units * (tiles + kUnitTiles) + kMinPer - 1) / kMinPer;
-        p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, 256 * waves_per_simd(D, p.mt)));
-        p.join = p.blocks > 1;
-        p.head_bytes = crossing_bytes(p.blocks);
-        p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * p.mt * part : 0);
-        return p;
+    if (kind == LTK_ATTEND_SELECTED) return list_plan(false, T, G, Hkv, D, entries);
+    if (kind == LTK_ATTEND_PACKED)
+        return list_plan(true, ((int64_t)T + group - 1) / group, (int64_t)group * G, Hkv, D, entries);
+    const int64_t rows = (int64_t)T * G, seqs = std::max(n_seq, 1), work = (int64_t)T * Hq * entries;
+    if (rows > 64 * seqs && work > kTileWork) {
+        const int waves = attend_tile_wide(rows, n_seq, work) ? 8 : 4;
+        return attend_tile_plan(waves, (rows / (32 * waves) + n_seq) * Hkv, D, entries);
     }
-    if (kind == LTK_ATTEND_SELECTED) group = 1;
-    p.mt = group * G > 16 ? 2 : 1;
-    const int64_t units = ((int64_t)T + group - 1) / group * list_tiles(group, G, 16 * p.mt) * Hkv;
-    // Lists are cut only while the units leave CUs with less than two workgroups,
-    // each part at least one 32-key tile a wave (580 units of 2,048 keys,
-    // D = 128: 54 us whole, 68 us cut in two and joined).
-    const int64_t most = std::max<int64_t>(1, (entries + kTile * kWaves - 1) / (kTile * kWaves));
-    p.splits = (int)std::min<int64_t>(most, std::max<int64_t>(1, 512 / std::max<int64_t>(units, 1)));
-    p.blocks = units * p.splits;
-    p.join = p.splits > 1;
-    p.ws_bytes = std::max<size_t>(256, p.join ? (size_t)p.blocks * p.mt * part : 0);
-    return p;
+    // Rows that share keys: 16 or 32 to a unit.  (64 rows in one unit read
+    // the cache once but leave one wave on a SIMD: eight rows of 64 heads on
+    // 8 over 1,048,576 tokens took 529 us so, and 507 us as two units of 32
+    // whose ranges run side by side and meet in L2; with units of 16, 760.)
+    const int mt = rows > 16 * seqs ? 2 : 1;
+    return few_rows_plan(mt, (rows / (16 * mt) + n_seq) * Hkv, D, entries);
+}
+
+// Calls of less work may need more: lists are cut while units are few, and the
+// dense kernels' parts differ.  For lists the largest over all numbers of groups
+// that are cut; for dense calls that of each kernel that a smaller call can reach,
+// each of which grows with rows, sequences and entries.
+size_t attend_workspace_bound(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group) {
+    const int G = Hq / Hkv;
+    size_t most = attend_plan(kind, T, Hq, Hkv, D, n_seq, entries, group).ws_bytes;
+    if (kind != LTK_ATTEND) {
+        const bool packed = kind == LTK_ATTEND_PACKED;
+        const int64_t groups = packed ? ((int64_t)T + group - 1) / group : T;
+        for (int64_t g = 1; g <= groups; ++g) {
+            const AttendPlan p = list_plan(packed, g, packed ? (int64_t)group * G : G, Hkv, D, entries);
+            most = std::max(most, p.ws_bytes);
+            if (p.blocks / p.splits > 256) break;   // (no list is cut from here on)
+        }
+        return most;
+    }
+    const int64_t rows = (int64_t)T * G, seqs = std::max(n_seq, 1), work = (int64_t)T * Hq * entries;
+    if (G <= 16 * seqs)
+        most = std::max(most, few_rows_plan(1, (std::min(rows / 16, seqs) + seqs) * Hkv, D, entries).ws_bytes);
+    if (rows > 16) most = std::max(most, few_rows_plan(2, (rows / 32 + seqs) * Hkv, D, entries).ws_bytes);
+    if (rows > 64 && work > kTileWork)
+        most = std::max(most, attend_tile_plan(4, (rows / 128 + seqs) * Hkv, D, entries).ws_bytes);
+    if (attend_tile_wide(rows, 1, work)) most = std::max(most, attend_tile_plan(8, (rows / 256 + seqs) * Hkv, D, entries).ws_bytes);
+    return most;
 }
 
 hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, void* ws, hipStream_t st) {

@@ -260,7 +260,12 @@ struct AttendPlan {
 };
 // `group` is the packed kind's (else 0).
 AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group);
-AttendPlan attend_tile_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group);
+// A bound of ws_bytes over all calls of no more rows, sequences and entries.
+size_t attend_workspace_bound(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group);
+// attend_tile.hip: units of 32 `waves` rows; `units` bounds their number.
+AttendPlan attend_tile_plan(int waves, int64_t units, int D, int64_t entries);
+AttendPlan attend_tile_list_plan(int64_t groups, int64_t pairs, int Hkv, int D, int64_t entries);
+bool attend_tile_wide(int64_t rows, int n_seq, int64_t work);
 
 hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, void* ws, hipStream_t st);
 hipError_t launch_attend_tile(int kind, int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st);

@@ -107,7 +107,7 @@ size_t litetopk_attend_workspace_bytes(int32_t kind, int32_t T, int32_t Hq, int3
         (head_dim != 64 && head_dim != 128) || (kind == LTK_ATTEND_PACKED && (group < 1 || group > 32 || !group_fits(group, Hq, n_kv_heads))))
         return 0;
     const AttendPlan p = attend_plan(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries, group);
-    return p.fits() ? p.ws_bytes : 0;
+    return p.fits() ? attend_workspace_bound(kind, T, Hq, n_kv_heads, head_dim, n_seq, entries, group) : 0;
 }
 
 int litetopk_attend(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void* q, int32_t T, int32_t Hq,

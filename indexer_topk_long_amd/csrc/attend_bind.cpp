@@ -209,9 +209,9 @@ struct Call {
 
     void workspace(int kind, int64_t entries, int group, PyObject* o) {
         const ltk_kv_cache& c = cache.c;
-        const size_t need =
-            litetopk_attend_workspace_bytes(kind, T, Hq, c.n_kv_heads, c.head_dim, batch.n_seq, entries, group);
         if (o == Py_None) {
+            const size_t need =
+                litetopk_attend_workspace_bytes(kind, T, Hq, c.n_kv_heads, c.head_dim, batch.n_seq, entries, group);
             // (sizes the library does not take: it says so itself, before it looks at the workspace)
             ws_bytes = need ? need : 256;
             ws = at::empty({(int64_t)ws_bytes}, on_device(cache.dev, at::kByte));
@@ -219,9 +219,6 @@ struct Call {
             if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "workspace must be a tensor");
             ws = THPVariable_Unpack(o);
             ws_bytes = (size_t)ws.numel() * ws.element_size();
-            if (ws_bytes < need)
-                refuse(PyExc_ValueError, "workspace too small: " + std::to_string(ws_bytes) + " bytes, " +
-                                             std::to_string(need) + " needed");
             if (!ws.is_cuda() || !ws.is_contiguous() || ws.get_device() != cache.dev)
                 refuse(PyExc_ValueError, "workspace must be a contiguous tensor on the cache's device");
         }
@@ -229,6 +226,9 @@ struct Call {
     }
 
     PyObject* result(int rc, const char* where, PyObject* out_o) {
+        if (rc == LTK_EWORKSPACE)
+            refuse(PyExc_ValueError, "workspace too small: " + std::to_string(ws_bytes) +
+                                         " bytes (attend_workspace_bytes gives what suffices)");
         if (rc != LTK_OK) failed(rc, where);
         if (own_out) return THPVariable_Wrap(out);
         in_place(out);

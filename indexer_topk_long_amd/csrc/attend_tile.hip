@@ -936,26 +936,29 @@ hipError_t launch_list(const AttendPlan& p, const AttendArgs& a, hipStream_t st)
 
 }  // namespace
 
-AttendPlan attend_tile_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group) {
+bool attend_tile_wide(int64_t rows, int n_seq, int64_t work) {
+    return rows >= kWide * (int64_t)std::max(n_seq, 1) && work >= kWideWork;
+}
+
+AttendPlan attend_tile_plan(int waves, int64_t units, int D, int64_t entries) {
     AttendPlan p{};
     p.tile = true;
-    const int G = Hq / Hkv;
-    if (kind == LTK_ATTEND) {
-        const bool wide = (int64_t)T * G >= kWide * (int64_t)std::max(n_seq, 1) && (int64_t)T * Hq * entries >= kWideWork;
-        p.waves = wide ? 8 : 4;
-        const int rows = 32 * p.waves;
-        const int64_t units = ((int64_t)T * G / rows + n_seq) * Hkv;
-        const int64_t most = (units * (entries + kKeys + kUnitKeys) + kMinKeys - 1) / kMinKeys;
-        // eight waves a CU; whole rounds of the XCDs
-        p.blocks = (std::max<int64_t>(1, std::min<int64_t>(most, 2048 / p.waves)) + 7) / 8 * 8;
-        p.join = true;
-        p.head_bytes = crossing_bytes(p.blocks);
-        p.ws_bytes = p.head_bytes + (p.join ? (size_t)p.blocks * 2 * rows * (D + 2) * sizeof(float) : 0);
-        return p;
-    }
+    p.waves = waves;
+    const int64_t most = (units * (entries + kKeys + kUnitKeys) + kMinKeys - 1) / kMinKeys;
+    // eight waves a CU; whole rounds of the XCDs
+    p.blocks = (std::max<int64_t>(1, std::min<int64_t>(most, 2048 / waves)) + 7) / 8 * 8;
+    p.join = true;
+    p.head_bytes = crossing_bytes(p.blocks);
+    p.ws_bytes = p.head_bytes + (size_t)p.blocks * 2 * 32 * waves * (D + 2) * sizeof(float);
+    return p;
+}
+
+AttendPlan attend_tile_list_plan(int64_t groups, int64_t pairs, int Hkv, int D, int64_t entries) {
+    AttendPlan p{};
+    p.tile = true;
     p.waves = kListWaves;
     constexpr int rows = kRows<kListWaves>;
-    const int64_t units = ((int64_t)T + group - 1) / group * ((group * G + rows - 1) / rows) * Hkv;
+    const int64_t units = groups * ((pairs + rows - 1) / rows) * Hkv;
     const int64_t most = (entries + kKeys - 1) / kKeys;
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 512 / std::max<int64_t>(units, 1)));
     p.blocks = units * p.splits;

@@ -84,3 +84,51 @@ def test_a_cache_that_autograd_follows_is_refused():
         ltk.attend(q, (followed, k, s, s), *batch)
     with torch.no_grad(), pytest.raises(ValueError, match="device tensor"):     # the next check
         ltk.attend(q, (followed, k, s, s), *batch)
+
+
+def _sizes(r):
+    Hkv = r.choice([1, 2, 4, 8])
+    Hq = Hkv * r.choice([1, 2, 4, 5, 8, 16, 40])
+    kind = r.randint(0, 2)
+    group = r.choice([1, 2, 8, 16, 32]) if kind == 2 else 0
+    n_seq = 1 if kind == 2 else r.choice([1, 2, 7, 64, 300])
+    log = lambda hi: int(round(2 ** r.uniform(0, hi)))
+    return kind, log(13), Hq, Hkv, r.choice([64, 128]), n_seq, log(16 if kind else 20), group
+
+
+def test_workspace_suffices_for_all_smaller_calls():
+    """One buffer sized for the largest call serves calls of fewer rows, sequences and entries."""
+    import random
+    r = random.Random(1)
+    for _ in range(3000):
+        kind, T, Hq, Hkv, D, n, e, group = _sizes(r)
+        size = ltk.attend_workspace_bytes(kind, T, Hq, Hkv, D, n, e, group)
+        for _ in range(6):
+            t, m, x = r.randint(1, T), r.randint(1, n), r.randint(1, e)
+            if r.random() < 0.3:
+                t = min(T, r.randint(1, 64))
+            assert ltk.attend_workspace_bytes(kind, t, Hq, Hkv, D, m, x, group) <= size, (kind, T, t, Hq, Hkv, D, n, m, e, x, group)
+
+
+def test_a_call_takes_what_the_size_function_gives():
+    """Also where a smaller call sets the size; without a device the call ends after its checks."""
+    import random
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: only where nothing can be launched")
+    r = random.Random(2)
+    for _ in range(1000):
+        kind, T, Hq, Hkv, D, n, e, group = _sizes(r)
+        page = 16
+        e = -(-e // page) * page if kind == 0 else e
+        size = ltk.attend_workspace_bytes(kind, T, Hq, Hkv, D, n, e, group)
+        kw = dict(T=T, Hq=Hq, n_kv_heads=Hkv, head_dim=D, n_seq=n, page_size=page, wsb=size)
+        kw.update({0: dict(max_pages=e // page), 1: dict(topk=e), 2: dict(cap=e, group=group)}[kind])
+        rc = _attend(["attend", "selected", "packed"][kind], **kw)
+        assert rc not in (EINVAL, EWS), kw
+
+
+def test_workspace_of_a_long_packed_call_serves_its_first_groups():
+    """64 heads on 8, groups of 16, lists of up to 32,768: 2,048 rows leave no list cut, 64 rows cut theirs."""
+    size = lambda T: ltk.attend_workspace_bytes(2, T, 64, 8, 128, 1, 32768, 16)
+    assert size(2048) >= size(512) >= size(64) > 1 << 24

@@ -264,3 +264,27 @@ def test_sparse_step(lib, T, Hkv, topk):
     qr = lib.kv_append(dev[1], dev[2], dc, dev[3], *_dev(cu, n, f), q=dev[0]).cpu()   # the same rows again: the same cache
     ref, tol, _ = ref_attend(qr, want, table, cu, n, D ** -0.5, idx=idx.cpu())
     _within(out, ref, tol, f"{T} rows")
+
+
+@pytest.mark.parametrize("G,group", [(8, 16), (2, 8)])
+def test_one_workspace_sized_for_the_largest_call(lib, G, group):
+    """A buffer of what the size function gives for the longest batch serves the short steps too, of every kind."""
+    import torch
+    import indexer_topk_long_amd as ltk
+    g = _gen(73)
+    L, T, Hkv, D, topk = 1500, 600, 4, 64, 700
+    cache, table, cu, n, q = _attend_case([T], [L], Hkv, G, 16, D, 74)
+    dc, dt, dn = _dev(*cache), table.cuda(), n.cuda()
+    idx = torch.stack([torch.randperm(L - T + 1, generator=g)[:topk] for _ in range(T)]).int().cuda()
+    sh, m, ln = ltk.dsa_pack(idx, L, group)
+    sizes = [ltk.attend_workspace_bytes(k, T, Hkv * G, Hkv, D, 1, e, gr)
+             for k, e, gr in ((0, table.shape[1] * 16, 0), (1, topk, 0), (2, group * topk, group))]
+    for t in (T, 1, 33, 3, 130, T):
+        r = slice(0, t)      # the first rows, as the sequence's last tokens
+        qt, ng = q[r].contiguous().cuda(), -(-t // group)
+        c = torch.tensor([0, t]).int().cuda()
+        calls = (lambda **k: ltk.attend(qt, dc, dt, c, dn, **k), lambda **k: ltk.attend_selected(qt, dc, dt, c, dn, idx[r], **k),
+                 lambda **k: ltk.attend_packed(qt, dc, dt, dn, sh[:ng], m[:ng], ln[:ng], group, **k))
+        for call, size in zip(calls, sizes):
+            ws = torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
+            assert torch.equal(call(workspace=ws), call()), t
