@@ -35,6 +35,7 @@ def sparse_step(q, k, v, cache, page_table, kv_len, index_q, index_k, index_w, t
     their packed selections (the same result, but for the order of the sums)
     where dsa_pack takes them: PACK_GROUP * topk <= 32768 and L <= 2^26.
 
+    Tensors are on one device; the step runs on that device's current stream.
     A refused call leaves the cache as it was: the append is the last step that
     can be refused.
     """
@@ -44,16 +45,17 @@ def sparse_step(q, k, v, cache, page_table, kv_len, index_q, index_k, index_w, t
                 f"out must be a contiguous bfloat16 tensor {tuple(q.shape)} on {q.device}")
     if scale is not None:   # finite, also times log2(e) in fp32
         _expect(abs(scale) * math.log2(math.e) <= torch.finfo(torch.float32).max, f"scale {scale} is out of range")
-    T, L, Hkv = q.shape[0], index_k.shape[0], k.shape[1]
-    at = torch.arange(T + 1, dtype=torch.int32, device=q.device)
-    cu = at[::max(T, 1)][:2].contiguous() if T else at.expand(2).contiguous()
-    pos = kv_len - T + at[:T]
-    idx = score_select(index_q, index_k, index_w, pos, topk, sample=sample, q_scale=index_q_scale,
-                       k_scale=index_k_scale, opts=opts)
-    packed = Hkv >= PACK_HEADS and T * Hkv >= PACK_WORK and PACK_GROUP * topk <= 32768 and L <= 1 << 26
-    if packed:
-        shared, masks, lens = dsa_pack(idx, L, PACK_GROUP)
-    qr = kv_append(k, v, cache, page_table, cu, kv_len, inv_freq, q=q, interleaved=interleaved)
-    if packed:
-        return attend_packed(qr, cache, page_table, kv_len, shared, masks, lens, PACK_GROUP, scale, out), idx
-    return attend_selected(qr, cache, page_table, cu, kv_len, idx, scale, out), idx
+    with torch.cuda.device_of(q):   # the selection runs on the current device's stream
+        T, L, Hkv = q.shape[0], index_k.shape[0], k.shape[1]
+        at = torch.arange(T + 1, dtype=torch.int32, device=q.device)
+        cu = at[::max(T, 1)][:2].contiguous() if T else at.expand(2).contiguous()
+        pos = kv_len - T + at[:T]
+        idx = score_select(index_q, index_k, index_w, pos, topk, sample=sample, q_scale=index_q_scale,
+                           k_scale=index_k_scale, opts=opts)
+        packed = Hkv >= PACK_HEADS and T * Hkv >= PACK_WORK and PACK_GROUP * topk <= 32768 and L <= 1 << 26
+        if packed:
+            shared, masks, lens = dsa_pack(idx, L, PACK_GROUP)
+        qr = kv_append(k, v, cache, page_table, cu, kv_len, inv_freq, q=q, interleaved=interleaved)
+        if packed:
+            return attend_packed(qr, cache, page_table, kv_len, shared, masks, lens, PACK_GROUP, scale, out), idx
+        return attend_selected(qr, cache, page_table, cu, kv_len, idx, scale, out), idx
