@@ -106,7 +106,8 @@ typedef enum {
  * (exact for a power of two, except for e4m3 subnormals).  A page begun with a
  * scale that is no power of two keeps it until it grows.  A page written from its first slot
  * starts a new scale.  Slots behind the last row are left as they are.
- * No page may receive rows from two sequences in one call. */
+ * No page may receive rows twice in one call: from two sequences, or at two places
+ * of a sequence's table. */
 int litetopk_kv_append(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void* k, const void* v,
                        const void* q, int32_t T, int32_t Hq, const double* inv_freq, int32_t rot_dim,
                        int32_t interleaved, void* q_out, void* stream);

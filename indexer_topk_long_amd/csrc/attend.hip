@@ -29,8 +29,8 @@
 // Two tiles a wave, one in use and one on its way: 8 KB a tile at D = 128, and
 // with two waves a SIMD 64 KB a CU on their way, which covers the latency of
 // memory.  64 decoding sequences of up to 16,384 tokens (64 heads on 8, D = 128,
-// 1.11 GB of cache) take 204 us, 5.4 TB/s (a copy reaches 5.0, reads alone 6.4);
-// the join adds 5.  Eight rows over 1,048,576 tokens (2.15 GB) take 500 to 540 us, 4.0 to
+// 1.11 GB of cache) take 202 us, 5.5 TB/s (a copy reaches 5.0, reads alone 6.4);
+// the join adds 5.  Eight rows over 1,048,576 tokens (2.15 GB) take 495 to 540 us, 4.0 to
 // 4.3 TB/s: each byte is converted for two units of 32 rows, and conversions,
 // exponentials and matrix instructions fill the issue slots.  145 rows on lists
 // of 2,048 keys each (four key/value heads) take 54 us, 4.9 TB/s of the lists'

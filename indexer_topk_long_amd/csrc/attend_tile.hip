@@ -15,20 +15,24 @@
 //    weights one lane holds after the first product, so weights go from the
 //    first product's result to the second's operand in place.
 // Two stages of LDS (64 KB at D = 128) and one barrier a step; the bytes of the
-// step after next are on their way in registers, and with eight waves those of
-// the step behind it too.  Two waves run on a SIMD: two workgroups of four waves
+// step after next are on their way in registers, and with eight waves or at
+// D = 64 those of the step behind it too, though not without a pause: there every
+// second step forms the constants of the pages at its head (PageLanes::scales,
+// whose branch the compiler turns into selects) and with them waits for every
+// load in flight.  Two waves run on a SIMD: two workgroups of four waves
 // or one of eight on a CU.
 //
 // Three chunks of up to 1,999 tokens after up to 16,384 (32 heads on 8, D = 128,
 // 7.9e11 operations) take 850 to 910 us, 870 to 930 TFLOP/s of the 1,200 that a
-// large matrix product reaches: matrix instructions take 42 % of the cycles and
-// vector instructions (conversions, exponentials, the statistics) 57 %, issued
-// between each other, at the 1.85 GHz that the card holds under that load.
+// large matrix product reaches, at the 1.85 GHz that the card holds under that
+// load: the matrix units are busy 42 % of the cycles, and 30 % of the waves'
+// cycles are waits, the one above among them.
 // 2,048 rows with a window of 4,096 (32 heads on 4, D = 64) take 116 to 131 us,
 // 530 to 590 TFLOP/s: half the products for the same exponentials.  Packed, 128
-// groups of 16 rows of 2,048 keys each (64 heads on 8, D = 128) take 457 to 484
+// groups of 16 rows of 2,048 keys each (64 heads on 8, D = 128) take 442 to 484
 // us: every key of a group's list, 2.3 times a row's own, goes through the
-// products of all its rows.
+// products of all its rows, and each wave reads every key's constants and masks
+// beside its operands (2.4 LDS instructions a matrix instruction, 1.1 above).
 #include <algorithm>
 #include <atomic>
 
@@ -106,8 +110,10 @@ __device__ __forceinline__ int per_step(int off) {
 // The thread's part of a step's bytes: two 16-byte key pieces, one value patch
 // (8 keys x 4 bytes), or both.  256 threads can hold the patches of D = 128 and
 // half as many pieces: four waves take both there.  At D = 64, and with eight
-// waves, the first waves take the values and the next the keys; waves w and
-// w + 4 share a SIMD, so with eight waves every SIMD has the same work.
+// waves, the first waves take the values and the next the keys.  Waves w and
+// w + 4 share a SIMD, so at D = 128 with eight waves every SIMD has the same
+// work; at D = 64 two waves take the values and two the keys, and of eight the
+// other four neither.
 template <int D, int NW>
 struct Part {
     static constexpr int kPatches = 2 * D;            // threads that take a value patch, and as many key pieces
@@ -547,7 +553,8 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 
     // step t computes from one stage while t + 1 is written to the other and
     // the loads of t + 2 are on their way; where a thread's bytes take 8
-    // registers, those of t + 3 too
+    // registers, those of t + 3 too (but see the pause above: even steps wait
+    // for all of them)
     if (t0 < t1) {
         constexpr bool kDeep = !Part<D, NW>::kBoth;
         Bytes ra, rb;
