@@ -833,7 +833,7 @@ AttendPlan few_rows_plan(int mt, int64_t units, int D, int64_t entries) {
     // to 4,096 30 against 25, 256 rows 223 against 215; D = 64, 200 rows of 32
     // heads, sequences of up to 3,000: 1,024 workgroups 81 us, 768 69, 512 76.)
     const int64_t tiles = (entries + kTile - 1) / kTile;
-    const int64_t most = (units * (tiles + kUnitTiles) + kMinPer - 1) / kMinPer;
+    const int64_t most = (std::min(units, kManyUnits) * (tiles + kUnitTiles) + kMinPer - 1) / kMinPer;
     p.blocks = std::max<int64_t>(1, std::min<int64_t>(most, 256 * waves_per_simd(D, mt)));
     p.join = p.blocks > 1;
     p.head_bytes = crossing_bytes(p.blocks);

@@ -262,6 +262,8 @@ struct AttendPlan {
 AttendPlan attend_plan(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group);
 // A bound of ws_bytes over all calls of no more rows, sequences and entries.
 size_t attend_workspace_bound(int kind, int T, int Hq, int Hkv, int D, int n_seq, int64_t entries, int group);
+// Units past this many change no launch: each is a range of keys at least.
+constexpr int64_t kManyUnits = 1 << 20;
 // attend_tile.hip: units of 32 `waves` rows; `units` bounds their number.
 AttendPlan attend_tile_plan(int waves, int64_t units, int D, int64_t entries);
 AttendPlan attend_tile_list_plan(int64_t groups, int64_t pairs, int Hkv, int D, int64_t entries);

@@ -951,7 +951,7 @@ AttendPlan attend_tile_plan(int waves, int64_t units, int D, int64_t entries) {
     AttendPlan p{};
     p.tile = true;
     p.waves = waves;
-    const int64_t most = (units * (entries + kKeys + kUnitKeys) + kMinKeys - 1) / kMinKeys;
+    const int64_t most = (std::min(units, kManyUnits) * (entries + kKeys + kUnitKeys) + kMinKeys - 1) / kMinKeys;
     // eight waves a CU; whole rounds of the XCDs
     p.blocks = (std::max<int64_t>(1, std::min<int64_t>(most, 2048 / waves)) + 7) / 8 * 8;
     p.join = true;

@@ -132,3 +132,11 @@ def test_workspace_of_a_long_packed_call_serves_its_first_groups():
     """64 heads on 8, groups of 16, lists of up to 32,768: 2,048 rows leave no list cut, 64 rows cut theirs."""
     size = lambda T: ltk.attend_workspace_bytes(2, T, 64, 8, 128, 1, 32768, 16)
     assert size(2048) >= size(512) >= size(64) > 1 << 24
+
+
+@pytest.mark.parametrize("T,G", [(1, 1), (1 << 10, 1), (1 << 9, 64)])
+def test_workspace_of_many_sequences_heads_and_positions(T, G):
+    """Units times key tiles pass 64 bits where the batch has 2^31 sequences: the launch is the largest one there too."""
+    size = lambda n, h: ltk.attend_workspace_bytes(0, T, h * G, h, 128, n, 2 ** 31 - 128)
+    for h in (1, 64, 1 << 15):
+        assert size(2 ** 31 - 1, h) == size(1 << 20, h) >= size(1 << 10, h)
