@@ -523,7 +523,8 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_k
     }
     __syncthreads();
     const int largest = uniform(ls.largest);
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(largest <= kWhole ? largest : kMinPer));
+    // (at least 1: a batch whose sequences have no rows has no work)
+    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(largest <= kWhole ? max(largest, 1) : kMinPer));
     const int64_t begin = (int64_t)blockIdx.x * per, end = min(begin + per, total);
     Crossing* crossing = reinterpret_cast<Crossing*>(a.head) + 2 * (int64_t)blockIdx.x;
     if (threadIdx.x == 0) crossing[0].n = crossing[1].n = 0;

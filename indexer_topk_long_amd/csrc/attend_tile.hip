@@ -647,7 +647,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
     }
     __syncthreads();
     const int largest = uniform(sc.largest);
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(largest <= kWhole ? largest : kMinKeys));
+    // (at least 1: a batch whose sequences have no rows has no work)
+    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(largest <= kWhole ? max(largest, 1) : kMinKeys));
     // Workgroups go to the eight XCDs in turn: each XCD takes a stretch of the
     // n8 ranges that hold work (so that the row tiles of one head read its keys
     // through one L2); the numbers behind those are the other workgroups'.

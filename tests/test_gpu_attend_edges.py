@@ -288,3 +288,35 @@ def test_one_workspace_sized_for_the_largest_call(lib, G, group):
         for call, size in zip(calls, sizes):
             ws = torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
             assert torch.equal(call(workspace=ws), call()), t
+
+
+@pytest.mark.parametrize("T,G,log2_work", [(3, 4, 0), (80, 4, 0), (80, 4, 24), (140, 4, 25)])
+@pytest.mark.parametrize("seqs", [1, 3, 600])
+def test_batches_whose_sequences_have_no_rows(lib, T, G, log2_work, seqs):
+    """Rows that belong to no sequence, as a captured step has them when its batch is empty: nothing is written; in the
+    next call over the same workspace they have sequences again."""
+    import torch
+    import indexer_topk_long_amd as ltk
+    say("no rows", T, G, log2_work, seqs)
+    Hkv, D = 2, 64
+    if log2_work:
+        T *= seqs                # (row, head) pairs for the many-row kernels
+    cache, table, cu, n, q = _attend_case([T] + [0] * (seqs - 1), [T + 200] + [90] * (seqs - 1), Hkv, G, 16, D, 76)
+    if log2_work:
+        table = _widen(table, 16, T, Hkv * G, log2_work)
+    dc, (dt, dcu, dn) = _dev(*cache), _dev(table, cu, n)
+    idx = torch.zeros(T, 7, dtype=torch.int32, device="cuda")
+    k = torch.ones(T, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    need = ltk.attend_workspace_bytes(0, T, Hkv * G, Hkv, D, seqs, table.shape[1] * 16)
+    ws = torch.randint(0, 256, (need,), dtype=torch.uint8, device="cuda")
+    want = lib.attend(q.cuda(), dc, dt, dcu, dn)
+    before = [t.clone() for t in dc]
+    for at in (0, T):
+        none = torch.full_like(dcu, at)
+        out = torch.full_like(q, 5.0).cuda()
+        lib.attend(q.cuda(), dc, dt, none, dn, out=out, workspace=ws)
+        lib.attend_selected(q.cuda(), dc, dt, none, dn, idx, out=out)
+        assert lib.kv_append(k, k, dc, dt, none, dn, None, q.cuda(), q_out=out) is out
+        assert bool((out == 5).all()), at
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(before, dc))
+        assert torch.equal(lib.attend(q.cuda(), dc, dt, dcu, dn, workspace=ws), want)
