@@ -110,9 +110,9 @@ int32_t size32(int64_t n, const char* name) {
 struct Cache {
     ltk_kv_cache c;
     int dev;
-    PyObject* tensors[4];   // borrowed
+    at::Tensor tensors[4];   // held: reading a later argument may run Python code that takes them from a list
     void written() const {
-        for (PyObject* o : tensors) in_place(THPVariable_Unpack(o));
+        for (const at::Tensor& t : tensors) in_place(t);
     }
 };
 Cache cache_of(PyObject* o) {
@@ -125,11 +125,11 @@ Cache cache_of(PyObject* o) {
     const auto s = k.sizes();
     Cache r;
     r.dev = dev;
-    for (int i = 0; i < 4; ++i) r.tensors[i] = e[i];
     r.c.k = k.data_ptr();
     r.c.v = tensor(e[1], "cache v", kFp8, {s[0], s[1], s[2], s[3]}, dev).data_ptr();
     r.c.k_scale = static_cast<float*>(tensor(e[2], "k_scale", kF32, {s[0], s[1]}, dev).data_ptr());
     r.c.v_scale = static_cast<float*>(tensor(e[3], "v_scale", kF32, {s[0], s[1]}, dev).data_ptr());
+    for (int i = 0; i < 4; ++i) r.tensors[i] = THPVariable_Unpack(e[i]);
     r.c.n_pages = size32(s[0], "the cache");
     r.c.n_kv_heads = size32(s[1], "the cache");
     r.c.page_size = size32(s[2], "the cache");

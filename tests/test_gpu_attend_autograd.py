@@ -77,3 +77,31 @@ def test_what_is_written_in_place_counts_versions(lib):
             call(inf)
     for _, call in calls.values():
         call(inf)                                    # .. nor outside it, of its tensors
+
+
+def test_a_cache_list_emptied_while_the_call_reads_its_arguments(lib):
+    """The call holds the tensors that it took from the list."""
+    import torch
+    cache, table, cu, n, q = _attend_case([2], [90], 2, 4, 16, 64, 88)
+    a = _dev(table, cu, n)
+    want = lib.attend(q.cuda(), _dev(*cache), *a, scale=0.25)
+    held = list(_dev(*cache))
+
+    class Scale:
+        def __float__(self):
+            held.clear()
+            self.other = [torch.full_like(t.cuda().view(torch.uint8), 0x7F) for t in cache]   # takes what was freed
+            return 0.25
+
+    assert torch.equal(lib.attend(q.cuda(), held, *a, scale=Scale()), want) and not held
+
+
+@pytest.mark.parametrize("at", [0, 1, 2, 3])
+@pytest.mark.parametrize("what", [None, 3, "k", [1.0]])
+def test_a_cache_entry_that_is_no_tensor_is_refused(lib, at, what):
+    cache, table, cu, n, q = _attend_case([2], [90], 2, 4, 16, 64, 88)
+    c = list(_dev(*cache))
+    c[at] = what
+    for wrong in (c, tuple(c)):
+        with pytest.raises(TypeError, match="must be a tensor"):
+            lib.attend(q.cuda(), wrong, *_dev(table, cu, n))
