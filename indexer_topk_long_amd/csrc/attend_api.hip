@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "attend.hpp"
+#include "litetopk_prompt.h"
 
 using namespace ltk;
 
@@ -149,6 +150,22 @@ int litetopk_attend_packed(const ltk_kv_cache* cache, const ltk_kv_batch* batch,
     a.group = group;
     a.cap = cap;
     return run_attend(LTK_ATTEND_PACKED, cache, a, cap, ws, ws_bytes, stream);
+}
+
+int litetopk_kv_read(const ltk_kv_cache* cache, const ltk_kv_batch* batch, int32_t T, int32_t type, void* k_out,
+                     void* v_out, void* stream) {
+    KvCache kc;
+    KvBatch kb;
+    int st = check_cache(cache, batch, T, true, kc, kb);
+    if (st != LTK_OK) return st;
+    if (type < LTK_ROWS_BF16 || type > LTK_ROWS_FP32) return LTK_EUNSUPPORTED;
+    if ((st = check_heads(T, kc.Hkv, kc.Hkv)) != LTK_OK) return st;
+    if ((T > 0 && (!k_out || !v_out)) || !aligned16(k_out) || !aligned16(v_out)) return LTK_EINVAL;
+    if (T == 0 || kb.n_seq == 0) return LTK_OK;
+    if ((st = litetopk_device_check()) != LTK_OK) return st;
+    return launch_kv_read(kc, kb, T, cache->head_dim, type, k_out, v_out, static_cast<hipStream_t>(stream)) == hipSuccess
+               ? LTK_OK
+               : LTK_EHIP;
 }
 
 }  // extern "C"

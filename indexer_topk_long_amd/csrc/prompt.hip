@@ -1,0 +1,271 @@
+// prompt.hip -- causal attention over packed 16-bit prompts on gfx950.
+#include <algorithm>
+
+#include "prompt.hpp"
+
+namespace ltk {
+
+namespace {
+
+constexpr int kKeys = 64;   // keys of a step
+
+template <int D>
+constexpr int kTileBytes = kKeys * D * 2;
+template <int D>
+constexpr int kStage = 2 * kTileBytes<D>;   // keys, then values
+
+__device__ __forceinline__ uint8_t* lds() {
+    extern __shared__ at_u32x4 prompt_lds[];
+    return reinterpret_cast<uint8_t*>(prompt_lds);
+}
+
+// Row tile of a unit: pairs [f0, f1) of sequence s and key/value head h.
+struct Unit {
+    PrSeq s;
+    int h, f0, f1, split;
+};
+
+// Copies rows key0 .. key0 + 63 of one head into a tile, the last row again
+// for those past the end.
+template <int D, int NW>
+__device__ __forceinline__ void copy_tile(const PrRows& x, int64_t row0, int h, int key0, int m, uint8_t* tile) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kRowsPer = 512 / D;              // rows of a wave's copy (1 KB)
+    constexpr int kCopies = kKeys / kRowsPer / NW;  // copies of a wave
+    const uint16_t* base = x.p + (row0 + key0) * x.row + (int64_t)h * x.head;
+    const int last = m - 1 - key0;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        const int r0 = (wave * kCopies + i) * kRowsPer, r = r0 + lane / (D / 8);
+        const int chunk = (lane % (D / 8)) ^ pr_swizzle<D>(r);
+        const uint32_t off = (uint32_t)min(r, last) * (uint32_t)x.row * 2u + (uint32_t)chunk * 16u;
+        lds_direct16_async(base, off, tile + r0 * (2 * D));
+    }
+}
+
+template <class E, int D, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
+    constexpr int RT = 32 * NW;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 31, g = lane >> 5;
+    const int h = (int)(blockIdx.x % a.Hkv);
+    const int64_t rest = blockIdx.x / a.Hkv;
+    const int split = (int)(rest % a.splits);
+    const int64_t un = rest / a.splits;
+    const int e = pr_find(a.cu, a, a.T, un, a.G, RT);
+    const PrSeq s = pr_seq(a, e);
+    const int64_t pairs = (int64_t)s.n * a.G;
+    const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));   // the longest first
+    if (tile < 0) return;
+    const int64_t f0 = tile * RT, f1 = min(f0 + RT, pairs);
+    const PrPair p0{uniform((int)(f0 / a.G)), uniform((int)(f0 % a.G))};
+    const int pos0 = s.pos0();
+
+    // the wave's rows
+    const int fw = 32 * wave;
+    const bool have = f0 + fw + c < f1;
+    const PrPair pr = pr_pair(a, p0, fw + c);
+    const int pos = have && s.in ? pos0 + pr.i : -1;
+    const int64_t row = have ? (int64_t)(s.r0 + pr.i) * a.Hq + h * a.G + pr.g : -1;
+    const int wlo = pos0 + pr_pair(a, p0, fw).i, whi = pos0 + (int)(min(f0 + fw + 31, f1 - 1) / a.G);
+    at_u32x4 q[D / 16];
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        q[j] = at_u32x4{0u, 0u, 0u, 0u};
+        if (have && s.in)
+            q[j] = *reinterpret_cast<const at_u32x4*>(a.q.p + (int64_t)(s.r0 + pr.i) * a.q.row +
+                                                      (int64_t)(h * a.G + pr.g) * a.q.head + 16 * j + 8 * g);
+    }
+    // keys of the unit: [lo, hi)
+    const int plo = pos0 + p0.i, phi = pos0 + uniform((int)((f1 - 1) / a.G));
+    const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
+    const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
+    int t0 = lo / kKeys, t1 = (hi + kKeys - 1) / kKeys;
+    const int per = uniform((t1 - t0 + a.splits - 1) / a.splits);
+    const int used = per > 0 ? (t1 - t0 + per - 1) / per : 1;
+    t0 += split * per;
+    t1 = min(t0 + per, t1);
+    if (split > 0 && t0 >= t1) return;
+
+    float m = 0.0f, over = -INFINITY, l = 0.0f;
+    pr_f32x16 o[D / 32];
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[t][r] = 0.0f;
+    const int from = a.window > 0 ? max(pos, 0) - a.window : -1;
+
+    auto copy = [&](int t) {
+        uint8_t* st = lds() + (t & 1) * kStage<D>;
+        copy_tile<D, NW>(a.k, s.k0, h, t * kKeys, s.m, st);
+        copy_tile<D, NW>(a.v, s.k0, h, t * kKeys, s.m, st + kTileBytes<D>);
+    };
+    if (t0 < t1) copy(t0);
+    pr_wait_copies();
+    __syncthreads();
+    for (int t = t0; t < t1; ++t) {
+        if (t + 1 < t1) copy(t + 1);
+        const uint8_t* kt = lds() + (t & 1) * kStage<D>;
+        const uint8_t* vt = kt + kTileBytes<D>;
+        const int key0 = t * kKeys;
+        pr_f32x16 x[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[b][r] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) x[b] = E::mfma(pr_read<D>(kt, 32 * b + c, 2 * j + g), q[j], x[b]);
+        }
+        const bool whole = key0 + kKeys - 1 <= wlo && (a.window <= 0 || key0 > whi - a.window);
+        float top = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float y = __builtin_fmaf(x[b][r], a.c2, -m);
+                const int key = key0 + 32 * b + 8 * (r / 4) + 4 * g + r % 4;
+                if (!whole) y = (key <= pos) & (key > from) ? y : -INFINITY;
+                x[b][r] = y;
+                top = fmaxf(top, y);
+            }
+        if (__ballot(top > over) != 0) {
+            const float up = pr_max_halves(top);
+            const bool move = up > over;
+            const float d = move ? up : 0.0f;
+            const float f = over == kSlack ? __builtin_amdgcn_exp2f(-d) : 1.0f;
+            m += d;
+            over = move ? kSlack : over;
+            l *= f;
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t) o[t] *= f;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[b][r] -= d;
+        }
+        at_u32x4 p[4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+                const float p0 = __builtin_amdgcn_exp2f(x[b][r]), p1 = __builtin_amdgcn_exp2f(x[b][r + 1]);
+                l += p0;
+                l += p1;
+                p[2 * b + r / 8][(r % 8) / 2] = E::pack(p0, p1);
+            }
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t) o[t] = E::mfma(pr_read_across<D>(vt, w, t), p[w], o[t]);
+        pr_wait_copies();
+        __syncthreads();
+    }
+    l = pr_sum_halves(l);
+    if (row < 0) return;
+    if (used <= 1) {
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        uint16_t* dst = a.out + row * D;
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<at_u32x2*>(dst + 32 * t + 8 * i + 4 * g) =
+                    at_u32x2{E::pack(o[t][4 * i] * inv, o[t][4 * i + 1] * inv),
+                             E::pack(o[t][4 * i + 2] * inv, o[t][4 * i + 3] * inv)};
+        if (a.lse && g == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -INFINITY;
+        return;
+    }
+    // a part: RT rows of D sums, then RT pairs (m, l)
+    float* part = a.part + ((un * a.Hkv + h) * a.splits + split) * (int64_t)(RT * (D + 2));
+    const int r = fw + c;
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<at_f32x4*>(part + (size_t)r * D + 32 * t + 8 * i + 4 * g) =
+                at_f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
+    if (g == 0) {
+        part[(size_t)RT * D + 2 * r] = l > 0.0f ? m : kNoRef;
+        part[(size_t)RT * D + 2 * r + 1] = l;
+    }
+}
+
+// Joins the parts of a unit, 8 rows a workgroup.
+template <class E, int D, int NW>
+__global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
+    constexpr int RT = 32 * NW;
+    const int h = (int)(blockIdx.x % a.Hkv);
+    const int64_t un = blockIdx.x / a.Hkv;
+    const int e = pr_find(a.cu, a, a.T, un, a.G, RT);
+    const PrSeq s = pr_seq(a, e);
+    const int64_t pairs = (int64_t)s.n * a.G;
+    const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));
+    if (tile < 0) return;
+    const int64_t f0 = tile * RT, f1 = min(f0 + RT, pairs);
+    const int plo = s.pos0() + (int)(f0 / a.G), phi = s.pos0() + (int)((f1 - 1) / a.G);
+    const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
+    const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
+    const int tiles = (hi + kKeys - 1) / kKeys - lo / kKeys, per = (tiles + a.splits - 1) / a.splits;
+    const int used = per > 0 ? (tiles + per - 1) / per : 1;
+    if (used <= 1) return;
+    const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
+    const int64_t f = f0 + r;
+    if (f >= f1) return;
+    const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(RT * (D + 2));
+    float m = kNoRef, l = 0.0f;
+    at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < used; ++i, part += RT * (D + 2)) m = fmaxf(m, part[(size_t)RT * D + 2 * r]);
+    part -= (int64_t)used * (RT * (D + 2));
+    for (int i = 0; i < used; ++i, part += RT * (D + 2)) {
+        const float f = __builtin_amdgcn_exp2f(part[(size_t)RT * D + 2 * r] - m);
+        l = __builtin_fmaf(f, part[(size_t)RT * D + 2 * r + 1], l);
+        o += *reinterpret_cast<const at_f32x4*>(part + (size_t)r * D + d) * f;
+    }
+    const int64_t row = (int64_t)(s.r0 + (int)(f / a.G)) * a.Hq + h * a.G + (int)(f % a.G);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    *reinterpret_cast<at_u32x2*>(a.out + row * D + d) =
+        at_u32x2{E::pack(o[0] * inv, o[1] * inv), E::pack(o[2] * inv, o[3] * inv)};
+    if (a.lse && d == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+constexpr int kWaves = 4;
+
+template <class E, int D>
+hipError_t launch(const PromptPlan& p, const PromptArgs& a, hipStream_t st) {
+    prompt_kernel<E, D, kWaves><<<(unsigned)p.fwd_blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);
+    if (a.splits > 1)
+        prompt_join_kernel<E, D, kWaves><<<dim3((unsigned)(p.fwd_blocks / a.splits), 4 * kWaves), 2 * D, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int window) {
+    PromptPlan p{};
+    const int64_t G = Hq / Hkv, rows = 32 * kWaves;
+    // Units are cut while they leave CUs with less than two workgroups, each part
+    // at least four steps.
+    const int64_t reach = window > 0 ? (int64_t)window + 2 * rows : S;   // keys that a unit's rows may see
+    const int64_t units = pr_units(T, G, 32 * kWaves, n_seq) * Hkv, steps = (std::min<int64_t>(reach, S) + kKeys - 1) / kKeys;
+    p.fwd_splits = (int)std::max<int64_t>(1, std::min<int64_t>(steps / 4, 512 / units));
+    p.fwd_blocks = units * p.fwd_splits;
+    p.fwd_bytes = std::max<size_t>(256, p.fwd_splits > 1 ? (size_t)p.fwd_blocks * rows * (D + 2) * 4 : 0);
+    const int64_t seen = window > 0 ? (int64_t)window + 2 * rows : T;   // rows that may see a unit's keys
+    const int64_t kv_units = pr_units(S, 1, 32 * kWaves, n_seq) * Hkv, kv_steps = (std::min<int64_t>(seen, T) * G + 63) / 64;
+    p.kv_splits = (int)std::max<int64_t>(1, std::min<int64_t>(kv_steps / 4, 512 / kv_units));
+    p.kv_blocks = kv_units * p.kv_splits;
+    p.delta_bytes = ((size_t)T * Hq * 4 + 255) / 256 * 256;
+    p.bwd_bytes = std::max<size_t>(256, p.delta_bytes + std::max(p.fwd_splits > 1 ? (size_t)p.fwd_blocks * rows * D * 4 : 0,
+                                                                 p.kv_splits > 1 ? (size_t)p.kv_blocks * rows * 2 * D * 4 : 0));
+    p.fits = grid_fits(std::max(p.fwd_blocks, p.kv_blocks), 64 * kWaves) && grid_fits((int64_t)T * Hq / 2 + 1, 16);
+    return p;
+}
+
+hipError_t launch_prompt(const PromptPlan& p, int type, int D, PromptArgs& a, void* ws, hipStream_t st) {
+    a.splits = p.fwd_splits;
+    a.part = static_cast<float*>(ws);
+    if (type == LTK_ROWS_BF16) return D == 64 ? launch<PrBf16, 64>(p, a, st) : launch<PrBf16, 128>(p, a, st);
+    return D == 64 ? launch<PrF16, 64>(p, a, st) : launch<PrF16, 128>(p, a, st);
+}
+
+}  // namespace ltk

@@ -1,0 +1,179 @@
+// prompt.hpp -- what the kernels over packed 16-bit prompts share: element
+// types, the batch as kernels see it, its cut into units, and the tiles in LDS.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "attend.hpp"
+#include "kernels_common.hpp"
+#include "litetopk_prompt.h"
+
+namespace ltk {
+
+typedef float pr_f32x16 __attribute__((ext_vector_type(16)));
+typedef short pr_i16x4 __attribute__((ext_vector_type(4)));
+typedef short pr_i16x8 __attribute__((ext_vector_type(8)));
+
+// Element types: rounding of two fp32, and the matrix product of 32 rows, 32
+// columns and 16 summands.  (Lane (c, g) = (lane % 32, lane / 32) holds the
+// summands 8 g .. 8 g + 7 of row or column c; of the result column c, rows
+// 8 (r / 4) + 4 g + r % 4.)
+struct PrBf16 {
+    static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_bf16(a, b); }
+    static __device__ __forceinline__ pr_f32x16 mfma(at_u32x4 a, at_u32x4 b, pr_f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(at_bf16x8, a), __builtin_bit_cast(at_bf16x8, b),
+                                                       c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return bf16_lo(w); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return bf16_hi(w); }
+};
+struct PrF16 {
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const at_f32x2 x{a, b};
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, at_f16x2));
+    }
+    static __device__ __forceinline__ pr_f32x16 mfma(at_u32x4 a, at_u32x4 b, pr_f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(at_f16x8, a), __builtin_bit_cast(at_f16x8, b), c,
+                                                      0, 0, 0);
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return (float)__builtin_bit_cast(at_f16x2, w)[0]; }
+    static __device__ __forceinline__ float hi(uint32_t w) { return (float)__builtin_bit_cast(at_f16x2, w)[1]; }
+};
+
+struct PrRows {
+    const uint16_t* p;
+    int64_t row, head;   // strides in elements
+};
+
+struct PromptArgs {
+    PrRows q, k, v, dout;
+    const uint16_t* out_in;   // backward: the forward call's out
+    uint16_t *out, *dq, *dk, *dv;
+    float* lse;
+    float* delta;             // backward: [T, Hq]
+    const int32_t *cu, *cu_k;
+    int n_seq, T, S, Hq, Hkv, G;
+    uint32_t div_g;           // ceil(2^32 / G); 0 for G == 1
+    float scale, c2;          // c2 = scale log2(e)
+    int window;
+    int splits;               // parts that a unit's keys (dk and dv: rows) are cut into
+    float* part;
+};
+
+// Quotient by G of x < G + 2^15 (exact while x (G - 1) < 2^32: larger groups divide).
+__device__ __forceinline__ int pr_div_g(const PromptArgs& a, int x) {
+    if (a.G == 1) return x;
+    if (a.G >= 1 << 15) return x / a.G;
+    return (int)__umulhi((uint32_t)x, a.div_g);
+}
+
+// The (row, head) pairs of a key/value head are numbered f = row * G + head of
+// the group.  A place among them, split once per tile; rows behind it follow by
+// a small quotient.
+struct PrPair {
+    int i, g;
+};
+__device__ __forceinline__ PrPair pr_pair(const PromptArgs& a, const PrPair& base, int off) {
+    const int x = base.g + off, i = pr_div_g(a, x);
+    return PrPair{base.i + i, x - i * a.G};
+}
+
+// Rows and keys of a stretch of the batch: [r0, r0 + n) and [k0, k0 + m), within
+// the tensors whatever cu holds.  Stretch 0 is what lies before the first
+// sequence, b + 1 is sequence b, n_seq + 1 what lies behind the last one: those
+// two have rows and keys that see nothing, so they are written as zeros.
+struct PrSeq {
+    int r0, n, k0, m;
+    bool in;   // a sequence
+    __device__ __forceinline__ int pos0() const { return m - n; }
+};
+__device__ __forceinline__ int pr_bound(const int32_t* cu, int e, int n_seq, int T) {
+    return e <= 0 ? 0 : e > n_seq + 1 ? T : min(max(cu[e - 1], 0), T);
+}
+__device__ __forceinline__ PrSeq pr_seq(const PromptArgs& a, int e) {
+    PrSeq s;
+    s.r0 = pr_bound(a.cu, e, a.n_seq, a.T);
+    s.n = max(pr_bound(a.cu, e + 1, a.n_seq, a.T) - s.r0, 0);
+    s.k0 = pr_bound(a.cu_k, e, a.n_seq, a.S);
+    s.m = max(pr_bound(a.cu_k, e + 1, a.n_seq, a.S) - s.k0, 0);
+    s.in = e >= 1 && e <= a.n_seq;
+    return s;
+}
+
+// Units of `per` rows of a stretch (each row counting mul), without a prefix
+// sum: stretch e has the numbers from  bound(e) mul / per + e  on, at least as
+// many as it can need; numbers past its own are empty.
+__device__ __forceinline__ int64_t pr_first(const int32_t* cu, const PromptArgs& a, int T, int e, int mul, int per) {
+    return (int64_t)pr_bound(cu, e, a.n_seq, T) * mul / per + e;
+}
+__device__ __forceinline__ int pr_find(const int32_t* cu, const PromptArgs& a, int T, int64_t u, int mul, int per) {
+    int lo = 0, hi = a.n_seq + 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pr_first(cu, a, T, mid, mul, per) <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+inline int64_t pr_units(int64_t T, int64_t mul, int per, int n_seq) { return T * mul / per + n_seq + 2; }
+
+// A tile in LDS: rows of D 16-bit values, whose 16-byte chunk x lies at chunk
+// x ^ swizzle(row), so that both ways of reading touch all banks: 16
+// consecutive rows at one chunk (operands along the row), and four consecutive
+// rows at four chunks (operands across rows, through the transposing read).
+// A 256-byte row (D = 128) fills the banks; of 128-byte rows two do.
+template <int D>
+__device__ __forceinline__ int pr_swizzle(int row) {
+    return D == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
+}
+// Operand along row `row`: its elements 16 j + 8 g ..
+template <int D>
+__device__ __forceinline__ at_u32x4 pr_read(const uint8_t* tile, int row, int chunk) {
+    return *reinterpret_cast<const at_u32x4*>(tile + row * (2 * D) + ((chunk ^ pr_swizzle<D>(row)) << 4));
+}
+// Operand across rows: element 32 t + c of the rows 16 w + 4 g + (0 .. 3) and
+// 16 w + 8 + 4 g + (0 .. 3), the rows whose scores lane (c, g) holds in
+// registers 8 (w % 2) .. 8 (w % 2) + 7 of a product over 32 rows.  The
+// transposing read takes four rows of 16 elements from 16 lanes (lane i: row
+// i / 4, elements 4 (i % 4) ..) and gives lane i element i of the four.
+template <int D>
+__device__ __forceinline__ at_u32x4 pr_read_across(const uint8_t* tile, int w, int t) {
+    const int lane = threadIdx.x & 63, i = lane & 15, half = (lane >> 4) & 1, g = lane >> 5;
+    const int row = 16 * w + 4 * g + (i >> 2), chunk = 4 * t + 2 * half + ((i & 3) >> 1), at8 = (i & 1) * 8;
+    typedef __attribute__((address_space(3))) pr_i16x4* LdsPtr;
+    const pr_i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (LdsPtr)(tile + row * (2 * D) + ((chunk ^ pr_swizzle<D>(row)) << 4) + at8));
+    const pr_i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (LdsPtr)(tile + (row + 8) * (2 * D) + ((chunk ^ pr_swizzle<D>(row + 8)) << 4) + at8));
+    const pr_i16x8 z{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    return __builtin_bit_cast(at_u32x4, z);
+}
+// Waits for the direct copies into LDS that the wave has issued.
+__device__ __forceinline__ void pr_wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ float pr_max_halves(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float pr_sum_halves(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+struct PromptPlan {
+    int64_t fwd_blocks;             // forward, and dq
+    int fwd_splits;
+    int64_t kv_blocks;              // dk and dv
+    int kv_splits;
+    size_t fwd_bytes, bwd_bytes;    // workspaces
+    size_t delta_bytes;             // of the backward pass's, before the parts
+    bool fits;
+};
+PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int window);
+hipError_t launch_prompt(const PromptPlan& p, int type, int D, PromptArgs& a, void* ws, hipStream_t st);
+hipError_t launch_prompt_backward(const PromptPlan& p, int type, int D, PromptArgs& a, void* ws, hipStream_t st);
+
+}  // namespace ltk

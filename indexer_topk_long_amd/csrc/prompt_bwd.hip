@@ -1,0 +1,483 @@
+// prompt_bwd.hip -- gradients of causal attention over packed 16-bit prompts on
+// gfx950.
+#include <algorithm>
+#include <atomic>
+
+#include "prompt.hpp"
+
+namespace ltk {
+
+namespace {
+
+constexpr int kKeys = 64;    // keys of a step (dq)
+constexpr int kPairs = 64;   // (row, head) pairs of a step (dk, dv)
+constexpr int kWaves = 4;
+constexpr int kUnit = 32 * kWaves;   // pairs (dq) or keys (dk, dv) of a unit
+
+template <int D>
+constexpr int kTileBytes = 64 * D * 2;
+template <int D>
+constexpr int kStage = 2 * kTileBytes<D>;
+
+__device__ __forceinline__ uint8_t* lds() {
+    extern __shared__ at_u32x4 prompt_bwd_lds[];
+    return reinterpret_cast<uint8_t*>(prompt_bwd_lds);
+}
+
+// Copies rows key0 .. key0 + 63 of one head into a tile, the last row again
+// for those past the end.
+template <int D, int NW>
+__device__ __forceinline__ void copy_tile(const PrRows& x, int64_t row0, int h, int key0, int m, uint8_t* tile) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kRowsPer = 512 / D;              // rows of a wave's copy (1 KB)
+    constexpr int kCopies = 64 / kRowsPer / NW;
+    const uint16_t* base = x.p + (row0 + key0) * x.row + (int64_t)h * x.head;
+    const int last = m - 1 - key0;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        const int r0 = (wave * kCopies + i) * kRowsPer, r = r0 + lane / (D / 8);
+        const int chunk = (lane % (D / 8)) ^ pr_swizzle<D>(r);
+        const uint32_t off = (uint32_t)min(r, last) * (uint32_t)x.row * 2u + (uint32_t)chunk * 16u;
+        lds_direct16_async(base, off, tile + r0 * (2 * D));
+    }
+}
+
+// delta = dout . out of every row and head.
+template <class E, int D>
+__global__ __launch_bounds__(256) void prompt_delta_kernel(PromptArgs a) {
+    constexpr int L = D / 8;
+    const int64_t r = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    if (r >= (int64_t)a.T * a.Hq) return;
+    const int t = (int)(r / a.Hq), h = (int)(r % a.Hq), d = 8 * (threadIdx.x % L);
+    const at_u32x4 x = *reinterpret_cast<const at_u32x4*>(a.out_in + r * D + d);
+    const at_u32x4 y = *reinterpret_cast<const at_u32x4*>(a.dout.p + t * a.dout.row + h * a.dout.head + d);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s = __builtin_fmaf(E::lo(x[i]), E::lo(y[i]), s);
+        s = __builtin_fmaf(E::hi(x[i]), E::hi(y[i]), s);
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    if (d == 0) a.delta[r] = s;
+}
+
+// dq: units are row tiles as in the forward pass.
+template <class E, int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a) {
+    constexpr int RT = kUnit;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 31, g = lane >> 5;
+    const int h = (int)(blockIdx.x % a.Hkv);
+    const int64_t rest = blockIdx.x / a.Hkv;
+    const int split = (int)(rest % a.splits);
+    const int64_t un = rest / a.splits;
+    const int e = pr_find(a.cu, a, a.T, un, a.G, RT);
+    const PrSeq s = pr_seq(a, e);
+    const int64_t pairs = (int64_t)s.n * a.G;
+    const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));   // the longest first
+    if (tile < 0) return;
+    const int64_t f0 = tile * RT, f1 = min(f0 + RT, pairs);
+    const PrPair p0{uniform((int)(f0 / a.G)), uniform((int)(f0 % a.G))};
+    const int pos0 = s.pos0();
+
+    const int fw = 32 * wave;
+    const bool have = f0 + fw + c < f1;
+    const PrPair pr = pr_pair(a, p0, fw + c);
+    const int pos = have && s.in ? pos0 + pr.i : -1;
+    const int64_t row = have ? (int64_t)(s.r0 + pr.i) * a.Hq + h * a.G + pr.g : -1;
+    const int wlo = pos0 + pr_pair(a, p0, fw).i, whi = pos0 + (int)(min(f0 + fw + 31, f1 - 1) / a.G);
+    at_u32x4 q[D / 16], dout[D / 16];
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        q[j] = dout[j] = at_u32x4{0u, 0u, 0u, 0u};
+        if (have && s.in) {
+            const int64_t t = s.r0 + pr.i, x = h * a.G + pr.g;
+            q[j] = *reinterpret_cast<const at_u32x4*>(a.q.p + t * a.q.row + x * a.q.head + 16 * j + 8 * g);
+            dout[j] = *reinterpret_cast<const at_u32x4*>(a.dout.p + t * a.dout.row + x * a.dout.head + 16 * j + 8 * g);
+        }
+    }
+    float lse2 = INFINITY, delta = 0.0f;
+    if (have && s.in) {
+        lse2 = a.lse[row] * 1.4426950408889634f;
+        lse2 = lse2 == -INFINITY ? INFINITY : lse2;   // (a row that sees no key: weights of 0)
+        delta = a.delta[row];
+    }
+    const int plo = pos0 + p0.i, phi = pos0 + uniform((int)((f1 - 1) / a.G));
+    const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
+    const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
+    int t0 = lo / kKeys, t1 = (hi + kKeys - 1) / kKeys;
+    const int per = uniform((t1 - t0 + a.splits - 1) / a.splits);
+    const int used = per > 0 ? (t1 - t0 + per - 1) / per : 1;
+    t0 += split * per;
+    t1 = min(t0 + per, t1);
+    if (split > 0 && t0 >= t1) return;
+
+    pr_f32x16 o[D / 32];
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[t][r] = 0.0f;
+    const int from = a.window > 0 ? max(pos, 0) - a.window : -1;
+
+    auto copy = [&](int t) {
+        uint8_t* st = lds() + (t & 1) * kStage<D>;
+        copy_tile<D, kWaves>(a.k, s.k0, h, t * kKeys, s.m, st);
+        copy_tile<D, kWaves>(a.v, s.k0, h, t * kKeys, s.m, st + kTileBytes<D>);
+    };
+    if (t0 < t1) copy(t0);
+    pr_wait_copies();
+    __syncthreads();
+    for (int t = t0; t < t1; ++t) {
+        if (t + 1 < t1) copy(t + 1);
+        const uint8_t* kt = lds() + (t & 1) * kStage<D>;
+        const uint8_t* vt = kt + kTileBytes<D>;
+        const int key0 = t * kKeys;
+        const bool whole = key0 + kKeys - 1 <= wlo && (a.window <= 0 || key0 > whi - a.window);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            pr_f32x16 x, y;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) x = E::mfma(pr_read<D>(kt, 32 * b + c, 2 * j + g), q[j], x);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) y = E::mfma(pr_read<D>(vt, 32 * b + c, 2 * j + g), dout[j], y);
+            at_u32x4 ds[2];
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+                float z[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float p = __builtin_fmaf(x[r + i], a.c2, -lse2);
+                    const int key = key0 + 32 * b + 8 * (r / 4) + 4 * g + r % 4 + i;
+                    if (!whole) p = (key <= pos) & (key > from) ? p : -INFINITY;
+                    z[i] = __builtin_amdgcn_exp2f(p) * (y[r + i] - delta);
+                }
+                ds[r / 8][(r % 8) / 2] = E::pack(z[0], z[1]);
+            }
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int t = 0; t < D / 32; ++t) o[t] = E::mfma(pr_read_across<D>(kt, 2 * b + w, t), ds[w], o[t]);
+        }
+        pr_wait_copies();
+        __syncthreads();
+    }
+    if (row < 0) return;
+    if (used <= 1) {
+        uint16_t* dst = a.dq + row * D;
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<at_u32x2*>(dst + 32 * t + 8 * i + 4 * g) =
+                    at_u32x2{E::pack(o[t][4 * i] * a.scale, o[t][4 * i + 1] * a.scale),
+                             E::pack(o[t][4 * i + 2] * a.scale, o[t][4 * i + 3] * a.scale)};
+        return;
+    }
+    float* part = a.part + ((un * a.Hkv + h) * a.splits + split) * (int64_t)(RT * D);
+    const int r = fw + c;
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<at_f32x4*>(part + (size_t)r * D + 32 * t + 8 * i + 4 * g) =
+                at_f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
+}
+
+// Sums the parts of a unit's dq, 8 rows a workgroup.
+template <class E, int D>
+__global__ __launch_bounds__(2 * D) void prompt_dq_join_kernel(PromptArgs a) {
+    constexpr int RT = kUnit;
+    const int h = (int)(blockIdx.x % a.Hkv);
+    const int64_t un = blockIdx.x / a.Hkv;
+    const int e = pr_find(a.cu, a, a.T, un, a.G, RT);
+    const PrSeq s = pr_seq(a, e);
+    const int64_t pairs = (int64_t)s.n * a.G;
+    const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));
+    if (tile < 0) return;
+    const int64_t f0 = tile * RT, f1 = min(f0 + RT, pairs);
+    const int plo = s.pos0() + (int)(f0 / a.G), phi = s.pos0() + (int)((f1 - 1) / a.G);
+    const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
+    const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
+    const int tiles = (hi + kKeys - 1) / kKeys - lo / kKeys, per = (tiles + a.splits - 1) / a.splits;
+    const int used = per > 0 ? (tiles + per - 1) / per : 1;
+    if (used <= 1) return;
+    const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
+    const int64_t f = f0 + r;
+    if (f >= f1) return;
+    const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(RT * D) + (size_t)r * D + d;
+    at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < used; ++i) o += *reinterpret_cast<const at_f32x4*>(part + (int64_t)i * (RT * D));
+    const int64_t row = (int64_t)(s.r0 + (int)(f / a.G)) * a.Hq + h * a.G + (int)(f % a.G);
+    *reinterpret_cast<at_u32x2*>(a.dq + row * D + d) =
+        at_u32x2{E::pack(o[0] * a.scale, o[1] * a.scale), E::pack(o[2] * a.scale, o[3] * a.scale)};
+}
+
+// What the dk and dv kernel knows of a step's pairs.
+struct PairInfo {
+    float lse2[kPairs], delta[kPairs];
+    int pos[kPairs];   // -1: no pair
+};
+template <int D>
+constexpr int kKvLds = 2 * kStage<D> + 2 * (int)sizeof(PairInfo);
+
+// Pairs [f0, f1) that may see keys [ka, kb) of a sequence.
+__device__ __forceinline__ void seeing(const PromptArgs& a, const PrSeq& s, int ka, int kb, int64_t& f0, int64_t& f1) {
+    const int pos0 = s.pos0();
+    const int i0 = max(ka - pos0, 0);
+    const int i1 = a.window > 0 ? (int)min((int64_t)s.n, (int64_t)kb - 1 + a.window - pos0) : s.n;
+    f0 = (int64_t)i0 * a.G;
+    f1 = s.in ? max((int64_t)i1 * a.G, f0) : f0;
+}
+
+// dk and dv: a unit is 128 keys of a key/value head, 32 a wave, whose rows of k
+// and v stay in registers; the pairs that see them pass through LDS.
+template <class E, int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 31, g = lane >> 5;
+    const int h = (int)(blockIdx.x % a.Hkv);
+    const int64_t rest = blockIdx.x / a.Hkv;
+    const int split = (int)(rest % a.splits);
+    const int64_t un = rest / a.splits;
+    const int e = pr_find(a.cu_k, a, a.S, un, 1, kUnit);
+    const PrSeq s = pr_seq(a, e);
+    const int64_t tile = un - pr_first(a.cu_k, a, a.S, e, 1, kUnit);   // (the first keys are seen by the most rows)
+    if (tile * kUnit >= s.m) return;
+    const int ka = (int)tile * kUnit, kb = min(ka + kUnit, s.m), pos0 = s.pos0();
+    const int kw = ka + 32 * wave, key = kw + c;
+    int64_t f0, f1;
+    seeing(a, s, ka, kb, f0, f1);
+    const int64_t steps_all = (f1 - f0 + kPairs - 1) / kPairs;
+    const int per = uniform((int)((steps_all + a.splits - 1) / a.splits));
+    const int used = per > 0 ? (int)((steps_all + per - 1) / per) : 1;
+    if (split > 0 && split >= used) return;
+    f0 += (int64_t)split * per * kPairs;
+    f1 = min(f0 + (int64_t)per * kPairs, f1);
+    const int steps = uniform((int)((f1 - f0 + kPairs - 1) / kPairs));
+
+    at_u32x4 kf[D / 16], vf[D / 16];
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        kf[j] = vf[j] = at_u32x4{0u, 0u, 0u, 0u};
+        if (key < kb && s.in) {
+            kf[j] = *reinterpret_cast<const at_u32x4*>(a.k.p + (int64_t)(s.k0 + key) * a.k.row + (int64_t)h * a.k.head +
+                                                       16 * j + 8 * g);
+            vf[j] = *reinterpret_cast<const at_u32x4*>(a.v.p + (int64_t)(s.k0 + key) * a.v.row + (int64_t)h * a.v.head +
+                                                       16 * j + 8 * g);
+        }
+    }
+    pr_f32x16 dk[D / 32], dv[D / 32];
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dk[t][r] = dv[t][r] = 0.0f;
+
+    PrPair at{uniform((int)(f0 / a.G)), uniform((int)(f0 % a.G))};   // the next step's first pair
+    PairInfo* info = reinterpret_cast<PairInfo*>(lds() + 2 * kStage<D>);
+    float n_lse = 0.0f, n_delta = 0.0f;
+    int n_pos = -1;
+    auto copy = [&](int t) {
+        uint8_t* st = lds() + (t & 1) * kStage<D>;
+        const int left = (int)min(f1 - f0 - (int64_t)t * kPairs, (int64_t)kPairs);   // pairs of the step
+        constexpr int kRowsPer = 512 / D, kCopies = kPairs / kRowsPer / kWaves;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int r0 = (wave * kCopies + i) * kRowsPer, r = r0 + lane / (D / 8);
+            const int chunk = (lane % (D / 8)) ^ pr_swizzle<D>(r);
+            const PrPair p = pr_pair(a, at, min(r, left - 1));
+            const int64_t y = s.r0 + p.i, x = h * a.G + p.g;
+            lds_direct16_async(a.q.p + y * a.q.row + x * a.q.head + 8 * chunk, st + r0 * (2 * D));
+            lds_direct16_async(a.dout.p + y * a.dout.row + x * a.dout.head + 8 * chunk, st + kTileBytes<D> + r0 * (2 * D));
+        }
+        if (threadIdx.x < kPairs) {
+            const PrPair p = pr_pair(a, at, min((int)threadIdx.x, left - 1));
+            const int64_t row = (int64_t)(s.r0 + p.i) * a.Hq + h * a.G + p.g;
+            n_lse = a.lse[row];
+            n_delta = a.delta[row];
+            n_pos = (int)threadIdx.x < left ? pos0 + p.i : -1;
+        }
+        const PrPair next = pr_pair(a, at, kPairs);
+        at = PrPair{uniform(next.i), uniform(next.g)};
+    };
+    auto store_info = [&](int t) {
+        if (threadIdx.x < kPairs) {
+            PairInfo& x = info[t & 1];
+            const float l = n_lse * 1.4426950408889634f;
+            x.lse2[threadIdx.x] = n_lse == -INFINITY ? INFINITY : l;
+            x.delta[threadIdx.x] = n_delta;
+            x.pos[threadIdx.x] = n_pos;
+        }
+    };
+    if (steps > 0) {
+        copy(0);
+        store_info(0);
+    }
+    pr_wait_copies();
+    __syncthreads();
+    for (int t = 0; t < steps; ++t) {
+        // first and last row of the step, before `at` moves on with the next copy
+        const int64_t ft = f0 + (int64_t)t * kPairs;
+        const int plo = pos0 + uniform((int)(ft / a.G)), phi = pos0 + uniform((int)((min(ft + kPairs, f1) - 1) / a.G));
+        const bool whole = kw + 31 <= plo && ft + kPairs <= f1 && (a.window <= 0 || kw > phi - a.window);
+        if (t + 1 < steps) copy(t + 1);
+        const uint8_t* qt = lds() + (t & 1) * kStage<D>;
+        const uint8_t* dt = qt + kTileBytes<D>;
+        const PairInfo& inf = info[t & 1];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            pr_f32x16 x, y;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) x = E::mfma(pr_read<D>(qt, 32 * b + c, 2 * j + g), kf[j], x);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) y = E::mfma(pr_read<D>(dt, 32 * b + c, 2 * j + g), vf[j], y);
+            at_u32x4 pf[2], ds[2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r0 = 32 * b + 8 * i + 4 * g;
+                const at_f32x4 lse2 = *reinterpret_cast<const at_f32x4*>(inf.lse2 + r0);
+                const at_f32x4 delta = *reinterpret_cast<const at_f32x4*>(inf.delta + r0);
+                float p[4], z[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p[r] = __builtin_fmaf(x[4 * i + r], a.c2, -lse2[r]);
+                if (!whole) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int pos = inf.pos[r0 + r];
+                        const int from = a.window > 0 ? max(pos, 0) - a.window : -1;
+                        p[r] = (key <= pos) & (key > from) ? p[r] : -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    p[r] = __builtin_amdgcn_exp2f(p[r]);
+                    z[r] = p[r] * (y[4 * i + r] - delta[r]);
+                }
+                pf[i / 2][2 * (i % 2)] = E::pack(p[0], p[1]);
+                pf[i / 2][2 * (i % 2) + 1] = E::pack(p[2], p[3]);
+                ds[i / 2][2 * (i % 2)] = E::pack(z[0], z[1]);
+                ds[i / 2][2 * (i % 2) + 1] = E::pack(z[2], z[3]);
+            }
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d) {
+                    dv[d] = E::mfma(pr_read_across<D>(dt, 2 * b + w, d), pf[w], dv[d]);
+                    dk[d] = E::mfma(pr_read_across<D>(qt, 2 * b + w, d), ds[w], dk[d]);
+                }
+        }
+        if (t + 1 < steps) store_info(t + 1);
+        pr_wait_copies();
+        __syncthreads();
+    }
+    if (key >= kb) return;
+    if (used <= 1) {
+        const int64_t row = (int64_t)(s.k0 + key) * a.Hkv + h;
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                *reinterpret_cast<at_u32x2*>(a.dk + row * D + 32 * t + 8 * i + 4 * g) =
+                    at_u32x2{E::pack(dk[t][4 * i] * a.scale, dk[t][4 * i + 1] * a.scale),
+                             E::pack(dk[t][4 * i + 2] * a.scale, dk[t][4 * i + 3] * a.scale)};
+                *reinterpret_cast<at_u32x2*>(a.dv + row * D + 32 * t + 8 * i + 4 * g) =
+                    at_u32x2{E::pack(dv[t][4 * i], dv[t][4 * i + 1]), E::pack(dv[t][4 * i + 2], dv[t][4 * i + 3])};
+            }
+        return;
+    }
+    // a part: 128 keys' dk, then their dv
+    float* part = a.part + ((un * a.Hkv + h) * a.splits + split) * (int64_t)(2 * kUnit * D) + (size_t)(32 * wave + c) * D;
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<at_f32x4*>(part + 32 * t + 8 * i + 4 * g) =
+                at_f32x4{dk[t][4 * i], dk[t][4 * i + 1], dk[t][4 * i + 2], dk[t][4 * i + 3]};
+            *reinterpret_cast<at_f32x4*>(part + (size_t)kUnit * D + 32 * t + 8 * i + 4 * g) =
+                at_f32x4{dv[t][4 * i], dv[t][4 * i + 1], dv[t][4 * i + 2], dv[t][4 * i + 3]};
+        }
+}
+
+// Sums the parts of a unit's dk and dv, 8 keys a workgroup.
+template <class E, int D>
+__global__ __launch_bounds__(2 * D) void prompt_dkv_join_kernel(PromptArgs a) {
+    const int h = (int)(blockIdx.x % a.Hkv);
+    const int64_t un = blockIdx.x / a.Hkv;
+    const int e = pr_find(a.cu_k, a, a.S, un, 1, kUnit);
+    const PrSeq s = pr_seq(a, e);
+    const int64_t tile = un - pr_first(a.cu_k, a, a.S, e, 1, kUnit);
+    if (tile * kUnit >= s.m) return;
+    const int ka = (int)tile * kUnit, kb = min(ka + kUnit, s.m);
+    int64_t f0, f1;
+    seeing(a, s, ka, kb, f0, f1);
+    const int64_t steps = (f1 - f0 + kPairs - 1) / kPairs;
+    const int per = (int)((steps + a.splits - 1) / a.splits), used = per > 0 ? (int)((steps + per - 1) / per) : 1;
+    if (used <= 1) return;
+    const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
+    if (ka + r >= kb) return;
+    const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(2 * kUnit * D) + (size_t)r * D + d;
+    at_f32x4 x{0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+    for (int i = 0; i < used; ++i, part += 2 * kUnit * D) {
+        x += *reinterpret_cast<const at_f32x4*>(part);
+        y += *reinterpret_cast<const at_f32x4*>(part + (size_t)kUnit * D);
+    }
+    const int64_t row = (int64_t)(s.k0 + ka + r) * a.Hkv + h;
+    *reinterpret_cast<at_u32x2*>(a.dk + row * D + d) =
+        at_u32x2{E::pack(x[0] * a.scale, x[1] * a.scale), E::pack(x[2] * a.scale, x[3] * a.scale)};
+    *reinterpret_cast<at_u32x2*>(a.dv + row * D + d) = at_u32x2{E::pack(y[0], y[1]), E::pack(y[2], y[3])};
+}
+
+// More than 64 KB of LDS is asked for once per device.
+template <class F>
+hipError_t allow_lds(F* kernel, int bytes, std::atomic<uint64_t>& allowed) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) & bit)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return hipSuccess;
+}
+
+template <class E, int D>
+hipError_t launch(const PromptPlan& p, PromptArgs& a, hipStream_t st) {
+    const int64_t rows = (int64_t)a.T * a.Hq;
+    constexpr int per = 256 / (D / 8);
+    if (rows > 0) prompt_delta_kernel<E, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
+    if (a.dq && rows > 0) {
+        a.splits = p.fwd_splits;
+        prompt_dq_kernel<E, D><<<(unsigned)p.fwd_blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);
+        if (a.splits > 1)
+            prompt_dq_join_kernel<E, D><<<dim3((unsigned)(p.fwd_blocks / a.splits), kUnit / 8), 2 * D, 0, st>>>(a);
+    }
+    if (a.dk && a.S > 0) {
+        a.splits = p.kv_splits;
+        if constexpr (kKvLds<D> > 65536) {
+            static std::atomic<uint64_t> allowed;
+            const hipError_t e = allow_lds(prompt_dkv_kernel<E, D>, kKvLds<D>, allowed);
+            if (e != hipSuccess) return e;
+        }
+        prompt_dkv_kernel<E, D><<<(unsigned)p.kv_blocks, 64 * kWaves, kKvLds<D>, st>>>(a);
+        if (a.splits > 1)
+            prompt_dkv_join_kernel<E, D><<<dim3((unsigned)(p.kv_blocks / a.splits), kUnit / 8), 2 * D, 0, st>>>(a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_prompt_backward(const PromptPlan& p, int type, int D, PromptArgs& a, void* ws, hipStream_t st) {
+    a.delta = static_cast<float*>(ws);
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.delta_bytes);
+    if (type == LTK_ROWS_BF16) return D == 64 ? launch<PrBf16, 64>(p, a, st) : launch<PrBf16, 128>(p, a, st);
+    return D == 64 ? launch<PrF16, 64>(p, a, st) : launch<PrF16, 128>(p, a, st);
+}
+
+}  // namespace ltk
