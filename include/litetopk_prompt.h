@@ -84,6 +84,30 @@ int litetopk_attend_prompt_backward(const ltk_prompt* p, const ltk_rows* q, cons
                                     const void* out, const float* lse, const ltk_rows* dout, void* dq, void* dk,
                                     void* dv, void* ws, size_t ws_bytes, void* stream);
 
+/* Causal attention over the cache (no window) for sequences that share their
+ * first tokens, as answers to one prompt do: the result of litetopk_attend, but
+ * the shared keys are read once for all rows of a group.
+ *
+ *  groups      [n_group + 1] int32, non-decreasing: group j is the sequences
+ *              groups[j] .. groups[j+1]-1; sequences in no group share nothing
+ *  shared_len  [n_group] int32: tokens that the group's sequences share (clamped
+ *              to the table).  Their keys are read through the page table of the
+ *              group's first sequence; those from shared_len on, which may lie
+ *              inside a page, through each sequence's own.  Every row of the group
+ *              sees all shared keys: they lie before the rows, shared_len <=
+ *              kv_len - rows for each of its sequences.
+ *
+ * The rest as for litetopk_attend.  Sums over the shared keys pass through the
+ * workspace in fp32. */
+int litetopk_attend_shared(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void* q, int32_t T, int32_t Hq,
+                           const int32_t* groups, const int32_t* shared_len, int32_t n_group, float scale, void* out,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace that suffices for that call and for all of no more rows, sequences,
+ * groups and entries (max_pages * page_size); 0 for invalid sizes. */
+size_t litetopk_attend_shared_workspace_bytes(int32_t T, int32_t Hq, int32_t n_kv_heads, int32_t head_dim, int32_t n_seq,
+                                              int32_t n_group, int64_t entries);
+
 /* Reads rows of the cache back: k_out and v_out [T, n_kv_heads, head_dim] of
  * `type`, contiguous, 16-byte aligned.  Row cu[b] + i holds the token at position
  * kv_len[b] - (cu[b+1] - cu[b]) + i of sequence b, as kv_append would place it:

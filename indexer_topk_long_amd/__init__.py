@@ -41,7 +41,7 @@ from .attention import (  # noqa: F401
     kv_append,
 )
 from .prefill import next_sample, prefill_chunked, prefill_workspace_bytes  # noqa: F401
-from .prompt import attend_prompt, kv_read  # noqa: F401
+from .prompt import attend_prompt, attend_shared, attend_shared_workspace_bytes, kv_read  # noqa: F401
 from .sparse import sparse_step  # noqa: F401
 
 __all__ = [
@@ -49,5 +49,5 @@ __all__ = [
     "Opts", "Stats", "LtkError", "next_sample", "prefill_chunked", "library", "exported_symbols",
     "dsa_pack", "dsa_gather", "prefill_workspace_bytes", "score_select_static", "unfused_retrieve",
     "kv_append", "attend", "attend_selected", "attend_packed", "attend_workspace_bytes",
-    "sparse_step", "attend_prompt", "kv_read",
+    "sparse_step", "attend_prompt", "attend_shared", "attend_shared_workspace_bytes", "kv_read",
 ]

@@ -194,7 +194,7 @@ __device__ __forceinline__ void tile_step(const KvTile<D>& t, Query query, const
 // The waves' states joined through LDS, then the unit's rows written: bf16
 // rows where this workgroup saw all of the unit's keys (part == NULL), else a
 // part.
-template <int D, int MT, class Row>
+template <int D, int MT, int PART = kAllKeys, class Row>
 __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT], float* sh, float* part, Row row_of) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
     constexpr int kStride = D + 4;   // floats per row in LDS: rows start 4 banks apart
@@ -233,7 +233,13 @@ __device__ __forceinline__ void finish(const AttendArgs& a, RowState<D> (&st)[MT
         }
         const int64_t row = row_of(mt * 16 + r);   // row * Hq + head, -1 past the unit
         if (row < 0) continue;
-        if (!part) {
+        if (PART == kSharedKeys && !part) {
+            float* dst = a.prior + row * (D + kPriorTail);
+#pragma unroll
+            for (int e = 0; e < D / 16; e += 4)
+                *reinterpret_cast<at_f32x4*>(dst + d0 + e) = at_f32x4{o[e], o[e + 1], o[e + 2], o[e + 3]};
+            if (d0 == 0) dst[D] = m, dst[D + 1] = sum;
+        } else if (!part) {
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
             uint32_t w[D / 32];
 #pragma unroll
@@ -290,23 +296,26 @@ struct SeqWork {
 
 // Key tiles of the rows at positions pos_lo .. pos_hi: [0, sink_tiles) and
 // from win_tile0 on, tiles in all; keys below n_sink or in [lo, hi) are seen.
+// (`own`: the first key that a sequence sees for itself.)
 struct KeyRange32 {
     int lo, hi, sink_tiles, win_tile0, tiles;
 };
-__device__ __forceinline__ KeyRange32 key_range(const AttendArgs& a, int pos_lo, int pos_hi) {
+template <int PART>
+__device__ __forceinline__ KeyRange32 key_range(const AttendArgs& a, int pos_lo, int pos_hi, int own) {
     KeyRange32 k;
     k.hi = min(max(pos_hi + 1, 0), a.bt.max_pages << a.c.page_shift);
     k.lo = a.window > 0 ? min(max(max(pos_lo, 0) - a.window + 1, 0), k.hi) : 0;
+    if constexpr (PART == kOwnKeys) k.lo = min(own, k.hi);
     k.sink_tiles = a.window > 0 ? (min(a.n_sink, k.lo) + kTile - 1) / kTile : 0;
     k.win_tile0 = max(k.lo / kTile, k.sink_tiles);
     k.tiles = k.sink_tiles + max((k.hi + kTile - 1) / kTile - k.win_tile0, 0);
     return k;
 }
 
-template <int MT>
+template <int MT, int PART>
 __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int b) {
     SeqWork w;
-    w.sr = seq_rows(a.bt, b, a.T);
+    w.sr = batch_rows<PART>(a, b);
     const int n = w.sr.r1 - w.sr.r0, end = w.sr.pos0 + n;
     w.row_tiles = (int)(((int64_t)n * a.G + 16 * MT - 1) / (16 * MT));
     // no row tile sees more: all tiles up to the last row's, or with a window
@@ -317,6 +326,8 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int b) {
         const int span = min(n, uniform((16 * MT + a.G - 1) / a.G) + 1);
         most = min(all, ((int64_t)a.n_sink + kTile - 1) / kTile + ((int64_t)a.window + span + kTile - 2) / kTile + 1);
     }
+    if constexpr (PART == kSharedKeys) most = (shared_keys(a, b) + kTile - 1) / kTile;
+    if constexpr (PART == kOwnKeys) most -= own_from(a, b) / kTile;
     w.tiles = max((int)most, 1);
     return w;
 }
@@ -336,10 +347,10 @@ struct Place {
 };
 
 // Work of sequence b (0 past the batch).
-template <int MT>
+template <int MT, int PART>
 __device__ __forceinline__ int64_t work_of(const AttendArgs& a, int b) {
-    if (b >= a.bt.n_seq) return 0;
-    const SeqWork w = seq_work<MT>(a, b);
+    if (b >= batch_size<PART>(a)) return 0;
+    const SeqWork w = seq_work<MT, PART>(a, b);
     return w.cost() * w.row_tiles * a.c.Hkv;
 }
 
@@ -381,12 +392,13 @@ __device__ __forceinline__ void load_queries(const AttendArgs& a, at_bf16x8 (&q)
 // ------------------------------------------------------------ dense keys
 
 // One unit's key tiles [t0, t1) against its rows [f0, f1) (flattened).
-template <int D, int MT>
+template <int D, int MT, int PART>
 __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& sr, int b, int h, int f0, int f1,
                                            const KeyRange32& kr, int t0, int t1, float* sh, float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
-    const int pos_lo = sr.pos0 + uniform(f0 / a.G), pos_hi = sr.pos0 + uniform((f1 - 1) / a.G);
+    const int pos_lo = PART == kSharedKeys ? kr.hi - 1 : sr.pos0 + uniform(f0 / a.G);
+    const int pos_hi = PART == kSharedKeys ? kr.hi - 1 : sr.pos0 + uniform((f1 - 1) / a.G);
     auto row_of = [&](int r) -> int64_t {
         const int f = f0 + r;
         if (f >= f1) return -1;
@@ -400,17 +412,30 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         row[mt] = row_of(mt * 16 + c);
-        pos[mt] = row[mt] < 0 ? -1 : sr.pos0 + (f0 + mt * 16 + c) / a.G;
+        pos[mt] = row[mt] < 0 ? -1 : PART == kSharedKeys ? kr.hi - 1 : sr.pos0 + (f0 + mt * 16 + c) / a.G;
         st[mt].m = 0.0f;
         st[mt].over = -INFINITY;
         st[mt].l = 0.0f;
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) st[mt].o[e] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // the first wave of the unit's first part begins from the shared keys' sums
+        if (PART == kOwnKeys && t0 == 0 && wave == 0 && row[mt] >= 0 && own_from(a, b) > 0) {
+            const float* src = a.prior + row[mt] * (D + kPriorTail);
+            if (src[D + 1] > 0.0f) {
+                st[mt].m = src[D];
+                st[mt].over = kSlack;
+                st[mt].l = g == 0 ? src[D + 1] : 0.0f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int e = 0; e < D / 16; ++e) st[mt].o[e][r] = src[(4 * g + r) * (D / 16) + e];
+            }
+        }
     }
     load_queries<D, MT>(a, q, row, g);
     auto query = [&](int mt, int j) { return q[mt][j]; };
 
-    const int32_t* table = a.bt.table + (size_t)b * a.bt.max_pages;
+    const int32_t* table = batch_table<PART>(a, b);
     const int page = 1 << a.c.page_shift;
     // the wave's steps are the tiles t0 + wave, t0 + wave + kWaves, ..; a lane
     // holds the page of one half of one of the next 32
@@ -463,7 +488,8 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     auto step = [&](KvTile<D>& t, const Where& w, const PageScale (&hs)[2]) {
         const int last = w.key0 + kTile - 1;
         const bool whole = w.pid[0] >= 0 && w.pid[1] >= 0 && last <= pos_lo && last < kr.hi &&
-                           (a.window <= 0 || w.key0 > pos_hi - a.window || last < a.n_sink);
+                           (a.window <= 0 || w.key0 > pos_hi - a.window || last < a.n_sink) &&
+                           (PART != kOwnKeys || w.key0 >= kr.lo);
         if (!whole) {
             // bytes of keys that no row sees may be NaN: their weights are 0, so the values must be finite
 #pragma unroll
@@ -478,7 +504,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
         }
         tile_step<D, MT>(t, query, hs, st, !whole, small, [&](int mt, int x, int i) {
             const int key = w.key0 + 16 * x + 4 * g + i;
-            const int from = a.window > 0 ? max(pos[mt], 0) - a.window : -1;
+            const int from = PART == kOwnKeys ? kr.lo - 1 : a.window > 0 ? max(pos[mt], 0) - a.window : -1;
             return (w.pid[x] >= 0) & (key <= pos[mt]) & (key < kr.hi) &
                    ((key > from) | (key < a.n_sink));
         });
@@ -502,11 +528,12 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
             if (n + 2 >= steps) break;
         }
     }
-    finish<D, MT>(a, st, sh, part, row_of);
+    finish<D, MT, PART>(a, st, sh, part, row_of);
 }
 
-template <int D, int MT>
+template <int D, int MT, int PART>
 __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_kernel(AttendArgs a) {
+    const int n_batch = batch_size<PART>(a);
     extern __shared__ __attribute__((aligned(16))) float sh[];
     __shared__ PlanLds ls;
     __shared__ Place place;
@@ -515,10 +542,10 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_k
     if (threadIdx.x == 0) ls.largest = 0;
     __syncthreads();
     int64_t total = 0, sum, w0 = 0, x0 = 0;
-    for (int b0 = 0; b0 < a.bt.n_seq; b0 += kPlanSeqs) {
-        w0 = work_of<MT>(a, b0 + threadIdx.x);
-        x0 = total + (a.bt.n_seq > 1 ? block_scan(w0, ls, sum) : (sum = work_of<MT>(a, 0)));
-        if (w0 > 0) atomicMax(&ls.largest, (int)min(seq_work<MT>(a, b0 + threadIdx.x).cost(), (int64_t)kWhole + 1));
+    for (int b0 = 0; b0 < n_batch; b0 += kPlanSeqs) {
+        w0 = work_of<MT, PART>(a, b0 + threadIdx.x);
+        x0 = total + (n_batch > 1 ? block_scan(w0, ls, sum) : (sum = work_of<MT, PART>(a, 0)));
+        if (w0 > 0) atomicMax(&ls.largest, (int)min(seq_work<MT, PART>(a, b0 + threadIdx.x).cost(), (int64_t)kWhole + 1));
         total += uniform(sum);
     }
     __syncthreads();
@@ -529,12 +556,12 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_k
     Crossing* crossing = reinterpret_cast<Crossing*>(a.head) + 2 * (int64_t)blockIdx.x;
     if (threadIdx.x == 0) crossing[0].n = crossing[1].n = 0;
     if (begin >= end) return;
-    if (a.bt.n_seq <= kPlanSeqs) {
+    if (n_batch <= kPlanSeqs) {
         if (x0 - w0 <= begin && begin < x0) place = Place{begin, x0 - w0, (int)threadIdx.x};
     } else {
         int64_t before = 0;
-        for (int b0 = 0; b0 < a.bt.n_seq; b0 += kPlanSeqs) {
-            const int64_t w = work_of<MT>(a, b0 + threadIdx.x), x = before + block_scan(w, ls, sum);
+        for (int b0 = 0; b0 < n_batch; b0 += kPlanSeqs) {
+            const int64_t w = work_of<MT, PART>(a, b0 + threadIdx.x), x = before + block_scan(w, ls, sum);
             if (x - w <= begin && begin < x) place = Place{begin, x - w, b0 + (int)threadIdx.x};
             before += uniform(sum);
             if (begin < before) break;
@@ -544,7 +571,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_k
     while (true) {
         const int b = uniform(place.b);
         const int64_t at = uniform(place.at), first = uniform(place.first);
-        const SeqWork w = seq_work<MT>(a, b);
+        const SeqWork w = seq_work<MT, PART>(a, b);
         const int units = w.row_tiles * a.c.Hkv, u = uniform((int)((at - first) / w.cost()));
         const int64_t us = first + u * w.cost(), tile0 = us + kUnitTiles;   // places of the unit and of its first tile
         const int64_t stop = min(end, us + w.cost());
@@ -563,13 +590,16 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_k
             if (u + 1 == units && stop == us + w.cost() && stop < end) {
                 n.first += units * w.cost();
                 do ++n.b;
-                while (seq_work<MT>(a, n.b).row_tiles == 0);
+                while (seq_work<MT, PART>(a, n.b).row_tiles == 0);
             }
             place = n;
         }
         if (t0 < t1) {   // (else the range ends before the unit's first tile)
-            const KeyRange32 kr = key_range(a, w.sr.pos0 + uniform(f0 / a.G), w.sr.pos0 + uniform((f1 - 1) / a.G));
-            dense_unit<D, MT>(a, w.sr, b, h, f0, f1, kr, t0, min(t1, kr.tiles), sh, part);
+            const int all = PART == kSharedKeys ? shared_keys(a, b) - 1 : 0;   // position that the shared keys end at
+            const KeyRange32 kr =
+                key_range<PART>(a, PART == kSharedKeys ? all : w.sr.pos0 + uniform(f0 / a.G),
+                                PART == kSharedKeys ? all : w.sr.pos0 + uniform((f1 - 1) / a.G), PART == kOwnKeys ? own_from(a, b) : 0);
+            dense_unit<D, MT, PART>(a, w.sr, b, h, f0, f1, kr, t0, min(t1, kr.tiles), sh, part);
         }
         __syncthreads();   // finish() has read its LDS
         if (uniform(place.at) >= end) return;
@@ -793,12 +823,20 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attend_list_join_kernel(Att
     join_wide<D, RT>(a, r, f % RT, used, slot0, slot0 + 1, 1);
 }
 
+template <int D, int MT, int PART>
+hipError_t launch_part(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
+    attend_kernel<D, MT, PART><<<(unsigned)p.blocks, 64 * kWaves, finish_lds<D, MT>(), st>>>(a);
+    if (p.join) launch_join<D, 16 * MT, PART>(p, a, st);
+    return hipGetLastError();
+}
+
 template <int KIND, int D, int MT>
-hipError_t launch(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
+hipError_t launch(const AttendPlan& p, const AttendArgs& a, hipStream_t st, int part) {
     const int64_t rows = (int64_t)a.T * a.Hq;
     if constexpr (KIND == LTK_ATTEND) {
-        attend_kernel<D, MT><<<(unsigned)p.blocks, 64 * kWaves, finish_lds<D, MT>(), st>>>(a);
-        if (p.join) launch_join<D, 16 * MT>(p, a, st);
+        return part == kAllKeys      ? launch_part<D, MT, kAllKeys>(p, a, st)
+               : part == kSharedKeys ? launch_part<D, MT, kSharedKeys>(p, a, st)
+                                     : launch_part<D, MT, kOwnKeys>(p, a, st);
     } else {
         constexpr size_t lds = std::max(finish_lds<D, MT>(), sizeof(ListLds));
         constexpr bool packed = KIND == LTK_ATTEND_PACKED;
@@ -809,13 +847,13 @@ hipError_t launch(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
 }
 
 template <int KIND, int D>
-hipError_t launch_rows(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
-    return p.mt == 1 ? launch<KIND, D, 1>(p, a, st) : launch<KIND, D, 2>(p, a, st);
+hipError_t launch_rows(const AttendPlan& p, const AttendArgs& a, hipStream_t st, int part) {
+    return p.mt == 1 ? launch<KIND, D, 1>(p, a, st, part) : launch<KIND, D, 2>(p, a, st, part);
 }
 
 template <int KIND>
-hipError_t launch_kind(int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
-    return D == 64 ? launch_rows<KIND, 64>(p, a, st) : launch_rows<KIND, 128>(p, a, st);
+hipError_t launch_kind(int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st, int part) {
+    return D == 64 ? launch_rows<KIND, 64>(p, a, st, part) : launch_rows<KIND, 128>(p, a, st, part);
 }
 
 }  // namespace
@@ -923,14 +961,14 @@ size_t attend_workspace_bound(int kind, int T, int Hq, int Hkv, int D, int n_seq
     return most;
 }
 
-hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, void* ws, hipStream_t st) {
+hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, void* ws, hipStream_t st, int part) {
     a.splits = p.splits;
     a.head = ws;
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.head_bytes);
-    if (p.tile) return launch_attend_tile(kind, D, p, a, st);
-    if (kind == LTK_ATTEND) return launch_kind<LTK_ATTEND>(D, p, a, st);
-    if (kind == LTK_ATTEND_SELECTED) return launch_kind<LTK_ATTEND_SELECTED>(D, p, a, st);
-    return launch_kind<LTK_ATTEND_PACKED>(D, p, a, st);
+    if (p.tile) return launch_attend_tile(kind, D, p, a, st, part);
+    if (kind == LTK_ATTEND) return launch_kind<LTK_ATTEND>(D, p, a, st, part);
+    if (kind == LTK_ATTEND_SELECTED) return launch_kind<LTK_ATTEND_SELECTED>(D, p, a, st, part);
+    return launch_kind<LTK_ATTEND_PACKED>(D, p, a, st, part);
 }
 
 }  // namespace ltk

@@ -186,7 +186,60 @@ struct AttendArgs {
     int splits;              // list kinds: key splits per unit
     void* head;              // attend: what the join needs to know
     float* part;             // partial rows and their statistics
+    // sequences that share their first tokens: group j is the sequences groups[j] .. groups[j + 1] - 1
+    const int32_t* groups;
+    const int32_t* shared_len;
+    int n_group;
+    float* prior;            // [T * Hq][D + kPriorTail]: every row's sums over its group's shared keys
 };
+
+// What a launch of the dense kernels attends to: all keys of a sequence; the
+// keys that a group shares, met by the rows of all its sequences and left as
+// sums in `prior`; or a sequence's own keys behind those, beginning from them.
+enum Part { kAllKeys, kSharedKeys, kOwnKeys };
+// A row of prior: D sums, the reference m, the divisor l.
+constexpr int kPriorTail = 4;
+
+__device__ __forceinline__ int group_at(const AttendArgs& a, int j) { return min(max(a.groups[j], 0), a.bt.n_seq); }
+__device__ __forceinline__ int shared_keys(const AttendArgs& a, int j) {
+    return min(max(a.shared_len[j], 0), a.bt.max_pages << a.c.page_shift);
+}
+// Keys that sequence b does not see for itself: those its group shares.
+__device__ __forceinline__ int own_from(const AttendArgs& a, int b) {
+    int lo = 0, hi = a.n_group - 1;
+    if (hi < 0) return 0;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (group_at(a, mid) <= b)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return group_at(a, lo) <= b && b < group_at(a, lo + 1) ? shared_keys(a, lo) : 0;
+}
+// The entries of the batch as a launch sees it: sequences, or groups with the
+// rows of all their sequences.
+template <int PART>
+__device__ __forceinline__ int batch_size(const AttendArgs& a) {
+    return PART == kSharedKeys ? a.n_group : a.bt.n_seq;
+}
+template <int PART>
+__device__ __forceinline__ SeqRows batch_rows(const AttendArgs& a, int b) {
+    if constexpr (PART == kSharedKeys) {
+        SeqRows s;
+        s.r0 = cu_at(a.bt, group_at(a, b), a.T);
+        s.r1 = max(cu_at(a.bt, group_at(a, b + 1), a.T), s.r0);
+        s.pos0 = 0;   // (rows see the shared keys whatever their positions are)
+        return s;
+    } else {
+        return seq_rows(a.bt, b, a.T);
+    }
+}
+template <int PART>
+__device__ __forceinline__ const int32_t* batch_table(const AttendArgs& a, int b) {
+    const int row = PART == kSharedKeys ? min(group_at(a, b), a.bt.n_seq - 1) : b;
+    return a.bt.table + (size_t)row * a.bt.max_pages;
+}
 
 // Page ids and scales of the next 64 groups of 16 keys, one a lane, so that a
 // loop over keys reads the page table and the scales once per 64 groups, a
@@ -271,7 +324,7 @@ AttendPlan attend_tile_plan(int waves, int64_t units, int D, int64_t entries);
 AttendPlan attend_tile_list_plan(int64_t groups, int64_t pairs, int Hkv, int D, int64_t entries);
 bool attend_tile_wide(int64_t rows, int n_seq, int64_t work);
 
-hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, void* ws, hipStream_t st);
-hipError_t launch_attend_tile(int kind, int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st);
+hipError_t launch_attend(int kind, int D, const AttendPlan& p, AttendArgs& a, void* ws, hipStream_t st, int part = kAllKeys);
+hipError_t launch_attend_tile(int kind, int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st, int part = kAllKeys);
 
 }  // namespace ltk

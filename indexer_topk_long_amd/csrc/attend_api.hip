@@ -2,6 +2,8 @@
 // checks and launches on the caller's stream.
 #include <math.h>
 
+#include <algorithm>
+
 #include "attend.hpp"
 #include "litetopk_prompt.h"
 
@@ -53,6 +55,11 @@ int run_attend(int kind, const ltk_kv_cache* cache, AttendArgs& a, int64_t entri
     if (st != LTK_OK) return st;
     return launch_attend(kind, cache->head_dim, p, a, ws, static_cast<hipStream_t>(stream)) == hipSuccess ? LTK_OK
                                                                                                           : LTK_EHIP;
+}
+
+// Sums over the shared keys of every row and head.
+size_t prior_bytes(int64_t T, int64_t Hq, int64_t D) {
+    return ((size_t)(T * Hq) * (size_t)(D + kPriorTail) * sizeof(float) + 255) / 256 * 256;
 }
 
 // The arguments every attend call shares.
@@ -150,6 +157,40 @@ int litetopk_attend_packed(const ltk_kv_cache* cache, const ltk_kv_batch* batch,
     a.group = group;
     a.cap = cap;
     return run_attend(LTK_ATTEND_PACKED, cache, a, cap, ws, ws_bytes, stream);
+}
+
+int litetopk_attend_shared(const ltk_kv_cache* cache, const ltk_kv_batch* batch, const void* q, int32_t T, int32_t Hq,
+                           const int32_t* groups, const int32_t* shared_len, int32_t n_group, float scale, void* out,
+                           void* ws, size_t ws_bytes, void* stream) {
+    AttendArgs a{};
+    int st = attend_args(cache, batch, q, T, Hq, scale, out, ws, true, a);
+    if (st != LTK_OK) return st;
+    if (n_group < 0 || (T > 0 && batch->n_seq > 0 && n_group > 0 && (!groups || !shared_len))) return LTK_EINVAL;
+    const int D = cache->head_dim;
+    const int64_t entries = (int64_t)batch->max_pages * cache->page_size;
+    if (n_group == 0) return run_attend(LTK_ATTEND, cache, a, entries, ws, ws_bytes, stream);
+    a.groups = groups;
+    a.shared_len = shared_len;
+    a.n_group = n_group;
+    const AttendPlan shared = attend_plan(LTK_ATTEND, T, Hq, a.c.Hkv, D, n_group, entries, 0);
+    const AttendPlan own = attend_plan(LTK_ATTEND, T, Hq, a.c.Hkv, D, batch->n_seq, entries, 0);
+    if (!shared.fits() || !own.fits()) return LTK_EINVAL;
+    const size_t prior = prior_bytes(T, Hq, D);
+    if (ws_bytes < prior + std::max(shared.ws_bytes, own.ws_bytes)) return LTK_EWORKSPACE;
+    if (T == 0 || batch->n_seq == 0) return LTK_OK;
+    if ((st = litetopk_device_check()) != LTK_OK) return st;
+    a.prior = static_cast<float*>(ws);
+    void* rest = static_cast<uint8_t*>(ws) + prior;   // (the second launch's parts may lie where the first one's did)
+    const hipStream_t on = static_cast<hipStream_t>(stream);
+    if (launch_attend(LTK_ATTEND, D, shared, a, rest, on, kSharedKeys) != hipSuccess) return LTK_EHIP;
+    return launch_attend(LTK_ATTEND, D, own, a, rest, on, kOwnKeys) == hipSuccess ? LTK_OK : LTK_EHIP;
+}
+
+size_t litetopk_attend_shared_workspace_bytes(int32_t T, int32_t Hq, int32_t n_kv_heads, int32_t head_dim, int32_t n_seq,
+                                              int32_t n_group, int64_t entries) {
+    const size_t own = litetopk_attend_workspace_bytes(LTK_ATTEND, T, Hq, n_kv_heads, head_dim, n_seq, entries, 0);
+    const size_t shared = litetopk_attend_workspace_bytes(LTK_ATTEND, T, Hq, n_kv_heads, head_dim, n_group, entries, 0);
+    return own && shared ? prior_bytes(T, Hq, head_dim) + std::max(own, shared) : 0;
 }
 
 int litetopk_kv_read(const ltk_kv_cache* cache, const ltk_kv_batch* batch, int32_t T, int32_t type, void* k_out,

@@ -48,9 +48,7 @@ struct Call {
         if (o == Py_None) {
             const size_t need =
                 litetopk_attend_workspace_bytes(kind, T, Hq, c.n_kv_heads, c.head_dim, batch.n_seq, entries, group);
-            // (sizes the library does not take: it says so itself, before it looks at the workspace)
-            ws_bytes = need ? need : 256;
-            ws = at::empty({(int64_t)ws_bytes}, on_device(cache.dev, at::kByte));
+            own_workspace(need);
         } else {
             if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "workspace must be a tensor");
             ws = THPVariable_Unpack(o);
@@ -58,6 +56,13 @@ struct Call {
             if (!ws.is_cuda() || !ws.is_contiguous() || ws.get_device() != cache.dev)
                 refuse(PyExc_ValueError, "workspace must be a contiguous tensor on the cache's device");
         }
+        ws_at = ws.data_ptr();
+    }
+
+    void own_workspace(size_t need) {
+        // (sizes the library does not take: it says so itself, before it looks at the workspace)
+        ws_bytes = need ? need : 256;
+        ws = at::empty({(int64_t)ws_bytes}, on_device(cache.dev, at::kByte));
         ws_at = ws.data_ptr();
     }
 
@@ -174,11 +179,35 @@ PyObject* attend_packed(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+PyObject* attend_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        expect_args(n, 10);
+        Call x(a[1], a[2], a[3], a[4], a[0], a[7], a[8]);
+        const at::Tensor& sl = tensor(a[6], "shared_len", kI32, {-1}, x.cache.dev);
+        const int32_t ng = size32(sl.size(0), "shared_len");
+        const at::Tensor& gr = tensor(a[5], "groups", kI32, {(int64_t)ng + 1}, x.cache.dev);
+        const ltk_kv_cache& c = x.cache.c;
+        if (a[9] == Py_None) {
+            const size_t need = litetopk_attend_shared_workspace_bytes(x.T, x.Hq, c.n_kv_heads, c.head_dim, x.batch.n_seq, ng,
+                                                                       (int64_t)x.batch.max_pages * c.page_size);
+            x.own_workspace(need);
+        } else {
+            x.workspace(LTK_ATTEND, 0, 0, a[9]);
+        }
+        const On on(x.cache.dev);
+        return x.result(litetopk_attend_shared(&c, &x.batch, x.q, x.T, x.Hq, static_cast<const int32_t*>(gr.data_ptr()),
+                                               static_cast<const int32_t*>(sl.data_ptr()), ng, x.scale, x.out.data_ptr(),
+                                               x.ws_at, x.ws_bytes, on.stream),
+                        "litetopk_attend_shared", a[8]);
+    });
+}
+
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr
 PyMethodDef kMethods[] = {{"kv_append", FAST(kv_append)},
                           {"attend", FAST(attend)},
                           {"attend_selected", FAST(attend_selected)},
                           {"attend_packed", FAST(attend_packed)},
+                          {"attend_shared", FAST(attend_shared)},
                           {"attend_prompt", FAST(ltk_bind::attend_prompt)},
                           {"kv_read", FAST(ltk_bind::kv_read)},
                           {nullptr, nullptr, 0, nullptr}};

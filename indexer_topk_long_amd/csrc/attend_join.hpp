@@ -69,14 +69,21 @@ __device__ __forceinline__ RowSum sum_parts(const AttendArgs& a, int at, int i0,
     }
     return s;
 }
-template <int D>
+template <int D, int PART>
 __device__ __forceinline__ void write_row(const AttendArgs& a, int64_t row, const RowSum& s) {
+    if constexpr (PART == kSharedKeys) {
+        float* p = a.prior + row * (D + kPriorTail);
+        const int d = 4 * (threadIdx.x % (D / 4));
+        *reinterpret_cast<at_f32x4*>(p + d) = s.o;
+        if (d == 0) p[D] = s.m, p[D + 1] = s.l;
+        return;
+    }
     const float inv = s.l > 0.0f ? 1.0f / s.l : 0.0f;
     *reinterpret_cast<at_u32x2*>(a.out + row * D + 4 * (threadIdx.x % (D / 4))) =
         at_u32x2{pack_bf16(s.o[0] * inv, s.o[1] * inv), pack_bf16(s.o[2] * inv, s.o[3] * inv)};
 }
 // One row by all lane groups, each every kJoinRows-th part.
-template <int D, int RT>
+template <int D, int RT, int PART = kAllKeys>
 __device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t row, int at, int n, int64_t slot0, int64_t slot1,
                                           int slot_step) {
     __shared__ float s_ml[kJoinRows][2];
@@ -97,7 +104,7 @@ __device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t row, int 
         all.l += by.divisor(s_ml[w][1]);
         all.o += *reinterpret_cast<const at_f32x4*>(&s_o[w][4 * lane]) * by.f;
     }
-    write_row<D>(a, row, all);
+    write_row<D, PART>(a, row, all);
 }
 
 // The workgroups (w, 0 .. join_hands<RT>() - 1) stand for workgroup w of the
@@ -108,7 +115,7 @@ template <int RT>
 constexpr int join_hands() {
     return RT > 64 ? RT / 32 : RT / kJoinRows;
 }
-template <int D, int RT>
+template <int D, int RT, int PART>
 __global__ __launch_bounds__(kJoinRows * D / 4) void attend_join_kernel(AttendArgs a) {
     const int grp = threadIdx.x / (D / 4);
 #pragma unroll
@@ -121,17 +128,17 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attend_join_kernel(AttendAr
         if (x.n < kJoinRows) {   // a row to a lane group
             for (int at = r0 + grp; at < r1; at += kJoinRows) {
                 const int64_t row = out_row(a, x.u, x.u.f0 + at);
-                if (row >= 0) write_row<D>(a, row, sum_parts<D, RT>(a, at, 0, 1, x.n, x.slot, slot1, 2));
+                if (row >= 0) write_row<D, PART>(a, row, sum_parts<D, RT>(a, at, 0, 1, x.n, x.slot, slot1, 2));
             }
         } else {
             for (int at = r0; at < r1; ++at)
-                join_wide<D, RT>(a, out_row(a, x.u, x.u.f0 + at), at, x.n, x.slot, slot1, 2);
+                join_wide<D, RT, PART>(a, out_row(a, x.u, x.u.f0 + at), at, x.n, x.slot, slot1, 2);
         }
     }
 }
-template <int D, int RT>
+template <int D, int RT, int PART>
 void launch_join(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
-    attend_join_kernel<D, RT><<<dim3((unsigned)p.blocks, join_hands<RT>()), kJoinRows * D / 4, 0, st>>>(a);
+    attend_join_kernel<D, RT, PART><<<dim3((unsigned)p.blocks, join_hands<RT>()), kJoinRows * D / 4, 0, st>>>(a);
 }
 
 }  // namespace

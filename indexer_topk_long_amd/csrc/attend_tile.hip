@@ -353,11 +353,22 @@ __device__ __forceinline__ void begin_rows(const AttendArgs& a, int64_t row, at_
 
 // Rows written as bf16 where the workgroup saw all of their keys (part ==
 // NULL), else as a part.
-template <int D, int NW>
+template <int D, int NW, int PART = kAllKeys>
 __device__ __forceinline__ void end_rows(const AttendArgs& a, int64_t row, const WaveState<D>& st, float* part) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
     const float l = sum_halves(st.l);
     if (row < 0) return;
+    if (PART == kSharedKeys && !part) {
+        float* dst = a.prior + row * (D + kPriorTail);
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<at_f32x4*>(dst + 32 * t + 8 * i + 4 * g) =
+                    at_f32x4{st.o[t][4 * i], st.o[t][4 * i + 1], st.o[t][4 * i + 2], st.o[t][4 * i + 3]};
+        if (g == 0) dst[D] = l > 0.0f ? st.m : kNoRef, dst[D + 1] = l;
+        return;
+    }
     if (!part) {
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         uint16_t* dst = a.out + row * D;
@@ -396,10 +407,10 @@ struct SeqLine {
     __device__ __forceinline__ int64_t cost(int i) const { return kUnitKeys + keys(i); }
     __device__ __forceinline__ int64_t before(int i) const { return i * (kUnitKeys + A) + Q * ((int64_t)i * (i - 1) / 2); }
 };
-template <int NW>
+template <int NW, int PART>
 __device__ __forceinline__ SeqLine seq_line(const AttendArgs& a, int b) {
     SeqLine s;
-    s.sr = seq_rows(a.bt, b, a.T);
+    s.sr = batch_rows<PART>(a, b);
     const int n = s.sr.r1 - s.sr.r0;
     s.tiles = (int)(((int64_t)n * a.G + kRows<NW> - 1) / kRows<NW>);
     s.Q = uniform((kRows<NW> + a.G - 1) / a.G);
@@ -408,6 +419,9 @@ __device__ __forceinline__ SeqLine seq_line(const AttendArgs& a, int b) {
     // a window's rows see at most the sinks, the window and the tiles' borders
     const int64_t win = (int64_t)a.n_sink + a.window + s.Q + 1 + 3 * kKeys;
     if (a.window > 0 && 2 * win < 2 * s.A + s.Q * (s.tiles - 1)) s.A = win, s.Q = 0;   // where that is less in all
+    if constexpr (PART == kSharedKeys) s.A = max(shared_keys(a, b), 1), s.Q = 0;
+    // (a range of own keys begins at a whole step)
+    if constexpr (PART == kOwnKeys) s.A = max(s.A - own_from(a, b) / kKeys * kKeys, (int64_t)1);
     return s;
 }
 
@@ -415,10 +429,12 @@ __device__ __forceinline__ SeqLine seq_line(const AttendArgs& a, int b) {
 struct KeyTiles {
     int lo, hi, sink_tiles, win_tile0, tiles;
 };
-__device__ __forceinline__ KeyTiles key_tiles(const AttendArgs& a, int pos_lo, int pos_hi) {
+template <int PART>
+__device__ __forceinline__ KeyTiles key_tiles(const AttendArgs& a, int pos_lo, int pos_hi, int own) {
     KeyTiles k;
     k.hi = min(max(pos_hi + 1, 0), a.bt.max_pages << a.c.page_shift);
     k.lo = a.window > 0 ? min(max(max(pos_lo, 0) - a.window + 1, 0), k.hi) : 0;
+    if constexpr (PART == kOwnKeys) k.lo = min(own, k.hi);
     k.sink_tiles = a.window > 0 ? (min(a.n_sink, k.lo) + kKeys - 1) / kKeys : 0;
     k.win_tile0 = max(k.lo / kKeys, k.sink_tiles);
     k.tiles = k.sink_tiles + max((k.hi + kKeys - 1) / kKeys - k.win_tile0, 0);
@@ -448,22 +464,36 @@ struct DenseScale {
     __device__ __forceinline__ uint32_t small(int hb) const { return s.small >> (2 * hb) & 3u; }
 };
 
-template <int D, int NW>
+template <int D, int NW, int PART>
 __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& sr, int b, const UnitRows& u,
                                            const KeyTiles& kt, int t0, int t1, float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
     const int fw = u.f0 + 32 * wave;                      // the wave's rows [fw, fw1)
     const int fw1 = min(fw + 32, u.f1);
-    const int pos_lo = sr.pos0 + uniform(fw / a.G), pos_hi = sr.pos0 + uniform((max(fw1, 1) - 1) / a.G);
+    const int pos_lo = PART == kSharedKeys ? kt.hi - 1 : sr.pos0 + uniform(fw / a.G);
+    const int pos_hi = PART == kSharedKeys ? kt.hi - 1 : sr.pos0 + uniform((max(fw1, 1) - 1) / a.G);
     const int64_t row = out_row(a, u, fw + c);
-    const int pos = row < 0 ? -1 : sr.pos0 + (fw + c) / a.G;
-    const int from = a.window > 0 ? max(max(pos, 0) - a.window, -1) : -1;   // the lane's row sees keys behind it, and the sinks
+    const int pos = row < 0 ? -1 : PART == kSharedKeys ? kt.hi - 1 : sr.pos0 + (fw + c) / a.G;
+    const int from = PART == kOwnKeys ? kt.lo - 1 : a.window > 0 ? max(max(pos, 0) - a.window, -1) : -1;   // the lane's row sees keys behind it, and the sinks
     at_bf16x8 q[D / 16];
     WaveState<D> st;
     begin_rows<D>(a, row, q, st);
+    // a unit's first part begins from the shared keys' sums
+    if (PART == kOwnKeys && t0 == 0 && row >= 0 && own_from(a, b) > 0) {
+        const float* src = a.prior + row * (D + kPriorTail);
+        if (src[D + 1] > 0.0f) {
+            st.m = src[D];
+            st.over = kSlack;
+            st.l = g == 0 ? src[D + 1] : 0.0f;
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) st.o[t][r] = src[32 * t + 8 * (r / 4) + 4 * g + r % 4];
+        }
+    }
 
-    const int32_t* table = a.bt.table + (size_t)b * a.bt.max_pages;
+    const int32_t* table = batch_table<PART>(a, b);
     const int page = 1 << a.c.page_shift;
     const Part<D, NW> p;
     auto key0_of = [&](int t) { return (t < kt.sink_tiles ? t : kt.win_tile0 + t - kt.sink_tiles) * kKeys; };
@@ -504,7 +534,8 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     };
     auto seen_by_all = [&](int key0, int ok, int lo, int hi) {   // every key of the step by rows at lo .. hi
         return ok == 15 && key0 + kKeys - 1 <= lo && key0 + kKeys <= kt.hi &&
-               (a.window <= 0 || key0 > hi - a.window || key0 + kKeys <= a.n_sink);
+               (a.window <= 0 || key0 > hi - a.window || key0 + kKeys <= a.n_sink) &&
+               (PART != kOwnKeys || key0 >= kt.lo);
     };
     // what a step's bytes need before they are converted
     auto settle_raw = [&](int t, int pages, Bytes& raw) {
@@ -590,7 +621,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
             for (int t = t0; t < t1; ++t) body(t, (t - t0) & 1, ra);
         }
     }
-    end_rows<D, NW>(a, row, st, part);
+    end_rows<D, NW, PART>(a, row, st, part);
 }
 
 template <int NW>
@@ -623,24 +654,25 @@ __device__ __forceinline__ int64_t scan_block(int64_t x, ScanLds<NW>& ls, int64_
     }
     return x;
 }
-template <int NW>
+template <int NW, int PART>
 __device__ __forceinline__ int64_t line_of(const AttendArgs& a, int b) {
-    if (b >= a.bt.n_seq) return 0;
-    const SeqLine s = seq_line<NW>(a, b);
+    if (b >= batch_size<PART>(a)) return 0;
+    const SeqLine s = seq_line<NW, PART>(a, b);
     return s.before(s.tiles) * a.c.Hkv;
 }
 
-template <int D, int NW>
+template <int D, int NW, int PART>
 __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
+    const int n_batch = batch_size<PART>(a);
     __shared__ ScanLds<NW> sc;
     if (threadIdx.x == 0) sc.largest = 0;
     __syncthreads();
     int64_t total = 0, sum, w0 = 0, x0 = 0;   // one look at up to 64 NW sequences gives the total and the place
-    for (int b0 = 0; b0 < a.bt.n_seq; b0 += 64 * NW) {
-        w0 = line_of<NW>(a, b0 + threadIdx.x);
-        x0 = total + (a.bt.n_seq > 1 ? scan_block<NW>(w0, sc, sum) : (sum = line_of<NW>(a, 0)));
+    for (int b0 = 0; b0 < n_batch; b0 += 64 * NW) {
+        w0 = line_of<NW, PART>(a, b0 + threadIdx.x);
+        x0 = total + (n_batch > 1 ? scan_block<NW>(w0, sc, sum) : (sum = line_of<NW, PART>(a, 0)));
         if (w0 > 0) {
-            const SeqLine s = seq_line<NW>(a, b0 + threadIdx.x);
+            const SeqLine s = seq_line<NW, PART>(a, b0 + threadIdx.x);
             atomicMax(&sc.largest, (int)min(s.cost(s.tiles - 1), (int64_t)kWhole + 1));
         }
         total += uniform(sum);
@@ -660,14 +692,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
     if (begin >= end) return;
     __shared__ Place place;
     int64_t before = 0;
-    for (int b0 = 0; b0 < a.bt.n_seq; b0 += 64 * NW) {
-        if (a.bt.n_seq > 64 * NW) {
-            w0 = line_of<NW>(a, b0 + threadIdx.x);
+    for (int b0 = 0; b0 < n_batch; b0 += 64 * NW) {
+        if (n_batch > 64 * NW) {
+            w0 = line_of<NW, PART>(a, b0 + threadIdx.x);
             x0 = before + scan_block<NW>(w0, sc, sum);
             before += uniform(sum);
         }
         if (x0 - w0 <= begin && begin < x0) {   // the sequence that the range begins in
-            const SeqLine s = seq_line<NW>(a, b0 + threadIdx.x);
+            const SeqLine s = seq_line<NW, PART>(a, b0 + threadIdx.x);
             const int64_t off = begin - (x0 - w0), head = s.before(s.tiles);
             const int h = (int)(off / head);
             int lo = 0, hi = s.tiles - 1;
@@ -686,7 +718,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
     while (true) {
         const int b = uniform(place.b), h = uniform(place.h), i = uniform(place.i);
         const int64_t at = uniform(place.at);
-        const SeqLine s = seq_line<NW>(a, b);
+        const SeqLine s = seq_line<NW, PART>(a, b);
         const int64_t us = uniform(place.first) + h * s.before(s.tiles) + s.before(i);
         const int64_t key0 = us + kUnitKeys, keys = s.keys(i), stop = min(end, us + s.cost(i));
         UnitRows u;
@@ -711,14 +743,17 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
                     n.h = 0;
                     n.first += a.c.Hkv * s.before(s.tiles);
                     n.b = n.at < end ? n.b + 1 : n.b;
-                    while (n.at < end && seq_line<NW>(a, n.b).tiles == 0) ++n.b;
+                    while (n.at < end && seq_line<NW, PART>(a, n.b).tiles == 0) ++n.b;
                 }
             }
             place = n;
         }
         if (k0 < k1) {   // (else the range ends before the unit's first key)
-            const KeyTiles kt = key_tiles(a, s.sr.pos0 + uniform(u.f0 / a.G), s.sr.pos0 + uniform((u.f1 - 1) / a.G));
-            dense_unit<D, NW>(a, s.sr, b, u, kt, (int)((k0 + kKeys - 1) / kKeys),
+            const int all = PART == kSharedKeys ? shared_keys(a, b) - 1 : 0;   // position that the shared keys end at
+            const KeyTiles kt =
+                key_tiles<PART>(a, PART == kSharedKeys ? all : s.sr.pos0 + uniform(u.f0 / a.G),
+                                PART == kSharedKeys ? all : s.sr.pos0 + uniform((u.f1 - 1) / a.G), PART == kOwnKeys ? own_from(a, b) : 0);
+            dense_unit<D, NW, PART>(a, s.sr, b, u, kt, (int)((k0 + kKeys - 1) / kKeys),
                               min((int)((k1 + kKeys - 1) / kKeys), kt.tiles), part);
         }
         __syncthreads();
@@ -913,11 +948,17 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void attend_tile_list_join_kerne
     join_wide<D, kRows<NW>>(a, r, f % kRows<NW>, used, slot0, slot0 + 1, 1);
 }
 
-template <int D, int NW>
-hipError_t launch_dense(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
-    attend_tile_kernel<D, NW><<<(unsigned)p.blocks, 64 * NW, 2 * kStageBytes<D>, st>>>(a);
-    if (p.join) launch_join<D, kRows<NW>>(p, a, st);
+template <int D, int NW, int PART>
+hipError_t launch_part(const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
+    attend_tile_kernel<D, NW, PART><<<(unsigned)p.blocks, 64 * NW, 2 * kStageBytes<D>, st>>>(a);
+    if (p.join) launch_join<D, kRows<NW>, PART>(p, a, st);
     return hipGetLastError();
+}
+template <int D, int NW>
+hipError_t launch_dense(const AttendPlan& p, const AttendArgs& a, hipStream_t st, int part) {
+    return part == kAllKeys      ? launch_part<D, NW, kAllKeys>(p, a, st)
+           : part == kSharedKeys ? launch_part<D, NW, kSharedKeys>(p, a, st)
+                                 : launch_part<D, NW, kOwnKeys>(p, a, st);
 }
 
 template <int D>
@@ -975,10 +1016,10 @@ AttendPlan attend_tile_list_plan(int64_t groups, int64_t pairs, int Hkv, int D, 
     return p;
 }
 
-hipError_t launch_attend_tile(int kind, int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st) {
+hipError_t launch_attend_tile(int kind, int D, const AttendPlan& p, const AttendArgs& a, hipStream_t st, int part) {
     if (kind != LTK_ATTEND) return D == 64 ? launch_list<64>(p, a, st) : launch_list<128>(p, a, st);
-    if (p.waves == 8) return D == 64 ? launch_dense<64, 8>(p, a, st) : launch_dense<128, 8>(p, a, st);
-    return D == 64 ? launch_dense<64, 4>(p, a, st) : launch_dense<128, 4>(p, a, st);
+    if (p.waves == 8) return D == 64 ? launch_dense<64, 8>(p, a, st, part) : launch_dense<128, 8>(p, a, st, part);
+    return D == 64 ? launch_dense<64, 4>(p, a, st, part) : launch_dense<128, 4>(p, a, st, part);
 }
 
 }  // namespace ltk

@@ -8,6 +8,7 @@ refuses LtkError.
 from __future__ import annotations
 
 from . import attention as _attention
+from ._binding import _c_i32, _c_i64, _c_sz, LtkError, library
 
 
 def _bind():
@@ -34,6 +35,33 @@ def attend_prompt(q, k, v, cu, cu_k=None, scale=None, window: int = 0, return_ls
     raises RuntimeError.  While a stream is captured, a leaf that an eager graph on
     another stream still holds is refused too."""
     return _bind().attend_prompt(q, k, v, cu, cu_k, scale, window, return_lse)
+
+
+def attend_shared(q, cache, page_table, cu, kv_len, groups, shared_len, scale=None, out=None, workspace=None):
+    """attend for sequences that share their first tokens, as answers to one
+    prompt do (litetopk_attend_shared): the same result without a window, but the
+    shared keys are read once for all rows of a group.
+
+    q, cache, page_table, cu and kv_len as for attend.  Group j is the sequences
+    groups[j] .. groups[j+1]-1 (int32 [n_group + 1], non-decreasing) and shares its
+    first shared_len[j] tokens (int32 [n_group]): they are read through the page
+    table of its first sequence, and lie before every row of the group.  Tokens
+    from shared_len[j] on, which may lie inside a page, are each sequence's own.
+    Sequences in no group share nothing.  Rows outside every sequence are not
+    written."""
+    return _bind().attend_shared(q, cache, page_table, cu, kv_len, groups, shared_len, scale, out, workspace)
+
+
+def attend_shared_workspace_bytes(T: int, Hq: int, n_kv_heads: int, head_dim: int, n_seq: int, n_group: int,
+                                  entries: int) -> int:
+    """Workspace bytes that suffice for an attend_shared call and for all with no
+    more rows, sequences, groups and entries (litetopk_attend_shared_workspace_bytes)."""
+    f = library().litetopk_attend_shared_workspace_bytes
+    f.restype, f.argtypes = _c_sz, [_c_i32] * 6 + [_c_i64]
+    n = f(T, Hq, n_kv_heads, head_dim, n_seq, n_group, entries)
+    if n == 0:
+        raise LtkError(-1, "litetopk_attend_shared_workspace_bytes")
+    return int(n)
 
 
 def kv_read(cache, page_table, cu, kv_len, T: int, dtype=None, out=None):
