@@ -52,7 +52,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
     const int64_t rest = blockIdx.x / a.Hkv;
     const int split = (int)(rest % a.splits);
     const int64_t un = rest / a.splits;
-    const int e = pr_find(a.cu, a, a.T, un, a.G, RT);
+    const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
     const PrSeq s = pr_seq(a, e);
     const int64_t pairs = (int64_t)s.n * a.G;
     const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));   // the longest first
@@ -100,13 +100,13 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
         copy_tile<D, NW>(a.k, s.k0, h, t * kKeys, s.m, st);
         copy_tile<D, NW>(a.v, s.k0, h, t * kKeys, s.m, st + kTileBytes<D>);
     };
+    const int along = pr_along<D>(), across = pr_across<D>();
     if (t0 < t1) copy(t0);
     pr_wait_copies();
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
         if (t + 1 < t1) copy(t + 1);
-        const uint8_t* kt = lds() + (t & 1) * kStage<D>;
-        const uint8_t* vt = kt + kTileBytes<D>;
+        const int stage = (t & 1) * kStage<D>, kt = pr_per_step(along) + stage, vt = pr_per_step(across) + stage + kTileBytes<D>;
         const int key0 = t * kKeys;
         pr_f32x16 x[2];
 #pragma unroll
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[b][r] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) x[b] = E::mfma(pr_read<D>(kt, 32 * b + c, 2 * j + g), q[j], x[b]);
+            for (int j = 0; j < D / 16; ++j) x[b] = E::mfma(pr_read<D>(lds(), kt, b, j), q[j], x[b]);
         }
         const bool whole = key0 + kKeys - 1 <= wlo && (a.window <= 0 || key0 > whi - a.window);
         float top = -INFINITY;
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
 #pragma unroll
         for (int w = 0; w < 4; ++w)
 #pragma unroll
-            for (int t = 0; t < D / 32; ++t) o[t] = E::mfma(pr_read_across<D>(vt, w, t), p[w], o[t]);
+            for (int t = 0; t < D / 32; ++t) o[t] = E::mfma(pr_read_across<D>(lds(), vt, w, t), p[w], o[t]);
         pr_wait_copies();
         __syncthreads();
     }
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
     constexpr int RT = 32 * NW;
     const int h = (int)(blockIdx.x % a.Hkv);
     const int64_t un = blockIdx.x / a.Hkv;
-    const int e = pr_find(a.cu, a, a.T, un, a.G, RT);
+    const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
     const PrSeq s = pr_seq(a, e);
     const int64_t pairs = (int64_t)s.n * a.G;
     const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));

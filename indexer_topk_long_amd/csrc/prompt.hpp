@@ -107,14 +107,18 @@ __device__ __forceinline__ PrSeq pr_seq(const PromptArgs& a, int e) {
 __device__ __forceinline__ int64_t pr_first(const int32_t* cu, const PromptArgs& a, int T, int e, int mul, int per) {
     return (int64_t)pr_bound(cu, e, a.n_seq, T) * mul / per + e;
 }
-__device__ __forceinline__ int pr_find(const int32_t* cu, const PromptArgs& a, int T, int64_t u, int mul, int per) {
-    int lo = 0, hi = a.n_seq + 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pr_first(cu, a, T, mid, mul, per) <= u)
-            lo = mid;
-        else
-            hi = mid - 1;
+// The stretch of number u, by all lanes of a wave: 64 stretches, or stretches of
+// stretches, at a look (bisection would be a chain of dependent loads: 16
+// sequences of up to 2,039 rows 288 us with it, ... without).
+template <int PER>
+__device__ __forceinline__ int pr_find(const int32_t* cu, const PromptArgs& a, int T, int64_t u, int mul) {
+    const int lane = threadIdx.x & 63, all = a.n_seq + 2;
+    int lo = 0, step = 1;
+    while (step < (all + 63) / 64) step *= 64;
+    for (; step >= 1; step /= 64) {
+        const int e = lo + lane * step;
+        const uint64_t at = __ballot(e < all && pr_first(cu, a, T, e, mul, PER) <= u);
+        lo += at ? (63 - __clzll((long long)at)) * step : 0;
     }
     return lo;
 }
@@ -129,25 +133,41 @@ template <int D>
 __device__ __forceinline__ int pr_swizzle(int row) {
     return D == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
 }
-// Operand along row `row`: its elements 16 j + 8 g ..
-template <int D>
-__device__ __forceinline__ at_u32x4 pr_read(const uint8_t* tile, int row, int chunk) {
-    return *reinterpret_cast<const at_u32x4*>(tile + row * (2 * D) + ((chunk ^ pr_swizzle<D>(row)) << 4));
+// Operands are read at a lane's place in a tile (an offset from the start of
+// LDS) with one XOR or a constant added.  The place goes through per_step in
+// every step: left to itself, the compiler keeps all XORs in registers over the
+// loop.
+__device__ __forceinline__ int pr_per_step(int off) {
+    asm volatile("" : "+v"(off));
+    return off;
 }
-// Operand across rows: element 32 t + c of the rows 16 w + 4 g + (0 .. 3) and
+// Operands along rows: elements 16 j + 8 g .. of row 32 b + c.
+template <int D>
+__device__ __forceinline__ int pr_along() {
+    const int lane = threadIdx.x & 63, c = lane & 31, g = lane >> 5;
+    return c * (2 * D) + ((g ^ pr_swizzle<D>(c)) << 4);
+}
+template <int D>
+__device__ __forceinline__ at_u32x4 pr_read(const uint8_t* lds, int along, int b, int j) {
+    return *reinterpret_cast<const at_u32x4*>(lds + (along ^ (32 * j)) + 32 * b * (2 * D));
+}
+// Operands across rows: element 32 t + c of the rows 16 w + 4 g + (0 .. 3) and
 // 16 w + 8 + 4 g + (0 .. 3), the rows whose scores lane (c, g) holds in
 // registers 8 (w % 2) .. 8 (w % 2) + 7 of a product over 32 rows.  The
 // transposing read takes four rows of 16 elements from 16 lanes (lane i: row
 // i / 4, elements 4 (i % 4) ..) and gives lane i element i of the four.
 template <int D>
-__device__ __forceinline__ at_u32x4 pr_read_across(const uint8_t* tile, int w, int t) {
+__device__ __forceinline__ int pr_across() {
     const int lane = threadIdx.x & 63, i = lane & 15, half = (lane >> 4) & 1, g = lane >> 5;
-    const int row = 16 * w + 4 * g + (i >> 2), chunk = 4 * t + 2 * half + ((i & 3) >> 1), at8 = (i & 1) * 8;
+    const int row = 4 * g + (i >> 2), chunk = 2 * half + ((i & 3) >> 1);
+    return row * (2 * D) + ((chunk ^ pr_swizzle<D>(row)) << 4) + (i & 1) * 8;
+}
+template <int D>
+__device__ __forceinline__ at_u32x4 pr_read_across(uint8_t* lds, int across, int w, int t) {
     typedef __attribute__((address_space(3))) pr_i16x4* LdsPtr;
-    const pr_i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (LdsPtr)(tile + row * (2 * D) + ((chunk ^ pr_swizzle<D>(row)) << 4) + at8));
-    const pr_i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (LdsPtr)(tile + (row + 8) * (2 * D) + ((chunk ^ pr_swizzle<D>(row + 8)) << 4) + at8));
+    const int at = across ^ (64 * t);   // (the second four rows' swizzle differs in one bit)
+    const pr_i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(lds + at + 16 * w * (2 * D)));
+    const pr_i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(lds + (at ^ 32) + (16 * w + 8) * (2 * D)));
     const pr_i16x8 z{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     return __builtin_bit_cast(at_u32x4, z);
 }

@@ -42,7 +42,8 @@ __device__ __forceinline__ void copy_tile(const PrRows& x, int64_t row0, int h, 
     }
 }
 
-// delta = dout . out of every row and head.
+// delta = dout . out of every row and head, where no dq is asked for (its launch
+// forms them too).
 template <class E, int D>
 __global__ __launch_bounds__(256) void prompt_delta_kernel(PromptArgs a) {
     constexpr int L = D / 8;
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
     const int64_t rest = blockIdx.x / a.Hkv;
     const int split = (int)(rest % a.splits);
     const int64_t un = rest / a.splits;
-    const int e = pr_find(a.cu, a, a.T, un, a.G, RT);
+    const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
     const PrSeq s = pr_seq(a, e);
     const int64_t pairs = (int64_t)s.n * a.G;
     const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));   // the longest first
@@ -88,21 +89,30 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
     const int64_t row = have ? (int64_t)(s.r0 + pr.i) * a.Hq + h * a.G + pr.g : -1;
     const int wlo = pos0 + pr_pair(a, p0, fw).i, whi = pos0 + (int)(min(f0 + fw + 31, f1 - 1) / a.G);
     at_u32x4 q[D / 16], dout[D / 16];
+    float lse2 = INFINITY, delta = 0.0f;
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-        q[j] = dout[j] = at_u32x4{0u, 0u, 0u, 0u};
-        if (have && s.in) {
-            const int64_t t = s.r0 + pr.i, x = h * a.G + pr.g;
+    for (int j = 0; j < D / 16; ++j) q[j] = dout[j] = at_u32x4{0u, 0u, 0u, 0u};
+    if (have && s.in) {
+        const int64_t t = s.r0 + pr.i, x = h * a.G + pr.g;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
             q[j] = *reinterpret_cast<const at_u32x4*>(a.q.p + t * a.q.row + x * a.q.head + 16 * j + 8 * g);
             dout[j] = *reinterpret_cast<const at_u32x4*>(a.dout.p + t * a.dout.row + x * a.dout.head + 16 * j + 8 * g);
         }
-    }
-    float lse2 = INFINITY, delta = 0.0f;
-    if (have && s.in) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            const at_u32x4 y = *reinterpret_cast<const at_u32x4*>(a.out_in + row * D + 16 * j + 8 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                delta = __builtin_fmaf(E::lo(dout[j][i]), E::lo(y[i]), delta);
+                delta = __builtin_fmaf(E::hi(dout[j][i]), E::hi(y[i]), delta);
+            }
+        }
         lse2 = a.lse[row] * 1.4426950408889634f;
         lse2 = lse2 == -INFINITY ? INFINITY : lse2;   // (a row that sees no key: weights of 0)
-        delta = a.delta[row];
     }
+    delta = pr_sum_halves(delta);
+    if (have && split == 0 && g == 0) a.delta[row] = delta;   // for the dk and dv launch
     const int plo = pos0 + p0.i, phi = pos0 + uniform((int)((f1 - 1) / a.G));
     const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
     const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
@@ -125,13 +135,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
         copy_tile<D, kWaves>(a.k, s.k0, h, t * kKeys, s.m, st);
         copy_tile<D, kWaves>(a.v, s.k0, h, t * kKeys, s.m, st + kTileBytes<D>);
     };
+    const int along = pr_along<D>(), across = pr_across<D>();
     if (t0 < t1) copy(t0);
     pr_wait_copies();
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
         if (t + 1 < t1) copy(t + 1);
-        const uint8_t* kt = lds() + (t & 1) * kStage<D>;
-        const uint8_t* vt = kt + kTileBytes<D>;
+        const int stage = (t & 1) * kStage<D>, kt = pr_per_step(along) + stage, ka = pr_per_step(across) + stage;
+        const int vt = kt + kTileBytes<D>;
         const int key0 = t * kKeys;
         const bool whole = key0 + kKeys - 1 <= wlo && (a.window <= 0 || key0 > whi - a.window);
 #pragma unroll
@@ -140,9 +151,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) x = E::mfma(pr_read<D>(kt, 32 * b + c, 2 * j + g), q[j], x);
+            for (int j = 0; j < D / 16; ++j) x = E::mfma(pr_read<D>(lds(), kt, b, j), q[j], x);
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) y = E::mfma(pr_read<D>(vt, 32 * b + c, 2 * j + g), dout[j], y);
+            for (int j = 0; j < D / 16; ++j) y = E::mfma(pr_read<D>(lds(), vt, b, j), dout[j], y);
             at_u32x4 ds[2];
 #pragma unroll
             for (int r = 0; r < 16; r += 2) {
@@ -159,7 +170,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
-                for (int t = 0; t < D / 32; ++t) o[t] = E::mfma(pr_read_across<D>(kt, 2 * b + w, t), ds[w], o[t]);
+                for (int t = 0; t < D / 32; ++t) o[t] = E::mfma(pr_read_across<D>(lds(), ka, 2 * b + w, t), ds[w], o[t]);
         }
         pr_wait_copies();
         __syncthreads();
@@ -192,7 +203,7 @@ __global__ __launch_bounds__(2 * D) void prompt_dq_join_kernel(PromptArgs a) {
     constexpr int RT = kUnit;
     const int h = (int)(blockIdx.x % a.Hkv);
     const int64_t un = blockIdx.x / a.Hkv;
-    const int e = pr_find(a.cu, a, a.T, un, a.G, RT);
+    const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
     const PrSeq s = pr_seq(a, e);
     const int64_t pairs = (int64_t)s.n * a.G;
     const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));
@@ -242,7 +253,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
     const int64_t rest = blockIdx.x / a.Hkv;
     const int split = (int)(rest % a.splits);
     const int64_t un = rest / a.splits;
-    const int e = pr_find(a.cu_k, a, a.S, un, 1, kUnit);
+    const int e = pr_find<kUnit>(a.cu_k, a, a.S, un, 1);
     const PrSeq s = pr_seq(a, e);
     const int64_t tile = un - pr_first(a.cu_k, a, a.S, e, 1, kUnit);   // (the first keys are seen by the most rows)
     if (tile * kUnit >= s.m) return;
@@ -279,6 +290,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
     PairInfo* info = reinterpret_cast<PairInfo*>(lds() + 2 * kStage<D>);
     float n_lse = 0.0f, n_delta = 0.0f;
     int n_pos = -1;
+    int now_lo = 0, now_hi = 0, next_lo = 0, next_hi = 0;   // first and last row of a step
     auto copy = [&](int t) {
         uint8_t* st = lds() + (t & 1) * kStage<D>;
         const int left = (int)min(f1 - f0 - (int64_t)t * kPairs, (int64_t)kPairs);   // pairs of the step
@@ -299,6 +311,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
             n_delta = a.delta[row];
             n_pos = (int)threadIdx.x < left ? pos0 + p.i : -1;
         }
+        now_lo = next_lo, now_hi = next_hi;
+        next_lo = pos0 + at.i;
+        next_hi = pos0 + uniform(pr_pair(a, at, left - 1).i);
         const PrPair next = pr_pair(a, at, kPairs);
         at = PrPair{uniform(next.i), uniform(next.g)};
     };
@@ -311,6 +326,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
             x.pos[threadIdx.x] = n_pos;
         }
     };
+    const int along = pr_along<D>(), across = pr_across<D>();
     if (steps > 0) {
         copy(0);
         store_info(0);
@@ -318,57 +334,67 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
     pr_wait_copies();
     __syncthreads();
     for (int t = 0; t < steps; ++t) {
-        // first and last row of the step, before `at` moves on with the next copy
-        const int64_t ft = f0 + (int64_t)t * kPairs;
-        const int plo = pos0 + uniform((int)(ft / a.G)), phi = pos0 + uniform((int)((min(ft + kPairs, f1) - 1) / a.G));
-        const bool whole = kw + 31 <= plo && ft + kPairs <= f1 && (a.window <= 0 || kw > phi - a.window);
-        if (t + 1 < steps) copy(t + 1);
-        const uint8_t* qt = lds() + (t & 1) * kStage<D>;
-        const uint8_t* dt = qt + kTileBytes<D>;
+        if (t + 1 < steps)
+            copy(t + 1);
+        else
+            now_lo = next_lo, now_hi = next_hi;
+        const bool whole = kw + 31 <= now_lo && f1 - f0 >= (int64_t)(t + 1) * kPairs && (a.window <= 0 || kw > now_hi - a.window);
+        const int stage = (t & 1) * kStage<D>;
         const PairInfo& inf = info[t & 1];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
+            // scores, weights, dv; then dout v, score gradients, dk: one set of
+            // scores at a time (with both the registers would not suffice)
+            const int qt = pr_per_step(along) + stage, qa = pr_per_step(across) + stage;
             pr_f32x16 x, y;
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) x = E::mfma(pr_read<D>(qt, 32 * b + c, 2 * j + g), kf[j], x);
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) y = E::mfma(pr_read<D>(dt, 32 * b + c, 2 * j + g), vf[j], y);
+            for (int j = 0; j < D / 16; ++j) x = E::mfma(pr_read<D>(lds(), qt, b, j), kf[j], x);
+            __builtin_amdgcn_sched_barrier(0);
             at_u32x4 pf[2], ds[2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r0 = 32 * b + 8 * i + 4 * g;
                 const at_f32x4 lse2 = *reinterpret_cast<const at_f32x4*>(inf.lse2 + r0);
-                const at_f32x4 delta = *reinterpret_cast<const at_f32x4*>(inf.delta + r0);
-                float p[4], z[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[r] = __builtin_fmaf(x[4 * i + r], a.c2, -lse2[r]);
+                for (int r = 0; r < 4; ++r) x[4 * i + r] = __builtin_fmaf(x[4 * i + r], a.c2, -lse2[r]);
                 if (!whole) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int pos = inf.pos[r0 + r];
                         const int from = a.window > 0 ? max(pos, 0) - a.window : -1;
-                        p[r] = (key <= pos) & (key > from) ? p[r] : -INFINITY;
+                        x[4 * i + r] = (key <= pos) & (key > from) ? x[4 * i + r] : -INFINITY;
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    p[r] = __builtin_amdgcn_exp2f(p[r]);
-                    z[r] = p[r] * (y[4 * i + r] - delta[r]);
-                }
-                pf[i / 2][2 * (i % 2)] = E::pack(p[0], p[1]);
-                pf[i / 2][2 * (i % 2) + 1] = E::pack(p[2], p[3]);
-                ds[i / 2][2 * (i % 2)] = E::pack(z[0], z[1]);
-                ds[i / 2][2 * (i % 2) + 1] = E::pack(z[2], z[3]);
+                for (int r = 0; r < 4; ++r) x[4 * i + r] = __builtin_amdgcn_exp2f(x[4 * i + r]);
+                pf[i / 2][2 * (i % 2)] = E::pack(x[4 * i], x[4 * i + 1]);
+                pf[i / 2][2 * (i % 2) + 1] = E::pack(x[4 * i + 2], x[4 * i + 3]);
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d) {
-                    dv[d] = E::mfma(pr_read_across<D>(dt, 2 * b + w, d), pf[w], dv[d]);
-                    dk[d] = E::mfma(pr_read_across<D>(qt, 2 * b + w, d), ds[w], dk[d]);
-                }
+                for (int d = 0; d < D / 32; ++d) dv[d] = E::mfma(pr_read_across<D>(lds(), qa + kTileBytes<D>, 2 * b + w, d), pf[w], dv[d]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) y = E::mfma(pr_read<D>(lds(), qt + kTileBytes<D>, b, j), vf[j], y);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const at_f32x4 delta = *reinterpret_cast<const at_f32x4*>(inf.delta + 32 * b + 8 * i + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[4 * i + r] = x[4 * i + r] * (y[4 * i + r] - delta[r]);
+                ds[i / 2][2 * (i % 2)] = E::pack(y[4 * i], y[4 * i + 1]);
+                ds[i / 2][2 * (i % 2) + 1] = E::pack(y[4 * i + 2], y[4 * i + 3]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d) dk[d] = E::mfma(pr_read_across<D>(lds(), qa, 2 * b + w, d), ds[w], dk[d]);
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (t + 1 < steps) store_info(t + 1);
         pr_wait_copies();
@@ -407,7 +433,7 @@ template <class E, int D>
 __global__ __launch_bounds__(2 * D) void prompt_dkv_join_kernel(PromptArgs a) {
     const int h = (int)(blockIdx.x % a.Hkv);
     const int64_t un = blockIdx.x / a.Hkv;
-    const int e = pr_find(a.cu_k, a, a.S, un, 1, kUnit);
+    const int e = pr_find<kUnit>(a.cu_k, a, a.S, un, 1);
     const PrSeq s = pr_seq(a, e);
     const int64_t tile = un - pr_first(a.cu_k, a, a.S, e, 1, kUnit);
     if (tile * kUnit >= s.m) return;
@@ -450,7 +476,7 @@ template <class E, int D>
 hipError_t launch(const PromptPlan& p, PromptArgs& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.T * a.Hq;
     constexpr int per = 256 / (D / 8);
-    if (rows > 0) prompt_delta_kernel<E, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
+    if (!a.dq && rows > 0) prompt_delta_kernel<E, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
     if (a.dq && rows > 0) {
         a.splits = p.fwd_splits;
         prompt_dq_kernel<E, D><<<(unsigned)p.fwd_blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);
