@@ -48,10 +48,9 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
     constexpr int RT = 32 * NW;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
-    const int h = (int)(blockIdx.x % a.Hkv);
-    const int64_t rest = blockIdx.x / a.Hkv;
-    const int split = (int)(rest % a.splits);
-    const int64_t un = rest / a.splits;
+    const PrPlace pl = pr_place(a);
+    const int h = pl.h, split = pl.part;
+    const int64_t un = pl.unit;
     const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
     const PrSeq s = pr_seq(a, e);
     const int64_t pairs = (int64_t)s.n * a.G;
@@ -81,11 +80,10 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
     const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
     const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
     int t0 = lo / kKeys, t1 = (hi + kKeys - 1) / kKeys;
-    const int per = uniform((t1 - t0 + a.splits - 1) / a.splits);
-    const int used = per > 0 ? (t1 - t0 + per - 1) / per : 1;
-    t0 += split * per;
-    t1 = min(t0 + per, t1);
-    if (split > 0 && t0 >= t1) return;
+    const PrParts parts = pr_parts(a, t1 - t0);
+    if (split >= parts.used) return;
+    t0 += split * parts.size;
+    t1 = min(t0 + parts.size, t1);
 
     float m = 0.0f, over = -INFINITY, l = 0.0f;
     pr_f32x16 o[D / 32];
@@ -162,7 +160,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
     }
     l = pr_sum_halves(l);
     if (row < 0) return;
-    if (used <= 1) {
+    if (parts.used <= 1) {
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         uint16_t* dst = a.out + row * D;
 #pragma unroll
@@ -194,8 +192,8 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
 template <class E, int D, int NW>
 __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
     constexpr int RT = 32 * NW;
-    const int h = (int)(blockIdx.x % a.Hkv);
-    const int64_t un = blockIdx.x / a.Hkv;
+    const int64_t un = blockIdx.x / (uint32_t)a.Hkv;
+    const int h = (int)(blockIdx.x - (uint32_t)un * (uint32_t)a.Hkv);
     const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
     const PrSeq s = pr_seq(a, e);
     const int64_t pairs = (int64_t)s.n * a.G;
@@ -205,8 +203,7 @@ __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
     const int plo = s.pos0() + (int)(f0 / a.G), phi = s.pos0() + (int)((f1 - 1) / a.G);
     const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
     const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
-    const int tiles = (hi + kKeys - 1) / kKeys - lo / kKeys, per = (tiles + a.splits - 1) / a.splits;
-    const int used = per > 0 ? (tiles + per - 1) / per : 1;
+    const int used = pr_parts(a, (hi + kKeys - 1) / kKeys - lo / kKeys).used;
     if (used <= 1) return;
     const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
     const int64_t f = f0 + r;
@@ -232,37 +229,49 @@ constexpr int kWaves = 4;
 
 template <class E, int D>
 hipError_t launch(const PromptPlan& p, const PromptArgs& a, hipStream_t st) {
-    prompt_kernel<E, D, kWaves><<<(unsigned)p.fwd_blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);
+    prompt_kernel<E, D, kWaves><<<(unsigned)p.rows.blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);
     if (a.splits > 1)
-        prompt_join_kernel<E, D, kWaves><<<dim3((unsigned)(p.fwd_blocks / a.splits), 4 * kWaves), 2 * D, 0, st>>>(a);
+        prompt_join_kernel<E, D, kWaves><<<dim3((unsigned)(p.rows.units * a.Hkv), 4 * kWaves), 2 * D, 0, st>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// Units are cut while there are too few of them for the card to run evenly: 512
+// workgroups run at once, and units of one sequence differ in length by up to
+// the whole of it, so that with two to a place the short ones fill up what the
+// long ones leave.  `steps` are those of a sequence of average length, `most` of
+// one that is all of the batch; a part has kLeast steps or more.
+static PromptCut cut(int64_t units, int Hkv, int64_t steps, int64_t most) {
+    constexpr int64_t kPlaces = 1024, kLeast = 8;
+    PromptCut c{units, units * Hkv, 1, 1 << 30};
+    if (c.blocks >= kPlaces || steps * most < kLeast * kLeast) return c;   // (the geometric mean of both)
+    const int64_t per = std::max(kLeast, (c.blocks * steps + kPlaces - 1) / kPlaces);
+    c.splits = (int)std::min((most + per - 1) / per, kPlaces / c.blocks + 1);
+    c.per = (int)per;
+    c.blocks *= c.splits;
+    return c;
+}
+
 PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int window) {
     PromptPlan p{};
-    const int64_t G = Hq / Hkv, rows = 32 * kWaves;
-    // Units are cut while they leave CUs with less than two workgroups, each part
-    // at least four steps.
-    const int64_t reach = window > 0 ? (int64_t)window + 2 * rows : S;   // keys that a unit's rows may see
-    const int64_t units = pr_units(T, G, 32 * kWaves, n_seq) * Hkv, steps = (std::min<int64_t>(reach, S) + kKeys - 1) / kKeys;
-    p.fwd_splits = (int)std::max<int64_t>(1, std::min<int64_t>(steps / 4, 512 / units));
-    p.fwd_blocks = units * p.fwd_splits;
-    p.fwd_bytes = std::max<size_t>(256, p.fwd_splits > 1 ? (size_t)p.fwd_blocks * rows * (D + 2) * 4 : 0);
-    const int64_t seen = window > 0 ? (int64_t)window + 2 * rows : T;   // rows that may see a unit's keys
-    const int64_t kv_units = pr_units(S, 1, 32 * kWaves, n_seq) * Hkv, kv_steps = (std::min<int64_t>(seen, T) * G + 63) / 64;
-    p.kv_splits = (int)std::max<int64_t>(1, std::min<int64_t>(kv_steps / 4, 512 / kv_units));
-    p.kv_blocks = kv_units * p.kv_splits;
+    const int64_t G = Hq / Hkv, seqs = std::max(n_seq, 1);
+    constexpr int rows = 32 * kWaves;
+    auto steps = [&](int64_t n, int64_t mul) {   // of 64, over n tokens that count mul, as far as a window reaches
+        return ((window > 0 ? std::min<int64_t>(n, (int64_t)window + 2 * rows) : n) * mul + 63) / 64;
+    };
+    p.rows = cut(pr_units(T, G, rows, n_seq), Hkv, steps((S + seqs - 1) / seqs, 1), steps(S, 1));
+    p.keys = cut(pr_units(S, 1, rows, n_seq), Hkv, steps((T + seqs - 1) / seqs, G), steps(T, G));
+    auto parts = [&](const PromptCut& c, int64_t floats) { return c.splits > 1 ? (size_t)(c.blocks * rows * floats) * 4 : 0; };
+    p.fwd_bytes = std::max<size_t>(256, parts(p.rows, D + 2));
     p.delta_bytes = ((size_t)T * Hq * 4 + 255) / 256 * 256;
-    p.bwd_bytes = std::max<size_t>(256, p.delta_bytes + std::max(p.fwd_splits > 1 ? (size_t)p.fwd_blocks * rows * D * 4 : 0,
-                                                                 p.kv_splits > 1 ? (size_t)p.kv_blocks * rows * 2 * D * 4 : 0));
-    p.fits = grid_fits(std::max(p.fwd_blocks, p.kv_blocks), 64 * kWaves) && grid_fits((int64_t)T * Hq / 2 + 1, 16);
+    p.bwd_bytes = std::max<size_t>(256, p.delta_bytes + std::max(parts(p.rows, D), parts(p.keys, 2 * D)));
+    p.fits = grid_fits(std::max(p.rows.blocks, p.keys.blocks), 64 * kWaves) && grid_fits((int64_t)T * Hq / 2 + 1, 16);
     return p;
 }
 
 hipError_t launch_prompt(const PromptPlan& p, int type, int D, PromptArgs& a, void* ws, hipStream_t st) {
-    a.splits = p.fwd_splits;
+    a.splits = p.rows.splits, a.per = p.rows.per, a.units = p.rows.units;
     a.part = static_cast<float*>(ws);
     if (type == LTK_ROWS_BF16) return D == 64 ? launch<PrBf16, 64>(p, a, st) : launch<PrBf16, 128>(p, a, st);
     return D == 64 ? launch<PrF16, 64>(p, a, st) : launch<PrF16, 128>(p, a, st);

@@ -57,9 +57,31 @@ struct PromptArgs {
     uint32_t div_g;           // ceil(2^32 / G); 0 for G == 1
     float scale, c2;          // c2 = scale log2(e)
     int window;
-    int splits;               // parts that a unit's keys (dk and dv: rows) are cut into
+    int splits, per;          // units are cut into parts of about `per` steps, `splits` of them at most
+    int64_t units;            // of a key/value head
     float* part;
 };
+
+// A unit's parts: `used` of them, of `size` steps each (the last one what is left).
+struct PrParts {
+    int size, used;
+};
+__device__ __forceinline__ PrParts pr_parts(const PromptArgs& a, int steps) {
+    if (a.splits <= 1 || steps <= a.per) return PrParts{max(steps, 1), 1};
+    const int n = min(a.splits, (int)((uint32_t)(steps + a.per - 1) / (uint32_t)a.per)), size = (int)((uint32_t)(steps + n - 1) / (uint32_t)n);
+    return PrParts{size, (int)((uint32_t)(steps + size - 1) / (uint32_t)size)};
+}
+// The unit, part and head of a workgroup.  Heads go round the XCDs, so that a
+// head's keys (dk, dv: rows) pass through one L2; first parts come before
+// second ones, so that the longest come first.
+struct PrPlace {
+    int64_t unit;
+    int part, h;
+};
+__device__ __forceinline__ PrPlace pr_place(const PromptArgs& a) {
+    const uint32_t b = blockIdx.x, rest = b / (uint32_t)a.Hkv, part = a.splits > 1 ? rest / (uint32_t)a.units : 0u;
+    return PrPlace{(int64_t)(rest - part * (uint32_t)a.units), (int)part, (int)(b - rest * (uint32_t)a.Hkv)};
+}
 
 // Quotient by G of x < G + 2^15 (exact while x (G - 1) < 2^32: larger groups divide).
 __device__ __forceinline__ int pr_div_g(const PromptArgs& a, int x) {
@@ -183,11 +205,12 @@ __device__ __forceinline__ float pr_sum_halves(float x) {
     return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+struct PromptCut {
+    int64_t units, blocks;   // of a key/value head; workgroups
+    int splits, per;
+};
 struct PromptPlan {
-    int64_t fwd_blocks;             // forward, and dq
-    int fwd_splits;
-    int64_t kv_blocks;              // dk and dv
-    int kv_splits;
+    PromptCut rows, keys;           // the launches over row tiles (forward, dq) and over key tiles (dk, dv)
     size_t fwd_bytes, bwd_bytes;    // workspaces
     size_t delta_bytes;             // of the backward pass's, before the parts
     bool fits;

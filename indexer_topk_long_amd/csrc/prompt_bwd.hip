@@ -69,10 +69,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
     constexpr int RT = kUnit;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
-    const int h = (int)(blockIdx.x % a.Hkv);
-    const int64_t rest = blockIdx.x / a.Hkv;
-    const int split = (int)(rest % a.splits);
-    const int64_t un = rest / a.splits;
+    const PrPlace pl = pr_place(a);
+    const int h = pl.h, split = pl.part;
+    const int64_t un = pl.unit;
     const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
     const PrSeq s = pr_seq(a, e);
     const int64_t pairs = (int64_t)s.n * a.G;
@@ -117,11 +116,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
     const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
     const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
     int t0 = lo / kKeys, t1 = (hi + kKeys - 1) / kKeys;
-    const int per = uniform((t1 - t0 + a.splits - 1) / a.splits);
-    const int used = per > 0 ? (t1 - t0 + per - 1) / per : 1;
-    t0 += split * per;
-    t1 = min(t0 + per, t1);
-    if (split > 0 && t0 >= t1) return;
+    const PrParts parts = pr_parts(a, t1 - t0);
+    if (split >= parts.used) return;
+    t0 += split * parts.size;
+    t1 = min(t0 + parts.size, t1);
 
     pr_f32x16 o[D / 32];
 #pragma unroll
@@ -176,7 +174,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
         __syncthreads();
     }
     if (row < 0) return;
-    if (used <= 1) {
+    if (parts.used <= 1) {
         uint16_t* dst = a.dq + row * D;
 #pragma unroll
         for (int t = 0; t < D / 32; ++t)
@@ -201,8 +199,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
 template <class E, int D>
 __global__ __launch_bounds__(2 * D) void prompt_dq_join_kernel(PromptArgs a) {
     constexpr int RT = kUnit;
-    const int h = (int)(blockIdx.x % a.Hkv);
-    const int64_t un = blockIdx.x / a.Hkv;
+    const int64_t un = blockIdx.x / (uint32_t)a.Hkv;
+    const int h = (int)(blockIdx.x - (uint32_t)un * (uint32_t)a.Hkv);
     const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
     const PrSeq s = pr_seq(a, e);
     const int64_t pairs = (int64_t)s.n * a.G;
@@ -212,8 +210,7 @@ __global__ __launch_bounds__(2 * D) void prompt_dq_join_kernel(PromptArgs a) {
     const int plo = s.pos0() + (int)(f0 / a.G), phi = s.pos0() + (int)((f1 - 1) / a.G);
     const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
     const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
-    const int tiles = (hi + kKeys - 1) / kKeys - lo / kKeys, per = (tiles + a.splits - 1) / a.splits;
-    const int used = per > 0 ? (tiles + per - 1) / per : 1;
+    const int used = pr_parts(a, (hi + kKeys - 1) / kKeys - lo / kKeys).used;
     if (used <= 1) return;
     const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
     const int64_t f = f0 + r;
@@ -249,10 +246,9 @@ template <class E, int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
-    const int h = (int)(blockIdx.x % a.Hkv);
-    const int64_t rest = blockIdx.x / a.Hkv;
-    const int split = (int)(rest % a.splits);
-    const int64_t un = rest / a.splits;
+    const PrPlace pl = pr_place(a);
+    const int h = pl.h, split = pl.part;
+    const int64_t un = pl.unit;
     const int e = pr_find<kUnit>(a.cu_k, a, a.S, un, 1);
     const PrSeq s = pr_seq(a, e);
     const int64_t tile = un - pr_first(a.cu_k, a, a.S, e, 1, kUnit);   // (the first keys are seen by the most rows)
@@ -261,12 +257,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
     const int kw = ka + 32 * wave, key = kw + c;
     int64_t f0, f1;
     seeing(a, s, ka, kb, f0, f1);
-    const int64_t steps_all = (f1 - f0 + kPairs - 1) / kPairs;
-    const int per = uniform((int)((steps_all + a.splits - 1) / a.splits));
-    const int used = per > 0 ? (int)((steps_all + per - 1) / per) : 1;
-    if (split > 0 && split >= used) return;
-    f0 += (int64_t)split * per * kPairs;
-    f1 = min(f0 + (int64_t)per * kPairs, f1);
+    const PrParts parts = pr_parts(a, uniform((int)((f1 - f0 + kPairs - 1) / kPairs)));
+    if (split >= parts.used) return;
+    f0 += (int64_t)split * parts.size * kPairs;
+    f1 = min(f0 + (int64_t)parts.size * kPairs, f1);
     const int steps = uniform((int)((f1 - f0 + kPairs - 1) / kPairs));
 
     at_u32x4 kf[D / 16], vf[D / 16];
@@ -401,7 +395,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
         __syncthreads();
     }
     if (key >= kb) return;
-    if (used <= 1) {
+    if (parts.used <= 1) {
         const int64_t row = (int64_t)(s.k0 + key) * a.Hkv + h;
 #pragma unroll
         for (int t = 0; t < D / 32; ++t)
@@ -431,17 +425,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
 // Sums the parts of a unit's dk and dv, 8 keys a workgroup.
 template <class E, int D>
 __global__ __launch_bounds__(2 * D) void prompt_dkv_join_kernel(PromptArgs a) {
-    const int h = (int)(blockIdx.x % a.Hkv);
-    const int64_t un = blockIdx.x / a.Hkv;
+    const int64_t un = blockIdx.x / (uint32_t)a.Hkv;
+    const int h = (int)(blockIdx.x - (uint32_t)un * (uint32_t)a.Hkv);
     const int e = pr_find<kUnit>(a.cu_k, a, a.S, un, 1);
     const PrSeq s = pr_seq(a, e);
-    const int64_t tile = un - pr_first(a.cu_k, a, a.S, e, 1, kUnit);
+    const int64_t tile = un - pr_first(a.cu_k, a, a.S, e, 1, kUnit);   // (the first keys are seen by the most rows)
     if (tile * kUnit >= s.m) return;
     const int ka = (int)tile * kUnit, kb = min(ka + kUnit, s.m);
     int64_t f0, f1;
     seeing(a, s, ka, kb, f0, f1);
-    const int64_t steps = (f1 - f0 + kPairs - 1) / kPairs;
-    const int per = (int)((steps + a.splits - 1) / a.splits), used = per > 0 ? (int)((steps + per - 1) / per) : 1;
+    const int used = pr_parts(a, (int)((f1 - f0 + kPairs - 1) / kPairs)).used;
     if (used <= 1) return;
     const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
     if (ka + r >= kb) return;
@@ -478,21 +471,21 @@ hipError_t launch(const PromptPlan& p, PromptArgs& a, hipStream_t st) {
     constexpr int per = 256 / (D / 8);
     if (!a.dq && rows > 0) prompt_delta_kernel<E, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
     if (a.dq && rows > 0) {
-        a.splits = p.fwd_splits;
-        prompt_dq_kernel<E, D><<<(unsigned)p.fwd_blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);
+        a.splits = p.rows.splits, a.per = p.rows.per, a.units = p.rows.units;
+        prompt_dq_kernel<E, D><<<(unsigned)p.rows.blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);
         if (a.splits > 1)
-            prompt_dq_join_kernel<E, D><<<dim3((unsigned)(p.fwd_blocks / a.splits), kUnit / 8), 2 * D, 0, st>>>(a);
+            prompt_dq_join_kernel<E, D><<<dim3((unsigned)(a.units * a.Hkv), kUnit / 8), 2 * D, 0, st>>>(a);
     }
     if (a.dk && a.S > 0) {
-        a.splits = p.kv_splits;
+        a.splits = p.keys.splits, a.per = p.keys.per, a.units = p.keys.units;
         if constexpr (kKvLds<D> > 65536) {
             static std::atomic<uint64_t> allowed;
             const hipError_t e = allow_lds(prompt_dkv_kernel<E, D>, kKvLds<D>, allowed);
             if (e != hipSuccess) return e;
         }
-        prompt_dkv_kernel<E, D><<<(unsigned)p.kv_blocks, 64 * kWaves, kKvLds<D>, st>>>(a);
+        prompt_dkv_kernel<E, D><<<(unsigned)p.keys.blocks, 64 * kWaves, kKvLds<D>, st>>>(a);
         if (a.splits > 1)
-            prompt_dkv_join_kernel<E, D><<<dim3((unsigned)(p.kv_blocks / a.splits), kUnit / 8), 2 * D, 0, st>>>(a);
+            prompt_dkv_join_kernel<E, D><<<dim3((unsigned)(a.units * a.Hkv), kUnit / 8), 2 * D, 0, st>>>(a);
     }
     return hipGetLastError();
 }
