@@ -44,7 +44,7 @@ __device__ __forceinline__ void copy_tile(const PrRows& x, int64_t row0, int h, 
 }
 
 template <class E, int D, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
     constexpr int RT = 32 * NW;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
@@ -93,18 +93,18 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
         for (int r = 0; r < 16; ++r) o[t][r] = 0.0f;
     const int from = a.window > 0 ? max(pos, 0) - a.window : -1;
 
-    auto copy = [&](int t) {
-        uint8_t* st = lds() + (t & 1) * kStage<D>;
-        copy_tile<D, NW>(a.k, s.k0, h, t * kKeys, s.m, st);
-        copy_tile<D, NW>(a.v, s.k0, h, t * kKeys, s.m, st + kTileBytes<D>);
-    };
+    auto copy_keys = [&](int t) { copy_tile<D, NW>(a.k, s.k0, h, t * kKeys, s.m, lds() + (t & 1) * kTileBytes<D>); };
+    auto copy_values = [&](int t) { copy_tile<D, NW>(a.v, s.k0, h, t * kKeys, s.m, lds() + 2 * kTileBytes<D>); };
     const int along = pr_along<D>(), across = pr_across<D>();
-    if (t0 < t1) copy(t0);
+    if (t0 < t1) {
+        copy_keys(t0);
+        copy_values(t0);
+    }
     pr_wait_copies();
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
-        if (t + 1 < t1) copy(t + 1);
-        const int stage = (t & 1) * kStage<D>, kt = pr_per_step(along) + stage, vt = pr_per_step(across) + stage + kTileBytes<D>;
+        if (t + 1 < t1) copy_keys(t + 1);
+        const int kt = pr_per_step(along) + (t & 1) * kTileBytes<D>, vt = pr_per_step(across) + 2 * kTileBytes<D>;
         const int key0 = t * kKeys;
         pr_f32x16 x[2];
 #pragma unroll
@@ -151,12 +151,19 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(PromptArgs a) {
                 l += p1;
                 p[2 * b + r / 8][(r % 8) / 2] = E::pack(p0, p1);
             }
+        // the values' copies are older than the next keys'
+        if (t + 1 < t1)
+            pr_wait_copies_but<D / 8 / NW>();
+        else
+            pr_wait_copies();
+        __syncthreads();
 #pragma unroll
         for (int w = 0; w < 4; ++w)
 #pragma unroll
             for (int t = 0; t < D / 32; ++t) o[t] = E::mfma(pr_read_across<D>(lds(), vt, w, t), p[w], o[t]);
         pr_wait_copies();
         __syncthreads();
+        if (t + 1 < t1) copy_values(t + 1);
     }
     l = pr_sum_halves(l);
     if (row < 0) return;
@@ -229,7 +236,7 @@ constexpr int kWaves = 4;
 
 template <class E, int D>
 hipError_t launch(const PromptPlan& p, const PromptArgs& a, hipStream_t st) {
-    prompt_kernel<E, D, kWaves><<<(unsigned)p.rows.blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);
+    prompt_kernel<E, D, kWaves><<<(unsigned)p.rows.blocks, 64 * kWaves, 3 * kTileBytes<D>, st>>>(a);
     if (a.splits > 1)
         prompt_join_kernel<E, D, kWaves><<<dim3((unsigned)(p.rows.units * a.Hkv), 4 * kWaves), 2 * D, 0, st>>>(a);
     return hipGetLastError();

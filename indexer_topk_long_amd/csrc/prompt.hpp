@@ -196,6 +196,12 @@ __device__ __forceinline__ at_u32x4 pr_read_across(uint8_t* lds, int across, int
 // Waits for the direct copies into LDS that the wave has issued.
 __device__ __forceinline__ void pr_wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// .. but for the newest N.
+template <int N>
+__device__ __forceinline__ void pr_wait_copies_but() {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
 __device__ __forceinline__ float pr_max_halves(float x) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
