@@ -46,7 +46,7 @@ typedef struct {
  *
  *   type       LTK_ROWS_BF16 or LTK_ROWS_FP16: that of q, k, v, out and all gradients
  *   n_q_heads  a multiple of n_kv_heads; query head h reads key/value head
- *              h / (n_q_heads / n_kv_heads)
+ *              h / (n_q_heads / n_kv_heads); fewer than 2^15 to one
  *   head_dim   64 or 128 (LTK_EUNSUPPORTED otherwise)
  *   T, S       rows of q, keys of k: T * n_q_heads and S * n_kv_heads <= 2^31 - 256
  *   scale      finite, also times log2(e)

@@ -7,8 +7,6 @@ namespace ltk {
 
 namespace {
 
-constexpr int kKeys = 64;   // keys of a step
-
 template <int D>
 constexpr int kTileBytes = kKeys * D * 2;
 template <int D>
@@ -232,8 +230,6 @@ __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
     if (a.lse && d == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-constexpr int kWaves = 4;
-
 template <class E, int D>
 hipError_t launch(const PromptPlan& p, const PromptArgs& a, hipStream_t st) {
     prompt_kernel<E, D, kWaves><<<(unsigned)p.rows.blocks, 64 * kWaves, 3 * kTileBytes<D>, st>>>(a);
@@ -264,15 +260,15 @@ PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int wind
     PromptPlan p{};
     const int64_t G = Hq / Hkv, seqs = std::max(n_seq, 1);
     constexpr int rows = 32 * kWaves;
-    auto steps = [&](int64_t n, int64_t mul) {   // of 64, over n tokens that count mul, as far as a window reaches
-        return ((window > 0 ? std::min<int64_t>(n, (int64_t)window + 2 * rows) : n) * mul + 63) / 64;
+    auto steps = [&](int64_t n, int64_t mul, int per) {   // over n tokens that count mul, as far as a window reaches
+        return ((window > 0 ? std::min<int64_t>(n, (int64_t)window + 2 * rows) : n) * mul + per - 1) / per;
     };
-    p.rows = cut(pr_units(T, G, rows, n_seq), Hkv, steps((S + seqs - 1) / seqs, 1), steps(S, 1));
-    p.keys = cut(pr_units(S, 1, rows, n_seq), Hkv, steps((T + seqs - 1) / seqs, G), steps(T, G));
+    p.rows = cut(pr_units(T, G, rows, n_seq), Hkv, steps((S + seqs - 1) / seqs, 1, kKeys), steps(S, 1, kKeys));
+    p.keys = cut(pr_units(S, 1, rows, n_seq), Hkv, steps((T + seqs - 1) / seqs, G, kPairs), steps(T, G, kPairs));
     auto parts = [&](const PromptCut& c, int64_t floats) { return c.splits > 1 ? (size_t)(c.blocks * rows * floats) * 4 : 0; };
     p.fwd_bytes = std::max<size_t>(256, parts(p.rows, D + 2));
-    p.delta_bytes = ((size_t)T * Hq * 4 + 255) / 256 * 256;
-    p.bwd_bytes = std::max<size_t>(256, p.delta_bytes + std::max(parts(p.rows, D), parts(p.keys, 2 * D)));
+    p.stat_bytes = ((size_t)T * Hq * 4 + 255) / 256 * 256;
+    p.bwd_bytes = std::max<size_t>(256, 2 * p.stat_bytes + std::max(parts(p.rows, D), parts(p.keys, 2 * D)));
     p.fits = grid_fits(std::max(p.rows.blocks, p.keys.blocks), 64 * kWaves) && grid_fits((int64_t)T * Hq / 2 + 1, 16);
     return p;
 }

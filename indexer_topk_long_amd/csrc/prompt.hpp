@@ -11,6 +11,10 @@
 
 namespace ltk {
 
+constexpr int kWaves = 4;    // of a workgroup
+constexpr int kKeys = 64;    // keys of a step (forward, dq)
+constexpr int kPairs = 32;   // (row, head) pairs of a step (dk, dv)
+
 typedef float pr_f32x16 __attribute__((ext_vector_type(16)));
 typedef short pr_i16x4 __attribute__((ext_vector_type(4)));
 typedef short pr_i16x8 __attribute__((ext_vector_type(8)));
@@ -51,10 +55,10 @@ struct PromptArgs {
     const uint16_t* out_in;   // backward: the forward call's out
     uint16_t *out, *dq, *dk, *dv;
     float* lse;
-    float* delta;             // backward: [T, Hq]
+    float *lse2, *delta;      // backward: [T, Hq], log2(e) lse and dout . out
     const int32_t *cu, *cu_k;
     int n_seq, T, S, Hq, Hkv, G;
-    uint32_t div_g;           // ceil(2^32 / G); 0 for G == 1
+    uint32_t div_g, one_g;    // ceil(2^32 / G), or 0 and all ones for G == 1
     float scale, c2;          // c2 = scale log2(e)
     int window;
     int splits, per;          // units are cut into parts of about `per` steps, `splits` of them at most
@@ -83,11 +87,9 @@ __device__ __forceinline__ PrPlace pr_place(const PromptArgs& a) {
     return PrPlace{(int64_t)(rest - part * (uint32_t)a.units), (int)part, (int)(b - rest * (uint32_t)a.Hkv)};
 }
 
-// Quotient by G of x < G + 2^15 (exact while x (G - 1) < 2^32: larger groups divide).
+// Quotient by G of x < G + 2^15 (exact while x (G - 1) < 2^32: G < 2^15).
 __device__ __forceinline__ int pr_div_g(const PromptArgs& a, int x) {
-    if (a.G == 1) return x;
-    if (a.G >= 1 << 15) return x / a.G;
-    return (int)__umulhi((uint32_t)x, a.div_g);
+    return (int)(__umulhi((uint32_t)x, a.div_g) + ((uint32_t)x & a.one_g));
 }
 
 // The (row, head) pairs of a key/value head are numbered f = row * G + head of
@@ -218,7 +220,7 @@ struct PromptCut {
 struct PromptPlan {
     PromptCut rows, keys;           // the launches over row tiles (forward, dq) and over key tiles (dk, dv)
     size_t fwd_bytes, bwd_bytes;    // workspaces
-    size_t delta_bytes;             // of the backward pass's, before the parts
+    size_t stat_bytes;              // of the backward pass's: lse2, and as much for delta, before the parts
     bool fits;
 };
 PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int window);

@@ -20,6 +20,7 @@ int check(const ltk_prompt* p) {
         return LTK_EINVAL;
     if ((int64_t)p->T * p->n_q_heads > kMaxRows || (int64_t)p->S * p->n_kv_heads > kMaxRows) return LTK_EINVAL;
     if (p->n_seq > kMaxRows || p->window < 0 || !isfinite(p->scale * 1.4426950408889634f)) return LTK_EINVAL;
+    if (p->n_q_heads / p->n_kv_heads >= 1 << 15) return LTK_EINVAL;   // (a group's quotients)
     if (p->head_dim != 64 && p->head_dim != 128) return LTK_EUNSUPPORTED;
     if (p->type != LTK_ROWS_BF16 && p->type != LTK_ROWS_FP16) return LTK_EUNSUPPORTED;
     if (!p->cu_k && p->S != p->T) return LTK_EINVAL;
@@ -52,6 +53,7 @@ int args(const ltk_prompt* p, const ltk_rows* q, const ltk_rows* k, const ltk_ro
     a.Hkv = p->n_kv_heads;
     a.G = a.Hq / a.Hkv;
     a.div_g = a.G == 1 ? 0u : (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
+    a.one_g = a.G == 1 ? ~0u : 0u;
     a.scale = p->scale;
     a.c2 = p->scale * 1.4426950408889634f;
     a.window = p->window;

@@ -9,9 +9,6 @@ namespace ltk {
 
 namespace {
 
-constexpr int kKeys = 64;    // keys of a step (dq)
-constexpr int kPairs = 64;   // (row, head) pairs of a step (dk, dv)
-constexpr int kWaves = 4;
 constexpr int kUnit = 32 * kWaves;   // pairs (dq) or keys (dk, dv) of a unit
 
 template <int D>
@@ -42,8 +39,11 @@ __device__ __forceinline__ void copy_tile(const PrRows& x, int64_t row0, int h, 
     }
 }
 
-// delta = dout . out of every row and head, where no dq is asked for (its launch
-// forms them too).
+// log2(e) lse, infinite for a row that sees no key (its weights are 0 then).
+__device__ __forceinline__ float base2(float lse) { return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f; }
+
+// lse2 and delta = dout . out of every row and head, where no dq is asked for (its
+// launch forms them too).
 template <class E, int D>
 __global__ __launch_bounds__(256) void prompt_delta_kernel(PromptArgs a) {
     constexpr int L = D / 8;
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(256) void prompt_delta_kernel(PromptArgs a) {
     }
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    if (d == 0) a.delta[r] = s;
+    if (d == 0) a.delta[r] = s, a.lse2[r] = base2(a.lse[r]);
 }
 
 // dq: units are row tiles as in the forward pass.
@@ -107,11 +107,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
                 delta = __builtin_fmaf(E::hi(dout[j][i]), E::hi(y[i]), delta);
             }
         }
-        lse2 = a.lse[row] * 1.4426950408889634f;
-        lse2 = lse2 == -INFINITY ? INFINITY : lse2;   // (a row that sees no key: weights of 0)
+        lse2 = base2(a.lse[row]);
     }
     delta = pr_sum_halves(delta);
-    if (have && split == 0 && g == 0) a.delta[row] = delta;   // for the dk and dv launch
+    if (have && split == 0 && g == 0) a.delta[row] = delta, a.lse2[row] = lse2;   // for the dk and dv launch
     const int plo = pos0 + p0.i, phi = pos0 + uniform((int)((f1 - 1) / a.G));
     const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
     const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
@@ -223,13 +222,17 @@ __global__ __launch_bounds__(2 * D) void prompt_dq_join_kernel(PromptArgs a) {
         at_u32x2{E::pack(o[0] * a.scale, o[1] * a.scale), E::pack(o[2] * a.scale, o[3] * a.scale)};
 }
 
-// What the dk and dv kernel knows of a step's pairs.
-struct PairInfo {
-    float lse2[kPairs], delta[kPairs];
-    int pos[kPairs];   // -1: no pair
-};
+// LDS of the dk and dv kernel: the unit's rows of v, two stages, constants of the threads.
 template <int D>
-constexpr int kKvLds = 2 * kStage<D> + 2 * (int)sizeof(PairInfo);
+constexpr int kPairTile = kPairs * D * 2;
+template <int D>
+constexpr int kKvStage = 2 * kPairTile<D> + 2 * kPairs * 4;   // rows of q, of dout, then the pairs' lse2 and delta
+template <int D>
+constexpr int kStagesAt = kUnit * D * 2;
+template <int D>
+constexpr int kMineAt = kStagesAt<D> + 2 * kKvStage<D>;
+template <int D>
+constexpr int kKvLds = kMineAt<D> + 64 * kWaves * 16;
 
 // Pairs [f0, f1) that may see keys [ka, kb) of a sequence.
 __device__ __forceinline__ void seeing(const PromptArgs& a, const PrSeq& s, int ka, int kb, int64_t& f0, int64_t& f1) {
@@ -240,8 +243,10 @@ __device__ __forceinline__ void seeing(const PromptArgs& a, const PrSeq& s, int 
     f1 = s.in ? max((int64_t)i1 * a.G, f0) : f0;
 }
 
-// dk and dv: a unit is 128 keys of a key/value head, 32 a wave, whose rows of k
-// and v stay in registers; the pairs that see them pass through LDS.
+// dk and dv: a unit is 128 keys of a key/value head, 32 a wave; the pairs that see
+// them pass through LDS, 32 a step.  A wave keeps its rows of k and both sums in
+// registers; those of v wait in LDS (with them in registers too, 25 and more of
+// the 256 spilled, and each reload waited for all copies on their way).
 template <class E, int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -254,7 +259,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
     const int64_t tile = un - pr_first(a.cu_k, a, a.S, e, 1, kUnit);   // (the first keys are seen by the most rows)
     if (tile * kUnit >= s.m) return;
     const int ka = (int)tile * kUnit, kb = min(ka + kUnit, s.m), pos0 = s.pos0();
-    const int kw = ka + 32 * wave, key = kw + c;
+    const int kw = ka + 32 * wave;
     int64_t f0, f1;
     seeing(a, s, ka, kb, f0, f1);
     const PrParts parts = pr_parts(a, uniform((int)((f1 - f0 + kPairs - 1) / kPairs)));
@@ -263,137 +268,163 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
     f1 = min(f0 + (int64_t)parts.size * kPairs, f1);
     const int steps = uniform((int)((f1 - f0 + kPairs - 1) / kPairs));
 
-    at_u32x4 kf[D / 16], vf[D / 16];
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-        kf[j] = vf[j] = at_u32x4{0u, 0u, 0u, 0u};
-        if (key < kb && s.in) {
-            kf[j] = *reinterpret_cast<const at_u32x4*>(a.k.p + (int64_t)(s.k0 + key) * a.k.row + (int64_t)h * a.k.head +
-                                                       16 * j + 8 * g);
-            vf[j] = *reinterpret_cast<const at_u32x4*>(a.v.p + (int64_t)(s.k0 + key) * a.v.row + (int64_t)h * a.v.head +
-                                                       16 * j + 8 * g);
-        }
-    }
     pr_f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dk[t][r] = dv[t][r] = 0.0f;
-
-    PrPair at{uniform((int)(f0 / a.G)), uniform((int)(f0 % a.G))};   // the next step's first pair
-    PairInfo* info = reinterpret_cast<PairInfo*>(lds() + 2 * kStage<D>);
-    float n_lse = 0.0f, n_delta = 0.0f;
-    int n_pos = -1;
-    int now_lo = 0, now_hi = 0, next_lo = 0, next_hi = 0;   // first and last row of a step
-    auto copy = [&](int t) {
-        uint8_t* st = lds() + (t & 1) * kStage<D>;
-        const int left = (int)min(f1 - f0 - (int64_t)t * kPairs, (int64_t)kPairs);   // pairs of the step
-        constexpr int kRowsPer = 512 / D, kCopies = kPairs / kRowsPer / kWaves;
+    at_u32x4 kf[D / 16];
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const int r0 = (wave * kCopies + i) * kRowsPer, r = r0 + lane / (D / 8);
-            const int chunk = (lane % (D / 8)) ^ pr_swizzle<D>(r);
-            const PrPair p = pr_pair(a, at, min(r, left - 1));
-            const int64_t y = s.r0 + p.i, x = h * a.G + p.g;
-            lds_direct16_async(a.q.p + y * a.q.row + x * a.q.head + 8 * chunk, st + r0 * (2 * D));
-            lds_direct16_async(a.dout.p + y * a.dout.row + x * a.dout.head + 8 * chunk, st + kTileBytes<D> + r0 * (2 * D));
+    for (int j = 0; j < D / 16; ++j) {
+        kf[j] = at_u32x4{0u, 0u, 0u, 0u};
+        if (kw + c < kb && s.in)
+            kf[j] = *reinterpret_cast<const at_u32x4*>(a.k.p + (int64_t)(s.k0 + kw + c) * a.k.row + (int64_t)h * a.k.head +
+                                                       16 * j + 8 * g);
+    }
+
+    PrPair at{uniform((int)((uint32_t)f0 / (uint32_t)a.G)), uniform((int)((uint32_t)f0 % (uint32_t)a.G))};   // a step's first pair
+    // A copy of 1 KB takes kRowsPer pairs.  Where those are heads of one row, or
+    // whole rows, a lane's place relative to the first of them never changes.
+    constexpr int kRowsPer = 512 / D, kCopies = kPairs / kRowsPer / kWaves;
+    const bool even = a.G % kRowsPer == 0 || kRowsPer % a.G == 0;
+    const int lr = lane / (D / 8), li = a.G < kRowsPer ? lr / a.G : 0, lg = a.G < kRowsPer ? lr % a.G : lr;
+    // What a thread needs once a step waits in LDS: the sums and k leave no
+    // registers for it.
+    at_u32x4* mine = reinterpret_cast<at_u32x4*>(lds() + kMineAt<D>) + threadIdx.x;
+    *mine = at_u32x4{2u * ((uint32_t)li * (uint32_t)a.q.row + (uint32_t)lg * (uint32_t)a.q.head),
+                     2u * ((uint32_t)li * (uint32_t)a.dout.row + (uint32_t)lg * (uint32_t)a.dout.head),
+                     ((lane % (D / 8)) ^ pr_swizzle<D>(lr)) * 16u, (uint32_t)(pr_along<D>() | pr_across<D>() << 16)};
+    auto copy = [&](int t, const at_u32x4& my) {   // of the step that begins at `at`
+        uint8_t* st = lds() + kStagesAt<D> + (t & 1) * kKvStage<D>;
+        const int left = (int)min(f1 - f0 - (int64_t)t * kPairs, (int64_t)kPairs);   // pairs of the step
+        if (even && left == kPairs) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int r0 = (wave * kCopies + i) * kRowsPer;
+                const PrPair p = pr_pair(a, at, r0);
+                const int64_t y = s.r0 + p.i, x = h * a.G + p.g;
+                // (the swizzle of row r0 + lr is that of row lr but for two bits)
+                const uint32_t chunk = my[2] ^ (uint32_t)(16 * pr_swizzle<D>(r0));
+                lds_direct16_async(a.q.p + y * a.q.row + x * a.q.head, my[0] + chunk, st + r0 * (2 * D));
+                lds_direct16_async(a.dout.p + y * a.dout.row + x * a.dout.head, my[1] + chunk, st + kPairTile<D> + r0 * (2 * D));
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < kCopies; ++i) {
+                const int ln = pr_per_step(lane), r0 = (wave * kCopies + i) * kRowsPer, r = r0 + ln / (D / 8);
+                const int chunk = (ln % (D / 8)) ^ pr_swizzle<D>(r);
+                const PrPair p = pr_pair(a, at, min(r, left - 1));
+                const int64_t y = s.r0 + p.i, x = h * a.G + p.g;
+                lds_direct16_async(a.q.p + y * a.q.row + x * a.q.head + 8 * chunk, st + r0 * (2 * D));
+                lds_direct16_async(a.dout.p + y * a.dout.row + x * a.dout.head + 8 * chunk, st + kPairTile<D> + r0 * (2 * D));
+            }
         }
-        if (threadIdx.x < kPairs) {
-            const PrPair p = pr_pair(a, at, min((int)threadIdx.x, left - 1));
-            const int64_t row = (int64_t)(s.r0 + p.i) * a.Hq + h * a.G + p.g;
-            n_lse = a.lse[row];
-            n_delta = a.delta[row];
-            n_pos = (int)threadIdx.x < left ? pos0 + p.i : -1;
+        if (wave == 0) {   // (uniform) lse2 by the first half of the lanes, delta by the others
+            const int ln = pr_per_step(lane);
+            const PrPair p = pr_pair(a, at, min(ln & 31, left - 1));
+            const float* src = ln < 32 ? a.lse2 : a.delta;
+            lds_direct4_async(src + (int64_t)(s.r0 + p.i) * a.Hq + h * a.G + p.g, st + 2 * kPairTile<D>);
         }
-        now_lo = next_lo, now_hi = next_hi;
-        next_lo = pos0 + at.i;
-        next_hi = pos0 + uniform(pr_pair(a, at, left - 1).i);
-        const PrPair next = pr_pair(a, at, kPairs);
-        at = PrPair{uniform(next.i), uniform(next.g)};
     };
-    auto store_info = [&](int t) {
-        if (threadIdx.x < kPairs) {
-            PairInfo& x = info[t & 1];
-            const float l = n_lse * 1.4426950408889634f;
-            x.lse2[threadIdx.x] = n_lse == -INFINITY ? INFINITY : l;
-            x.delta[threadIdx.x] = n_delta;
-            x.pos[threadIdx.x] = n_pos;
-        }
-    };
-    const int along = pr_along<D>(), across = pr_across<D>();
+    // (a scale of 0 is taken as the least one, so that a hidden score stays infinite)
+    const float c2 = a.c2 == 0.0f ? 0x1p-126f : a.c2;
     if (steps > 0) {
-        copy(0);
-        store_info(0);
+        copy_tile<D, kWaves>(a.v, s.k0, h, ka, s.m, lds());
+        copy_tile<D, kWaves>(a.v, s.k0, h, min(ka + 64, s.m - 1), s.m, lds() + kTileBytes<D>);
+        copy(0, *mine);
     }
     pr_wait_copies();
     __syncthreads();
     for (int t = 0; t < steps; ++t) {
-        if (t + 1 < steps)
-            copy(t + 1);
-        else
-            now_lo = next_lo, now_hi = next_hi;
-        const bool whole = kw + 31 <= now_lo && f1 - f0 >= (int64_t)(t + 1) * kPairs && (a.window <= 0 || kw > now_hi - a.window);
-        const int stage = (t & 1) * kStage<D>;
-        const PairInfo& inf = info[t & 1];
+        const PrPair now = at;
+        const int left = (int)min(f1 - f0 - (int64_t)t * kPairs, (int64_t)kPairs);
+        const int plo = pos0 + now.i, phi = pos0 + uniform(pr_pair(a, now, left - 1).i);
+        const bool whole = kw + 31 <= plo && left == kPairs && (a.window <= 0 || kw > phi - a.window);
+        const PrPair next = pr_pair(a, at, kPairs);
+        at = PrPair{uniform(next.i), uniform(next.g)};
+        const at_u32x4 my = *mine;
+        const int along = my[3] & 0xffff, across = my[3] >> 16;
+        if (t + 1 < steps) copy(t + 1, my);
+        const int stage = kStagesAt<D> + (t & 1) * kKvStage<D>;
+        const float* stat = reinterpret_cast<const float*>(lds() + stage + 2 * kPairTile<D>) + 4 * g;
+
+        // N matrix instructions each: scores, dout v, dv, dk.  The weights are formed
+        // between those of dout v, the score gradients between those of dv; what they
+        // read from LDS is read kAhead of them before.
+        constexpr int N = D / 16, kAhead = 2;
+        at_u32x4 frag[kAhead], vfrag[kAhead];
+        at_f32x2 sf[kAhead];
+        int place = 0, vplace = 0;
+        auto fetch = [&](int n) {
+            if (n >= 4 * N) return;
+            const int k = n / N, j = n % N;
+            if (j == 0) place = pr_per_step(k < 2 ? along : across) + stage + (k == 1 || k == 2 ? kPairTile<D> : 0);
+            if (n == N) vplace = pr_per_step(along) + wave * (64 * D);
+            frag[n % kAhead] = k < 2 ? pr_read<D>(lds(), place, 0, j) : pr_read_across<D>(lds(), place, j / (D / 32), j % (D / 32));
+            if (k == 1) vfrag[n % kAhead] = pr_read<D>(lds(), vplace, 0, j);
+        };
+        // lse2, then delta, of scores 2 i and 2 i + 1
+        auto fetch_stat = [&](int i) {
+            if (i < 16) sf[i % kAhead] = *reinterpret_cast<const at_f32x2*>(stat + (i / 8) * kPairs + 8 * (i % 8 / 2) + 2 * (i % 2));
+        };
+        pr_f32x16 x, y;
+        at_u32x4 pf[2], ds[2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            // scores, weights, dv; then dout v, score gradients, dk: one set of
-            // scores at a time (with both the registers would not suffice)
-            const int qt = pr_per_step(along) + stage, qa = pr_per_step(across) + stage;
-            pr_f32x16 x, y;
+        for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
+        for (int i = 0; i < kAhead; ++i) fetch(i);
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) x = E::mfma(pr_read<D>(lds(), qt, b, j), kf[j], x);
-            __builtin_amdgcn_sched_barrier(0);
-            at_u32x4 pf[2], ds[2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r0 = 32 * b + 8 * i + 4 * g;
-                const at_f32x4 lse2 = *reinterpret_cast<const at_f32x4*>(inf.lse2 + r0);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[4 * i + r] = __builtin_fmaf(x[4 * i + r], a.c2, -lse2[r]);
-                if (!whole) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int pos = inf.pos[r0 + r];
-                        const int from = a.window > 0 ? max(pos, 0) - a.window : -1;
-                        x[4 * i + r] = (key <= pos) & (key > from) ? x[4 * i + r] : -INFINITY;
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[4 * i + r] = __builtin_amdgcn_exp2f(x[4 * i + r]);
-                pf[i / 2][2 * (i % 2)] = E::pack(x[4 * i], x[4 * i + 1]);
-                pf[i / 2][2 * (i % 2) + 1] = E::pack(x[4 * i + 2], x[4 * i + 3]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-#pragma unroll
-                for (int d = 0; d < D / 32; ++d) dv[d] = E::mfma(pr_read_across<D>(lds(), qa + kTileBytes<D>, 2 * b + w, d), pf[w], dv[d]);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) y = E::mfma(pr_read<D>(lds(), qt + kTileBytes<D>, b, j), vf[j], y);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const at_f32x4 delta = *reinterpret_cast<const at_f32x4*>(inf.delta + 32 * b + 8 * i + 4 * g);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) y[4 * i + r] = x[4 * i + r] * (y[4 * i + r] - delta[r]);
-                ds[i / 2][2 * (i % 2)] = E::pack(y[4 * i], y[4 * i + 1]);
-                ds[i / 2][2 * (i % 2) + 1] = E::pack(y[4 * i + 2], y[4 * i + 3]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-#pragma unroll
-                for (int d = 0; d < D / 32; ++d) dk[d] = E::mfma(pr_read_across<D>(lds(), qa, 2 * b + w, d), ds[w], dk[d]);
+        for (int j = 0; j < N; ++j) {
+            x = E::mfma(frag[j % kAhead], kf[j], x);
+            fetch(j + kAhead);
+            if (j >= N - kAhead) fetch_stat(j - (N - kAhead));
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (t + 1 < steps) store_info(t + 1);
+        if (!whole) {   // hidden pairs' scores: to weights of 0
+            const int ln = pr_per_step(lane), first = 4 * (ln >> 5), key = kw + (ln & 31);
+            const float hidden = c2 > 0.0f ? -INFINITY : INFINITY;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int f = first + 8 * (r / 4) + r % 4, pos = pos0 + pr_pair(a, now, f).i;
+                const int from = a.window > 0 ? max(pos, 0) - a.window : -1;
+                x[r] = (f < left) & (key <= pos) & (key > from) ? x[r] : hidden;
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            y = E::mfma(frag[j % kAhead], vfrag[j % kAhead], y);
+            fetch(N + j + kAhead);
+#pragma unroll
+            for (int i = 8 / N * j; i < 8 / N * (j + 1); ++i) {
+                x[2 * i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i], c2, -sf[i % kAhead][0]));
+                x[2 * i + 1] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i + 1], c2, -sf[i % kAhead][1]));
+                pf[i / 4][i % 4] = E::pack(x[2 * i], x[2 * i + 1]);
+                fetch_stat(i + kAhead);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            dv[j % (D / 32)] = E::mfma(frag[j % kAhead], pf[j / (D / 32)], dv[j % (D / 32)]);
+            fetch(2 * N + j + kAhead);
+#pragma unroll
+            for (int i = 8 / N * j; i < 8 / N * (j + 1); ++i) {
+                ds[i / 4][i % 4] = E::pack(x[2 * i] * (y[2 * i] - sf[i % kAhead][0]), x[2 * i + 1] * (y[2 * i + 1] - sf[i % kAhead][1]));
+                fetch_stat(8 + i + kAhead);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            dk[j % (D / 32)] = E::mfma(frag[j % kAhead], ds[j / (D / 32)], dk[j % (D / 32)]);
+            fetch(3 * N + j + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         pr_wait_copies();
         __syncthreads();
     }
+    const int key = kw + c;
     if (key >= kb) return;
     if (parts.used <= 1) {
         const int64_t row = (int64_t)(s.k0 + key) * a.Hkv + h;
@@ -493,8 +524,9 @@ hipError_t launch(const PromptPlan& p, PromptArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_prompt_backward(const PromptPlan& p, int type, int D, PromptArgs& a, void* ws, hipStream_t st) {
-    a.delta = static_cast<float*>(ws);
-    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.delta_bytes);
+    a.lse2 = static_cast<float*>(ws);
+    a.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.stat_bytes);
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 2 * p.stat_bytes);
     if (type == LTK_ROWS_BF16) return D == 64 ? launch<PrBf16, 64>(p, a, st) : launch<PrBf16, 128>(p, a, st);
     return D == 64 ? launch<PrF16, 64>(p, a, st) : launch<PrF16, 128>(p, a, st);
 }
