@@ -17,12 +17,6 @@ __device__ __forceinline__ uint8_t* lds() {
     return reinterpret_cast<uint8_t*>(prompt_lds);
 }
 
-// Row tile of a unit: pairs [f0, f1) of sequence s and key/value head h.
-struct Unit {
-    PrSeq s;
-    int h, f0, f1, split;
-};
-
 // Copies rows key0 .. key0 + 63 of one head into a tile, the last row again
 // for those past the end.
 template <int D, int NW>
@@ -47,24 +41,21 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
     const PrPlace pl = pr_place(a);
-    const int h = pl.h, split = pl.part;
-    const int64_t un = pl.unit;
-    const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
-    const PrSeq s = pr_seq(a, e);
-    const int64_t pairs = (int64_t)s.n * a.G;
-    const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));   // the longest first
-    if (tile < 0) return;
-    const int64_t f0 = tile * RT, f1 = min(f0 + RT, pairs);
-    const PrPair p0{uniform((int)(f0 / a.G)), uniform((int)(f0 % a.G))};
-    const int pos0 = s.pos0();
+    const int h = pl.h;
+    PrRowUnit u;
+    if (!pr_row_unit(a, pl.unit, u)) return;
+    const PrParts parts = pr_parts(a, u.t1 - u.t0);
+    if (pl.part >= parts.used) return;
+    const int t0 = u.t0 + pl.part * parts.size, t1 = min(t0 + parts.size, u.t1);
+    const PrSeq& s = u.s;
 
     // the wave's rows
     const int fw = 32 * wave;
-    const bool have = f0 + fw + c < f1;
-    const PrPair pr = pr_pair(a, p0, fw + c);
-    const int pos = have && s.in ? pos0 + pr.i : -1;
+    const bool have = fw + c < u.count;
+    const PrPair pr = pr_pair(a, u.first, fw + c);
+    const int pos = have && s.in ? s.pos0() + pr.i : -1;
     const int64_t row = have ? (int64_t)(s.r0 + pr.i) * a.Hq + h * a.G + pr.g : -1;
-    const int wlo = pos0 + pr_pair(a, p0, fw).i, whi = pos0 + (int)(min(f0 + fw + 31, f1 - 1) / a.G);
+    const int wlo = s.pos0() + pr_pair(a, u.first, fw).i, whi = s.pos0() + pr_pair(a, u.first, min(fw + 31, u.count - 1)).i;
     at_u32x4 q[D / 16];
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
@@ -73,16 +64,6 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
             q[j] = *reinterpret_cast<const at_u32x4*>(a.q.p + (int64_t)(s.r0 + pr.i) * a.q.row +
                                                       (int64_t)(h * a.G + pr.g) * a.q.head + 16 * j + 8 * g);
     }
-    // keys of the unit: [lo, hi)
-    const int plo = pos0 + p0.i, phi = pos0 + uniform((int)((f1 - 1) / a.G));
-    const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
-    const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
-    int t0 = lo / kKeys, t1 = (hi + kKeys - 1) / kKeys;
-    const PrParts parts = pr_parts(a, t1 - t0);
-    if (split >= parts.used) return;
-    t0 += split * parts.size;
-    t1 = min(t0 + parts.size, t1);
-
     float m = 0.0f, over = -INFINITY, l = 0.0f;
     pr_f32x16 o[D / 32];
 #pragma unroll
@@ -179,7 +160,7 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
         return;
     }
     // a part: RT rows of D sums, then RT pairs (m, l)
-    float* part = a.part + ((un * a.Hkv + h) * a.splits + split) * (int64_t)(RT * (D + 2));
+    float* part = a.part + ((pl.unit * a.Hkv + h) * a.splits + pl.part) * (int64_t)(RT * (D + 2));
     const int r = fw + c;
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
@@ -199,20 +180,12 @@ __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
     constexpr int RT = 32 * NW;
     const int64_t un = blockIdx.x / (uint32_t)a.Hkv;
     const int h = (int)(blockIdx.x - (uint32_t)un * (uint32_t)a.Hkv);
-    const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
-    const PrSeq s = pr_seq(a, e);
-    const int64_t pairs = (int64_t)s.n * a.G;
-    const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));
-    if (tile < 0) return;
-    const int64_t f0 = tile * RT, f1 = min(f0 + RT, pairs);
-    const int plo = s.pos0() + (int)(f0 / a.G), phi = s.pos0() + (int)((f1 - 1) / a.G);
-    const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
-    const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
-    const int used = pr_parts(a, (hi + kKeys - 1) / kKeys - lo / kKeys).used;
+    PrRowUnit u;
+    if (!pr_row_unit(a, un, u)) return;
+    const int used = pr_parts(a, u.t1 - u.t0).used;
     if (used <= 1) return;
     const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
-    const int64_t f = f0 + r;
-    if (f >= f1) return;
+    if (r >= u.count) return;
     const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(RT * (D + 2));
     float m = kNoRef, l = 0.0f;
     at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
@@ -223,7 +196,8 @@ __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
         l = __builtin_fmaf(f, part[(size_t)RT * D + 2 * r + 1], l);
         o += *reinterpret_cast<const at_f32x4*>(part + (size_t)r * D + d) * f;
     }
-    const int64_t row = (int64_t)(s.r0 + (int)(f / a.G)) * a.Hq + h * a.G + (int)(f % a.G);
+    const PrPair p = pr_pair(a, u.first, r);
+    const int64_t row = (int64_t)(u.s.r0 + p.i) * a.Hq + h * a.G + p.g;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     *reinterpret_cast<at_u32x2*>(a.out + row * D + d) =
         at_u32x2{E::pack(o[0] * inv, o[1] * inv), E::pack(o[2] * inv, o[3] * inv)};
@@ -240,17 +214,18 @@ hipError_t launch(const PromptPlan& p, const PromptArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Units are cut while there are too few of them for the card to run evenly: 512
-// workgroups run at once, and units of one sequence differ in length by up to
-// the whole of it, so that with two to a place the short ones fill up what the
-// long ones leave.  `steps` are those of a sequence of average length, `most` of
-// one that is all of the batch; a part has kLeast steps or more.
-static PromptCut cut(int64_t units, int Hkv, int64_t steps, int64_t most) {
-    constexpr int64_t kPlaces = 1024, kLeast = 8;
-    PromptCut c{units, units * Hkv, 1, 1 << 30};
-    if (c.blocks >= kPlaces || steps * most < kLeast * kLeast) return c;   // (the geometric mean of both)
-    const int64_t per = std::max(kLeast, (c.blocks * steps + kPlaces - 1) / kPlaces);
-    c.splits = (int)std::min((most + per - 1) / per, kPlaces / c.blocks + 1);
+// Units are cut while there are too few of them for the card to run evenly:
+// `places` workgroups run at once, and the units of one sequence differ in length
+// by up to the whole of it, so that with two to a place the short ones fill up
+// what the long ones leave.  `units` are about those with rows, `steps` those of
+// a sequence of average length, `most` of one that is all of the batch; a part
+// has kLeast steps or more.
+static PromptCut cut(int64_t all, int64_t units, int Hkv, int64_t steps, int64_t most, int64_t places) {
+    constexpr int64_t kLeast = 8;
+    PromptCut c{all, all * Hkv, 1, 1 << 30};
+    if (units * Hkv >= 2 * places || steps * most < kLeast * kLeast) return c;   // (the geometric mean of both)
+    const int64_t per = std::max(kLeast, (units * Hkv * steps + places - 1) / places);
+    c.splits = (int)std::min((most + per - 1) / per, 2 * places / c.blocks + 1);
     c.per = (int)per;
     c.blocks *= c.splits;
     return c;
@@ -263,13 +238,18 @@ PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int wind
     auto steps = [&](int64_t n, int64_t mul, int per) {   // over n tokens that count mul, as far as a window reaches
         return ((window > 0 ? std::min<int64_t>(n, (int64_t)window + 2 * rows) : n) * mul + per - 1) / per;
     };
-    p.rows = cut(pr_units(T, G, rows, n_seq), Hkv, steps((S + seqs - 1) / seqs, 1, kKeys), steps(S, 1, kKeys));
-    p.keys = cut(pr_units(S, 1, rows, n_seq), Hkv, steps((T + seqs - 1) / seqs, G, kPairs), steps(T, G, kPairs));
+    // (about: a sequence's last unit is half full)
+    const int64_t row_units = pr_units(T, G, rows, n_seq), row_about = (int64_t)T * G / rows + (seqs + 1) / 2;
+    const int64_t key_units = pr_units(S, 1, rows, n_seq), key_about = (int64_t)S / rows + (seqs + 1) / 2;
+    const int64_t s0 = steps((S + seqs - 1) / seqs, 1, kKeys), s1 = steps(S, 1, kKeys);
+    p.rows = cut(row_units, row_about, Hkv, s0, s1, 640);   // three a CU, less what the rounding up of parts adds
+    p.grad = cut(row_units, row_about, Hkv, s0, s1, 512);
+    p.keys = cut(key_units, key_about, Hkv, steps((T + seqs - 1) / seqs, G, kPairs), steps(T, G, kPairs), 1024);
     auto parts = [&](const PromptCut& c, int64_t floats) { return c.splits > 1 ? (size_t)(c.blocks * rows * floats) * 4 : 0; };
     p.fwd_bytes = std::max<size_t>(256, parts(p.rows, D + 2));
     p.stat_bytes = ((size_t)T * Hq * 4 + 255) / 256 * 256;
-    p.bwd_bytes = std::max<size_t>(256, 2 * p.stat_bytes + std::max(parts(p.rows, D), parts(p.keys, 2 * D)));
-    p.fits = grid_fits(std::max(p.rows.blocks, p.keys.blocks), 64 * kWaves) && grid_fits((int64_t)T * Hq / 2 + 1, 16);
+    p.bwd_bytes = std::max<size_t>(256, 2 * p.stat_bytes + std::max(parts(p.grad, D), parts(p.keys, 2 * D)));
+    p.fits = grid_fits(std::max({p.rows.blocks, p.grad.blocks, p.keys.blocks}), 64 * kWaves) && grid_fits((int64_t)T * Hq / 2 + 1, 16);
     return p;
 }
 

@@ -115,38 +115,71 @@ struct PrSeq {
 __device__ __forceinline__ int pr_bound(const int32_t* cu, int e, int n_seq, int T) {
     return e <= 0 ? 0 : e > n_seq + 1 ? T : min(max(cu[e - 1], 0), T);
 }
-__device__ __forceinline__ PrSeq pr_seq(const PromptArgs& a, int e) {
-    PrSeq s;
-    s.r0 = pr_bound(a.cu, e, a.n_seq, a.T);
-    s.n = max(pr_bound(a.cu, e + 1, a.n_seq, a.T) - s.r0, 0);
-    s.k0 = pr_bound(a.cu_k, e, a.n_seq, a.S);
-    s.m = max(pr_bound(a.cu_k, e + 1, a.n_seq, a.S) - s.k0, 0);
-    s.in = e >= 1 && e <= a.n_seq;
-    return s;
-}
 
-// Units of `per` rows of a stretch (each row counting mul), without a prefix
-// sum: stretch e has the numbers from  bound(e) mul / per + e  on, at least as
-// many as it can need; numbers past its own are empty.
-__device__ __forceinline__ int64_t pr_first(const int32_t* cu, const PromptArgs& a, int T, int e, int mul, int per) {
-    return (int64_t)pr_bound(cu, e, a.n_seq, T) * mul / per + e;
-}
-// The stretch of number u, by all lanes of a wave: 64 stretches, or stretches of
-// stretches, at a look (bisection would be a chain of dependent loads: 16
-// sequences of up to 2,039 rows 288 us with it, ... without).
-template <int PER>
-__device__ __forceinline__ int pr_find(const int32_t* cu, const PromptArgs& a, int T, int64_t u, int mul) {
+// Units of PER rows of a stretch (each row counting mul), without a prefix sum:
+// stretch e has the numbers from  bound(e) mul / PER + e  on, at least as many as
+// it can need; numbers past its own are empty.
+//
+// The stretch of unit u and the unit's number in it, by all lanes of a wave: 64
+// stretches, or stretches of stretches, at a look, whose bounds serve for the
+// result (bisection would be a chain of dependent loads).
+template <int PER, bool KEYS>
+__device__ __forceinline__ PrSeq pr_seq_of(const PromptArgs& a, int64_t u, int mul, int64_t& number) {
     const int lane = threadIdx.x & 63, all = a.n_seq + 2;
+    auto first = [&](int bound, int e) { return (int64_t)bound * mul / PER + e; };
+    auto rows = [&](int e) { return pr_bound(a.cu, e, a.n_seq, a.T); };
+    auto keys = [&](int e) { return pr_bound(a.cu_k, e, a.n_seq, a.S); };
     int lo = 0, step = 1;
     while (step < (all + 63) / 64) step *= 64;
-    for (; step >= 1; step /= 64) {
+    for (; step > 1; step /= 64) {
         const int e = lo + lane * step;
-        const uint64_t at = __ballot(e < all && pr_first(cu, a, T, e, mul, PER) <= u);
+        const uint64_t at = __ballot(e < all && first(KEYS ? keys(e) : rows(e), e) <= u);
         lo += at ? (63 - __clzll((long long)at)) * step : 0;
     }
-    return lo;
+    const int mine = min(lo + lane, all), r = rows(mine), k = keys(mine);
+    const uint64_t at = __ballot(lo + lane < all && first(KEYS ? k : r, mine) <= u);
+    const int i = at ? 63 - __clzll((long long)at) : 0, e = lo + i;
+    auto bound = [&](int x, int j, bool key) {   // of stretch lo + j
+        return j < 64 ? __builtin_amdgcn_readlane(x, j) : uniform(key ? keys(lo + j) : rows(lo + j));
+    };
+    PrSeq s;
+    s.r0 = bound(r, i, false);
+    s.n = max(bound(r, i + 1, false) - s.r0, 0);
+    s.k0 = bound(k, i, true);
+    s.m = max(bound(k, i + 1, true) - s.k0, 0);
+    s.in = e >= 1 && e <= a.n_seq;
+    number = u - first(KEYS ? s.k0 : s.r0, e);
+    return s;
 }
 inline int64_t pr_units(int64_t T, int64_t mul, int per, int n_seq) { return T * mul / per + n_seq + 2; }
+
+// A row tile: 32 kWaves pairs of a sequence and key/value head, and the steps of
+// keys that they see.
+struct PrRowUnit {
+    PrSeq s;
+    PrPair first;   // its first pair
+    int count;      // of its pairs
+    int lo, hi;     // first and last position of its rows
+    int t0, t1;     // steps of kKeys keys
+};
+__device__ __forceinline__ bool pr_row_unit(const PromptArgs& a, int64_t un, PrRowUnit& u) {
+    constexpr int RT = 32 * kWaves;
+    int64_t number;
+    u.s = pr_seq_of<RT, false>(a, un, a.G, number);
+    const uint32_t pairs = (uint32_t)u.s.n * (uint32_t)a.G;   // < 2^31
+    const int64_t tile = (int64_t)((pairs + RT - 1) / RT) - 1 - number;   // the longest first
+    if (tile < 0) return false;
+    const uint32_t f0 = (uint32_t)tile * RT, i = f0 / (uint32_t)a.G;
+    u.first = PrPair{(int)i, (int)(f0 - i * (uint32_t)a.G)};
+    u.count = (int)min(pairs - f0, (uint32_t)RT);
+    u.lo = u.s.pos0() + u.first.i;
+    u.hi = u.s.pos0() + pr_pair(a, u.first, u.count - 1).i;
+    const int end = u.s.in ? min(max(u.hi + 1, 0), u.s.m) : 0;
+    const int from = a.window > 0 ? min(max(max(u.lo, 0) - a.window + 1, 0), end) : 0;
+    u.t0 = from / kKeys;
+    u.t1 = (end + kKeys - 1) / kKeys;
+    return true;
+}
 
 // A tile in LDS: rows of D 16-bit values, whose 16-byte chunk x lies at chunk
 // x ^ swizzle(row), so that both ways of reading touch all banks: 16
@@ -218,7 +251,7 @@ struct PromptCut {
     int splits, per;
 };
 struct PromptPlan {
-    PromptCut rows, keys;           // the launches over row tiles (forward, dq) and over key tiles (dk, dv)
+    PromptCut rows, grad, keys;     // the launches over row tiles (forward; dq) and over key tiles (dk, dv)
     size_t fwd_bytes, bwd_bytes;    // workspaces
     size_t stat_bytes;              // of the backward pass's: lse2, and as much for delta, before the parts
     bool fits;

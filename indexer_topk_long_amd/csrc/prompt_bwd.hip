@@ -70,23 +70,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
     const PrPlace pl = pr_place(a);
-    const int h = pl.h, split = pl.part;
-    const int64_t un = pl.unit;
-    const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
-    const PrSeq s = pr_seq(a, e);
-    const int64_t pairs = (int64_t)s.n * a.G;
-    const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));   // the longest first
-    if (tile < 0) return;
-    const int64_t f0 = tile * RT, f1 = min(f0 + RT, pairs);
-    const PrPair p0{uniform((int)(f0 / a.G)), uniform((int)(f0 % a.G))};
-    const int pos0 = s.pos0();
+    const int h = pl.h;
+    PrRowUnit u;
+    if (!pr_row_unit(a, pl.unit, u)) return;
+    const PrParts parts = pr_parts(a, u.t1 - u.t0);
+    if (pl.part >= parts.used) return;
+    const int t0 = u.t0 + pl.part * parts.size, t1 = min(t0 + parts.size, u.t1);
+    const PrSeq& s = u.s;
 
+    // the wave's rows
     const int fw = 32 * wave;
-    const bool have = f0 + fw + c < f1;
-    const PrPair pr = pr_pair(a, p0, fw + c);
-    const int pos = have && s.in ? pos0 + pr.i : -1;
+    const bool have = fw + c < u.count;
+    const PrPair pr = pr_pair(a, u.first, fw + c);
+    const int pos = have && s.in ? s.pos0() + pr.i : -1;
     const int64_t row = have ? (int64_t)(s.r0 + pr.i) * a.Hq + h * a.G + pr.g : -1;
-    const int wlo = pos0 + pr_pair(a, p0, fw).i, whi = pos0 + (int)(min(f0 + fw + 31, f1 - 1) / a.G);
+    const int wlo = s.pos0() + pr_pair(a, u.first, fw).i, whi = s.pos0() + pr_pair(a, u.first, min(fw + 31, u.count - 1)).i;
     at_u32x4 q[D / 16], dout[D / 16];
     float lse2 = INFINITY, delta = 0.0f;
 #pragma unroll
@@ -110,16 +108,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
         lse2 = base2(a.lse[row]);
     }
     delta = pr_sum_halves(delta);
-    if (have && split == 0 && g == 0) a.delta[row] = delta, a.lse2[row] = lse2;   // for the dk and dv launch
-    const int plo = pos0 + p0.i, phi = pos0 + uniform((int)((f1 - 1) / a.G));
-    const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
-    const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
-    int t0 = lo / kKeys, t1 = (hi + kKeys - 1) / kKeys;
-    const PrParts parts = pr_parts(a, t1 - t0);
-    if (split >= parts.used) return;
-    t0 += split * parts.size;
-    t1 = min(t0 + parts.size, t1);
-
+    if (have && pl.part == 0 && g == 0) a.delta[row] = delta, a.lse2[row] = lse2;   // for the dk and dv launch
     pr_f32x16 o[D / 32];
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
@@ -184,7 +173,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
                              E::pack(o[t][4 * i + 2] * a.scale, o[t][4 * i + 3] * a.scale)};
         return;
     }
-    float* part = a.part + ((un * a.Hkv + h) * a.splits + split) * (int64_t)(RT * D);
+    float* part = a.part + ((pl.unit * a.Hkv + h) * a.splits + pl.part) * (int64_t)(RT * D);
     const int r = fw + c;
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
@@ -200,24 +189,17 @@ __global__ __launch_bounds__(2 * D) void prompt_dq_join_kernel(PromptArgs a) {
     constexpr int RT = kUnit;
     const int64_t un = blockIdx.x / (uint32_t)a.Hkv;
     const int h = (int)(blockIdx.x - (uint32_t)un * (uint32_t)a.Hkv);
-    const int e = pr_find<RT>(a.cu, a, a.T, un, a.G);
-    const PrSeq s = pr_seq(a, e);
-    const int64_t pairs = (int64_t)s.n * a.G;
-    const int64_t tile = (pairs + RT - 1) / RT - 1 - (un - pr_first(a.cu, a, a.T, e, a.G, RT));
-    if (tile < 0) return;
-    const int64_t f0 = tile * RT, f1 = min(f0 + RT, pairs);
-    const int plo = s.pos0() + (int)(f0 / a.G), phi = s.pos0() + (int)((f1 - 1) / a.G);
-    const int hi = s.in ? min(max(phi + 1, 0), s.m) : 0;
-    const int lo = a.window > 0 ? min(max(max(plo, 0) - a.window + 1, 0), hi) : 0;
-    const int used = pr_parts(a, (hi + kKeys - 1) / kKeys - lo / kKeys).used;
+    PrRowUnit u;
+    if (!pr_row_unit(a, un, u)) return;
+    const int used = pr_parts(a, u.t1 - u.t0).used;
     if (used <= 1) return;
     const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
-    const int64_t f = f0 + r;
-    if (f >= f1) return;
+    if (r >= u.count) return;
     const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(RT * D) + (size_t)r * D + d;
     at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
     for (int i = 0; i < used; ++i) o += *reinterpret_cast<const at_f32x4*>(part + (int64_t)i * (RT * D));
-    const int64_t row = (int64_t)(s.r0 + (int)(f / a.G)) * a.Hq + h * a.G + (int)(f % a.G);
+    const PrPair p = pr_pair(a, u.first, r);
+    const int64_t row = (int64_t)(u.s.r0 + p.i) * a.Hq + h * a.G + p.g;
     *reinterpret_cast<at_u32x2*>(a.dq + row * D + d) =
         at_u32x2{E::pack(o[0] * a.scale, o[1] * a.scale), E::pack(o[2] * a.scale, o[3] * a.scale)};
 }
@@ -254,9 +236,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
     const PrPlace pl = pr_place(a);
     const int h = pl.h, split = pl.part;
     const int64_t un = pl.unit;
-    const int e = pr_find<kUnit>(a.cu_k, a, a.S, un, 1);
-    const PrSeq s = pr_seq(a, e);
-    const int64_t tile = un - pr_first(a.cu_k, a, a.S, e, 1, kUnit);   // (the first keys are seen by the most rows)
+    int64_t tile;   // (the first keys are seen by the most rows)
+    const PrSeq s = pr_seq_of<kUnit, true>(a, un, 1, tile);
     if (tile * kUnit >= s.m) return;
     const int ka = (int)tile * kUnit, kb = min(ka + kUnit, s.m), pos0 = s.pos0();
     const int kw = ka + 32 * wave;
@@ -351,21 +332,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
         // N matrix instructions each: scores, dout v, dv, dk.  The weights are formed
         // between those of dout v, the score gradients between those of dv; what they
         // read from LDS is read kAhead of them before.
-        constexpr int N = D / 16, kAhead = 2;
-        at_u32x4 frag[kAhead], vfrag[kAhead];
-        at_f32x2 sf[kAhead];
+        constexpr int N = D / 16, kAhead = 4, kNear = 2;
+        at_u32x4 frag[kAhead], vfrag[kNear];
+        at_f32x2 sf[kNear];
         int place = 0, vplace = 0;
         auto fetch = [&](int n) {
             if (n >= 4 * N) return;
             const int k = n / N, j = n % N;
             if (j == 0) place = pr_per_step(k < 2 ? along : across) + stage + (k == 1 || k == 2 ? kPairTile<D> : 0);
-            if (n == N) vplace = pr_per_step(along) + wave * (64 * D);
             frag[n % kAhead] = k < 2 ? pr_read<D>(lds(), place, 0, j) : pr_read_across<D>(lds(), place, j / (D / 32), j % (D / 32));
-            if (k == 1) vfrag[n % kAhead] = pr_read<D>(lds(), vplace, 0, j);
+        };
+        auto fetch_v = [&](int j) {
+            if (j < 0 || j >= N) return;
+            if (j == 0) vplace = pr_per_step(along) + wave * (64 * D);
+            vfrag[j % kNear] = pr_read<D>(lds(), vplace, 0, j);
         };
         // lse2, then delta, of scores 2 i and 2 i + 1
         auto fetch_stat = [&](int i) {
-            if (i < 16) sf[i % kAhead] = *reinterpret_cast<const at_f32x2*>(stat + (i / 8) * kPairs + 8 * (i % 8 / 2) + 2 * (i % 2));
+            if (i < 16) sf[i % kNear] = *reinterpret_cast<const at_f32x2*>(stat + (i / 8) * kPairs + 8 * (i % 8 / 2) + 2 * (i % 2));
         };
         pr_f32x16 x, y;
         at_u32x4 pf[2], ds[2];
@@ -377,7 +361,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
         for (int j = 0; j < N; ++j) {
             x = E::mfma(frag[j % kAhead], kf[j], x);
             fetch(j + kAhead);
-            if (j >= N - kAhead) fetch_stat(j - (N - kAhead));
+            fetch_v(j - (N - kNear));
+            if (j >= N - kNear) fetch_stat(j - (N - kNear));
             __builtin_amdgcn_sched_barrier(0);
         }
         if (!whole) {   // hidden pairs' scores: to weights of 0
@@ -393,14 +378,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
         }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            y = E::mfma(frag[j % kAhead], vfrag[j % kAhead], y);
+            y = E::mfma(frag[j % kAhead], vfrag[j % kNear], y);
             fetch(N + j + kAhead);
+            fetch_v(j + kNear);
 #pragma unroll
             for (int i = 8 / N * j; i < 8 / N * (j + 1); ++i) {
-                x[2 * i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i], c2, -sf[i % kAhead][0]));
-                x[2 * i + 1] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i + 1], c2, -sf[i % kAhead][1]));
+                x[2 * i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i], c2, -sf[i % kNear][0]));
+                x[2 * i + 1] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i + 1], c2, -sf[i % kNear][1]));
                 pf[i / 4][i % 4] = E::pack(x[2 * i], x[2 * i + 1]);
-                fetch_stat(i + kAhead);
+                fetch_stat(i + kNear);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -410,8 +396,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
             fetch(2 * N + j + kAhead);
 #pragma unroll
             for (int i = 8 / N * j; i < 8 / N * (j + 1); ++i) {
-                ds[i / 4][i % 4] = E::pack(x[2 * i] * (y[2 * i] - sf[i % kAhead][0]), x[2 * i + 1] * (y[2 * i + 1] - sf[i % kAhead][1]));
-                fetch_stat(8 + i + kAhead);
+                ds[i / 4][i % 4] = E::pack(x[2 * i] * (y[2 * i] - sf[i % kNear][0]), x[2 * i + 1] * (y[2 * i + 1] - sf[i % kNear][1]));
+                fetch_stat(8 + i + kNear);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -458,9 +444,8 @@ template <class E, int D>
 __global__ __launch_bounds__(2 * D) void prompt_dkv_join_kernel(PromptArgs a) {
     const int64_t un = blockIdx.x / (uint32_t)a.Hkv;
     const int h = (int)(blockIdx.x - (uint32_t)un * (uint32_t)a.Hkv);
-    const int e = pr_find<kUnit>(a.cu_k, a, a.S, un, 1);
-    const PrSeq s = pr_seq(a, e);
-    const int64_t tile = un - pr_first(a.cu_k, a, a.S, e, 1, kUnit);   // (the first keys are seen by the most rows)
+    int64_t tile;   // (the first keys are seen by the most rows)
+    const PrSeq s = pr_seq_of<kUnit, true>(a, un, 1, tile);
     if (tile * kUnit >= s.m) return;
     const int ka = (int)tile * kUnit, kb = min(ka + kUnit, s.m);
     int64_t f0, f1;
@@ -502,8 +487,8 @@ hipError_t launch(const PromptPlan& p, PromptArgs& a, hipStream_t st) {
     constexpr int per = 256 / (D / 8);
     if (!a.dq && rows > 0) prompt_delta_kernel<E, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
     if (a.dq && rows > 0) {
-        a.splits = p.rows.splits, a.per = p.rows.per, a.units = p.rows.units;
-        prompt_dq_kernel<E, D><<<(unsigned)p.rows.blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);
+        a.splits = p.grad.splits, a.per = p.grad.per, a.units = p.grad.units;
+        prompt_dq_kernel<E, D><<<(unsigned)p.grad.blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);
         if (a.splits > 1)
             prompt_dq_join_kernel<E, D><<<dim3((unsigned)(a.units * a.Hkv), kUnit / 8), 2 * D, 0, st>>>(a);
     }
