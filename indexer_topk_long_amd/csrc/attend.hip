@@ -534,6 +534,7 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 template <int D, int MT, int PART>
 __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_kernel(AttendArgs a) {
     const int n_batch = batch_size<PART>(a);
+    if constexpr (PART == kSharedKeys) note_own(a);
     extern __shared__ __attribute__((aligned(16))) float sh[];
     __shared__ PlanLds ls;
     __shared__ Place place;

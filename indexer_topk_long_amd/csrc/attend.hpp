@@ -190,6 +190,7 @@ struct AttendArgs {
     const int32_t* groups;
     const int32_t* shared_len;
     int n_group;
+    int32_t* own;            // [n_seq]: keys that a sequence does not see for itself, as the shared keys' launch notes them
     float* prior;            // [T * Hq][D + kPriorTail]: every row's sums over its group's shared keys
 };
 
@@ -204,8 +205,12 @@ __device__ __forceinline__ int group_at(const AttendArgs& a, int j) { return min
 __device__ __forceinline__ int shared_keys(const AttendArgs& a, int j) {
     return min(max(a.shared_len[j], 0), a.bt.max_pages << a.c.page_shift);
 }
-// Keys that sequence b does not see for itself: those its group shares.
-__device__ __forceinline__ int own_from(const AttendArgs& a, int b) {
+// Keys that sequence b does not see for itself: those its group shares.  Found
+// once, by the shared keys' launch (its threads all call note_own): looked for by
+// every workgroup of the second launch, several times a unit, it cost the
+// smallest calls 7 us.
+__device__ __forceinline__ int own_from(const AttendArgs& a, int b) { return a.own[b]; }
+__device__ __forceinline__ int find_own(const AttendArgs& a, int b) {
     int lo = 0, hi = a.n_group - 1;
     if (hi < 0) return 0;
     while (lo < hi) {
@@ -216,6 +221,11 @@ __device__ __forceinline__ int own_from(const AttendArgs& a, int b) {
             hi = mid - 1;
     }
     return group_at(a, lo) <= b && b < group_at(a, lo + 1) ? shared_keys(a, lo) : 0;
+}
+__device__ __forceinline__ void note_own(const AttendArgs& a) {
+    const int64_t threads = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < a.bt.n_seq; b += threads)
+        a.own[b] = find_own(a, (int)b);
 }
 // The entries of the batch as a launch sees it: sequences, or groups with the
 // rows of all their sequences.

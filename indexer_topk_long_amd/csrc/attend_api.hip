@@ -57,9 +57,11 @@ int run_attend(int kind, const ltk_kv_cache* cache, AttendArgs& a, int64_t entri
                                                                                                           : LTK_EHIP;
 }
 
-// Sums over the shared keys of every row and head.
-size_t prior_bytes(int64_t T, int64_t Hq, int64_t D) {
-    return ((size_t)(T * Hq) * (size_t)(D + kPriorTail) * sizeof(float) + 255) / 256 * 256;
+// What the shared keys' launch leaves for the other: own, then the sums of every
+// row and head.
+size_t own_bytes(int64_t n_seq) { return ((size_t)n_seq * sizeof(int32_t) + 255) / 256 * 256; }
+size_t prior_bytes(int64_t T, int64_t Hq, int64_t D, int64_t n_seq) {
+    return own_bytes(n_seq) + ((size_t)(T * Hq) * (size_t)(D + kPriorTail) * sizeof(float) + 255) / 256 * 256;
 }
 
 // The arguments every attend call shares.
@@ -175,11 +177,12 @@ int litetopk_attend_shared(const ltk_kv_cache* cache, const ltk_kv_batch* batch,
     const AttendPlan shared = attend_plan(LTK_ATTEND, T, Hq, a.c.Hkv, D, n_group, entries, 0);
     const AttendPlan own = attend_plan(LTK_ATTEND, T, Hq, a.c.Hkv, D, batch->n_seq, entries, 0);
     if (!shared.fits() || !own.fits()) return LTK_EINVAL;
-    const size_t prior = prior_bytes(T, Hq, D);
+    const size_t prior = prior_bytes(T, Hq, D, batch->n_seq);
     if (ws_bytes < prior + std::max(shared.ws_bytes, own.ws_bytes)) return LTK_EWORKSPACE;
     if (T == 0 || batch->n_seq == 0) return LTK_OK;
     if ((st = litetopk_device_check()) != LTK_OK) return st;
-    a.prior = static_cast<float*>(ws);
+    a.own = static_cast<int32_t*>(ws);
+    a.prior = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + own_bytes(batch->n_seq));
     void* rest = static_cast<uint8_t*>(ws) + prior;   // (the second launch's parts may lie where the first one's did)
     const hipStream_t on = static_cast<hipStream_t>(stream);
     if (launch_attend(LTK_ATTEND, D, shared, a, rest, on, kSharedKeys) != hipSuccess) return LTK_EHIP;
@@ -190,7 +193,7 @@ size_t litetopk_attend_shared_workspace_bytes(int32_t T, int32_t Hq, int32_t n_k
                                               int32_t n_group, int64_t entries) {
     const size_t own = litetopk_attend_workspace_bytes(LTK_ATTEND, T, Hq, n_kv_heads, head_dim, n_seq, entries, 0);
     const size_t shared = litetopk_attend_workspace_bytes(LTK_ATTEND, T, Hq, n_kv_heads, head_dim, n_group, entries, 0);
-    return own && shared ? prior_bytes(T, Hq, head_dim) + std::max(own, shared) : 0;
+    return own && shared ? prior_bytes(T, Hq, head_dim, n_seq) + std::max(own, shared) : 0;
 }
 
 int litetopk_kv_read(const ltk_kv_cache* cache, const ltk_kv_batch* batch, int32_t T, int32_t type, void* k_out,

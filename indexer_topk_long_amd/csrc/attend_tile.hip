@@ -664,6 +664,7 @@ __device__ __forceinline__ int64_t line_of(const AttendArgs& a, int b) {
 template <int D, int NW, int PART>
 __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
     const int n_batch = batch_size<PART>(a);
+    if constexpr (PART == kSharedKeys) note_own(a);
     __shared__ ScanLds<NW> sc;
     if (threadIdx.x == 0) sc.largest = 0;
     __syncthreads();

@@ -219,12 +219,11 @@ hipError_t launch(const PromptPlan& p, const PromptArgs& a, hipStream_t st) {
 // by up to the whole of it, so that with two to a place the short ones fill up
 // what the long ones leave.  `units` are about those with rows, `steps` those of
 // a sequence of average length, `most` of one that is all of the batch; a part
-// has kLeast steps or more.
-static PromptCut cut(int64_t all, int64_t units, int Hkv, int64_t steps, int64_t most, int64_t places) {
-    constexpr int64_t kLeast = 8;
+// has `least` steps or more (the joining launch costs as much as four or so).
+static PromptCut cut(int64_t all, int64_t units, int Hkv, int64_t steps, int64_t most, int64_t places, int64_t least) {
     PromptCut c{all, all * Hkv, 1, 1 << 30};
-    if (units * Hkv >= 2 * places || steps * most < kLeast * kLeast) return c;   // (the geometric mean of both)
-    const int64_t per = std::max(kLeast, (units * Hkv * steps + places - 1) / places);
+    if (units * Hkv >= 2 * places || steps * most < least * least) return c;   // (the geometric mean of both)
+    const int64_t per = std::max(least, (units * Hkv * steps + places - 1) / places);
     c.splits = (int)std::min((most + per - 1) / per, 2 * places / c.blocks + 1);
     c.per = (int)per;
     c.blocks *= c.splits;
@@ -242,9 +241,9 @@ PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int wind
     const int64_t row_units = pr_units(T, G, rows, n_seq), row_about = (int64_t)T * G / rows + (seqs + 1) / 2;
     const int64_t key_units = pr_units(S, 1, rows, n_seq), key_about = (int64_t)S / rows + (seqs + 1) / 2;
     const int64_t s0 = steps((S + seqs - 1) / seqs, 1, kKeys), s1 = steps(S, 1, kKeys);
-    p.rows = cut(row_units, row_about, Hkv, s0, s1, 640);   // three a CU, less what the rounding up of parts adds
-    p.grad = cut(row_units, row_about, Hkv, s0, s1, 512);
-    p.keys = cut(key_units, key_about, Hkv, steps((T + seqs - 1) / seqs, G, kPairs), steps(T, G, kPairs), 1024);
+    p.rows = cut(row_units, row_about, Hkv, s0, s1, 640, 8);   // three a CU, less what the rounding up of parts adds
+    p.grad = cut(row_units, row_about, Hkv, s0, s1, 512, 8);
+    p.keys = cut(key_units, key_about, Hkv, steps((T + seqs - 1) / seqs, G, kPairs), steps(T, G, kPairs), 1024, 16);
     auto parts = [&](const PromptCut& c, int64_t floats) { return c.splits > 1 ? (size_t)(c.blocks * rows * floats) * 4 : 0; };
     p.fwd_bytes = std::max<size_t>(256, parts(p.rows, D + 2));
     p.stat_bytes = ((size_t)T * Hq * 4 + 255) / 256 * 256;
