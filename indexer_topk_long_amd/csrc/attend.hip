@@ -394,7 +394,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs& a, at_bf16x8 (&q)
 // One unit's key tiles [t0, t1) against its rows [f0, f1) (flattened).
 template <int D, int MT, int PART>
 __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& sr, int b, int h, int f0, int f1,
-                                           const KeyRange32& kr, int t0, int t1, float* sh, float* part) {
+                                           const KeyRange32& kr, int t0, int t1, int own, float* sh, float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
     const int pos_lo = PART == kSharedKeys ? kr.hi - 1 : sr.pos0 + uniform(f0 / a.G);
@@ -419,17 +419,16 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) st[mt].o[e] = at_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // the first wave of the unit's first part begins from the shared keys' sums
-        if (PART == kOwnKeys && t0 == 0 && wave == 0 && row[mt] >= 0 && own_from(a, b) > 0) {
+        if (PART == kOwnKeys && t0 == 0 && wave == 0 && row[mt] >= 0 && own > 0) {
             const float* src = a.prior + row[mt] * (D + kPriorTail);
-            if (src[D + 1] > 0.0f) {
-                st[mt].m = src[D];
-                st[mt].over = kSlack;
-                st[mt].l = g == 0 ? src[D + 1] : 0.0f;
+            const float m = src[D], l = src[D + 1];   // (without a key: zeros, and no reference)
+            st[mt].m = l > 0.0f ? m : 0.0f;
+            st[mt].over = l > 0.0f ? kSlack : -INFINITY;
+            st[mt].l = g == 0 ? l : 0.0f;
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                    for (int e = 0; e < D / 16; ++e) st[mt].o[e][r] = src[(4 * g + r) * (D / 16) + e];
-            }
+                for (int e = 0; e < D / 16; ++e) st[mt].o[e][r] = src[(4 * g + r) * (D / 16) + e];
         }
     }
     load_queries<D, MT>(a, q, row, g);
@@ -597,10 +596,10 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd(D, MT))) void attend_k
         }
         if (t0 < t1) {   // (else the range ends before the unit's first tile)
             const int all = PART == kSharedKeys ? shared_keys(a, b) - 1 : 0;   // position that the shared keys end at
-            const KeyRange32 kr =
-                key_range<PART>(a, PART == kSharedKeys ? all : w.sr.pos0 + uniform(f0 / a.G),
-                                PART == kSharedKeys ? all : w.sr.pos0 + uniform((f1 - 1) / a.G), PART == kOwnKeys ? own_from(a, b) : 0);
-            dense_unit<D, MT, PART>(a, w.sr, b, h, f0, f1, kr, t0, min(t1, kr.tiles), sh, part);
+            const int own = PART == kOwnKeys ? own_from(a, b) : 0;
+            const KeyRange32 kr = key_range<PART>(a, PART == kSharedKeys ? all : w.sr.pos0 + uniform(f0 / a.G),
+                                                  PART == kSharedKeys ? all : w.sr.pos0 + uniform((f1 - 1) / a.G), own);
+            dense_unit<D, MT, PART>(a, w.sr, b, h, f0, f1, kr, t0, min(t1, kr.tiles), own, sh, part);
         }
         __syncthreads();   // finish() has read its LDS
         if (uniform(place.at) >= end) return;

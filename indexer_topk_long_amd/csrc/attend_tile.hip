@@ -466,7 +466,7 @@ struct DenseScale {
 
 template <int D, int NW, int PART>
 __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& sr, int b, const UnitRows& u,
-                                           const KeyTiles& kt, int t0, int t1, float* part) {
+                                           const KeyTiles& kt, int t0, int t1, int own, float* part) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
     const int fw = u.f0 + 32 * wave;                      // the wave's rows [fw, fw1)
@@ -480,17 +480,16 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     WaveState<D> st;
     begin_rows<D>(a, row, q, st);
     // a unit's first part begins from the shared keys' sums
-    if (PART == kOwnKeys && t0 == 0 && row >= 0 && own_from(a, b) > 0) {
+    if (PART == kOwnKeys && t0 == 0 && row >= 0 && own > 0) {
         const float* src = a.prior + row * (D + kPriorTail);
-        if (src[D + 1] > 0.0f) {
-            st.m = src[D];
-            st.over = kSlack;
-            st.l = g == 0 ? src[D + 1] : 0.0f;
+        const float m = src[D], l = src[D + 1];   // (without a key: zeros, and no reference)
+        st.m = l > 0.0f ? m : 0.0f;
+        st.over = l > 0.0f ? kSlack : -INFINITY;
+        st.l = g == 0 ? l : 0.0f;
 #pragma unroll
-            for (int t = 0; t < D / 32; ++t)
+        for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) st.o[t][r] = src[32 * t + 8 * (r / 4) + 4 * g + r % 4];
-        }
+            for (int r = 0; r < 16; ++r) st.o[t][r] = src[32 * t + 8 * (r / 4) + 4 * g + r % 4];
     }
 
     const int32_t* table = batch_table<PART>(a, b);
@@ -751,11 +750,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendArgs a) {
         }
         if (k0 < k1) {   // (else the range ends before the unit's first key)
             const int all = PART == kSharedKeys ? shared_keys(a, b) - 1 : 0;   // position that the shared keys end at
-            const KeyTiles kt =
-                key_tiles<PART>(a, PART == kSharedKeys ? all : s.sr.pos0 + uniform(u.f0 / a.G),
-                                PART == kSharedKeys ? all : s.sr.pos0 + uniform((u.f1 - 1) / a.G), PART == kOwnKeys ? own_from(a, b) : 0);
+            const int own = PART == kOwnKeys ? own_from(a, b) : 0;
+            const KeyTiles kt = key_tiles<PART>(a, PART == kSharedKeys ? all : s.sr.pos0 + uniform(u.f0 / a.G),
+                                                PART == kSharedKeys ? all : s.sr.pos0 + uniform((u.f1 - 1) / a.G), own);
             dense_unit<D, NW, PART>(a, s.sr, b, u, kt, (int)((k0 + kKeys - 1) / kKeys),
-                              min((int)((k1 + kKeys - 1) / kKeys), kt.tiles), part);
+                              min((int)((k1 + kKeys - 1) / kKeys), kt.tiles), own, part);
         }
         __syncthreads();
         if (uniform(place.at) >= end) return;
