@@ -243,7 +243,7 @@ PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int wind
     const int64_t s0 = steps((S + seqs - 1) / seqs, 1, kKeys), s1 = steps(S, 1, kKeys);
     p.rows = cut(row_units, row_about, Hkv, s0, s1, 640, 8);   // three a CU, less what the rounding up of parts adds
     p.grad = cut(row_units, row_about, Hkv, s0, s1, 512, 8);
-    p.keys = cut(key_units, key_about, Hkv, steps((T + seqs - 1) / seqs, G, kPairs), steps(T, G, kPairs), 1024, 16);
+    p.keys = cut(key_units, key_about, Hkv, steps((T + seqs - 1) / seqs, G, kPairs), steps(T, G, kPairs), 768, 16);
     auto parts = [&](const PromptCut& c, int64_t floats) { return c.splits > 1 ? (size_t)(c.blocks * rows * floats) * 4 : 0; };
     p.fwd_bytes = std::max<size_t>(256, parts(p.rows, D + 2));
     p.stat_bytes = ((size_t)T * Hq * 4 + 255) / 256 * 256;
