@@ -1,4 +1,6 @@
 // prompt.hip -- causal attention over packed 16-bit prompts on gfx950.
+#include <math.h>
+
 #include <algorithm>
 
 #include "prompt.hpp"
@@ -189,8 +191,9 @@ __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
     const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(RT * (D + 2));
     float m = kNoRef, l = 0.0f;
     at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i = 0; i < used; ++i, part += RT * (D + 2)) m = fmaxf(m, part[(size_t)RT * D + 2 * r]);
-    part -= (int64_t)used * (RT * (D + 2));
+#pragma unroll 8
+    for (int i = 0; i < used; ++i) m = fmaxf(m, part[(int64_t)i * (RT * (D + 2)) + (size_t)RT * D + 2 * r]);
+#pragma unroll 8
     for (int i = 0; i < used; ++i, part += RT * (D + 2)) {
         const float f = __builtin_amdgcn_exp2f(part[(size_t)RT * D + 2 * r] - m);
         l = __builtin_fmaf(f, part[(size_t)RT * D + 2 * r + 1], l);
@@ -214,36 +217,49 @@ hipError_t launch(const PromptPlan& p, const PromptArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Units are cut while there are too few of them for the card to run evenly:
-// `places` workgroups run at once, and the units of one sequence differ in length
-// by up to the whole of it, so that with two to a place the short ones fill up
-// what the long ones leave.  `units` are about those with rows, `steps` those of
-// a sequence of average length, `most` of one that is all of the batch; a part
-// has `least` steps or more (the joining launch costs as much as four or so).
-static PromptCut cut(int64_t all, int64_t units, int Hkv, int64_t steps, int64_t most, int64_t places, int64_t least) {
+// Units are cut while there are too few of them for the card to run evenly: the
+// units of one sequence differ in length by up to the whole of it, so that with
+// more than one for each of the `places` workgroups that run at once the short
+// ones fill up what the long ones leave.  Below that, a part is about what a
+// place has to do.  `units` are about those with rows, `mean` the steps of one in
+// a sequence of average length, `most` those in a sequence that is all of the
+// batch.  The parts pass through memory and the joining launch costs some steps'
+// time: parts have `least` steps or more, and cutting has to take that many off
+// the longest unit (about the geometric mean of twice the mean and the most).
+static PromptCut cut(int64_t all, double units, double mean, int64_t most, int Hkv, int64_t places, int64_t least) {
     PromptCut c{all, all * Hkv, 1, 1 << 30};
-    if (units * Hkv >= 2 * places || steps * most < least * least) return c;   // (the geometric mean of both)
-    const int64_t per = std::max(least, (units * Hkv * steps + places - 1) / places);
-    c.splits = (int)std::min((most + per - 1) / per, 2 * places / c.blocks + 1);
+    const int64_t per = std::max(least, (int64_t)(1.1 * units * Hkv * mean / places) + 1);
+    if (units * Hkv >= 1.25 * places || sqrt(2.0 * mean * most) < per + least) return c;
+    c.splits = (int)std::min((most + per - 1) / per, 3 * places / c.blocks + 1);
     c.per = (int)per;
     c.blocks *= c.splits;
     return c;
+}
+
+// Mean of min(x, cap) over lo <= x <= hi.
+static double mean_capped(double lo, double hi, double cap) {
+    if (cap >= hi) return 0.5 * (lo + hi);
+    if (cap <= lo) return cap;
+    return (0.5 * (cap * cap - lo * lo) + cap * (hi - cap)) / (hi - lo);
 }
 
 PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int window) {
     PromptPlan p{};
     const int64_t G = Hq / Hkv, seqs = std::max(n_seq, 1);
     constexpr int rows = 32 * kWaves;
-    auto steps = [&](int64_t n, int64_t mul, int per) {   // over n tokens that count mul, as far as a window reaches
-        return ((window > 0 ? std::min<int64_t>(n, (int64_t)window + 2 * rows) : n) * mul + per - 1) / per;
-    };
+    const double n = (double)T / seqs, m = (double)S / seqs, reach = window > 0 ? (double)window + rows : (double)S + rows;
     // (about: a sequence's last unit is half full)
-    const int64_t row_units = pr_units(T, G, rows, n_seq), row_about = (int64_t)T * G / rows + (seqs + 1) / 2;
-    const int64_t key_units = pr_units(S, 1, rows, n_seq), key_about = (int64_t)S / rows + (seqs + 1) / 2;
-    const int64_t s0 = steps((S + seqs - 1) / seqs, 1, kKeys), s1 = steps(S, 1, kKeys);
-    p.rows = cut(row_units, row_about, Hkv, s0, s1, 640, 8);   // three a CU, less what the rounding up of parts adds
-    p.grad = cut(row_units, row_about, Hkv, s0, s1, 512, 8);
-    p.keys = cut(key_units, key_about, Hkv, steps((T + seqs - 1) / seqs, G, kPairs), steps(T, G, kPairs), 768, 16);
+    const int64_t row_units = pr_units(T, G, rows, n_seq), key_units = pr_units(S, 1, rows, n_seq);
+    const double row_about = (double)T * G / rows + 0.5 * seqs, key_about = (double)S / rows + 0.5 * seqs;
+    const double uneven = n_seq > 1 ? 1.2 : 1.0;   // (of unequal sequences the long ones have most of the steps)
+    const double row_mean = uneven * mean_capped(std::max(m - n, 0.0), m, reach) / kKeys + 0.5;
+    const double key_mean = uneven * mean_capped(0.0, m, std::min(n, reach)) * G / kPairs + 0.5;
+    const int64_t row_most = (int64_t)std::min((double)S, reach) / kKeys + 1, key_most = (int64_t)(std::min((double)T, reach) * G / kPairs) + 1;
+    // workgroups that a CU holds, by registers and LDS: three of the forward pass,
+    // two of the others at D = 128; at D = 64 four, three and two
+    p.rows = cut(row_units, row_about, row_mean, row_most, Hkv, D == 64 ? 1024 : 768, 8);
+    p.grad = cut(row_units, row_about, row_mean, row_most, Hkv, D == 64 ? 768 : 512, 8);
+    p.keys = cut(key_units, key_about, key_mean, key_most, Hkv, 512, 16);
     auto parts = [&](const PromptCut& c, int64_t floats) { return c.splits > 1 ? (size_t)(c.blocks * rows * floats) * 4 : 0; };
     p.fwd_bytes = std::max<size_t>(256, parts(p.rows, D + 2));
     p.stat_bytes = ((size_t)T * Hq * 4 + 255) / 256 * 256;

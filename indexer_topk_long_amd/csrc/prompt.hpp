@@ -66,13 +66,17 @@ struct PromptArgs {
     float* part;
 };
 
-// A unit's parts: `used` of them, of `size` steps each (the last one what is left).
+// A unit's parts: `used` of them, of `size` steps each, the last one what is left.
+// (Whole ones first and the rests after them make an even load; equal parts of
+// every unit: 256 units over 512 places 1.5 times the even time, these 1.3.)
 struct PrParts {
     int size, used;
 };
 __device__ __forceinline__ PrParts pr_parts(const PromptArgs& a, int steps) {
     if (a.splits <= 1 || steps <= a.per) return PrParts{max(steps, 1), 1};
-    const int n = min(a.splits, (int)((uint32_t)(steps + a.per - 1) / (uint32_t)a.per)), size = (int)((uint32_t)(steps + n - 1) / (uint32_t)n);
+    const int n = (int)((uint32_t)(steps + a.per - 1) / (uint32_t)a.per);
+    if (n <= a.splits) return PrParts{a.per, n};
+    const int size = (int)((uint32_t)(steps + a.splits - 1) / (uint32_t)a.splits);
     return PrParts{size, (int)((uint32_t)(steps + size - 1) / (uint32_t)size)};
 }
 // The unit, part and head of a workgroup.  Heads go round the XCDs, so that a

@@ -197,6 +197,7 @@ __global__ __launch_bounds__(2 * D) void prompt_dq_join_kernel(PromptArgs a) {
     if (r >= u.count) return;
     const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(RT * D) + (size_t)r * D + d;
     at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
     for (int i = 0; i < used; ++i) o += *reinterpret_cast<const at_f32x4*>(part + (int64_t)i * (RT * D));
     const PrPair p = pr_pair(a, u.first, r);
     const int64_t row = (int64_t)(u.s.r0 + p.i) * a.Hq + h * a.G + p.g;
@@ -456,6 +457,7 @@ __global__ __launch_bounds__(2 * D) void prompt_dkv_join_kernel(PromptArgs a) {
     if (ka + r >= kb) return;
     const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(2 * kUnit * D) + (size_t)r * D + d;
     at_f32x4 x{0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+#pragma unroll 4
     for (int i = 0; i < used; ++i, part += 2 * kUnit * D) {
         x += *reinterpret_cast<const at_f32x4*>(part);
         y += *reinterpret_cast<const at_f32x4*>(part + (size_t)kUnit * D);
