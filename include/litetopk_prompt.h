@@ -26,8 +26,9 @@ extern "C" {
 typedef enum { LTK_ROWS_BF16 = 0, LTK_ROWS_FP16 = 1, LTK_ROWS_FP32 = 2 } ltk_row_type;
 
 /* A tensor [rows, heads, head_dim] of 16-bit values: element (t, h, d) lies at
- * t * row_stride + h * head_stride + d.  Strides are multiples of 8 elements, 0 ..
- * 2^23 (a broadcast input has 0), and the address of 16 bytes. */
+ * t * row_stride + h * head_stride + d.  Strides are multiples of 8 elements
+ * (a broadcast input has 0), row strides up to 2^23 and head strides up to 2^27;
+ * the address is one of 16 bytes. */
 typedef struct {
     void* data;
     int64_t row_stride, head_stride;
@@ -49,6 +50,8 @@ typedef struct {
  *              h / (n_q_heads / n_kv_heads); fewer than 2^15 to one
  *   head_dim   64 or 128 (LTK_EUNSUPPORTED otherwise)
  *   T, S       rows of q, keys of k: T * n_q_heads and S * n_kv_heads <= 2^31 - 256
+ *              (calls that would launch 2^32 threads are refused: 2 for every row and
+ *              query head or key, and 256 for every sequence and key/value head)
  *   scale      finite, also times log2(e)
  *   window     >= 0 (0: none) */
 typedef struct {
@@ -65,24 +68,27 @@ typedef struct {
 size_t litetopk_attend_prompt_workspace_bytes(const ltk_prompt* p, int32_t backward);
 
 /* out [T, n_q_heads, head_dim] and lse [T, n_q_heads] fp32 (the natural logarithm
- * of the sum of exp(scale q.k); may be NULL) are contiguous.
+ * of the sum of exp(scale q.k); may be NULL) are contiguous.  rest, like out, or
+ * NULL: what the rounding of out left out, rounded itself; the backward pass
+ * takes out + rest, so that the rounding of out is not in its gradients.
  *
  * Scores, statistics and sums are fp32; a weight is rounded once to the type of
  * q for its product with the value. */
 int litetopk_attend_prompt(const ltk_prompt* p, const ltk_rows* q, const ltk_rows* k, const ltk_rows* v, void* out,
-                           float* lse, void* ws, size_t ws_bytes, void* stream);
+                           void* rest, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* dq [T, n_q_heads, head_dim], dk and dv [S, n_kv_heads, head_dim], contiguous,
- * from dout and what the forward call returned (out contiguous, lse).
+ * from dout and what the forward call returned (rest may be NULL).  dq, or dk and
+ * dv, may be NULL where they are not wanted.
  *
- * With P = exp(scale q.k - lse) and delta = dout . out:
+ * With P = exp(scale q.k - lse) and delta = dout . (out + rest):
  *   dv = P^T dout,  dS = P (dout v^T - delta),  dq = scale dS k,  dk = scale dS^T q.
  * P and dS are rounded once to the type of q for these products (in fp16, values
  * of dS below 2^-24 vanish and those past 65504 are infinite: scale the loss);
  * sums are fp32, in a fixed order. */
 int litetopk_attend_prompt_backward(const ltk_prompt* p, const ltk_rows* q, const ltk_rows* k, const ltk_rows* v,
-                                    const void* out, const float* lse, const ltk_rows* dout, void* dq, void* dk,
-                                    void* dv, void* ws, size_t ws_bytes, void* stream);
+                                    const void* out, const void* rest, const float* lse, const ltk_rows* dout,
+                                    void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, void* stream);
 
 /* Causal attention over the cache (no window) for sequences that share their
  * first tokens, as answers to one prompt do: the result of litetopk_attend, but

@@ -150,14 +150,12 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
     if (row < 0) return;
     if (parts.used <= 1) {
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        uint16_t* dst = a.out + row * D;
 #pragma unroll
         for (int t = 0; t < D / 32; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<at_u32x2*>(dst + 32 * t + 8 * i + 4 * g) =
-                    at_u32x2{E::pack(o[t][4 * i] * inv, o[t][4 * i + 1] * inv),
-                             E::pack(o[t][4 * i + 2] * inv, o[t][4 * i + 3] * inv)};
+                pr_store_out<E>(a, row * D + 32 * t + 8 * i + 4 * g,
+                                at_f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]}, inv);
         if (a.lse && g == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -INFINITY;
         return;
     }
@@ -202,8 +200,7 @@ __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
     const PrPair p = pr_pair(a, u.first, r);
     const int64_t row = (int64_t)(u.s.r0 + p.i) * a.Hq + h * a.G + p.g;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    *reinterpret_cast<at_u32x2*>(a.out + row * D + d) =
-        at_u32x2{E::pack(o[0] * inv, o[1] * inv), E::pack(o[2] * inv, o[3] * inv)};
+    pr_store_out<E>(a, row * D + d, o, inv);
     if (a.lse && d == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -264,7 +261,8 @@ PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int wind
     p.fwd_bytes = std::max<size_t>(256, parts(p.rows, D + 2));
     p.stat_bytes = ((size_t)T * Hq * 4 + 255) / 256 * 256;
     p.bwd_bytes = std::max<size_t>(256, 2 * p.stat_bytes + std::max(parts(p.grad, D), parts(p.keys, 2 * D)));
-    p.fits = grid_fits(std::max({p.rows.blocks, p.grad.blocks, p.keys.blocks}), 64 * kWaves) && grid_fits((int64_t)T * Hq / 2 + 1, 16);
+    // (the last: delta's launch)
+    p.fits = grid_fits(std::max({p.rows.blocks, p.grad.blocks, p.keys.blocks, ((int64_t)T * Hq + rows - 1) / rows}), 64 * kWaves);
     return p;
 }
 

@@ -52,8 +52,8 @@ struct PrRows {
 
 struct PromptArgs {
     PrRows q, k, v, dout;
-    const uint16_t* out_in;   // backward: the forward call's out
-    uint16_t *out, *dq, *dk, *dv;
+    const uint16_t *out_in, *rest_in;   // backward: the forward call's out and rest
+    uint16_t *out, *rest, *dq, *dk, *dv;
     float* lse;
     float *lse2, *delta;      // backward: [T, Hq], log2(e) lse and dout . out
     const int32_t *cu, *cu_k;
@@ -231,6 +231,17 @@ __device__ __forceinline__ at_u32x4 pr_read_across(uint8_t* lds, int across, int
     const pr_i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(lds + (at ^ 32) + (16 * w + 8) * (2 * D)));
     const pr_i16x8 z{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     return __builtin_bit_cast(at_u32x4, z);
+}
+// Four dimensions of a row's result, and where asked for what their rounding left
+// out, rounded itself.
+template <class E>
+__device__ __forceinline__ void pr_store_out(const PromptArgs& a, int64_t at, const at_f32x4& o, float inv) {
+    const float x0 = o[0] * inv, x1 = o[1] * inv, x2 = o[2] * inv, x3 = o[3] * inv;
+    const uint32_t lo = E::pack(x0, x1), hi = E::pack(x2, x3);
+    *reinterpret_cast<at_u32x2*>(a.out + at) = at_u32x2{lo, hi};
+    if (a.rest)
+        *reinterpret_cast<at_u32x2*>(a.rest + at) =
+            at_u32x2{E::pack(x0 - E::lo(lo), x1 - E::hi(lo)), E::pack(x2 - E::lo(hi), x3 - E::hi(hi))};
 }
 // Waits for the direct copies into LDS that the wave has issued.
 __device__ __forceinline__ void pr_wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }

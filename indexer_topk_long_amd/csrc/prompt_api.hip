@@ -9,8 +9,8 @@ using namespace ltk;
 namespace {
 
 constexpr int64_t kMaxRows = 0x7fffffff - 255;
-// A tile's 64 rows lie within 32 bits of bytes.
-constexpr int64_t kMaxRowStride = 1 << 23, kMaxHeadStride = (int64_t)1 << 40;
+// A tile's 64 rows, and the eight heads of a copy, lie within 32 bits of bytes.
+constexpr int64_t kMaxRowStride = 1 << 23, kMaxHeadStride = 1 << 27;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -72,23 +72,24 @@ size_t litetopk_attend_prompt_workspace_bytes(const ltk_prompt* p, int32_t backw
 }
 
 int litetopk_attend_prompt(const ltk_prompt* p, const ltk_rows* q, const ltk_rows* k, const ltk_rows* v, void* out,
-                           float* lse, void* ws, size_t ws_bytes, void* stream) {
+                           void* rest, float* lse, void* ws, size_t ws_bytes, void* stream) {
     PromptArgs a{};
     PromptPlan plan;
     int st = args(p, q, k, v, a, plan);
     if (st != LTK_OK) return st;
-    if ((p->T > 0 && (!out || !ws)) || !aligned16(out) || !aligned16(ws) || ((uintptr_t)lse & 3u)) return LTK_EINVAL;
+    if ((p->T > 0 && (!out || !ws)) || !aligned16(out) || !aligned16(rest) || !aligned16(ws) || ((uintptr_t)lse & 3u)) return LTK_EINVAL;
     if (ws_bytes < plan.fwd_bytes) return LTK_EWORKSPACE;
     if (p->T == 0) return LTK_OK;
     if ((st = litetopk_device_check()) != LTK_OK) return st;
     a.out = static_cast<uint16_t*>(out);
+    a.rest = static_cast<uint16_t*>(rest);
     a.lse = lse;
     return launch_prompt(plan, p->type, p->head_dim, a, ws, static_cast<hipStream_t>(stream)) == hipSuccess ? LTK_OK : LTK_EHIP;
 }
 
 int litetopk_attend_prompt_backward(const ltk_prompt* p, const ltk_rows* q, const ltk_rows* k, const ltk_rows* v,
-                                    const void* out, const float* lse, const ltk_rows* dout, void* dq, void* dk,
-                                    void* dv, void* ws, size_t ws_bytes, void* stream) {
+                                    const void* out, const void* rest, const float* lse, const ltk_rows* dout,
+                                    void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, void* stream) {
     PromptArgs a{};
     PromptPlan plan;
     int st = args(p, q, k, v, a, plan);
@@ -96,13 +97,14 @@ int litetopk_attend_prompt_backward(const ltk_prompt* p, const ltk_rows* q, cons
     if ((st = rows(dout, p->T > 0, a.dout)) != LTK_OK) return st;
     if (p->T > 0 && (!out || !lse)) return LTK_EINVAL;
     if ((dk == nullptr) != (dv == nullptr)) return LTK_EINVAL;
-    if (!aligned16(out) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(ws) || ((uintptr_t)lse & 3u))
+    if (!aligned16(out) || !aligned16(rest) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(ws) || ((uintptr_t)lse & 3u))
         return LTK_EINVAL;
     if ((p->T > 0 || p->S > 0) && !ws) return LTK_EINVAL;
     if (ws_bytes < plan.bwd_bytes) return LTK_EWORKSPACE;
     if ((p->T == 0 || !dq) && (p->S == 0 || !dk)) return LTK_OK;
     if ((st = litetopk_device_check()) != LTK_OK) return st;
     a.out_in = static_cast<const uint16_t*>(out);
+    a.rest_in = static_cast<const uint16_t*>(rest);
     a.lse = const_cast<float*>(lse);
     a.dq = static_cast<uint16_t*>(dq);
     a.dk = static_cast<uint16_t*>(dk);

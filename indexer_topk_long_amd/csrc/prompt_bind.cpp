@@ -41,7 +41,7 @@ const at::Tensor& rows_tensor(PyObject* o, const char* name, const at::Tensor* l
 
 // Rows as the library takes them; other strides are laid out anew, in `held`.
 ltk_rows rows_of(const at::Tensor& t, at::Tensor& held) {
-    constexpr int64_t kRow = 1 << 23, kHead = (int64_t)1 << 40;
+    constexpr int64_t kRow = 1 << 23, kHead = 1 << 27;
     held = t;
     const int64_t r = t.size(0) > 1 ? t.stride(0) : 0, h = t.size(1) > 1 ? t.stride(1) : 0;
     const bool fits = (t.size(2) <= 1 || t.stride(2) == 1) && r % 8 == 0 && h % 8 == 0 && r <= kRow && h <= kHead &&
@@ -83,17 +83,18 @@ struct Status {
 };
 
 void forward_call(const at::Tensor& q, const at::Tensor& k, const at::Tensor& v, const at::Tensor& cu, const at::Tensor& cu_k,
-                  double scale, int64_t window, bool with_lse, at::Tensor& out, at::Tensor& lse) {
+                  double scale, int64_t window, bool with_lse, at::Tensor& out, at::Tensor& lse, at::Tensor* rest = nullptr) {
     const Shape s = shape_of(q, k, cu, cu_k, scale, window);
     const On on(s.dev);
     at::Tensor held[3];
     const ltk_rows qr = rows_of(q, held[0]), kr = rows_of(k, held[1]), vr = rows_of(v, held[2]);
     out = at::empty({s.p.T, s.p.n_q_heads, s.p.head_dim}, q.options().memory_format(c10::nullopt));
+    if (rest) *rest = at::empty_like(out);
     if (with_lse) lse = at::empty({s.p.T, s.p.n_q_heads}, q.options().dtype(at::kFloat));
     const size_t need = litetopk_attend_prompt_workspace_bytes(&s.p, 0);
     // (sizes the library does not take: it says so itself, before it looks at the workspace)
     const at::Tensor ws = at::empty({(int64_t)(need ? need : 256)}, on_device(s.dev, at::kByte));
-    const int rc = litetopk_attend_prompt(&s.p, &qr, &kr, &vr, out.data_ptr(), with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
+    const int rc = litetopk_attend_prompt(&s.p, &qr, &kr, &vr, out.data_ptr(), rest ? rest->data_ptr() : nullptr, with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
                                           ws.data_ptr(), need ? need : 256, on.stream);
     if (rc != LTK_OK) throw Status{rc, "litetopk_attend_prompt"};
 }
@@ -102,9 +103,9 @@ struct PromptFn : public torch::autograd::Function<PromptFn> {
     static variable_list forward(AutogradContext* ctx, const at::Tensor& q, const at::Tensor& k, const at::Tensor& v,
                                  const at::Tensor& cu, const std::optional<at::Tensor>& cu_k_, double scale, int64_t window) {
         const at::Tensor cu_k = cu_k_.value_or(at::Tensor());
-        at::Tensor out, lse;
-        forward_call(q, k, v, cu, cu_k, scale, window, true, out, lse);
-        ctx->save_for_backward({q, k, v, cu, cu_k, out, lse});
+        at::Tensor out, lse, rest;
+        forward_call(q, k, v, cu, cu_k, scale, window, true, out, lse, &rest);
+        ctx->save_for_backward({q, k, v, cu, cu_k, out, lse, rest});
         ctx->saved_data["scale"] = scale;
         ctx->saved_data["window"] = window;
         ctx->set_materialize_grads(false);
@@ -116,7 +117,7 @@ struct PromptFn : public torch::autograd::Function<PromptFn> {
         variable_list none(7);
         if (!grads[0].defined()) return none;
         const auto saved = ctx->get_saved_variables();
-        const at::Tensor &q = saved[0], &k = saved[1], &v = saved[2], &out = saved[5], &lse = saved[6];
+        const at::Tensor &q = saved[0], &k = saved[1], &v = saved[2], &out = saved[5], &lse = saved[6], &rest = saved[7];
         const Shape s = shape_of(q, k, saved[3], saved[4], ctx->saved_data["scale"].toDouble(), ctx->saved_data["window"].toInt());
         const On on(s.dev);
         at::Tensor held[4], dq, dk, dv;
@@ -127,7 +128,7 @@ struct PromptFn : public torch::autograd::Function<PromptFn> {
         const size_t need = litetopk_attend_prompt_workspace_bytes(&s.p, 1);
         const at::Tensor ws = at::empty({(int64_t)need}, on_device(s.dev, at::kByte));
         auto at_or_null = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-        const int rc = litetopk_attend_prompt_backward(&s.p, &qr, &kr, &vr, out.data_ptr(), static_cast<const float*>(lse.data_ptr()),
+        const int rc = litetopk_attend_prompt_backward(&s.p, &qr, &kr, &vr, out.data_ptr(), rest.data_ptr(), static_cast<const float*>(lse.data_ptr()),
                                                        &dr, at_or_null(dq), at_or_null(dk), at_or_null(dv), ws.data_ptr(), need,
                                                        on.stream);
         TORCH_CHECK(rc == LTK_OK, "litetopk_attend_prompt_backward: status ", rc);

@@ -42,25 +42,42 @@ __device__ __forceinline__ void copy_tile(const PrRows& x, int64_t row0, int h, 
 // log2(e) lse, infinite for a row that sees no key (its weights are 0 then).
 __device__ __forceinline__ float base2(float lse) { return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f; }
 
-// lse2 and delta = dout . out of every row and head, where no dq is asked for (its
-// launch forms them too).
+// A lane's share of delta = dout . (out + rest): dimensions 16 j + 8 g ..; the
+// lanes c and c + 32 of a wave share a row.
 template <class E, int D>
-__global__ __launch_bounds__(256) void prompt_delta_kernel(PromptArgs a) {
-    constexpr int L = D / 8;
-    const int64_t r = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-    if (r >= (int64_t)a.T * a.Hq) return;
-    const int t = (int)(r / a.Hq), h = (int)(r % a.Hq), d = 8 * (threadIdx.x % L);
-    const at_u32x4 x = *reinterpret_cast<const at_u32x4*>(a.out_in + r * D + d);
-    const at_u32x4 y = *reinterpret_cast<const at_u32x4*>(a.dout.p + t * a.dout.row + h * a.dout.head + d);
+__device__ __forceinline__ float delta_share(const PromptArgs& a, int64_t row, int g, const at_u32x4 (&dout)[D / 16]) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        s = __builtin_fmaf(E::lo(x[i]), E::lo(y[i]), s);
-        s = __builtin_fmaf(E::hi(x[i]), E::hi(y[i]), s);
-    }
+    for (int j = 0; j < D / 16; ++j) {
+        const at_u32x4 y = *reinterpret_cast<const at_u32x4*>(a.out_in + row * D + 16 * j + 8 * g);
+        at_u32x4 z{0u, 0u, 0u, 0u};
+        if (a.rest_in) z = *reinterpret_cast<const at_u32x4*>(a.rest_in + row * D + 16 * j + 8 * g);
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    if (d == 0) a.delta[r] = s, a.lse2[r] = base2(a.lse[r]);
+        for (int i = 0; i < 4; ++i) {
+            s = __builtin_fmaf(E::lo(dout[j][i]), E::lo(y[i]) + E::lo(z[i]), s);
+            s = __builtin_fmaf(E::hi(dout[j][i]), E::hi(y[i]) + E::hi(z[i]), s);
+        }
+    }
+    return s;
+}
+
+// lse2 and delta of every row and head, where no dq is asked for (its launch forms
+// them too, in the same order).
+template <class E, int D>
+__global__ __launch_bounds__(64 * kWaves) void prompt_delta_kernel(PromptArgs a) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, g = lane >> 5;
+    const int64_t r = (int64_t)blockIdx.x * kUnit + 32 * wave + c;
+    float s = 0.0f;
+    if (r < (int64_t)a.T * a.Hq) {
+        const int t = (int)(r / a.Hq), h = (int)(r % a.Hq);
+        at_u32x4 dout[D / 16];
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+            dout[j] = *reinterpret_cast<const at_u32x4*>(a.dout.p + t * a.dout.row + h * a.dout.head + 16 * j + 8 * g);
+        s = delta_share<E, D>(a, r, g, dout);
+    }
+    s = pr_sum_halves(s);
+    if (r < (int64_t)a.T * a.Hq && g == 0) a.delta[r] = s, a.lse2[r] = base2(a.lse[r]);
 }
 
 // dq: units are row tiles as in the forward pass.
@@ -96,15 +113,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
             q[j] = *reinterpret_cast<const at_u32x4*>(a.q.p + t * a.q.row + x * a.q.head + 16 * j + 8 * g);
             dout[j] = *reinterpret_cast<const at_u32x4*>(a.dout.p + t * a.dout.row + x * a.dout.head + 16 * j + 8 * g);
         }
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            const at_u32x4 y = *reinterpret_cast<const at_u32x4*>(a.out_in + row * D + 16 * j + 8 * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                delta = __builtin_fmaf(E::lo(dout[j][i]), E::lo(y[i]), delta);
-                delta = __builtin_fmaf(E::hi(dout[j][i]), E::hi(y[i]), delta);
-            }
-        }
+        delta = delta_share<E, D>(a, row, g, dout);
         lse2 = base2(a.lse[row]);
     }
     delta = pr_sum_halves(delta);
@@ -486,8 +495,7 @@ hipError_t allow_lds(F* kernel, int bytes, std::atomic<uint64_t>& allowed) {
 template <class E, int D>
 hipError_t launch(const PromptPlan& p, PromptArgs& a, hipStream_t st) {
     const int64_t rows = (int64_t)a.T * a.Hq;
-    constexpr int per = 256 / (D / 8);
-    if (!a.dq && rows > 0) prompt_delta_kernel<E, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
+    if (!a.dq && rows > 0) prompt_delta_kernel<E, D><<<(unsigned)((rows + kUnit - 1) / kUnit), 64 * kWaves, 0, st>>>(a);
     if (a.dq && rows > 0) {
         a.splits = p.grad.splits, a.per = p.grad.per, a.units = p.grad.units;
         prompt_dq_kernel<E, D><<<(unsigned)p.grad.blocks, 64 * kWaves, 2 * kStage<D>, st>>>(a);

@@ -10,8 +10,9 @@ x_s, weights P_s, n keys, and E the error of a score in fp32,
   out   u |out| + (u + 2 E + n 2^-23) sum_s P_s |v_s| [+ 2^-25 n max|v|]
   lse   E + n 2^-24 + 2^-22 |lse|
 The backward pass forms P again (error 2 E relative), and from what the forward
-pass returned delta = dout . out, off by
-  d = sum_d |dout_d| (tol(out)_d + D 2^-24 |out_d|),
+pass returned delta = dout . (out + rest), where rest holds what rounding left
+out of out, to u of itself, off by
+  d = sum_d |dout_d| (tol(out)_d - (u - u^2) |out_d| + D 2^-24 |out_d|),
 and dP = dout . v, off by D 2^-24 sum_d |dout_d v_d| =: p:
   dS    e_s = |dS_s| (u + 2 E + 2^-22) + P_s (d + p) [+ 2^-25]
   dq    u |dq| + scale sum_s (e_s + n 2^-23 |dS_s|) |k_s|
@@ -84,7 +85,7 @@ def ref(q, k, v, cu, cu_k, scale, window=0, dout=None):
             do = dout[r0:r1, h].double()
             dP = do @ vh.T
             dS = P * (dP - (do * o).sum(-1, keepdim=True))
-            d = (do.abs() * (ot + D * 2.0 ** -24 * o.abs())).sum(-1, keepdim=True)
+            d = (do.abs() * (ot + (u * u - u + D * 2.0 ** -24) * o.abs())).sum(-1, keepdim=True)
             p = D * 2.0 ** -24 * (do.abs() @ vh.abs().T)
             e = dS.abs() * (u + 2 * E + 2.0 ** -22) + P * (d + p) + tiny * see
             N = G * max(1, r1 - r0)
