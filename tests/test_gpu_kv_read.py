@@ -139,3 +139,27 @@ def test_refusals(lib, what):
         err = RuntimeError
     with pytest.raises(err):
         lib.kv_read(c, table.cuda(), cu.cuda(), n.cuda(), **a)
+
+
+def test_offsets_past_32_bits(lib):
+    """Rows of outputs of more than 2^31 elements, from a cache of more than 2^31 bytes."""
+    import torch
+    Hkv, page, D, n = 128, 128, 128, 1100
+    T = n * page
+    ids = torch.randperm(n, generator=_gen(3)).int().cuda()
+    byte = torch.zeros(n, Hkv, page, D, dtype=torch.uint8, device="cuda")
+    mark = (torch.arange(n * page, device="cuda") % 100 + 1).to(torch.uint8)
+    byte.view(n, Hkv, page, D)[:, :, :, 0] = mark.view(n, 1, page)
+    byte[:, :, :, D - 1] = torch.arange(Hkv, device="cuda").to(torch.uint8)[None, :, None]
+    scale = torch.ones(n, Hkv, device="cuda")
+    data = byte.view(torch.float8_e4m3fn)
+    cu, kv_len = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, T], [T]))
+    k, v = lib.kv_read((data, data, scale, scale), ids[None], cu, kv_len, T)
+    assert k.numel() > 1 << 31
+    value = torch.arange(256, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).to(torch.bfloat16)
+    want0 = value[mark.view(n, page)[ids.long()].reshape(-1).long()]
+    for x in (k, v):
+        assert torch.equal(x[:, 0, 0], want0) and torch.equal(x[:, Hkv - 1, 0], want0)
+        # (byte 127 is NaN, whose sign is no matter)
+        assert torch.equal(x[T - 1, :, D - 1].nan_to_num(nan=-1.0), value[:Hkv].nan_to_num(nan=-1.0))
+        assert not bool(x[:, :, 1:D - 1].any())

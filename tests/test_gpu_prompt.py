@@ -346,3 +346,62 @@ def test_streams(lib):
         got = (out.detach(),) + torch.autograd.grad(out, mine, dout)
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [2, 5, 8, 12, 16, 24, 40])
+def test_groups(lib, G, D):
+    """Heads that fill copies of rows evenly and such that do not."""
+    _case(lib, [90, 33], [90, 50], 2 * G, 2, D, "bfloat16", 100 + G)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (6, 2)])
+def test_long_sequences_cut_in_both_passes(lib, Hq, Hkv):
+    """Lengths at which units are cut in parts by rule, whole parts and rests, beside short sequences."""
+    _case(lib, [1700, 65, 400], None, Hq, Hkv, 64, "bfloat16", 111)
+    _case(lib, [300, 20], [2300, 1000], Hq, Hkv, 128, "bfloat16", 112)
+
+
+def test_offsets_past_32_bits(lib):
+    """The last sequence of tensors of more than 2^31 elements gets what it gets alone."""
+    import torch
+    T0, n, H, D, w = (1 << 17) - 100, 300, 128, 128, 64
+    T = T0 + n
+    small = [x.cuda() for x in make(120, [n], [n], H, 4, D, torch.bfloat16)]
+    q, dout = (torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.zeros(T, 4, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert q.numel() > 1 << 31
+    for x, y in zip((q, k, v, dout), small):
+        x[T0:] = y
+    leaves = [x.requires_grad_() for x in (q, k, v)]
+    cu = torch.tensor([0, T0, T], dtype=torch.int32, device="cuda")
+    out = lib.attend_prompt(*leaves, cu, window=w)
+    got = (out.detach(),) + torch.autograd.grad(out, leaves, dout)
+    mine = [x.clone().requires_grad_() for x in small[:3]]
+    out = lib.attend_prompt(*mine, cu[:2].clone().fill_(0).index_fill_(0, torch.tensor([1], device="cuda"), n), window=w)
+    want = (out.detach(),) + torch.autograd.grad(out, mine, small[3])
+    # (units of the two calls may be cut differently: sums in another order, then one rounding)
+    for a, b in zip(got, want):
+        assert torch.allclose(a[T0:].float(), b.float(), rtol=2.0 ** -6, atol=2.0 ** -6)
+        assert bool((a[:T0] == 0).all())
+
+
+def test_on_another_device_context(lib):
+    """The call runs on its tensors' device and stream whatever thread makes it."""
+    import threading
+    import torch
+    q, k, v, dout = [x.cuda() for x in make(130, [60], [60], 4, 2, 64, torch.bfloat16)]
+    cu = lens_to_cu([60]).cuda()
+    leaves = [x.requires_grad_() for x in (q, k, v)]
+    out = lib.attend_prompt(*leaves, cu)
+    want = (out.detach(),) + torch.autograd.grad(out, leaves, dout)
+    res = {}
+
+    def work(i):
+        for _ in range(10):
+            o = lib.attend_prompt(*leaves, cu)
+            res[i] = (o.detach(),) + torch.autograd.grad(o, leaves, dout)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    [t.start() for t in threads], [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert len(res) == 3 and all(torch.equal(a, b) for r in res.values() for a, b in zip(r, want))
