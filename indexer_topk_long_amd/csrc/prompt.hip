@@ -150,12 +150,16 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
     if (row < 0) return;
     if (parts.used <= 1) {
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        pr_store_row<E, D>(a.out + row * D, g, o, inv);
+        if (a.rest) {
 #pragma unroll
-        for (int t = 0; t < D / 32; ++t)
+            for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                pr_store_out<E>(a, row * D + 32 * t + 8 * i + 4 * g,
-                                at_f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]}, inv);
+                for (int i = 0; i < 16; i += 8)
+                    pr_store16(a.rest + row * D + 32 * t + 2 * i, g, pr_rest<E>(o[t][i] * inv, o[t][i + 1] * inv),
+                               pr_rest<E>(o[t][i + 2] * inv, o[t][i + 3] * inv), pr_rest<E>(o[t][i + 4] * inv, o[t][i + 5] * inv),
+                               pr_rest<E>(o[t][i + 6] * inv, o[t][i + 7] * inv));
+        }
         if (a.lse && g == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -INFINITY;
         return;
     }
@@ -200,7 +204,10 @@ __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
     const PrPair p = pr_pair(a, u.first, r);
     const int64_t row = (int64_t)(u.s.r0 + p.i) * a.Hq + h * a.G + p.g;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    pr_store_out<E>(a, row * D + d, o, inv);
+    o *= inv;
+    *reinterpret_cast<at_u32x2*>(a.out + row * D + d) = at_u32x2{E::pack(o[0], o[1]), E::pack(o[2], o[3])};
+    if (a.rest)
+        *reinterpret_cast<at_u32x2*>(a.rest + row * D + d) = at_u32x2{pr_rest<E>(o[0], o[1]), pr_rest<E>(o[2], o[3])};
     if (a.lse && d == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -INFINITY;
 }
 

@@ -232,16 +232,31 @@ __device__ __forceinline__ at_u32x4 pr_read_across(uint8_t* lds, int across, int
     const pr_i16x8 z{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     return __builtin_bit_cast(at_u32x4, z);
 }
-// Four dimensions of a row's result, and where asked for what their rounding left
-// out, rounded itself.
+// Stores 16 elements of a row from the lanes c and c + 32 that share it: lane
+// (c, g) holds 4 g .. 4 g + 3 of the first eight in (a0, a1), of the other eight
+// in (b0, b1), packed.  The halves exchange words, so that each lane stores eight
+// side by side.
+__device__ __forceinline__ void pr_store16(uint16_t* dst, int g, uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1) {
+    const auto x = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+    *reinterpret_cast<at_u32x4*>(dst + 8 * g) = at_u32x4{x[0], y[0], x[1], y[1]};
+}
+// A lane's part of a row of D accumulators times f: dimensions 32 t + 8 i + 4 g ..
+// in registers 4 i .. of set t.
+template <class E, int D>
+__device__ __forceinline__ void pr_store_row(uint16_t* dst, int g, const pr_f32x16 (&o)[D / 32], float f) {
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; i += 8)
+            pr_store16(dst + 32 * t + 2 * i, g, E::pack(o[t][i] * f, o[t][i + 1] * f), E::pack(o[t][i + 2] * f, o[t][i + 3] * f),
+                       E::pack(o[t][i + 4] * f, o[t][i + 5] * f), E::pack(o[t][i + 6] * f, o[t][i + 7] * f));
+}
+// What rounding x and y to E's type leaves out, rounded itself.
 template <class E>
-__device__ __forceinline__ void pr_store_out(const PromptArgs& a, int64_t at, const at_f32x4& o, float inv) {
-    const float x0 = o[0] * inv, x1 = o[1] * inv, x2 = o[2] * inv, x3 = o[3] * inv;
-    const uint32_t lo = E::pack(x0, x1), hi = E::pack(x2, x3);
-    *reinterpret_cast<at_u32x2*>(a.out + at) = at_u32x2{lo, hi};
-    if (a.rest)
-        *reinterpret_cast<at_u32x2*>(a.rest + at) =
-            at_u32x2{E::pack(x0 - E::lo(lo), x1 - E::hi(lo)), E::pack(x2 - E::lo(hi), x3 - E::hi(hi))};
+__device__ __forceinline__ uint32_t pr_rest(float x, float y) {
+    const uint32_t w = E::pack(x, y);
+    return E::pack(x - E::lo(w), y - E::hi(w));
 }
 // Waits for the direct copies into LDS that the wave has issued.
 __device__ __forceinline__ void pr_wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }

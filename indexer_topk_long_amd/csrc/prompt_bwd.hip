@@ -172,14 +172,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
     }
     if (row < 0) return;
     if (parts.used <= 1) {
-        uint16_t* dst = a.dq + row * D;
-#pragma unroll
-        for (int t = 0; t < D / 32; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<at_u32x2*>(dst + 32 * t + 8 * i + 4 * g) =
-                    at_u32x2{E::pack(o[t][4 * i] * a.scale, o[t][4 * i + 1] * a.scale),
-                             E::pack(o[t][4 * i + 2] * a.scale, o[t][4 * i + 3] * a.scale)};
+        pr_store_row<E, D>(a.dq + row * D, g, o, a.scale);
         return;
     }
     float* part = a.part + ((pl.unit * a.Hkv + h) * a.splits + pl.part) * (int64_t)(RT * D);
@@ -424,16 +417,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
     if (key >= kb) return;
     if (parts.used <= 1) {
         const int64_t row = (int64_t)(s.k0 + key) * a.Hkv + h;
-#pragma unroll
-        for (int t = 0; t < D / 32; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                *reinterpret_cast<at_u32x2*>(a.dk + row * D + 32 * t + 8 * i + 4 * g) =
-                    at_u32x2{E::pack(dk[t][4 * i] * a.scale, dk[t][4 * i + 1] * a.scale),
-                             E::pack(dk[t][4 * i + 2] * a.scale, dk[t][4 * i + 3] * a.scale)};
-                *reinterpret_cast<at_u32x2*>(a.dv + row * D + 32 * t + 8 * i + 4 * g) =
-                    at_u32x2{E::pack(dv[t][4 * i], dv[t][4 * i + 1]), E::pack(dv[t][4 * i + 2], dv[t][4 * i + 3])};
-            }
+        pr_store_row<E, D>(a.dk + row * D, g, dk, a.scale);
+        pr_store_row<E, D>(a.dv + row * D, g, dv, 1.0f);
         return;
     }
     // a part: 128 keys' dk, then their dv
