@@ -83,6 +83,16 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
     }
     pr_wait_copies();
     __syncthreads();
+    if (fw >= u.count) {   // a wave without rows only copies (as often as the others wait for each other)
+        for (int t = t0; t < t1; ++t) {
+            if (t + 1 < t1) copy_keys(t + 1);
+            pr_wait_copies();
+            __syncthreads();
+            __syncthreads();
+            if (t + 1 < t1) copy_values(t + 1);
+        }
+        return;
+    }
     for (int t = t0; t < t1; ++t) {
         if (t + 1 < t1) copy_keys(t + 1);
         const int kt = pr_per_step(along) + (t & 1) * kTileBytes<D>, vt = pr_per_step(across) + 2 * kTileBytes<D>;

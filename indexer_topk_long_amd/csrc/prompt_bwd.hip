@@ -134,6 +134,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
     if (t0 < t1) copy(t0);
     pr_wait_copies();
     __syncthreads();
+    if (fw >= u.count) {   // a wave without rows only copies
+        for (int t = t0; t < t1; ++t) {
+            if (t + 1 < t1) copy(t + 1);
+            pr_wait_copies();
+            __syncthreads();
+        }
+        return;
+    }
     for (int t = t0; t < t1; ++t) {
         if (t + 1 < t1) copy(t + 1);
         const int stage = (t & 1) * kStage<D>, kt = pr_per_step(along) + stage, ka = pr_per_step(across) + stage;
