@@ -1,5 +1,25 @@
 // prompt_bwd.hip -- gradients of causal attention over packed 16-bit prompts on
-// gfx950.
+// gfx950: bound by the matrix cores and the vector work beside them.
+//
+// With P = 2^(y - lse2), lse2 = log2(e) lse, and delta = dout . (out + rest):
+//   dv = P^T dout,  dP = dout v^T,  dS = P (dP - delta),
+//   dq = scale dS k,  dk = scale dS^T q,
+// the last two and dv summed over the query heads of a key/value head.  P and dS
+// are rounded once to 16 bits for their products (operands of one type); sums are
+// fp32.  Two launches, so that no sum needs atomics and the same call gives the
+// same bits; scores and dout v^T are formed in both, seven products in place of
+// five:
+//  - dq: as the forward pass, 128 pairs a workgroup, queries and dout in
+//    registers, 64 keys a step through LDS.  It notes lse2 and delta for the other.
+//  - dk and dv: 128 keys of a key/value head a workgroup, 32 a wave; the pairs
+//    that see them pass through LDS, 32 a step, heads of a group side by side.
+//    Scores stand the other way round here (pairs on the rows), so that weights
+//    and score gradients are operands of the products over pairs in place.
+//
+// One sequence of 8,192 rows (32 heads on 8, D = 128, bf16): dq 840 to 910 us (930
+// TFLOP/s of its three products), dk and dv 1,220 to 1,280 us (850 to 900 of their
+// four; the matrix units are busy 51 % of the cycles in which a CU has work, and 7
+// % of them it has none); with the forward pass 2,500 to 2,570 us.
 #include <algorithm>
 #include <atomic>
 
@@ -239,7 +259,8 @@ __device__ __forceinline__ void seeing(const PromptArgs& a, const PrSeq& s, int 
 // dk and dv: a unit is 128 keys of a key/value head, 32 a wave; the pairs that see
 // them pass through LDS, 32 a step.  A wave keeps its rows of k and both sums in
 // registers; those of v wait in LDS (with them in registers too, 25 and more of
-// the 256 spilled, and each reload waited for all copies on their way).
+// the 256 spilled, and each reload waited for all copies on their way: one
+// sequence of 8,192 rows 1,587 us against 1,376).
 template <class E, int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
