@@ -260,7 +260,8 @@ __device__ __forceinline__ void seeing(const PromptArgs& a, const PrSeq& s, int 
 // them pass through LDS, 32 a step.  A wave keeps its rows of k and both sums in
 // registers; those of v wait in LDS (with them in registers too, 25 and more of
 // the 256 spilled, and each reload waited for all copies on their way: one
-// sequence of 8,192 rows 1,587 us against 1,376).
+// sequence of 8,192 rows 1,587 us against 1,376, the vector work between the
+// matrix instructions included, for which there were no registers either).
 template <class E, int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
