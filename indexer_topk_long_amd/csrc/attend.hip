@@ -486,9 +486,13 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
     };
     auto step = [&](KvTile<D>& t, const Where& w, const PageScale (&hs)[2]) {
         const int last = w.key0 + kTile - 1;
-        const bool whole = w.pid[0] >= 0 && w.pid[1] >= 0 && last <= pos_lo && last < kr.hi &&
-                           (a.window <= 0 || w.key0 > pos_hi - a.window || last < a.n_sink) &&
-                           (PART != kOwnKeys || w.key0 >= kr.lo);
+        bool whole;
+        if constexpr (PART == kOwnKeys) {   // (no window)
+            whole = w.pid[0] >= 0 && w.pid[1] >= 0 && last <= pos_lo && last < kr.hi && w.key0 >= kr.lo;
+        } else {
+            whole = w.pid[0] >= 0 && w.pid[1] >= 0 && last <= pos_lo && last < kr.hi &&
+                    (a.window <= 0 || w.key0 > pos_hi - a.window || last < a.n_sink);
+        }
         if (!whole) {
             // bytes of keys that no row sees may be NaN: their weights are 0, so the values must be finite
 #pragma unroll

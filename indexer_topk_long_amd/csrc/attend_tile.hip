@@ -532,9 +532,12 @@ __device__ __forceinline__ void dense_unit(const AttendArgs& a, const SeqRows& s
         return (p0 >= 0 ? 1 : 0) | (p1 >= 0 ? 2 : 0) | (p2 >= 0 ? 4 : 0) | (p3 >= 0 ? 8 : 0);
     };
     auto seen_by_all = [&](int key0, int ok, int lo, int hi) {   // every key of the step by rows at lo .. hi
-        return ok == 15 && key0 + kKeys - 1 <= lo && key0 + kKeys <= kt.hi &&
-               (a.window <= 0 || key0 > hi - a.window || key0 + kKeys <= a.n_sink) &&
-               (PART != kOwnKeys || key0 >= kt.lo);
+        if constexpr (PART == kOwnKeys) {   // (no window)
+            return ok == 15 && key0 + kKeys - 1 <= lo && key0 + kKeys <= kt.hi && key0 >= kt.lo;
+        } else {
+            return ok == 15 && key0 + kKeys - 1 <= lo && key0 + kKeys <= kt.hi &&
+                   (a.window <= 0 || key0 > hi - a.window || key0 + kKeys <= a.n_sink);
+        }
     };
     // what a step's bytes need before they are converted
     auto settle_raw = [&](int t, int pages, Bytes& raw) {

@@ -148,7 +148,8 @@ void leaf_of_capture(const at::Tensor& t, const char* name, int dev) {
     const auto acc = torch::autograd::impl::try_get_grad_accumulator(t);
     if (!acc) return;
     const auto st = acc->stream();
-    if (st && *st != c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).unwrap())
+    // (by number: torch keeps the node's stream under another device type's name)
+    if (st && (st->device_index() != dev || st->id() != c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).id()))
         refuse(PyExc_RuntimeError, std::string(name) + " belongs to an earlier graph that is still alive, made on another stream: "
                                                        "a backward pass captured now would end the process (drop that graph's "
                                                        "results first)");

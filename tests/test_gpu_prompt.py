@@ -405,3 +405,32 @@ def test_on_another_device_context(lib):
     [t.start() for t in threads], [t.join() for t in threads]
     torch.cuda.synchronize()
     assert len(res) == 3 and all(torch.equal(a, b) for r in res.values() for a, b in zip(r, want))
+
+
+def test_captured_with_a_leaf_used_twice(lib):
+    """The second call finds the leaf held by the captured graph itself: no other stream waits."""
+    import torch
+    rows = [70, 41]
+    cu = lens_to_cu(rows).cuda()
+    q, k, v, dout = [x.cuda() for x in make(140, rows, rows, 4, 2, 64, torch.bfloat16)]
+    leaves = [x.requires_grad_() for x in (q, k, v)]
+
+    def step():
+        a = lib.attend_prompt(*leaves, cu)
+        b = lib.attend_prompt(a, k, v, cu)
+        return (b.detach(),) + torch.autograd.grad(b, leaves, dout)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for i in range(3):
+        with torch.no_grad():
+            q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(i)))
+        graph.replay()
+        torch.cuda.synchronize()
+        held = [x.clone() for x in got]
+        assert all(torch.equal(x, y) for x, y in zip(held, step()))
