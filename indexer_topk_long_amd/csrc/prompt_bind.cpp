@@ -8,7 +8,9 @@
 #include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/variable.h>
 
-#include <initializer_list>
+#include <memory>
+#include <unordered_set>
+#include <vector>
 
 namespace ltk_bind {
 
@@ -140,19 +142,26 @@ struct PromptFn : public torch::autograd::Function<PromptFn> {
 };
 
 // While a stream is captured, the backward pass of a leaf whose accumulator was
-// made on another stream (by an eager graph that still lives) would make that
-// stream wait for the capture, which ends the process: refused here, before
-// anything is enqueued.
-void leaf_of_capture(const at::Tensor& t, const char* name, int dev) {
-    if (!t.requires_grad() || t.grad_fn()) return;
-    const auto acc = torch::autograd::impl::try_get_grad_accumulator(t);
-    if (!acc) return;
-    const auto st = acc->stream();
-    // (by number: torch keeps the node's stream under another device type's name)
-    if (st && (st->device_index() != dev || st->id() != c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).id()))
-        refuse(PyExc_RuntimeError, std::string(name) + " belongs to an earlier graph that is still alive, made on another stream: "
-                                                       "a backward pass captured now would end the process (drop that graph's "
-                                                       "results first)");
+// made on the default stream (by an eager graph that still lives) would make that
+// stream, which cannot be part of a capture, wait for it, and end the process:
+// refused here, before anything is enqueued.  (Accumulators of other streams, as a
+// warm-up leaves them, join the capture.)
+void leaves_of_capture(const at::Tensor& t, const char* name) {
+    if (!t.requires_grad()) return;
+    std::vector<std::shared_ptr<torch::autograd::Node>> todo;
+    std::unordered_set<torch::autograd::Node*> seen;
+    todo.push_back(t.grad_fn() ? t.grad_fn() : torch::autograd::impl::try_get_grad_accumulator(t));
+    while (!todo.empty()) {
+        const auto node = todo.back();
+        todo.pop_back();
+        if (!node || !seen.insert(node.get()).second) continue;
+        const auto st = node->num_outputs() == 0 ? node->stream() : std::nullopt;   // an accumulator
+        if (st && st->id() == 0)
+            refuse(PyExc_RuntimeError, std::string(name) + " depends on a leaf of a graph of the default stream that is still alive: a "
+                                                           "backward pass captured now would end the process (drop that graph's "
+                                                           "results, warm up on another stream, or call under torch.no_grad())");
+        for (const auto& e : node->next_edges()) todo.push_back(e.function);
+    }
 }
 
 const at::Tensor& offsets(PyObject* o, const char* name, int64_t n, int dev) {
@@ -197,9 +206,9 @@ PyObject* attend_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 {
                     const On on(dev);
                     if (c10::hip::currentStreamCaptureStatusMayInitCtx() != c10::hip::CaptureStatus::None) {
-                        leaf_of_capture(q, "q", dev);
-                        leaf_of_capture(k, "k", dev);
-                        leaf_of_capture(v, "v", dev);
+                        leaves_of_capture(q, "q");
+                        leaves_of_capture(k, "k");
+                        leaves_of_capture(v, "v");
                     }
                 }
                 const variable_list r = PromptFn::apply(q, k, v, cu, cu_k.defined() ? std::optional<at::Tensor>(cu_k) : std::nullopt, scale,

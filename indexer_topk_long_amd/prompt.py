@@ -32,8 +32,9 @@ def attend_prompt(q, k, v, cu, cu_k=None, scale=None, window: int = 0, return_ls
     zeros.
 
     Differentiable in q, k and v, once: a second derivative or a forward one
-    raises RuntimeError.  While a stream is captured, a leaf that an eager graph on
-    another stream still holds is refused too."""
+    raises RuntimeError.  While a stream is captured, inputs that depend on a leaf
+    which an eager graph of the default stream still holds are refused too (but under
+    torch.no_grad()): the captured backward pass would end the process."""
     return _bind().attend_prompt(q, k, v, cu, cu_k, scale, window, return_lse)
 
 

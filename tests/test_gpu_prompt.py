@@ -321,6 +321,16 @@ def test_capture_beside_an_eager_graph_of_the_same_leaf_is_refused(lib):
         with torch.cuda.graph(graph):
             lib.attend_prompt(q, k, v, cu)
     torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="still alive"):   # .. also where the call's inputs are made of the leaf
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            lib.attend_prompt((q * 2)[:, :], k, v, cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.no_grad(), torch.cuda.graph(graph):           # (no backward pass can follow)
+        out = lib.attend_prompt(q, k, v, cu)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, alive)
     (g,) = torch.autograd.grad(alive, q, dout)
     assert bool(g.isfinite().all())
 
@@ -434,3 +444,25 @@ def test_captured_with_a_leaf_used_twice(lib):
         torch.cuda.synchronize()
         held = [x.clone() for x in got]
         assert all(torch.equal(x, y) for x, y in zip(held, step()))
+
+
+def test_captured_while_the_warm_up_on_a_side_stream_lives(lib):
+    import torch
+    rows = [70, 41]
+    cu = lens_to_cu(rows).cuda()
+    q, k, v, dout = [x.cuda() for x in make(141, rows, rows, 4, 2, 64, torch.bfloat16)]
+    leaves = [x.requires_grad_() for x in (q, k, v)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        alive = lib.attend_prompt(*leaves, cu)
+        want = torch.autograd.grad(alive, leaves, dout, retain_graph=True)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(lib.attend_prompt(*leaves, cu), leaves, dout)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and alive.grad_fn is not None
