@@ -101,7 +101,9 @@ int litetopk_attend_prompt_backward(const ltk_prompt* p, const ltk_rows* q, cons
  *              group's first sequence; those from shared_len on, which may lie
  *              inside a page, through each sequence's own.  Every row of the group
  *              sees all shared keys: they lie before the rows, shared_len <=
- *              kv_len - rows for each of its sequences.
+ *              kv_len - rows for each of its sequences.  (A page that sequences
+ *              have copied and appended to may have another scale in each, so for
+ *              litetopk_attend's very bytes share whole pages.)
  *
  * The rest as for litetopk_attend.  Sums over the shared keys pass through the
  * workspace in fp32. */

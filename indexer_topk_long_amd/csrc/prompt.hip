@@ -46,35 +46,14 @@ namespace {
 
 template <int D>
 constexpr int kTileBytes = kKeys * D * 2;
-template <int D>
-constexpr int kStage = 2 * kTileBytes<D>;   // keys, then values
 
 __device__ __forceinline__ uint8_t* lds() {
     extern __shared__ at_u32x4 prompt_lds[];
     return reinterpret_cast<uint8_t*>(prompt_lds);
 }
 
-// Copies rows key0 .. key0 + 63 of one head into a tile, the last row again
-// for those past the end.
-template <int D, int NW>
-__device__ __forceinline__ void copy_tile(const PrRows& x, int64_t row0, int h, int key0, int m, uint8_t* tile) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    constexpr int kRowsPer = 512 / D;              // rows of a wave's copy (1 KB)
-    constexpr int kCopies = kKeys / kRowsPer / NW;  // copies of a wave
-    const uint16_t* base = x.p + (row0 + key0) * x.row + (int64_t)h * x.head;
-    const int last = m - 1 - key0;
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-        const int r0 = (wave * kCopies + i) * kRowsPer, r = r0 + lane / (D / 8);
-        const int chunk = (lane % (D / 8)) ^ pr_swizzle<D>(r);
-        const uint32_t off = (uint32_t)min(r, last) * (uint32_t)x.row * 2u + (uint32_t)chunk * 16u;
-        lds_direct16_async(base, off, tile + r0 * (2 * D));
-    }
-}
-
-template <class E, int D, int NW>
-__global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
-    constexpr int RT = 32 * NW;
+template <class E, int D>
+__global__ __launch_bounds__(64 * kWaves, 3) void prompt_kernel(PromptArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
     const PrPlace pl = pr_place(a);
@@ -109,8 +88,8 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
         for (int r = 0; r < 16; ++r) o[t][r] = 0.0f;
     const int from = a.window > 0 ? max(pos, 0) - a.window : -1;
 
-    auto copy_keys = [&](int t) { copy_tile<D, NW>(a.k, s.k0, h, t * kKeys, s.m, lds() + (t & 1) * kTileBytes<D>); };
-    auto copy_values = [&](int t) { copy_tile<D, NW>(a.v, s.k0, h, t * kKeys, s.m, lds() + 2 * kTileBytes<D>); };
+    auto copy_keys = [&](int t) { pr_copy_tile<D>(a.k, s.k0, h, t * kKeys, s.m, lds() + (t & 1) * kTileBytes<D>); };
+    auto copy_values = [&](int t) { pr_copy_tile<D>(a.v, s.k0, h, t * kKeys, s.m, lds() + 2 * kTileBytes<D>); };
     const int along = pr_along<D>(), across = pr_across<D>();
     if (t0 < t1) {
         copy_keys(t0);
@@ -121,8 +100,12 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
     if (fw >= u.count) {   // a wave without rows only copies (as often as the others wait for each other)
         for (int t = t0; t < t1; ++t) {
             if (t + 1 < t1) copy_keys(t + 1);
-            pr_wait_copies();
+            if (t + 1 < t1)
+                pr_wait_copies_but<D / 8 / kWaves>();
+            else
+                pr_wait_copies();
             __syncthreads();
+            pr_wait_copies();
             __syncthreads();
             if (t + 1 < t1) copy_values(t + 1);
         }
@@ -179,7 +162,7 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
             }
         // the values' copies are older than the next keys'
         if (t + 1 < t1)
-            pr_wait_copies_but<D / 8 / NW>();
+            pr_wait_copies_but<D / 8 / kWaves>();
         else
             pr_wait_copies();
         __syncthreads();
@@ -208,8 +191,8 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
         if (a.lse && g == 0) a.lse[row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f : -INFINITY;
         return;
     }
-    // a part: RT rows of D sums, then RT pairs (m, l)
-    float* part = a.part + ((pl.unit * a.Hkv + h) * a.splits + pl.part) * (int64_t)(RT * (D + 2));
+    // a part: kUnit rows of D sums, then kUnit pairs (m, l)
+    float* part = a.part + ((pl.unit * a.Hkv + h) * a.splits + pl.part) * (int64_t)(kUnit * (D + 2));
     const int r = fw + c;
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
@@ -218,15 +201,14 @@ __global__ __launch_bounds__(64 * NW, 3) void prompt_kernel(PromptArgs a) {
             *reinterpret_cast<at_f32x4*>(part + (size_t)r * D + 32 * t + 8 * i + 4 * g) =
                 at_f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
     if (g == 0) {
-        part[(size_t)RT * D + 2 * r] = l > 0.0f ? m : kNoRef;
-        part[(size_t)RT * D + 2 * r + 1] = l;
+        part[(size_t)kUnit * D + 2 * r] = l > 0.0f ? m : kNoRef;
+        part[(size_t)kUnit * D + 2 * r + 1] = l;
     }
 }
 
 // Joins the parts of a unit, 8 rows a workgroup.
-template <class E, int D, int NW>
+template <class E, int D>
 __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
-    constexpr int RT = 32 * NW;
     const int64_t un = blockIdx.x / (uint32_t)a.Hkv;
     const int h = (int)(blockIdx.x - (uint32_t)un * (uint32_t)a.Hkv);
     PrRowUnit u;
@@ -235,15 +217,15 @@ __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
     if (used <= 1) return;
     const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
     if (r >= u.count) return;
-    const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(RT * (D + 2));
+    const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(kUnit * (D + 2));
     float m = kNoRef, l = 0.0f;
     at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
-    for (int i = 0; i < used; ++i) m = fmaxf(m, part[(int64_t)i * (RT * (D + 2)) + (size_t)RT * D + 2 * r]);
+    for (int i = 0; i < used; ++i) m = fmaxf(m, part[(int64_t)i * (kUnit * (D + 2)) + (size_t)kUnit * D + 2 * r]);
 #pragma unroll 8
-    for (int i = 0; i < used; ++i, part += RT * (D + 2)) {
-        const float f = __builtin_amdgcn_exp2f(part[(size_t)RT * D + 2 * r] - m);
-        l = __builtin_fmaf(f, part[(size_t)RT * D + 2 * r + 1], l);
+    for (int i = 0; i < used; ++i, part += kUnit * (D + 2)) {
+        const float f = __builtin_amdgcn_exp2f(part[(size_t)kUnit * D + 2 * r] - m);
+        l = __builtin_fmaf(f, part[(size_t)kUnit * D + 2 * r + 1], l);
         o += *reinterpret_cast<const at_f32x4*>(part + (size_t)r * D + d) * f;
     }
     const PrPair p = pr_pair(a, u.first, r);
@@ -258,9 +240,9 @@ __global__ __launch_bounds__(2 * D) void prompt_join_kernel(PromptArgs a) {
 
 template <class E, int D>
 hipError_t launch(const PromptPlan& p, const PromptArgs& a, hipStream_t st) {
-    prompt_kernel<E, D, kWaves><<<(unsigned)p.rows.blocks, 64 * kWaves, 3 * kTileBytes<D>, st>>>(a);
+    prompt_kernel<E, D><<<(unsigned)p.rows.blocks, 64 * kWaves, 3 * kTileBytes<D>, st>>>(a);
     if (a.splits > 1)
-        prompt_join_kernel<E, D, kWaves><<<dim3((unsigned)(p.rows.units * a.Hkv), 4 * kWaves), 2 * D, 0, st>>>(a);
+        prompt_join_kernel<E, D><<<dim3((unsigned)(p.rows.units * a.Hkv), 4 * kWaves), 2 * D, 0, st>>>(a);
     return hipGetLastError();
 }
 
@@ -295,11 +277,10 @@ static double mean_capped(double lo, double hi, double cap) {
 PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int window) {
     PromptPlan p{};
     const int64_t G = Hq / Hkv, seqs = std::max(n_seq, 1);
-    constexpr int rows = 32 * kWaves;
-    const double n = (double)T / seqs, m = (double)S / seqs, reach = window > 0 ? (double)window + rows : (double)S + rows;
+    const double n = (double)T / seqs, m = (double)S / seqs, reach = window > 0 ? (double)window + kUnit : (double)S + kUnit;
     // (about: a sequence's last unit is half full)
-    const int64_t row_units = pr_units(T, G, rows, n_seq), key_units = pr_units(S, 1, rows, n_seq);
-    const double row_about = (double)T * G / rows + 0.5 * seqs, key_about = (double)S / rows + 0.5 * seqs;
+    const int64_t row_units = pr_units(T, G, kUnit, n_seq), key_units = pr_units(S, 1, kUnit, n_seq);
+    const double row_about = (double)T * G / kUnit + 0.5 * seqs, key_about = (double)S / kUnit + 0.5 * seqs;
     const double uneven = n_seq > 1 ? 1.2 : 1.0;   // (of unequal sequences the long ones have most of the steps)
     const double row_mean = uneven * mean_capped(std::max(m - n, 0.0), m, reach) / kKeys + 0.5;
     const double key_mean = uneven * mean_capped(0.0, m, std::min(n, reach)) * G / kPairs + 0.5;
@@ -309,12 +290,12 @@ PromptPlan prompt_plan(int T, int S, int Hq, int Hkv, int D, int n_seq, int wind
     p.rows = cut(row_units, row_about, row_mean, row_most, Hkv, D == 64 ? 1024 : 768, 8);
     p.grad = cut(row_units, row_about, row_mean, row_most, Hkv, D == 64 ? 768 : 512, 8);
     p.keys = cut(key_units, key_about, key_mean, key_most, Hkv, 512, 16);
-    auto parts = [&](const PromptCut& c, int64_t floats) { return c.splits > 1 ? (size_t)(c.blocks * rows * floats) * 4 : 0; };
+    auto parts = [&](const PromptCut& c, int64_t floats) { return c.splits > 1 ? (size_t)(c.blocks * kUnit * floats) * 4 : 0; };
     p.fwd_bytes = std::max<size_t>(256, parts(p.rows, D + 2));
     p.stat_bytes = ((size_t)T * Hq * 4 + 255) / 256 * 256;
     p.bwd_bytes = std::max<size_t>(256, 2 * p.stat_bytes + std::max(parts(p.grad, D), parts(p.keys, 2 * D)));
     // (the last: delta's launch)
-    p.fits = grid_fits(std::max({p.rows.blocks, p.grad.blocks, p.keys.blocks, ((int64_t)T * Hq + rows - 1) / rows}), 64 * kWaves);
+    p.fits = grid_fits(std::max({p.rows.blocks, p.grad.blocks, p.keys.blocks, ((int64_t)T * Hq + kUnit - 1) / kUnit}), 64 * kWaves);
     return p;
 }
 

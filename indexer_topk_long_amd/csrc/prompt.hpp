@@ -12,6 +12,7 @@
 namespace ltk {
 
 constexpr int kWaves = 4;    // of a workgroup
+constexpr int kUnit = 32 * kWaves;   // pairs of a row tile, or keys of a key tile
 constexpr int kKeys = 64;    // keys of a step (forward, dq)
 constexpr int kPairs = 32;   // (row, head) pairs of a step (dk, dv)
 
@@ -157,7 +158,7 @@ __device__ __forceinline__ PrSeq pr_seq_of(const PromptArgs& a, int64_t u, int m
 }
 inline int64_t pr_units(int64_t T, int64_t mul, int per, int n_seq) { return T * mul / per + n_seq + 2; }
 
-// A row tile: 32 kWaves pairs of a sequence and key/value head, and the steps of
+// A row tile: kUnit pairs of a sequence and key/value head, and the steps of
 // keys that they see.
 struct PrRowUnit {
     PrSeq s;
@@ -167,15 +168,14 @@ struct PrRowUnit {
     int t0, t1;     // steps of kKeys keys
 };
 __device__ __forceinline__ bool pr_row_unit(const PromptArgs& a, int64_t un, PrRowUnit& u) {
-    constexpr int RT = 32 * kWaves;
     int64_t number;
-    u.s = pr_seq_of<RT, false>(a, un, a.G, number);
+    u.s = pr_seq_of<kUnit, false>(a, un, a.G, number);
     const uint32_t pairs = (uint32_t)u.s.n * (uint32_t)a.G;   // < 2^31
-    const int64_t tile = (int64_t)((pairs + RT - 1) / RT) - 1 - number;   // the longest first
+    const int64_t tile = (int64_t)((pairs + kUnit - 1) / kUnit) - 1 - number;   // the longest first
     if (tile < 0) return false;
-    const uint32_t f0 = (uint32_t)tile * RT, i = f0 / (uint32_t)a.G;
+    const uint32_t f0 = (uint32_t)tile * kUnit, i = f0 / (uint32_t)a.G;
     u.first = PrPair{(int)i, (int)(f0 - i * (uint32_t)a.G)};
-    u.count = (int)min(pairs - f0, (uint32_t)RT);
+    u.count = (int)min(pairs - f0, (uint32_t)kUnit);
     u.lo = u.s.pos0() + u.first.i;
     u.hi = u.s.pos0() + pr_pair(a, u.first, u.count - 1).i;
     const int end = u.s.in ? min(max(u.hi + 1, 0), u.s.m) : 0;
@@ -257,6 +257,23 @@ template <class E>
 __device__ __forceinline__ uint32_t pr_rest(float x, float y) {
     const uint32_t w = E::pack(x, y);
     return E::pack(x - E::lo(w), y - E::hi(w));
+}
+// Copies rows key0 .. key0 + 63 of one head into a tile, the last row again
+// for those past the end.
+template <int D>
+__device__ __forceinline__ void pr_copy_tile(const PrRows& x, int64_t row0, int h, int key0, int m, uint8_t* tile) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kRowsPer = 512 / D;              // rows of a wave's copy (1 KB)
+    constexpr int kCopies = 64 / kRowsPer / kWaves;  // copies of a wave
+    const uint16_t* base = x.p + (row0 + key0) * x.row + (int64_t)h * x.head;
+    const int last = m - 1 - key0;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        const int r0 = (wave * kCopies + i) * kRowsPer, r = r0 + lane / (D / 8);
+        const int chunk = (lane % (D / 8)) ^ pr_swizzle<D>(r);
+        const uint32_t off = (uint32_t)min(r, last) * (uint32_t)x.row * 2u + (uint32_t)chunk * 16u;
+        lds_direct16_async(base, off, tile + r0 * (2 * D));
+    }
 }
 // Waits for the direct copies into LDS that the wave has issued.
 __device__ __forceinline__ void pr_wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }

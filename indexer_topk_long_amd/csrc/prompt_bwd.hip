@@ -29,8 +29,6 @@ namespace ltk {
 
 namespace {
 
-constexpr int kUnit = 32 * kWaves;   // pairs (dq) or keys (dk, dv) of a unit
-
 template <int D>
 constexpr int kTileBytes = 64 * D * 2;
 template <int D>
@@ -39,24 +37,6 @@ constexpr int kStage = 2 * kTileBytes<D>;
 __device__ __forceinline__ uint8_t* lds() {
     extern __shared__ at_u32x4 prompt_bwd_lds[];
     return reinterpret_cast<uint8_t*>(prompt_bwd_lds);
-}
-
-// Copies rows key0 .. key0 + 63 of one head into a tile, the last row again
-// for those past the end.
-template <int D, int NW>
-__device__ __forceinline__ void copy_tile(const PrRows& x, int64_t row0, int h, int key0, int m, uint8_t* tile) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    constexpr int kRowsPer = 512 / D;              // rows of a wave's copy (1 KB)
-    constexpr int kCopies = 64 / kRowsPer / NW;
-    const uint16_t* base = x.p + (row0 + key0) * x.row + (int64_t)h * x.head;
-    const int last = m - 1 - key0;
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-        const int r0 = (wave * kCopies + i) * kRowsPer, r = r0 + lane / (D / 8);
-        const int chunk = (lane % (D / 8)) ^ pr_swizzle<D>(r);
-        const uint32_t off = (uint32_t)min(r, last) * (uint32_t)x.row * 2u + (uint32_t)chunk * 16u;
-        lds_direct16_async(base, off, tile + r0 * (2 * D));
-    }
 }
 
 // log2(e) lse, infinite for a row that sees no key (its weights are 0 then).
@@ -103,7 +83,6 @@ __global__ __launch_bounds__(64 * kWaves) void prompt_delta_kernel(PromptArgs a)
 // dq: units are row tiles as in the forward pass.
 template <class E, int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a) {
-    constexpr int RT = kUnit;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, g = lane >> 5;
     const PrPlace pl = pr_place(a);
@@ -147,8 +126,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
 
     auto copy = [&](int t) {
         uint8_t* st = lds() + (t & 1) * kStage<D>;
-        copy_tile<D, kWaves>(a.k, s.k0, h, t * kKeys, s.m, st);
-        copy_tile<D, kWaves>(a.v, s.k0, h, t * kKeys, s.m, st + kTileBytes<D>);
+        pr_copy_tile<D>(a.k, s.k0, h, t * kKeys, s.m, st);
+        pr_copy_tile<D>(a.v, s.k0, h, t * kKeys, s.m, st + kTileBytes<D>);
     };
     const int along = pr_along<D>(), across = pr_across<D>();
     if (t0 < t1) copy(t0);
@@ -203,7 +182,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
         pr_store_row<E, D>(a.dq + row * D, g, o, a.scale);
         return;
     }
-    float* part = a.part + ((pl.unit * a.Hkv + h) * a.splits + pl.part) * (int64_t)(RT * D);
+    float* part = a.part + ((pl.unit * a.Hkv + h) * a.splits + pl.part) * (int64_t)(kUnit * D);
     const int r = fw + c;
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
@@ -216,7 +195,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
 // Sums the parts of a unit's dq, 8 rows a workgroup.
 template <class E, int D>
 __global__ __launch_bounds__(2 * D) void prompt_dq_join_kernel(PromptArgs a) {
-    constexpr int RT = kUnit;
     const int64_t un = blockIdx.x / (uint32_t)a.Hkv;
     const int h = (int)(blockIdx.x - (uint32_t)un * (uint32_t)a.Hkv);
     PrRowUnit u;
@@ -225,10 +203,10 @@ __global__ __launch_bounds__(2 * D) void prompt_dq_join_kernel(PromptArgs a) {
     if (used <= 1) return;
     const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), d = 4 * (threadIdx.x % (D / 4));
     if (r >= u.count) return;
-    const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(RT * D) + (size_t)r * D + d;
+    const float* part = a.part + (un * a.Hkv + h) * a.splits * (int64_t)(kUnit * D) + (size_t)r * D + d;
     at_f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
-    for (int i = 0; i < used; ++i) o += *reinterpret_cast<const at_f32x4*>(part + (int64_t)i * (RT * D));
+    for (int i = 0; i < used; ++i) o += *reinterpret_cast<const at_f32x4*>(part + (int64_t)i * (kUnit * D));
     const PrPair p = pr_pair(a, u.first, r);
     const int64_t row = (int64_t)(u.s.r0 + p.i) * a.Hq + h * a.G + p.g;
     *reinterpret_cast<at_u32x2*>(a.dq + row * D + d) =
@@ -343,8 +321,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
     // (a scale of 0 is taken as the least one, so that a hidden score stays infinite)
     const float c2 = a.c2 == 0.0f ? 0x1p-126f : a.c2;
     if (steps > 0) {
-        copy_tile<D, kWaves>(a.v, s.k0, h, ka, s.m, lds());
-        copy_tile<D, kWaves>(a.v, s.k0, h, min(ka + 64, s.m - 1), s.m, lds() + kTileBytes<D>);
+        pr_copy_tile<D>(a.v, s.k0, h, ka, s.m, lds());
+        pr_copy_tile<D>(a.v, s.k0, h, min(ka + 64, s.m - 1), s.m, lds() + kTileBytes<D>);
         copy(0, *mine);
     }
     pr_wait_copies();

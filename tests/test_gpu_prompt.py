@@ -466,3 +466,9 @@ def test_captured_while_the_warm_up_on_a_side_stream_lives(lib):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)) and alive.grad_fn is not None
+
+
+def test_more_sequences_than_one_look_covers(lib):
+    """4,300 sequences, most of them empty or of one row: found over two levels of looks."""
+    rows = [(i * 7) % 3 if i % 2 else 0 for i in range(4300)]
+    _case(lib, rows, None, 1, 1, 64, "bfloat16", 151)

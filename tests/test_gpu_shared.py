@@ -233,3 +233,9 @@ def test_refusals(lib, what, err):
         q.requires_grad_()
     with pytest.raises(err):
         lib.attend_shared(q, cache, table, cu, kv_len, bounds, lens)
+
+
+def test_many_groups(lib):
+    """More groups and sequences than a workgroup looks at together."""
+    groups = [(1 + (5 * i) % 40, [(1, 45 + i % 30)] * (1 + i % 2)) for i in range(290)]
+    _check(lib, shared_case(16, groups, 1, 2, 16, 64))
