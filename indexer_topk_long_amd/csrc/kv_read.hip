@@ -3,7 +3,8 @@
 //
 // A thread takes 8 bytes of a row and head, keys and values alike, and the
 // same of the heads after it: the row's sequence, position and page are looked
-// up once for all of them.
+// up once for all of them.  82,870 rows of eight heads (D = 128, to bf16) take 102 to
+// 104 us, 4.9 TB/s, where a large copy reaches 5.05; 100 rows 2.9 us.
 #include <algorithm>
 
 #include "prompt.hpp"
