@@ -88,10 +88,12 @@ __device__ __forceinline__ void lds_direct4(const void* g, void* lds) {
 // and orders the copies itself: wait_vm on all but the newest tiles' loads,
 // then a barrier.  Vector memory operations complete in issue order, so the
 // compiler's own vmcnt waits stay correct with these copies in flight.
+// A load into LDS needs one wait state after a scalar write of M0; the compiler
+// adds none inside an asm string, so the string holds it (s_nop 0).
 __device__ __forceinline__ void lds_direct16_async(const void* g, void* lds) {
     const uint32_t off = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds);
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "s"(off) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "s"(off) : "memory", "m0");
 }
 // The same copy from a wave-uniform base (SGPRs) plus a per-lane 32-bit byte
 // offset, so that no per-load address arithmetic is needed.
@@ -107,19 +109,19 @@ __device__ __forceinline__ uint64_t uniform_ptr(const void* p) {
 __device__ __forceinline__ void lds_direct16_async(const void* base, uint32_t off, void* lds) {
     const uint32_t m = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds);
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(uniform_ptr(base)), "s"(m)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(uniform_ptr(base)), "s"(m)
                  : "memory", "m0");
 }
 __device__ __forceinline__ void lds_direct4_async(const void* base, uint32_t off, void* lds) {
     const uint32_t m = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds);
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(uniform_ptr(base)), "s"(m)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(off), "s"(uniform_ptr(base)), "s"(m)
                  : "memory", "m0");
 }
 __device__ __forceinline__ void lds_direct4_async(const void* g, void* lds) {
     const uint32_t off = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds);
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" : : "v"(g), "s"(off) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(g), "s"(off) : "memory", "m0");
 }
 
 // Smallest fp32 score whose bin is >= thr (bin_of is monotone), found by
