@@ -38,12 +38,12 @@ sys.path.insert(0, ROOT)
 KERNEL_SOURCES = ["device.hpp", "kernels_common.hpp", "internal.hpp", "indexer.hip"]
 RETR_SOURCES = ["device.hpp", "kernels_common.hpp", "internal.hpp", "retrieve.hip"]
 DSA_SOURCES = ["device.hpp", "internal.hpp", "dsa.hip"]
-SCAN_TRAFFIC = {"digest": "a2b5049f774f6b45", "workload": "prefill-1m-fp8",
-                "bytes": 2228843 * 1024 * 2.0 + 152471 * 1024 * 1.0}
-RETR_TRAFFIC = {"digest": "ddb385e3e0aa1fa1", "workload": "retrieval-8m-d768-bf16",
-                "bytes": 8615774 * 1024 * 2.0 + 1730362 * 1024 * 1.0}
-DECODE_TRAFFIC = {"digest": "a2b5049f774f6b45", "workload": "decode-1m-fp8",
-                  "bytes": 67674 * 1024 * 2.0 + 46 * 1024 * 1.0}
+SCAN_TRAFFIC = {"digest": "1b9012cc9c283f8f", "workload": "prefill-1m-fp8",
+                "bytes": 2228837 * 1024 * 2.0 + 152432 * 1024 * 1.0}
+RETR_TRAFFIC = {"digest": "386e7fb184134986", "workload": "retrieval-8m-d768-bf16",
+                "bytes": 9379937 * 1024 * 2.0 + 1728934 * 1024 * 1.0}
+DECODE_TRAFFIC = {"digest": "1b9012cc9c283f8f", "workload": "decode-1m-fp8",
+                  "bytes": 67672 * 1024 * 2.0 + 46 * 1024 * 1.0}
 DSA_TRAFFIC = {"digest": "712d6bd147e58a78", "workload": "dsa-1m-fp8",
                "pack_bytes": 33067 * 1024 * 2.0 + 134174 * 1024 * 1.0,
                "gather_bytes": 744743 * 1024 * 2.0 + 2708540 * 1024 * 1.0}
