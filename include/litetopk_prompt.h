@@ -120,9 +120,10 @@ size_t litetopk_attend_shared_workspace_bytes(int32_t T, int32_t Hq, int32_t n_k
  * `type`, contiguous, 16-byte aligned.  Row cu[b] + i holds the token at position
  * kv_len[b] - (cu[b+1] - cu[b]) + i of sequence b, as kv_append would place it:
  * its bytes' values times the page's scale, formed in fp32 and rounded to `type`
- * (exact in fp32, and in bf16 for the powers of two that kv_append writes).  A
- * row before its sequence's first token, past the table or on a page that is none
- * is zeros; rows outside every sequence are not written. */
+ * (exact in fp32, and in bf16 for the powers of two that kv_append writes).  T may
+ * end inside a sequence: its first rows are read then.  A row before its sequence's
+ * first token, past the table or on a page that is none is zeros; rows outside every
+ * sequence are not written. */
 int litetopk_kv_read(const ltk_kv_cache* cache, const ltk_kv_batch* batch, int32_t T, int32_t type, void* k_out,
                      void* v_out, void* stream);
 

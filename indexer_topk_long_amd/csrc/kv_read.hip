@@ -52,14 +52,14 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
     const int d = 8 * (threadIdx.x % L);
     if (row >= a.T) return;
     const int t = (int)row, b = row_seq(a.bt, t, a.T);
-    const SeqRows sr = seq_rows(a.bt, b, a.T);
-    if (t < sr.r0 || t >= sr.r1) return;
-    const int pos = sr.pos0 + (t - sr.r0);
+    // T may end inside a sequence: its rows keep their positions, which count from its last one
+    const int r1 = a.bt.cu[b + 1];
+    if (t < a.bt.cu[b] || t >= r1) return;
+    const int64_t pos = (int64_t)max(a.bt.len[b], 0) - r1 + t, page = pos >> a.c.page_shift;
     int id = -1;
-    if (pos >= 0 && (pos >> a.c.page_shift) < a.bt.max_pages)
-        id = a.bt.table[(size_t)b * a.bt.max_pages + (pos >> a.c.page_shift)];
+    if (pos >= 0 && page < a.bt.max_pages) id = a.bt.table[(size_t)b * a.bt.max_pages + page];
     const bool have = id >= 0 && id < a.c.n_pages;
-    const int slot = pos & ((1 << a.c.page_shift) - 1);
+    const int slot = (int)pos & ((1 << a.c.page_shift) - 1);
 #pragma unroll 4
     for (int h = blockIdx.y; h < a.c.Hkv; h += gridDim.y) {
         at_u32x2 kw{0u, 0u}, vw = kw;
