@@ -123,7 +123,8 @@ size_t litetopk_attend_shared_workspace_bytes(int32_t T, int32_t Hq, int32_t n_k
  * (exact in fp32, and in bf16 for the powers of two that kv_append writes).  T may
  * end inside a sequence: its first rows are read then.  A row before its sequence's
  * first token, past the table or on a page that is none is zeros; rows outside every
- * sequence are not written. */
+ * sequence are not written.  T * n_kv_heads <= 2^31 - 256; calls that would launch
+ * 2^32 threads are refused (LTK_EINVAL): head_dim / 8 for every row. */
 int litetopk_kv_read(const ltk_kv_cache* cache, const ltk_kv_batch* batch, int32_t T, int32_t type, void* k_out,
                      void* v_out, void* stream);
 

@@ -311,6 +311,7 @@ hipError_t launch_kv_append(const AppendPlan& p, const KvCache& c, const KvBatch
                             const uint16_t* v, const uint16_t* q, int T, int Hq, const double* inv_freq, int rot,
                             int interleaved, uint16_t* q_out, hipStream_t st);
 
+bool kv_read_fits(int T, int D);
 hipError_t launch_kv_read(const KvCache& c, const KvBatch& bt, int T, int D, int type, void* k, void* v, hipStream_t st);
 
 // Launch of an attend call, fixed by its sizes alone so that the workspace

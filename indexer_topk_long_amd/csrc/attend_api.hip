@@ -204,6 +204,7 @@ int litetopk_kv_read(const ltk_kv_cache* cache, const ltk_kv_batch* batch, int32
     if (st != LTK_OK) return st;
     if (type < LTK_ROWS_BF16 || type > LTK_ROWS_FP32) return LTK_EUNSUPPORTED;
     if ((st = check_heads(T, kc.Hkv, kc.Hkv)) != LTK_OK) return st;
+    if (!kv_read_fits(T, cache->head_dim)) return LTK_EINVAL;
     if ((T > 0 && (!k_out || !v_out)) || !aligned16(k_out) || !aligned16(v_out)) return LTK_EINVAL;
     if (T == 0 || kb.n_seq == 0) return LTK_OK;
     if ((st = litetopk_device_check()) != LTK_OK) return st;

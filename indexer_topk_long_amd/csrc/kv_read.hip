@@ -88,9 +88,12 @@ hipError_t launch(const ReadArgs& a, int D, const dim3& grid, hipStream_t st) {
 
 }  // namespace
 
+static int64_t row_blocks(int T, int D) { return ((int64_t)T * (D / 8) + kThreads - 1) / kThreads; }
+
+bool kv_read_fits(int T, int D) { return grid_fits(row_blocks(T, D), kThreads); }
+
 hipError_t launch_kv_read(const KvCache& c, const KvBatch& bt, int T, int D, int type, void* k, void* v, hipStream_t st) {
-    const int rows = kThreads / (D / 8);
-    const int64_t blocks = ((int64_t)T + rows - 1) / rows;
+    const int64_t blocks = row_blocks(T, D);
     const int64_t spread = std::max<int64_t>(1, std::min<int64_t>(c.Hkv, 2048 / blocks));
     const ReadArgs a{c, bt, T, k, v};
     const dim3 grid((unsigned)blocks, (unsigned)spread);
