@@ -117,8 +117,9 @@ size_t litetopk_attend_shared_workspace_bytes(int32_t T, int32_t Hq, int32_t n_k
                                               int32_t n_group, int64_t entries);
 
 /* Reads rows of the cache back: k_out and v_out [T, n_kv_heads, head_dim] of
- * `type`, contiguous, 16-byte aligned.  Row cu[b] + i holds the token at position
- * kv_len[b] - (cu[b+1] - cu[b]) + i of sequence b, as kv_append would place it:
+ * `type`, contiguous, 16-byte aligned, without memory in common.  Row cu[b] + i
+ * holds the token at position kv_len[b] - (cu[b+1] - cu[b]) + i of sequence b, as
+ * kv_append would place it:
  * its bytes' values times the page's scale, formed in fp32 and rounded to `type`
  * (exact in fp32, and in bf16 for the powers of two that kv_append writes).  T may
  * end inside a sequence: its first rows are read then.  A row before its sequence's

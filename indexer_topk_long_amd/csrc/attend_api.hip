@@ -207,6 +207,10 @@ int litetopk_kv_read(const ltk_kv_cache* cache, const ltk_kv_batch* batch, int32
     if (!kv_read_fits(T, cache->head_dim)) return LTK_EINVAL;
     if ((T > 0 && (!k_out || !v_out)) || !aligned16(k_out) || !aligned16(v_out)) return LTK_EINVAL;
     if (T == 0 || kb.n_seq == 0) return LTK_OK;
+    // (rows of both would be written in no order)
+    const size_t bytes = (size_t)T * kc.Hkv * cache->head_dim * (type == LTK_ROWS_FP32 ? 4 : 2);
+    const uintptr_t ka = (uintptr_t)k_out, va = (uintptr_t)v_out;
+    if ((ka < va ? va - ka : ka - va) < bytes) return LTK_EINVAL;
     if ((st = litetopk_device_check()) != LTK_OK) return st;
     return launch_kv_read(kc, kb, T, cache->head_dim, type, k_out, v_out, static_cast<hipStream_t>(stream)) == hipSuccess
                ? LTK_OK

@@ -251,6 +251,9 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2) refuse(PyExc_TypeError, "out must be a pair of tensors (k, v)");
             out[0] = tensor(PyTuple_GET_ITEM(a[6], 0), "out k", kind, {T, c.n_kv_heads, c.head_dim}, cache.dev);
             out[1] = tensor(PyTuple_GET_ITEM(a[6], 1), "out v", kind, {T, c.n_kv_heads, c.head_dim}, cache.dev);
+            const auto ka = (uintptr_t)out[0].data_ptr(), va = (uintptr_t)out[1].data_ptr();
+            if ((ka < va ? va - ka : ka - va) < out[0].nbytes())
+                refuse(PyExc_ValueError, "out k and out v share memory");
         }
         const On on(cache.dev);
         const int rc = litetopk_kv_read(&c, &b, T, type == at::kBFloat16 ? LTK_ROWS_BF16 : type == at::kHalf ? LTK_ROWS_FP16 : LTK_ROWS_FP32,

@@ -70,7 +70,8 @@ def kv_read(cache, page_table, cu, kv_len, T: int, dtype=None, out=None):
     dtype (bfloat16, the default, float16 or float32).  Row cu[b] + i is the token
     at position kv_len[b] - (cu[b+1] - cu[b]) + i of sequence b, where kv_append
     puts a row of that number; T may end inside a sequence, whose first rows are read
-    then.  Rows without a token are zeros.  out is a pair of tensors to write to.  Rows outside every sequence are not written."""
+    then.  Rows without a token are zeros.  out is a pair of tensors to write to,
+    which share no memory.  Rows outside every sequence are not written."""
     if dtype is None:
         import torch
         dtype = torch.bfloat16

@@ -29,3 +29,18 @@ def test_offsets_at_the_ends_of_32_bits(lib):
     cu = torch.tensor([-(2 ** 31), 2 ** 31 - 1], dtype=torch.int32, device="cuda")
     for x in lib.kv_read(cache, table.cuda(), cu, n.cuda(), 20):
         assert not bool(x.any())
+
+
+def test_out_tensors_that_share_memory_are_refused(lib):
+    import torch
+    g = _gen(33)
+    table, cu, n, pages = make_batch(g, [20], [20], 16)
+    cache = [x.cuda() for x in make_cache(g, pages, 2, 16, 64)]
+    args = cache, table.cuda(), cu.cuda(), n.cuda(), 20
+    both = torch.zeros(40, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for pair in ((both[:20],) * 2, (both[:20], both[19:39]), (both[1:21], both[:20])):
+        with pytest.raises(ValueError, match="share memory"):
+            lib.kv_read(*args, out=pair)
+    assert not bool(both.any())
+    got, want = lib.kv_read(*args, out=(both[20:], both[:20])), lib.kv_read(*args)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

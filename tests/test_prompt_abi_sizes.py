@@ -1,7 +1,7 @@
 """Sizes and places that the prompts' operators refuse before any device call."""
 import pytest
 
-from tests.test_attend_abi import EINVAL, OK
+from tests.test_attend_abi import EINVAL, OK, P
 from tests.test_prompt_abi import _read, lib  # noqa: F401
 
 
@@ -11,3 +11,12 @@ def test_reads_of_2_to_the_32_threads(D, most):
     assert _read(T=most, **kw) == OK
     for T in (most + 1, 1 << 30, (1 << 31) - 256):
         assert _read(T=T, **kw) == EINVAL
+
+
+@pytest.mark.parametrize("at", [0, 16, -16, 2 * 4 * 2 * 128 - 16, 16 - 2 * 4 * 2 * 128])
+def test_reads_into_one_place_twice(at):
+    """T 4, two heads, D 128: 2,048 bytes each in 16 bits, 4,096 in 32."""
+    for type_ in (0, 1, 2):
+        assert _read(ko=P, vo=P + at, type=type_, n_kv_heads=2) == EINVAL
+    assert _read(ko=P, vo=P + 2048 + at % 2048, type=2, n_kv_heads=2) == EINVAL
+    assert _read(ko=P, vo=P + at, T=0) == OK
