@@ -66,10 +66,10 @@ struct Call {
         ws_at = ws.data_ptr();
     }
 
-    PyObject* result(int rc, const char* where, PyObject* out_o) {
+    PyObject* result(int rc, const char* where, PyObject* out_o, const char* sizes = "attend_workspace_bytes") {
         if (rc == LTK_EWORKSPACE)
             refuse(PyExc_ValueError, "workspace too small: " + std::to_string(ws_bytes) +
-                                         " bytes (attend_workspace_bytes gives what suffices)");
+                                         " bytes (" + sizes + " gives what suffices)");
         if (rc != LTK_OK) failed(rc, where);
         if (own_out) return THPVariable_Wrap(out);
         in_place(out);
@@ -198,7 +198,7 @@ PyObject* attend_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return x.result(litetopk_attend_shared(&c, &x.batch, x.q, x.T, x.Hq, static_cast<const int32_t*>(gr.data_ptr()),
                                                static_cast<const int32_t*>(sl.data_ptr()), ng, x.scale, x.out.data_ptr(),
                                                x.ws_at, x.ws_bytes, on.stream),
-                        "litetopk_attend_shared", a[8]);
+                        "litetopk_attend_shared", a[8], "attend_shared_workspace_bytes");
     });
 }
 
