@@ -52,7 +52,8 @@ ltk_rows rows_of(const at::Tensor& t, at::Tensor& held) {
         held = t.contiguous();
         // (contiguous already, but not aligned)
         if (((uintptr_t)held.data_ptr() & 15u) != 0) held = held.clone();
-        return {held.data_ptr(), held.stride(0), held.stride(1)};
+        // (not its own strides: those of dimensions of size 1 stay what they were)
+        return {held.data_ptr(), t.size(0) > 1 ? t.size(1) * t.size(2) : 0, t.size(2)};
     }
     return {t.data_ptr(), r, h};
 }
