@@ -183,7 +183,7 @@ PyObject* attend_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (v.size(0) != k.size(0))
             refuse(PyExc_ValueError, "k has " + std::to_string(k.size(0)) + " rows, v " + std::to_string(v.size(0)));
         const int dev = q.get_device();
-        size32(q.size(0), "q"), size32(q.size(1), "q"), size32(k.size(0), "k"), size32(k.size(1), "k");
+        size32(q.size(0), "q"), size32(q.size(1), "q"), size32(q.size(2), "q"), size32(k.size(0), "k"), size32(k.size(1), "k");
         if (k.size(1) < 1 || q.size(1) < 1 || q.size(1) % k.size(1) != 0)
             refuse(PyExc_ValueError, "q has " + std::to_string(q.size(1)) + " heads, k " + std::to_string(k.size(1)) +
                                          ": not a multiple");

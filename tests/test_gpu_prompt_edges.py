@@ -26,3 +26,11 @@ def test_any_stride_of_a_dimension_of_one(lib, shape, strides):
     got = (out,) + torch.autograd.grad(out, leaves, lay(data[3]))
     for name, x in zip(("out", "dq", "dk", "dv"), got):
         check(name, x, want[name])
+
+
+def test_a_head_dim_past_32_bits_is_refused(lib):
+    import torch
+    q = torch.empty(0, 1, (1 << 32) + 64, dtype=torch.bfloat16, device="cuda")
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="too large"):
+        lib.attend_prompt(q, q, q, cu)
