@@ -70,8 +70,9 @@ typedef struct {
  * last positions: row cu[b] + i is at position kv_len[b] - (cu[b+1] - cu[b]) + i.
  * kv_len counts the rows of the call.  Token s of sequence b is in page
  * page_table[b][s / page_size], slot s % page_size.
- * n_seq >= 0, max_pages >= 1, max_pages * page_size <= 2^31 - 128 (key offsets
- * past a tile's end stay in int32). */
+ * 0 <= n_seq <= 2^30 (the sum of two sequences' numbers stays in int32),
+ * max_pages >= 1, max_pages * page_size <= 2^31 - 128 (key offsets past a tile's end
+ * stay in int32). */
 typedef struct {
     const int32_t* page_table;   /* [n_seq, max_pages] */
     const int32_t* cu;           /* [n_seq + 1] */

@@ -94,8 +94,9 @@ int litetopk_attend_prompt_backward(const ltk_prompt* p, const ltk_rows* q, cons
  * first tokens, as answers to one prompt do: the result of litetopk_attend, but
  * the shared keys are read once for all rows of a group.
  *
- *  groups      [n_group + 1] int32, non-decreasing: group j is the sequences
- *              groups[j] .. groups[j+1]-1; sequences in no group share nothing
+ *  groups      [n_group + 1] int32, non-decreasing, n_group <= 2^30: group j is the
+ *              sequences groups[j] .. groups[j+1]-1; sequences in no group share
+ *              nothing
  *  shared_len  [n_group] int32: tokens that the group's sequences share (clamped
  *              to the table).  Their keys are read through the page table of the
  *              group's first sequence; those from shared_len on, which may lie

@@ -15,6 +15,8 @@ namespace {
 constexpr int64_t kMaxTokens = 0x7fffffff - 127;
 // Rows times query heads: a unit's rows past the last one stay in 32 bits.
 constexpr int64_t kMaxRows = 0x7fffffff - 255;
+// Sequences or groups: the sum of two of their numbers stays in 32 bits.
+constexpr int32_t kMaxSeqs = 1 << 30;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -23,7 +25,8 @@ int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ?
 // Sizes and pointers of the cache and the batch; T rows.
 int check_cache(const ltk_kv_cache* c, const ltk_kv_batch* b, int32_t T, bool need_cu, KvCache& kc, KvBatch& kb) {
     if (!c || !b || T < 0) return LTK_EINVAL;
-    if (c->n_pages < 1 || c->n_kv_heads < 1 || b->n_seq < 0 || b->max_pages < 1) return LTK_EINVAL;
+    if (c->n_pages < 1 || c->n_kv_heads < 1 || b->n_seq < 0 || b->n_seq > kMaxSeqs || b->max_pages < 1)
+        return LTK_EINVAL;
     if (c->head_dim != 64 && c->head_dim != 128) return LTK_EUNSUPPORTED;
     const int sh = page_shift(c->page_size);
     if (sh < 0) return LTK_EUNSUPPORTED;
@@ -167,7 +170,7 @@ int litetopk_attend_shared(const ltk_kv_cache* cache, const ltk_kv_batch* batch,
     AttendArgs a{};
     int st = attend_args(cache, batch, q, T, Hq, scale, out, ws, true, a);
     if (st != LTK_OK) return st;
-    if (n_group < 0 || (T > 0 && batch->n_seq > 0 && n_group > 0 && (!groups || !shared_len))) return LTK_EINVAL;
+    if (n_group < 0 || n_group > kMaxSeqs || (T > 0 && batch->n_seq > 0 && n_group > 0 && (!groups || !shared_len))) return LTK_EINVAL;
     const int D = cache->head_dim;
     const int64_t entries = (int64_t)batch->max_pages * cache->page_size;
     if (n_group == 0) return run_attend(LTK_ATTEND, cache, a, entries, ws, ws_bytes, stream);
