@@ -73,7 +73,8 @@ size_t litetopk_attend_prompt_workspace_bytes(const ltk_prompt* p, int32_t backw
  * takes out + rest, so that the rounding of out is not in its gradients.
  *
  * Scores, statistics and sums are fp32; a weight is rounded once to the type of
- * q for its product with the value. */
+ * q for its product with the value (relative to the row's largest one, in fp16 to
+ * at best 2^-25 of it). */
 int litetopk_attend_prompt(const ltk_prompt* p, const ltk_rows* q, const ltk_rows* k, const ltk_rows* v, void* out,
                            void* rest, float* lse, void* ws, size_t ws_bytes, void* stream);
 
@@ -83,9 +84,10 @@ int litetopk_attend_prompt(const ltk_prompt* p, const ltk_rows* q, const ltk_row
  *
  * With P = exp(scale q.k - lse) and delta = dout . (out + rest):
  *   dv = P^T dout,  dS = P (dout v^T - delta),  dq = scale dS k,  dk = scale dS^T q.
- * P and dS are rounded once to the type of q for these products (in fp16, values
- * of dS below 2^-24 vanish and those past 65504 are infinite: scale the loss);
- * sums are fp32, in a fixed order. */
+ * P and dS are rounded once to the type of q for these products; sums are fp32, in
+ * a fixed order.  In fp16, values of dS below 2^-25 vanish and those past 65504 are
+ * infinite (scale the loss), and P is held 2^14 times its size, so that only
+ * weights below 2^-39 vanish from dv. */
 int litetopk_attend_prompt_backward(const ltk_prompt* p, const ltk_rows* q, const ltk_rows* k, const ltk_rows* v,
                                     const void* out, const void* rest, const float* lse, const ltk_rows* dout,
                                     void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, void* stream);

@@ -24,7 +24,13 @@ typedef short pr_i16x8 __attribute__((ext_vector_type(8)));
 // columns and 16 summands.  (Lane (c, g) = (lane % 32, lane / 32) holds the
 // summands 8 g .. 8 g + 7 of row or column c; of the result column c, rows
 // 8 (r / 4) + 4 g + r % 4.)
+//
+// kUp, kDown = 2^-kUp: the weights of dv's product, at most 1, are held 2^kUp times
+// their size, and dv is scaled back in fp32.  fp16's normal range ends at 2^-14:
+// unscaled, weights below 2^-25 (a key that no row looks at much, in a long
+// sequence) would leave nothing in dv, whatever the loss is scaled by.
 struct PrBf16 {
+    static constexpr float kUp = 0.0f, kDown = 1.0f;
     static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_bf16(a, b); }
     static __device__ __forceinline__ pr_f32x16 mfma(at_u32x4 a, at_u32x4 b, pr_f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(at_bf16x8, a), __builtin_bit_cast(at_bf16x8, b),
@@ -34,6 +40,7 @@ struct PrBf16 {
     static __device__ __forceinline__ float hi(uint32_t w) { return bf16_hi(w); }
 };
 struct PrF16 {
+    static constexpr float kUp = 14.0f, kDown = 0x1p-14f;
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         const at_f32x2 x{a, b};
         return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, at_f16x2));
@@ -56,7 +63,7 @@ struct PromptArgs {
     const uint16_t *out_in, *rest_in;   // backward: the forward call's out and rest
     uint16_t *out, *rest, *dq, *dk, *dv;
     float* lse;
-    float *lse2, *delta;      // backward: [T, Hq], log2(e) lse and dout . out
+    float *lse2, *delta;      // backward, for dk and dv: [T, Hq], log2(e) lse - kUp and kDown dout . (out + rest)
     const int32_t *cu, *cu_k;
     int n_seq, T, S, Hq, Hkv, G;
     uint32_t div_g, one_g;    // ceil(2^32 / G), or 0 and all ones for G == 1

@@ -5,8 +5,9 @@
 //   dv = P^T dout,  dP = dout v^T,  dS = P (dP - delta),
 //   dq = scale dS k,  dk = scale dS^T q,
 // the last two and dv summed over the query heads of a key/value head.  P and dS
-// are rounded once to 16 bits for their products (operands of one type); sums are
-// fp32.  Two launches, so that no sum needs atomics and the same call gives the
+// are rounded once to 16 bits for their products (operands of one type; in fp16 dv's
+// weights 2^14 times their size, see kUp, which no step's time shows: 8,192 rows in
+// fp16 2,600 us a training step with and without); sums are fp32.  Two launches, so that no sum needs atomics and the same call gives the
 // same bits; scores and dout v^T are formed in both, seven products in place of
 // five:
 //  - dq: as the forward pass, 128 pairs a workgroup, queries and dout in
@@ -41,6 +42,13 @@ __device__ __forceinline__ uint8_t* lds() {
 
 // log2(e) lse, infinite for a row that sees no key (its weights are 0 then).
 __device__ __forceinline__ float base2(float lse) { return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f; }
+// A row's two numbers as the dk and dv launch takes them: its weights come out
+// 2^kUp times their size, and its score gradients as they are.
+template <class E>
+__device__ __forceinline__ void note_stats(const PromptArgs& a, int64_t row, float lse2, float delta) {
+    a.lse2[row] = lse2 - E::kUp;
+    a.delta[row] = delta * E::kDown;
+}
 
 // A lane's share of delta = dout . (out + rest): dimensions 16 j + 8 g ..; the
 // lanes c and c + 32 of a wave share a row.
@@ -77,7 +85,7 @@ __global__ __launch_bounds__(64 * kWaves) void prompt_delta_kernel(PromptArgs a)
         s = delta_share<E, D>(a, r, g, dout);
     }
     s = pr_sum_halves(s);
-    if (r < (int64_t)a.T * a.Hq && g == 0) a.delta[r] = s, a.lse2[r] = base2(a.lse[r]);
+    if (r < (int64_t)a.T * a.Hq && g == 0) note_stats<E>(a, r, base2(a.lse[r]), s);
 }
 
 // dq: units are row tiles as in the forward pass.
@@ -116,7 +124,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dq_kernel(PromptArgs a)
         lse2 = base2(a.lse[row]);
     }
     delta = pr_sum_halves(delta);
-    if (have && pl.part == 0 && g == 0) a.delta[row] = delta, a.lse2[row] = lse2;   // for the dk and dv launch
+    if (have && pl.part == 0 && g == 0) note_stats<E>(a, row, lse2, delta);
     pr_f32x16 o[D / 32];
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
@@ -362,6 +370,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
         auto fetch_stat = [&](int i) {
             if (i < 16) sf[i % kNear] = *reinterpret_cast<const at_f32x2*>(stat + (i / 8) * kPairs + 8 * (i % 8 / 2) + 2 * (i % 2));
         };
+        auto less_delta = [](float dp, float delta) {   // (the factor is a power of two: dp - delta, rounded, times it)
+            return E::kUp == 0.0f ? dp - delta : __builtin_fmaf(dp, E::kDown, -delta);
+        };
         pr_f32x16 x, y;
         at_u32x4 pf[2], ds[2];
 #pragma unroll
@@ -407,7 +418,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
             fetch(2 * N + j + kAhead);
 #pragma unroll
             for (int i = 8 / N * j; i < 8 / N * (j + 1); ++i) {
-                ds[i / 4][i % 4] = E::pack(x[2 * i] * (y[2 * i] - sf[i % kNear][0]), x[2 * i + 1] * (y[2 * i + 1] - sf[i % kNear][1]));
+                const float z0 = less_delta(y[2 * i], sf[i % kNear][0]), z1 = less_delta(y[2 * i + 1], sf[i % kNear][1]);
+                ds[i / 4][i % 4] = E::pack(x[2 * i] * z0, x[2 * i + 1] * z1);
                 fetch_stat(8 + i + kNear);
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -426,7 +438,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_dkv_kernel(PromptArgs a
     if (parts.used <= 1) {
         const int64_t row = (int64_t)(s.k0 + key) * a.Hkv + h;
         pr_store_row<E, D>(a.dk + row * D, g, dk, a.scale);
-        pr_store_row<E, D>(a.dv + row * D, g, dv, 1.0f);
+        pr_store_row<E, D>(a.dv + row * D, g, dv, E::kDown);
         return;
     }
     // a part: 128 keys' dk, then their dv
@@ -467,6 +479,7 @@ __global__ __launch_bounds__(2 * D) void prompt_dkv_join_kernel(PromptArgs a) {
     const int64_t row = (int64_t)(s.k0 + ka + r) * a.Hkv + h;
     *reinterpret_cast<at_u32x2*>(a.dk + row * D + d) =
         at_u32x2{E::pack(x[0] * a.scale, x[1] * a.scale), E::pack(x[2] * a.scale, x[3] * a.scale)};
+    y *= E::kDown;
     *reinterpret_cast<at_u32x2*>(a.dv + row * D + d) = at_u32x2{E::pack(y[0], y[1]), E::pack(y[2], y[3])};
 }
 

@@ -34,3 +34,47 @@ def test_a_head_dim_past_32_bits_is_refused(lib):
     cu = torch.zeros(1, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError, match="too large"):
         lib.attend_prompt(q, q, q, cu)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 2])
+@pytest.mark.parametrize("n", [250, 900])
+def test_gradients_of_values_with_small_weights_in_fp16(lib, n, G, D):
+    """Weights of 2^-30 to 2^-24, beside one of about 1, under a scaled loss: dv to fp16's own precision.
+
+    The bounds of prompt_ref, but for its 2^-25 of a weight: dv_s = sum_i P_is dout_i is off by
+      u |dv_s| + sum_i (P_is (u + 2 E + N 2^-23) + 2^-39) |dout_i| + 2^-25
+    over the N rows and heads, where 2^-39 is half a step of fp16 below 2^-14 for weights held 2^14 times
+    their size, and 2^-25 that of the result."""
+    import torch
+    m, u = n + 70, 2.0 ** -11
+    g = torch.Generator().manual_seed(n + G + D)
+    q, k = torch.zeros(n, G, D, dtype=torch.float16), torch.zeros(m, 1, D, dtype=torch.float16)
+    q[:, :, 0] = 1
+    k[1:, 0, 0] = (-17.0 - 3.5 * torch.rand(m - 1, generator=g)).half()
+    v = torch.randn(m, 1, D, generator=g).half()
+    dout = (2.0 ** 12 * torch.randn(n, G, D, generator=g)).half()
+    cu, ck = lens_to_cu([n]), lens_to_cu([m])
+    leaves = [x.cuda().requires_grad_() for x in (q, k, v)]
+    out = lib.attend_prompt(*leaves, cu.cuda(), ck.cuda(), scale=1.0)
+    got = dict(zip(("dq", "dk", "dv"), torch.autograd.grad(out, leaves, dout.cuda())))
+    want = ref(q, k, v, cu, ck, 1.0, 0, dout)
+    for name in ("dq", "dk"):
+        check(name, got[name], want[name])
+    x = k[:, 0, 0].double().expand(n, m).masked_fill(torch.arange(m) > m - n + torch.arange(n)[:, None], -torch.inf)
+    P = torch.softmax(x, -1)
+    assert float(P[:, 1:].max()) < 2.0 ** -24 and float(P[-1, 1:].min()) > 2.0 ** -30
+    lse = torch.logsumexp(x, -1).abs().max()
+    E = (D + 8) * 2.0 ** -24 * (2 * 20.5 + float(lse)) + 2.0 ** -22
+    val = torch.zeros(m, D, dtype=torch.float64)
+    size = torch.zeros_like(val)
+    for h in range(G):
+        val += P.T @ dout[:, h].double()
+        size += (P * (u + 2 * E + n * G * 2.0 ** -23) + 2.0 ** -39 * (P > 0)).T @ dout[:, h].double().abs()
+    top = torch.finfo(torch.float16).max        # (of the key of weight 1 the sum passes it, and is infinite)
+    check("dv", got["dv"][:, 0].clamp(-top, top), (val.clamp(-top, top), size + u * val.abs() + 2.0 ** -25))
+    # where dq is not asked for, the same bits
+    k1, v1 = (x.cuda().requires_grad_() for x in (k, v))
+    out = lib.attend_prompt(q.cuda(), k1, v1, cu.cuda(), ck.cuda(), scale=1.0)
+    dk, dv = torch.autograd.grad(out, (k1, v1), dout.cuda())
+    assert torch.equal(dk, got["dk"]) and torch.equal(dv, got["dv"])
