@@ -90,6 +90,7 @@ inline const at::Tensor& tensor(PyObject* o, const char* name, Kind kind, std::i
     without_grad(t, name);
     if (!t.is_cuda() || !t.is_contiguous())
         refuse(PyExc_ValueError, std::string(name) + " must be a contiguous device tensor");
+    if (t.is_neg()) refuse(PyExc_ValueError, std::string(name) + " is a view of negated values: resolve_neg() lays them out");
     if (dev >= 0 && t.get_device() != dev)
         refuse(PyExc_ValueError, std::string(name) + " is on cuda:" + std::to_string(t.get_device()) + ", the cache on cuda:" +
                                      std::to_string(dev) + ": all tensors must share one device");

@@ -41,15 +41,16 @@ const at::Tensor& rows_tensor(PyObject* o, const char* name, const at::Tensor* l
     return t;
 }
 
-// Rows as the library takes them; other strides are laid out anew, in `held`.
+// Rows as the library takes them; other strides, and values that wait for their
+// negation, are laid out anew, in `held`.
 ltk_rows rows_of(const at::Tensor& t, at::Tensor& held) {
     constexpr int64_t kRow = 1 << 23, kHead = 1 << 27;
     held = t;
     const int64_t r = t.size(0) > 1 ? t.stride(0) : 0, h = t.size(1) > 1 ? t.stride(1) : 0;
-    const bool fits = (t.size(2) <= 1 || t.stride(2) == 1) && r % 8 == 0 && h % 8 == 0 && r <= kRow && h <= kHead &&
+    const bool fits = !t.is_neg() && (t.size(2) <= 1 || t.stride(2) == 1) && r % 8 == 0 && h % 8 == 0 && r <= kRow && h <= kHead &&
                       ((uintptr_t)t.data_ptr() & 15u) == 0;
     if (!fits && t.numel() > 0) {
-        held = t.contiguous();
+        held = t.resolve_neg().contiguous();
         // (contiguous already, but not aligned)
         if (((uintptr_t)held.data_ptr() & 15u) != 0) held = held.clone();
         // (not its own strides: those of dimensions of size 1 stay what they were)

@@ -78,3 +78,24 @@ def test_gradients_of_values_with_small_weights_in_fp16(lib, n, G, D):
     out = lib.attend_prompt(q.cuda(), k1, v1, cu.cuda(), ck.cuda(), scale=1.0)
     dk, dv = torch.autograd.grad(out, (k1, v1), dout.cuda())
     assert torch.equal(dk, got["dk"]) and torch.equal(dv, got["dv"])
+
+
+def test_views_of_negated_values(lib):
+    """A tensor whose negation waits for its first use: taken as what it stands for, or refused."""
+    import torch
+    q, k, v, dout = [x.cuda() for x in make(5, [50], [50], 4, 2, 64, torch.bfloat16)]
+    cu = lens_to_cu([50]).cuda()
+    neg = torch._neg_view
+    leaves = [neg(x).detach().requires_grad_() for x in (q, k, v)]
+    out = lib.attend_prompt(*leaves, cu)
+    got = (out,) + torch.autograd.grad(out, leaves, neg(dout))
+    plain = [(-x).requires_grad_() for x in (q, k, v)]
+    out = lib.attend_prompt(*plain, cu)
+    want = (out,) + torch.autograd.grad(out, plain, -dout)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    cache = [torch.zeros(4, 2, 16, 64, device="cuda").to(torch.float8_e4m3fn) for _ in range(2)]
+    scale = torch.ones(4, 2, device="cuda")
+    table, n = torch.zeros(1, 4, dtype=torch.int32, device="cuda"), torch.full((1,), 50, dtype=torch.int32, device="cuda")
+    for c, x in (((*cache, neg(scale), scale), q), ((*cache, scale, scale), neg(q))):
+        with pytest.raises(ValueError, match="negated"):
+            lib.attend(x, c, table, cu, n)
