@@ -197,8 +197,9 @@ struct AttendArgs {
 // What a launch of the dense kernels attends to: all keys of a sequence; the
 // keys that a group shares, met by the rows of all its sequences and left as
 // sums in `prior`; or a sequence's own keys behind those, beginning from them.
-// (64 rows, 64 heads on 8, D = 128: 32,768 shared tokens take 96 us in the wide
-// kernel, 720 TFLOP/s, and 8 to join; up to 1,000 own tokens each 23 and 5.)
+// (64 rows, 64 heads on 8, D = 128: 32,768 shared tokens take 96 to 99 us in the wide
+// kernel, 700 to 720 TFLOP/s, and 8 to join; up to 1,000 own tokens each 23 and 5.
+// 64 sequences of eight rows each: 580 us in all with 100 own tokens, 611 with 1,000.)
 enum Part { kAllKeys, kSharedKeys, kOwnKeys };
 // A row of prior: D sums, the reference m, the divisor l.
 constexpr int kPriorTail = 4;

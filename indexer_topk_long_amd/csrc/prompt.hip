@@ -27,13 +27,15 @@
 //    sequence of 16,384 rows 4,450 us against 4,105.)
 //
 // One sequence of 16,384 rows (64 heads on 8, D = 128, bf16: 4.4e12 operations)
-// takes 4,100 to 4,300 us, 1,020 to 1,070 TFLOP/s of the 1,207 that a large matrix
+// takes 4,080 to 4,330 us, 1,020 to 1,080 TFLOP/s of the 1,207 that a large matrix
 // product reaches: the matrix units are busy 56 % of the cycles, the vector units
-// 57 %.  16 prompts of up to 2,039 rows (32 on 8) take 227 to 237 us, 720 to 750
+// 57 %.  The causal test costs every step something, where no key is hidden too: it
+// is compiled to a scalar branch for each of a lane's 32 scores, and nothing moves
+// between them.  16 prompts of up to 2,039 rows (32 on 8) take 224 to 246 us, 690 to 760
 // TFLOP/s: units are 11 steps long on average, and finding the unit, its first
 // tile and its stores take 14 % of a unit's time.  Two of up to 8,111 with a
-// window of 1,024 (D = 64, fp16) take 160 us, 690 TFLOP/s: half the products for
-// the same exponentials.  The smallest calls take 6 us: launch, offsets, tile.
+// window of 1,024 (D = 64, fp16) take 155 to 166 us, 670 to 710 TFLOP/s: half the
+// products for the same exponentials and branches.  The smallest calls take 6 us: launch, offsets, tile.
 #include <math.h>
 
 #include <algorithm>
@@ -255,13 +257,22 @@ hipError_t launch(const PromptPlan& p, const PromptArgs& a, hipStream_t st) {
 // place has to do.  `units` are about those with rows, `mean` the steps of one in
 // a sequence of average length, `most` those in a sequence that is all of the
 // batch.  The parts pass through memory and the joining launch costs some steps'
-// time: parts have `least` steps or more, and cutting has to take that many off
-// the longest unit (about the geometric mean of twice the mean and the most).
+// time: parts have `least` steps or more, but for a unit's last one, and cutting
+// has to take that many off the longest unit (about the geometric mean of twice
+// the mean and the most).
 // (Forward, 32 heads on 8, D = 128: 1,024 units for the 768 places 180 us whole
 // and 197 cut, four prompts of 1,024 rows 57 whole and 84 cut, one of 2,048, 512
 // units, 72 cut; a step of 8,192 rows 3,065 us with dk and dv whole, 2,510 cut.
 // 64 heads on 8, 1,000 rows: dq's 500 units of 16 steps or less cut cost the step
 // 12 us of 177.)
+//
+// The rule goes by totals, which is all that the host knows, so it does not see one
+// sequence that is far longer than all others: its units stay whole where the others
+// make enough units, and there are few parts a unit where they make many.  (One row
+// each, 32 heads on 8, D = 128: 250 sequences, one of 65,536 keys and the others of
+// 500, 2,360 us, 250 of as many keys in all 153; 128 such, 840 and 136.  A training
+// step of 100 sequences of 256 rows beside one of 8,192: 3,550 us, the long one alone
+// 2,420.)
 static PromptCut cut(int64_t all, double units, double mean, int64_t most, int Hkv, int64_t places, int64_t least) {
     PromptCut c{all, all * Hkv, 1, 1 << 30};
     const int64_t per = std::max(least, (int64_t)(1.1 * units * Hkv * mean / places) + 1);

@@ -5,11 +5,11 @@
 //   dv = P^T dout,  dP = dout v^T,  dS = P (dP - delta),
 //   dq = scale dS k,  dk = scale dS^T q,
 // the last two and dv summed over the query heads of a key/value head.  P and dS
-// are rounded once to 16 bits for their products (operands of one type; in fp16 dv's
-// weights 2^14 times their size, see kUp, which no step's time shows: 8,192 rows in
-// fp16 2,600 us a training step with and without); sums are fp32.  Two launches, so that no sum needs atomics and the same call gives the
-// same bits; scores and dout v^T are formed in both, seven products in place of
-// five:
+// are rounded once to 16 bits for their products (operands of one type; in fp16
+// dv's weights 2^14 times their size, see kUp: a step of 8,192 rows takes 2,600 us
+// with and without); sums are fp32.  Two launches, so that no sum needs atomics and
+// the same call gives the same bits; scores and dout v^T are formed in both, seven
+// products in place of five:
 //  - dq: as the forward pass, 128 pairs a workgroup, queries and dout in
 //    registers, 64 keys a step through LDS.  It notes lse2 and delta for the other.
 //  - dk and dv: 128 keys of a key/value head a workgroup, 32 a wave; the pairs
@@ -18,9 +18,10 @@
 //    and score gradients are operands of the products over pairs in place.
 //
 // One sequence of 8,192 rows (32 heads on 8, D = 128, bf16): dq 840 to 910 us (930
-// TFLOP/s of its three products), dk and dv 1,220 to 1,280 us (850 to 900 of their
-// four; the matrix units are busy 51 % of the cycles in which a CU has work, and 7
-// % of them it has none); with the forward pass 2,500 to 2,570 us.
+// TFLOP/s of its three products; some of its scores' causal tests are branches, and
+// the others are made in every step), dk and dv 1,190 to 1,280 us (850 to 920 of
+// their four; the matrix units are busy 51 % of the cycles in which a CU has work,
+// and 7 % of them it has none); with the forward pass 2,440 to 2,590 us.
 #include <algorithm>
 #include <atomic>
 
