@@ -73,8 +73,8 @@ size_t litetopk_attend_prompt_workspace_bytes(const ltk_prompt* p, int32_t backw
  * takes out + rest, so that the rounding of out is not in its gradients.
  *
  * Scores, statistics and sums are fp32; a weight is rounded once to the type of
- * q for its product with the value (relative to the row's largest one, in fp16 to
- * at best 2^-25 of it). */
+ * q for its product with the value (in fp16, weights below 2^-32 of the row's
+ * largest may vanish). */
 int litetopk_attend_prompt(const ltk_prompt* p, const ltk_rows* q, const ltk_rows* k, const ltk_rows* v, void* out,
                            void* rest, float* lse, void* ws, size_t ws_bytes, void* stream);
 
@@ -122,12 +122,11 @@ size_t litetopk_attend_shared_workspace_bytes(int32_t T, int32_t Hq, int32_t n_k
 /* Reads rows of the cache back: k_out and v_out [T, n_kv_heads, head_dim] of
  * `type`, contiguous, 16-byte aligned, without memory in common.  Row cu[b] + i
  * holds the token at position kv_len[b] - (cu[b+1] - cu[b]) + i of sequence b, as
- * kv_append would place it:
- * its bytes' values times the page's scale, formed in fp32 and rounded to `type`
- * (exact in fp32, and in bf16 for the powers of two that kv_append writes).  T may
- * end inside a sequence: its first rows are read then.  A row before its sequence's
- * first token, past the table or on a page that is none is zeros; rows outside every
- * sequence are not written.  T * n_kv_heads <= 2^31 - 256; calls that would launch
+ * kv_append would place it: its bytes' values times the page's scale, formed in fp32
+ * and rounded to `type` (exact in fp32, and in bf16 for the powers of two that
+ * kv_append writes).  T may end inside a sequence: its first rows are read then.  A
+ * row before its sequence's first token, past the table or on a page that is none is
+ * zeros; rows outside every sequence are not written.  T * n_kv_heads <= 2^31 - 256; calls that would launch
  * 2^32 threads are refused (LTK_EINVAL): head_dim / 8 for every row. */
 int litetopk_kv_read(const ltk_kv_cache* cache, const ltk_kv_batch* batch, int32_t T, int32_t type, void* k_out,
                      void* v_out, void* stream);

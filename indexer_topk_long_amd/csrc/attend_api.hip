@@ -170,7 +170,8 @@ int litetopk_attend_shared(const ltk_kv_cache* cache, const ltk_kv_batch* batch,
     AttendArgs a{};
     int st = attend_args(cache, batch, q, T, Hq, scale, out, ws, true, a);
     if (st != LTK_OK) return st;
-    if (n_group < 0 || n_group > kMaxSeqs || (T > 0 && batch->n_seq > 0 && n_group > 0 && (!groups || !shared_len))) return LTK_EINVAL;
+    if (n_group < 0 || n_group > kMaxSeqs) return LTK_EINVAL;
+    if (T > 0 && batch->n_seq > 0 && n_group > 0 && (!groups || !shared_len)) return LTK_EINVAL;
     const int D = cache->head_dim;
     const int64_t entries = (int64_t)batch->max_pages * cache->page_size;
     if (n_group == 0) return run_attend(LTK_ATTEND, cache, a, entries, ws, ws_bytes, stream);

@@ -4,7 +4,8 @@
 //   y_s = scale log2(e) (q . k_s),  out = sum 2^(y_s - m) v_s / l,
 //   l = sum 2^(y_s - m),  lse = ln(2) (m + log2 l),
 // one pass with a running reference m that moves only where a score passes it by
-// 8 (kSlack): most steps need no exchange between lanes and scale nothing.
+// 8 (kSlack): most steps need no exchange between lanes and scale nothing.  In fp16
+// m lies 7 below the score that it moved to (kLift).
 //
 // A workgroup of four waves takes 128 (row, head) pairs of one key/value head,
 // 32 a wave, and 64 keys a step.  The query heads that share a key/value head lie
@@ -35,7 +36,8 @@
 // TFLOP/s: units are 11 steps long on average, and finding the unit, its first
 // tile and its stores take 14 % of a unit's time.  Two of up to 8,111 with a
 // window of 1,024 (D = 64, fp16) take 155 to 166 us, 670 to 710 TFLOP/s: half the
-// products for the same exponentials and branches.  The smallest calls take 6 us: launch, offsets, tile.
+// products for the same exponentials and branches.  The smallest calls take 6 us:
+// launch, offsets, tile.
 #include <math.h>
 
 #include <algorithm>
@@ -140,10 +142,10 @@ __global__ __launch_bounds__(64 * kWaves, 3) void prompt_kernel(PromptArgs a) {
         if (__ballot(top > over) != 0) {
             const float up = pr_max_halves(top);
             const bool move = up > over;
-            const float d = move ? up : 0.0f;
-            const float f = over == kSlack ? __builtin_amdgcn_exp2f(-d) : 1.0f;
+            const float d = move ? up - E::kLift : 0.0f;
+            const float f = over == E::kLift + kSlack ? __builtin_amdgcn_exp2f(-d) : 1.0f;
             m += d;
-            over = move ? kSlack : over;
+            over = move ? E::kLift + kSlack : over;
             l *= f;
 #pragma unroll
             for (int t = 0; t < D / 32; ++t) o[t] *= f;

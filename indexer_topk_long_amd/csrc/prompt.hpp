@@ -29,8 +29,13 @@ typedef short pr_i16x8 __attribute__((ext_vector_type(8)));
 // their size, and dv is scaled back in fp32.  fp16's normal range ends at 2^-14:
 // unscaled, weights below 2^-25 (a key that no row looks at much, in a long
 // sequence) would leave nothing in dv, whatever the loss is scaled by.
+//
+// kLift: the forward pass' weights are at most 2^kLift when its reference moves, and
+// at most 2^(kLift + kSlack) until it moves again: below fp16's 65504, and as far
+// above its smallest values as that allows (many small weights may be all there is
+// of a result).
 struct PrBf16 {
-    static constexpr float kUp = 0.0f, kDown = 1.0f;
+    static constexpr float kUp = 0.0f, kDown = 1.0f, kLift = 0.0f;
     static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_bf16(a, b); }
     static __device__ __forceinline__ pr_f32x16 mfma(at_u32x4 a, at_u32x4 b, pr_f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(at_bf16x8, a), __builtin_bit_cast(at_bf16x8, b),
@@ -40,7 +45,7 @@ struct PrBf16 {
     static __device__ __forceinline__ float hi(uint32_t w) { return bf16_hi(w); }
 };
 struct PrF16 {
-    static constexpr float kUp = 14.0f, kDown = 0x1p-14f;
+    static constexpr float kUp = 14.0f, kDown = 0x1p-14f, kLift = 7.0f;
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         const at_f32x2 x{a, b};
         return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, at_f16x2));

@@ -99,3 +99,33 @@ def test_views_of_negated_values(lib):
     for c, x in (((*cache, neg(scale), scale), q), ((*cache, scale, scale), neg(q))):
         with pytest.raises(ValueError, match="negated"):
             lib.attend(x, c, table, cu, n)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", [1, 4096])                 # keys in parts, each with its own largest weight, or whole
+@pytest.mark.parametrize("n,m", [(1, 40000), (70, 20000), (300, 9000)])
+def test_many_small_weights_in_fp16(lib, n, m, heads, D):
+    """Weights of 2^-30 to 2^-24.5 of the largest, whose own value is 0: what they sum to.
+
+    The bound of prompt_ref for out, with 2^-32 of the row's largest weight in place of 2^-25 (half a step of fp16
+    below 2^-14 for weights held 2^7 times their size) and half a step of the result below 2^-14:
+      u |out| + (u + 2 E + m 2^-23) sum_s P_s |v_s| + 2^-32 m max|v| + 2^-25."""
+    import torch
+    u = 2.0 ** -11
+    g = torch.Generator().manual_seed(m + D)
+    q, k = torch.zeros(n, 1, D, dtype=torch.float16), torch.zeros(m, 1, D, dtype=torch.float16)
+    q[:, :, 0] = 1
+    k[1:, 0, 0] = (-17.0 - 3.5 * torch.rand(m - 1, generator=g)).half()
+    v = (1 + 0.25 * torch.randn(m, 1, D, generator=g)).half()
+    v[0] = 0
+    dev = [t.cuda().expand(-1, heads, -1) for t in (q, k, v)]
+    out = lib.attend_prompt(*dev, lens_to_cu([n]).cuda(), lens_to_cu([m]).cuda(), scale=1.0)
+    assert bool((out == out[:, :1]).all())
+    x = k[:, 0, 0].double().expand(n, m).masked_fill(torch.arange(m) > m - n + torch.arange(n)[:, None], -torch.inf)
+    P = torch.softmax(x, -1)
+    assert float(P[:, 1:].max()) < 2.0 ** -24
+    E = (D + 8) * 2.0 ** -24 * (2 * 20.5 + 0.1) + 2.0 ** -22
+    val, size = P @ v[:, 0].double(), P @ v[:, 0].double().abs()
+    tol = u * val.abs() + (u + 2 * E + m * 2.0 ** -23) * size + 2.0 ** -32 * m * float(v.abs().max()) + 2.0 ** -25
+    assert float((tol / val).max()) < 0.25               # (so that sums without them are told apart)
+    check("out", out[:, 0], (val, tol))
