@@ -28,7 +28,7 @@
 //    sequence of 16,384 rows 4,450 us against 4,105.)
 //
 // One sequence of 16,384 rows (64 heads on 8, D = 128, bf16: 4.4e12 operations)
-// takes 4,080 to 4,330 us, 1,020 to 1,080 TFLOP/s of the 1,207 that a large matrix
+// takes 4,080 to 4,380 us, 1,000 to 1,080 TFLOP/s of the 1,207 that a large matrix
 // product reaches: the matrix units are busy 56 % of the cycles, the vector units
 // 57 %.  The causal test costs every step something, where no key is hidden too: it
 // is compiled to a scalar branch for each of a lane's 32 scores, and nothing moves
